@@ -148,7 +148,8 @@ rlcs_status rlcs_qk_norm_rope_backward(
  * arrays; token i attends to tokens j <= i of its own sequence:
  *   P_ij = softmax_j(scale * q_i . k_j),  o_i = sum_j P_ij v_j
  *   lse_i = log sum_j exp(scale * q_i . k_j)            (natural logarithm)
- * Query head h reads key/value head h / (Hq/Hk); Hq is a multiple of Hk. q
+ * for scale > 0. Query head h reads key/value head h / (Hq/Hk); Hq is a
+ * multiple of Hk. q
  * [tokens, Hq, D], k and v [tokens, Hk, D], with token and head strides that
  * are multiples of 8 and 16-byte aligned bases (RLCS_ERR_MISALIGNED
  * otherwise). D is a multiple of 8 up to 128. cu_seqlens [sequences + 1]

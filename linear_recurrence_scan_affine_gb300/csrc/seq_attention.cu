@@ -4,6 +4,7 @@
 // The softmax runs over the keys in one pass with a running maximum and sum;
 // scores are kept in base 2 (scale * log2 e folded into one factor).
 #include "seq_common.cuh"
+#include "tensor_core.cuh"
 
 namespace rlcs {
 namespace seq {
@@ -91,27 +92,258 @@ __device__ __forceinline__ void attend(const float *qs, const bf *k, int64_t kt,
   }
 }
 
-__global__ void __launch_bounds__(128) attention_kernel(const AttnArgs p) {
-  __shared__ float qs[4][128];
-  pdl_wait();
+// ---------------------------------------------------------------------------
+// Tiles of 128 tokens of one sequence
+// ---------------------------------------------------------------------------
+constexpr int kTile = 128;
+
+// Tile `index` in the order of sequences, longest rows first within each
+// (its last tile first): the sequence's bounds and the tile's number, or
+// false past the last tile. One warp; every lane gets the result.
+struct Tile {
+  int lo, len, first;  // the sequence's first token and length; the tile's first row in it
+};
+__device__ __forceinline__ bool find_tile(const int32_t *cu, int64_t sequences, int64_t tokens,
+                                          int64_t index, int lane, Tile &t) {
+  for (int64_t s0 = 0; s0 < sequences; s0 += 32) {
+    int lo = 0, len = 0;
+    if (s0 + lane < sequences) {
+      const int64_t a = cu[s0 + lane] < 0 ? 0 : cu[s0 + lane];
+      const int64_t b = cu[s0 + lane + 1] < tokens ? cu[s0 + lane + 1] : tokens;
+      lo = (int)a;
+      len = b > a ? (int)(b - a) : 0;
+    }
+    const int tiles = (len + kTile - 1) / kTile;
+    int upto = tiles;  // tiles of this group's sequences up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(kFull, upto, o);
+      if (lane >= o) upto += n;
+    }
+    const unsigned hit = __ballot_sync(kFull, index < upto);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      t.lo = __shfl_sync(kFull, lo, src);
+      t.len = __shfl_sync(kFull, len, src);
+      t.first = (__shfl_sync(kFull, upto, src) - 1 - (int)index) * kTile;
+      return true;
+    }
+    index -= __shfl_sync(kFull, upto, 31);
+  }
+  return false;
+}
+
+// Tiles that well-formed bounds can need.
+int64_t tile_bound(int64_t sequences, int64_t tokens) {
+  return tokens / kTile + (sequences < tokens ? sequences : tokens);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Record a wait that ran out where rlcs_check_status looks for it.
+__device__ __forceinline__ void report_timeout(WsHeader *ws) {
+  atomicMax(&ws->status, (uint32_t)RLCS_ERR_TIMEOUT);
+}
+
+// ---------------------------------------------------------------------------
+// Forward: a block per query tile and head, two blocks per SM.
+//
+// Warps 0..3 (a query row per thread) turn scores into weights; warp 4 copies
+// tiles in; warp 5 issues the products. Per key tile, in tensor memory:
+//   S = Q K^T (128 fp32 columns), P over S (64 columns of bf16 pairs),
+//   O += P V (DP fp32 columns).
+// Products run in the order they are issued, so the next tile's S follows
+// the product that reads P. While one block's weights are formed the other
+// block's products keep the tensor cores busy. Key tiles run from the
+// diagonal down, so only the first needs the mask. The running maximum is
+// raised only when it grows by more than 2^8 (weights then stay within fp32
+// and bf16 range, and the final division removes the common factor), so O is
+// rarely rescaled.
+// ---------------------------------------------------------------------------
+template <int DP>
+struct ForwardSmem {
+  alignas(1024) unsigned char q[DP * 256], k[DP * 256], v[DP * 256];
+  uint64_t q_full, k_full, k_empty, v_full, v_empty, s_full, p_ready, o_full;
+  uint32_t tmem;
+  int abort;
+};
+
+struct ForwardArgs {
+  const int32_t *cu;
+  bf *o;
+  float *lse;
+  WsHeader *ws;
+  int64_t sequences, tokens;
+  int Hq, group, D;
+  float scale2;  // scale * log2 e
+};
+
+template <int DP>
+__global__ void __launch_bounds__(192, 2)
+    attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, const ForwardArgs p) {
+  extern __shared__ unsigned char raw[];
+  ForwardSmem<DP> &sm = *reinterpret_cast<ForwardSmem<DP> *>(
+      raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023));
+  pdl_wait();  // before tensor memory is taken: an earlier grid's blocks may still need it
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = (int64_t)blockIdx.x * 4 + warp, i = row / p.Hq, h = row % p.Hq;
-  if (i >= p.tokens) return;
-  int64_t lo, hi;
-  sequence_of(p, i, lo, hi);
-  if (lo == hi) return;
-  stage(qs[warp], p.q + i * p.qt + h * p.qh, lane, p.D);
-  __syncwarp();
-  const int64_t g = h / p.group;
-  float acc[4] = {}, m, l;
-  attend(qs[warp], p.k + lo * p.kt + g * p.kh, p.kt, p.v + lo * p.vt + g * p.vh, p.vt, i - lo + 1,
-         p.D, p.scale * kLog2e, lane, acc, m, l);
+  const int h = blockIdx.x % p.Hq;
+  Tile t;
+  if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.Hq, lane, t)) return;
+  const int steps = t.first / kTile + 1;
+  const int rows = t.len - t.first < kTile ? t.len - t.first : kTile;
+  if (threadIdx.x == 0) {
+    for (uint64_t *b : {&sm.q_full, &sm.k_full, &sm.k_empty, &sm.v_full, &sm.v_empty, &sm.s_full,
+                        &sm.o_full})
+      mbar_init(b, 1);
+    mbar_init(&sm.p_ready, 128);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) tc::tmem_alloc(&sm.tmem, 256);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tS = sm.tmem, tO = sm.tmem + 128;
+  volatile int *abort = &sm.abort;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      tc::load_tile<DP>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
+      for (int it = 0; it < steps; ++it) {
+        const int row = t.lo + t.first - it * kTile;
+        if (it > 0 && !tc::mbar_wait(&sm.k_empty, (it - 1) & 1, abort)) break;
+        tc::load_tile<DP>(sm.k, &mk, &sm.k_full, h / p.group, row);
+        if (it > 0 && !tc::mbar_wait(&sm.v_empty, (it - 1) & 1, abort)) break;
+        tc::load_tile<DP>(sm.v, &mv, &sm.v_full, h / p.group, row);
+      }
+    }
+  } else if (warp == 5) {
+    const uint32_t q = tc::smem_addr(sm.q), k = tc::smem_addr(sm.k), v = tc::smem_addr(sm.v);
+    bool ok = tc::warp_wait(&sm.q_full, 0, abort);
+    for (int it = 0; it < steps && ok; ++it) {
+      ok = tc::warp_wait(&sm.k_full, it & 1, abort);
+      if (!ok) break;
+      if (lane == 0) {
+        tc::product_nt<DP>(tS, q, k);
+        tc::commit(&sm.k_empty);
+        tc::commit(&sm.s_full);
+      }
+      __syncwarp();
+      ok = tc::warp_wait(&sm.v_full, it & 1, abort);
+      if (!ok) break;
+      // values past the sequence's end meet weights of zero: they must be finite
+      if (it == 0 && rows < kTile) tc::clear_rows<DP>(sm.v, rows, lane);
+      __syncwarp();
+      ok = tc::warp_wait(&sm.p_ready, it & 1, abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (lane == 0) {
+        tc::product_nn<DP>(tO, tS, v, it > 0);
+        tc::commit(&sm.v_empty);
+        if (it + 1 == steps) tc::commit(&sm.o_full);
+      }
+      __syncwarp();
+    }
+  } else {
+    const int r = threadIdx.x;  // this thread's row of the tile
+    const uint32_t mine = (uint32_t)(warp * 32) << 16;
+    float m = 0.0f, l = 0.0f;
+    bool ok = true;
+    for (int it = 0; it < steps; ++it) {
+      ok = tc::warp_wait(&sm.s_full, it & 1, abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      uint32_t s[4][32];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (lane + 32 * e < p.D)
-      p.o[(i * p.Hq + h) * p.D + lane + 32 * e] = __float2bfloat16_rn(acc[e] / l);
-  if (p.lse && lane == 0) p.lse[h * p.tokens + i] = (m + log2f(l)) * kLn2;
+      for (int c = 0; c < 4; ++c) tc::ld32(tS + mine + c * 32, s[c]);
+      tc::wait_ld();
+      if (it == 0) {  // the diagonal tile
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c > r) s[c / 32][c % 32] = 0xff800000u;
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 128; ++c) top = fmaxf(top, __uint_as_float(s[c / 32][c % 32]));
+      top *= p.scale2;
+      if (it == 0) {
+        m = top == -INFINITY ? 0.0f : top;
+      } else {
+        const bool raise = top > m + 8.0f;
+        if (__any_sync(kFull, raise)) {
+          const float f = raise ? ex2(m - top) : 1.0f;
+          if (raise) m = top;
+          l *= f;
+#pragma unroll
+          for (int c = 0; c < DP / 32; ++c) {
+            uint32_t o[32];
+            tc::ld32(tO + mine + c * 32, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tc::st32(tO + mine + c * 32, o);
+          }
+        }
+      }
+      float sum[4] = {};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int e = c * 64 + 2 * i;
+          const float a = ex2(fmaf(__uint_as_float(s[e / 32][e % 32]), p.scale2, -m));
+          const float b = ex2(fmaf(__uint_as_float(s[e / 32][e % 32 + 1]), p.scale2, -m));
+          sum[i % 4] += a + b;
+          w[i] = pack_bf16(a, b);
+        }
+        tc::st32(tS + mine + c * 32, w);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tc::wait_st();
+      tc::fence_before_sync();
+      tc::mbar_arrive(&sm.p_ready);
+    }
+    if (ok) ok = tc::warp_wait(&sm.o_full, 0, abort);
+    if (ok) {
+      tc::fence_after_sync();
+      const float inv = 1.0f / l;
+      const int64_t row = (int64_t)t.lo + t.first + r;
+      bf *o = p.o + (row * p.Hq + h) * p.D;
+#pragma unroll
+      for (int c = 0; c < DP / 32; ++c) {
+        uint32_t a[32];
+        tc::ld32(tO + mine + c * 32, a);
+        tc::wait_ld();
+        if (r < rows)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c * 32 + i * 8 < p.D) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16(__uint_as_float(a[i * 8 + 2 * e]) * inv,
+                                 __uint_as_float(a[i * 8 + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4 *>(o + c * 32 + i * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+      }
+      if (p.lse && r < rows) p.lse[(int64_t)h * p.tokens + row] = (m + log2f(l)) * kLn2;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (sm.abort) {  // copies in flight land before the block's shared memory is given back
+    for (int i = 0; i < 1000; ++i) __nanosleep(2000);
+    if (threadIdx.x == 0) report_timeout(p.ws);
+  }
+  if (warp == 5) tc::tmem_dealloc(sm.tmem, 256);
 }
 
 // delta_i = sum_d dout_id out_id
@@ -239,7 +471,21 @@ bool attn_sizes(int64_t sequences, int64_t tokens, int64_t Hq, int64_t Hk, int64
                 rlcs_dtype t) {
   return sequences >= 0 && tokens >= 0 && tokens <= INT32_MAX && sequences < INT32_MAX && Hq > 0 &&
          Hk > 0 && Hq % Hk == 0 && D > 0 && D <= 128 && D % 8 == 0 && t == RLCS_BF16 &&
-         scale == scale && product_fits(tokens, Hq, D) && tokens * Hq < (int64_t)4 * INT32_MAX;
+         scale > 0.0 && scale <= 3.0e38 && product_fits(tokens, Hq, D) && tile_bound(sequences, tokens) * Hq < (int64_t)INT32_MAX &&
+         tokens * Hq < (int64_t)4 * INT32_MAX;
+}
+
+template <int DP>
+cudaError_t launch_forward(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                           const ForwardArgs &a, int64_t grid, cudaStream_t st) {
+  // at least 76 KB, so that no third block of 64-wide heads waits on an SM
+  // for tensor memory that two blocks hold
+  constexpr size_t need = sizeof(ForwardSmem<DP>) + 1024, least = 76 * 1024;
+  constexpr size_t smem = need < least ? least : need;
+  const cudaError_t e = allow_dynamic_smem<attention_kernel<DP>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_ex(attention_kernel<DP>, dim3((unsigned)grid), dim3(192), smem, st, true, mq, mk, mv,
+                   a);
 }
 
 dim3 row_grid(int64_t rows) { return dim3((unsigned)ceil_div(rows, 4)); }
@@ -283,28 +529,25 @@ rlcs_status rlcs_attention(const void *q, int64_t q_token_stride, int64_t q_head
   if (outputs_overlap(outs, ins)) return RLCS_ERR_INVALID_ARG;
   if (!scratch || scratch_bytes < rlcs_attention_scratch_bytes(tokens, Hq) || !aligned(scratch, 16))
     return RLCS_ERR_WORKSPACE;
-  AttnArgs a = {};
-  a.q = static_cast<const bf *>(q);
-  a.k = static_cast<const bf *>(k);
-  a.v = static_cast<const bf *>(v);
-  a.qt = q_token_stride;
-  a.qh = q_head_stride;
-  a.kt = k_token_stride;
-  a.kh = k_head_stride;
-  a.vt = v_token_stride;
-  a.vh = v_head_stride;
-  a.cu = cu_seqlens;
-  a.o = static_cast<bf *>(out);
-  a.lse = lse;
-  a.sequences = sequences;
-  a.tokens = tokens;
-  a.Hq = Hq;
-  a.Hk = Hk;
-  a.D = (int)D;
-  a.group = (int)(Hq / Hk);
-  a.scale = (float)scale;
-  return launched(launch_ex(attention_kernel, row_grid(tokens * Hq), dim3(128), 0,
-                            reinterpret_cast<cudaStream_t>(stream), true, a));
+  CUtensorMap mq, mk, mv;
+  if (!tc::make_map(&mq, q, tokens, Hq, D, q_token_stride, q_head_stride) ||
+      !tc::make_map(&mk, k, tokens, Hk, D, k_token_stride, k_head_stride) ||
+      !tc::make_map(&mv, v, tokens, Hk, D, v_token_stride, v_head_stride))
+    return RLCS_ERR_CUDA;
+  const ForwardArgs a = {cu_seqlens,
+                         static_cast<bf *>(out),
+                         lse,
+                         static_cast<WsHeader *>(scratch),
+                         sequences,
+                         tokens,
+                         (int)Hq,
+                         (int)(Hq / Hk),
+                         (int)D,
+                         (float)(scale * 1.4426950408889634)};
+  const int64_t grid = tile_bound(sequences, tokens) * Hq;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return launched(D <= 64 ? launch_forward<64>(mq, mk, mv, a, grid, st)
+                          : launch_forward<128>(mq, mk, mv, a, grid, st));
 }
 
 rlcs_status rlcs_attention_backward(
