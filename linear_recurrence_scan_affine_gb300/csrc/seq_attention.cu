@@ -14,31 +14,6 @@ using bf = __nv_bfloat16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-struct AttnArgs {
-  const bf *q, *k, *v, *dout, *out;
-  int64_t qt, qh, kt, kh, vt, vh;  // token and head strides
-  const int32_t *cu;
-  float *lse;    // [Hq, tokens]
-  float *delta;  // [Hq, tokens]
-  bf *o, *dq, *dk, *dv;
-  int64_t sequences, tokens, Hq, Hk;
-  int D, group;
-  float scale;
-};
-
-// The sequence that holds token i: [lo, hi), empty if none does.
-__device__ __forceinline__ void sequence_of(const AttnArgs &p, int64_t i, int64_t &lo, int64_t &hi) {
-  int64_t a = 0, b = p.sequences;  // the last s with cu[s] <= i
-  while (b - a > 1) {
-    const int64_t m = (a + b) / 2;
-    if (p.cu[m] <= i) a = m;
-    else b = m;
-  }
-  lo = p.cu[a] < 0 ? 0 : p.cu[a];
-  hi = p.cu[a + 1] < p.tokens ? p.cu[a + 1] : p.tokens;
-  if (i < lo || i >= hi) lo = hi = i;
-}
-
 __device__ __forceinline__ float dot_row(const float *s, const bf *r, int D) {
   float t = 0.0f;
   for (int d = 0; d < D; d += 8) {
@@ -149,6 +124,35 @@ __device__ __forceinline__ void report_timeout(WsHeader *ws) {
   atomicMax(&ws->status, (uint32_t)RLCS_ERR_TIMEOUT);
 }
 
+// A wait that ran out: let copies in flight land, then record it.
+__device__ __forceinline__ void settle(int abort, WsHeader *ws) {
+  if (!abort) return;
+  for (int i = 0; i < 1000; ++i) __nanosleep(2000);
+  if (threadIdx.x == 0) report_timeout(ws);
+}
+
+// One row of an fp32 accumulator, times f, to DP bf16 in global memory.
+template <int DP>
+__device__ __forceinline__ void write_row(uint32_t acc, bf *out, int D, float f, bool on) {
+#pragma unroll
+  for (int c = 0; c < DP / 32; ++c) {
+    uint32_t a[32];
+    tc::ld32(acc + c * 32, a);
+    tc::wait_ld();
+    if (on)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c * 32 + i * 8 < D) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16(__uint_as_float(a[i * 8 + 2 * e]) * f,
+                             __uint_as_float(a[i * 8 + 2 * e + 1]) * f);
+          *reinterpret_cast<uint4 *>(out + c * 32 + i * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Forward: a block per query tile and head, two blocks per SM.
 //
@@ -164,6 +168,14 @@ __device__ __forceinline__ void report_timeout(WsHeader *ws) {
 // and bf16 range, and the final division removes the common factor), so O is
 // rarely rescaled.
 // ---------------------------------------------------------------------------
+// The swizzle of tiles in shared memory counts from 1024-byte boundaries;
+// `raw` is declared on one. A block that finds it elsewhere does nothing.
+__device__ __forceinline__ bool aligned_tiles(const void *raw, WsHeader *ws) {
+  if ((tc::smem_addr(raw) & 1023) == 0) return true;
+  if (threadIdx.x == 0) atomicMax(&ws->status, (uint32_t)RLCS_ERR_CUDA);
+  return false;
+}
+
 template <int DP>
 struct ForwardSmem {
   alignas(1024) unsigned char q[DP * 256], k[DP * 256], v[DP * 256];
@@ -186,14 +198,14 @@ template <int DP>
 __global__ void __launch_bounds__(192, 2)
     attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv, const ForwardArgs p) {
-  extern __shared__ unsigned char raw[];
-  ForwardSmem<DP> &sm = *reinterpret_cast<ForwardSmem<DP> *>(
-      raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023));
+  extern __shared__ __align__(1024) unsigned char raw[];
+  ForwardSmem<DP> &sm = *reinterpret_cast<ForwardSmem<DP> *>(raw);
   pdl_wait();  // before tensor memory is taken: an earlier grid's blocks may still need it
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.x % p.Hq;
   Tile t;
+  if (!aligned_tiles(raw, p.ws)) return;
   if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.Hq, lane, t)) return;
   const int steps = t.first / kTile + 1;
   const int rows = t.len - t.first < kTile ? t.len - t.first : kTile;
@@ -315,118 +327,436 @@ __global__ void __launch_bounds__(192, 2)
       tc::fence_after_sync();
       const float inv = 1.0f / l;
       const int64_t row = (int64_t)t.lo + t.first + r;
-      bf *o = p.o + (row * p.Hq + h) * p.D;
-#pragma unroll
-      for (int c = 0; c < DP / 32; ++c) {
-        uint32_t a[32];
-        tc::ld32(tO + mine + c * 32, a);
-        tc::wait_ld();
-        if (r < rows)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (c * 32 + i * 8 < p.D) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16(__uint_as_float(a[i * 8 + 2 * e]) * inv,
-                                 __uint_as_float(a[i * 8 + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4 *>(o + c * 32 + i * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-      }
+      write_row<DP>(tO + mine, p.o + (row * p.Hq + h) * p.D, p.D, inv, r < rows);
       if (p.lse && r < rows) p.lse[(int64_t)h * p.tokens + row] = (m + log2f(l)) * kLn2;
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (sm.abort) {  // copies in flight land before the block's shared memory is given back
-    for (int i = 0; i < 1000; ++i) __nanosleep(2000);
-    if (threadIdx.x == 0) report_timeout(p.ws);
-  }
+  settle(sm.abort, p.ws);
   if (warp == 5) tc::tmem_dealloc(sm.tmem, 256);
 }
 
-// delta_i = sum_d dout_id out_id
-__global__ void __launch_bounds__(128) attention_delta_kernel(const AttnArgs p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), i = row / p.Hq, h = row % p.Hq;
-  if (i >= p.tokens) return;
-  float t = 0.0f;
-  for (int d = lane; d < p.D; d += 32)
-    t = fmaf(__bfloat162float(p.dout[row * p.D + d]), __bfloat162float(p.out[row * p.D + d]), t);
-  t = warp_sum(t);
-  if (lane == 0) p.delta[h * p.tokens + i] = t;
-}
+// ---------------------------------------------------------------------------
+// Gradient. delta_i = sum_d dout_id out_id first, then two kernels that each
+// form P and dS again from q, k, lse: dk and dv by key tiles, dq by query
+// tiles. Recomputing costs two of seven products, and buys results without
+// atomics: every sum has one fixed order.
+//
+// Blocks of 320 threads, one per SM (all 512 columns of tensor memory). Warps
+// 0..7 work on the scores, a tensor-memory lane per thread, warps 0..3 on
+// columns 0..63 and 4..7 on 64..127; warp 8 copies tiles; warp 9 issues
+// products. A warpgroup writes its bf16 half over its own fp32 columns, so
+// the halves of an operand start 64 columns apart.
+// ---------------------------------------------------------------------------
+struct BackwardArgs {
+  const int32_t *cu;
+  const float *lse, *delta;  // [Hq, tokens]
+  bf *dq, *dk, *dv;
+  WsHeader *ws;
+  int64_t sequences, tokens;
+  int Hq, Hk, group, D;
+  float scale, scale2;  // scale2 = scale * log2 e
+};
 
-__global__ void __launch_bounds__(128) attention_dq_kernel(const AttnArgs p) {
-  __shared__ float qs[4][128], ds[4][128];
+// 8 elements per lane, 16 lanes per row.
+__global__ void __launch_bounds__(256)
+    attention_delta_kernel(const bf *dout, const bf *out, float *delta, int64_t tokens, int Hq,
+                           int D) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = (int64_t)blockIdx.x * 4 + warp, i = row / p.Hq, h = row % p.Hq;
-  if (i >= p.tokens) return;
-  int64_t lo, hi;
-  sequence_of(p, i, lo, hi);
-  if (lo == hi) return;
-  stage(qs[warp], p.q + i * p.qt + h * p.qh, lane, p.D);
-  stage(ds[warp], p.dout + row * p.D, lane, p.D);
-  __syncwarp();
-  const int64_t g = h / p.group;
-  const float lse = p.lse[h * p.tokens + i] * kLog2e, delta = p.delta[h * p.tokens + i];
-  float acc[4] = {};
-  for (int64_t j0 = lo; j0 <= i; j0 += 32) {
-    const int64_t j = j0 + lane;
-    float t = 0.0f;
-    if (j <= i) {
-      const float pj = exp2f(dot_row(qs[warp], p.k + j * p.kt + g * p.kh, p.D) * p.scale * kLog2e -
-                             lse);
-      t = pj * (dot_row(ds[warp], p.v + j * p.vt + g * p.vh, p.D) - delta);
+  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int d = (threadIdx.x & 15) * 8;
+  float t = 0.0f;
+  if (row < tokens * Hq && d < D) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(dout + row * D + d);
+    const uint4 b = *reinterpret_cast<const uint4 *>(out + row * D + d);
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), t);
+      t = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), t);
     }
-    for (int e = 0; e < 32 && j0 + e <= i; ++e)
-      add_row(acc, __shfl_sync(kFull, t, e), p.k + (j0 + e) * p.kt + g * p.kh, lane, p.D);
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (lane + 32 * e < p.D)
-      p.dq[row * p.D + lane + 32 * e] = __float2bfloat16_rn(acc[e] * p.scale);
+  for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
+  if (row < tokens * Hq && d == 0) delta[(row % Hq) * tokens + row / Hq] = t;
 }
 
-__global__ void __launch_bounds__(128) attention_dkv_kernel(const AttnArgs p) {
-  __shared__ float ks[4][128], vs[4][128];
+// C[128 x DP] (+)= A B with A's two 64-wide halves 64 columns apart.
+template <int DP>
+__device__ __forceinline__ void product_halves(uint32_t d, uint32_t a, uint32_t b, bool add) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    tc::mma_ts(d, a + (k / 4) * 64 + (k % 4) * 8, tc::operand(b + k * 2048, 16384),
+               tc::instr(DP, true), add || k > 0);
+}
+
+__device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <int DP>
+struct KvSmem {
+  alignas(1024) unsigned char k[DP * 256], v[DP * 256], q[3][DP * 256], dout[2][DP * 256];
+  float lse[2][128], delta[2][128];
+  uint64_t k_full, v_full, q_full[3], q_empty[3], do_full[2], do_empty[2];
+  uint64_t s_full, dp_full, p_ready, ds_ready, done;
+  uint32_t tmem;
+  int abort;
+};
+
+// dk, dv: a block per key tile and key/value head, over the query tiles at
+// and after it of every query head of the group. In tensor memory:
+//   S^T = K Q^T and dP^T = V dO^T (128 columns each), P^T and dS^T over them,
+//   dV += P^T dO and dK += dS^T Q (DP columns each).
+// Issue order dV(i), S(i+1), dK(i), dP(i+1): P(i+1) is formed while dK(i) and
+// dP(i+1) run, dS(i+1) while dV(i+1) and S(i+2) run.
+template <int DP>
+__global__ void __launch_bounds__(320, 1)
+    attention_dkv_kernel(const __grid_constant__ CUtensorMap mq,
+                         const __grid_constant__ CUtensorMap mk,
+                         const __grid_constant__ CUtensorMap mv,
+                         const __grid_constant__ CUtensorMap mdo, const BackwardArgs p) {
+  extern __shared__ __align__(1024) unsigned char raw[];
+  KvSmem<DP> &sm = *reinterpret_cast<KvSmem<DP> *>(raw);
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = (int64_t)blockIdx.x * 4 + warp, j = row / p.Hk, g = row % p.Hk;
-  if (j >= p.tokens) return;
-  int64_t lo, hi;
-  sequence_of(p, j, lo, hi);
-  if (lo == hi) return;
-  stage(ks[warp], p.k + j * p.kt + g * p.kh, lane, p.D);
-  stage(vs[warp], p.v + j * p.vt + g * p.vh, lane, p.D);
-  __syncwarp();
-  float dk[4] = {}, dv[4] = {};
-  for (int64_t h = g * p.group; h < (g + 1) * p.group; ++h)
-    for (int64_t i0 = j; i0 < hi; i0 += 32) {
-      const int64_t i = i0 + lane;
-      float pj = 0.0f, t = 0.0f;
-      if (i < hi) {
-        pj = exp2f((dot_row(ks[warp], p.q + i * p.qt + h * p.qh, p.D) * p.scale -
-                    p.lse[h * p.tokens + i]) * kLog2e);
-        t = pj * (dot_row(vs[warp], p.dout + (i * p.Hq + h) * p.D, p.D) - p.delta[h * p.tokens + i]);
-      }
-      for (int e = 0; e < 32 && i0 + e < hi; ++e) {
-        add_row(dv, __shfl_sync(kFull, pj, e), p.dout + ((i0 + e) * p.Hq + h) * p.D, lane, p.D);
-        add_row(dk, __shfl_sync(kFull, t, e), p.q + (i0 + e) * p.qt + h * p.qh, lane, p.D);
+  const int g = blockIdx.x % p.Hk;
+  Tile t;
+  if (!aligned_tiles(raw, p.ws)) return;
+  if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.Hk, lane, t)) return;
+  const int tiles = (t.len + kTile - 1) / kTile;
+  const int jt = tiles - 1 - t.first / kTile;  // the first key tile has the most query tiles
+  const int per_head = tiles - jt, steps = per_head * p.group;
+  const int rows = t.len - jt * kTile < kTile ? t.len - jt * kTile : kTile;
+  const int tail = t.len - (tiles - 1) * kTile;  // rows of the sequence's last tile
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3; ++i) mbar_init(&sm.q_full[i], 1), mbar_init(&sm.q_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.do_full[i], 1), mbar_init(&sm.do_empty[i], 1);
+    for (uint64_t *b : {&sm.k_full, &sm.v_full, &sm.s_full, &sm.dp_full, &sm.done}) mbar_init(b, 1);
+    mbar_init(&sm.p_ready, 256);
+    mbar_init(&sm.ds_ready, 256);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) tc::tmem_alloc(&sm.tmem, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tS = sm.tmem, tP = sm.tmem + 128, tV = sm.tmem + 256, tK = sm.tmem + 384;
+  volatile int *abort = &sm.abort;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      tc::load_tile<DP>(sm.k, &mk, &sm.k_full, g, t.lo + jt * kTile);
+      tc::load_tile<DP>(sm.v, &mv, &sm.v_full, g, t.lo + jt * kTile);
+      for (int i = 0; i < steps; ++i) {
+        const int h = g * p.group + i / per_head, row = t.lo + (jt + i % per_head) * kTile;
+        const int a = i % 3, b = i & 1;
+        if (i >= 3 && !tc::mbar_wait(&sm.q_empty[a], (i / 3 - 1) & 1, abort)) break;
+        tc::load_tile<DP>(sm.q[a], &mq, &sm.q_full[a], h, row);
+        if (i >= 2 && !tc::mbar_wait(&sm.do_empty[b], (i / 2 - 1) & 1, abort)) break;
+        tc::load_tile<DP>(sm.dout[b], &mdo, &sm.do_full[b], h, row);
       }
     }
+  } else if (warp == 9) {
+    const uint32_t k = tc::smem_addr(sm.k), v = tc::smem_addr(sm.v);
+    // rows past the sequence's end are another sequence's: they meet weights
+    // of zero as a second operand, so they must be finite
+    auto scores = [&](int i) {
+      const int a = i % 3;
+      if (!tc::warp_wait(&sm.q_full[a], (i / 3) & 1, abort)) return false;
+      if (i % per_head == per_head - 1 && tail < kTile) tc::clear_rows<DP>(sm.q[a], tail, lane);
+      __syncwarp();
+      if (lane == 0) {
+        tc::product_nt<DP>(tS, k, tc::smem_addr(sm.q[a]));
+        tc::commit(&sm.s_full);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto grads = [&](int i) {
+      const int b = i & 1;
+      if (!tc::warp_wait(&sm.do_full[b], (i / 2) & 1, abort)) return false;
+      if (i % per_head == per_head - 1 && tail < kTile) tc::clear_rows<DP>(sm.dout[b], tail, lane);
+      __syncwarp();
+      if (lane == 0) {
+        tc::product_nt<DP>(tP, v, tc::smem_addr(sm.dout[b]));
+        tc::commit(&sm.dp_full);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = tc::warp_wait(&sm.k_full, 0, abort) && scores(0) &&
+              tc::warp_wait(&sm.v_full, 0, abort) && grads(0);
+    for (int i = 0; i < steps && ok; ++i) {
+      ok = tc::warp_wait(&sm.p_ready, i & 1, abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (lane == 0) {
+        product_halves<DP>(tV, tS, tc::smem_addr(sm.dout[i & 1]), i > 0);
+        tc::commit(&sm.do_empty[i & 1]);
+      }
+      __syncwarp();
+      if (i + 1 < steps && !(ok = scores(i + 1))) break;
+      ok = tc::warp_wait(&sm.ds_ready, i & 1, abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (lane == 0) {
+        product_halves<DP>(tK, tP, tc::smem_addr(sm.q[i % 3]), i > 0);
+        tc::commit(&sm.q_empty[i % 3]);
+        if (i + 1 == steps) tc::commit(&sm.done);
+      }
+      __syncwarp();
+      if (i + 1 < steps) ok = grads(i + 1);
+    }
+  } else {
+    const int r = threadIdx.x & 127, half = warp >> 2;  // this thread's key row, its column half
+    const uint32_t mine = ((uint32_t)((warp & 3) * 32) << 16) + half * 64;
+    // Column statistics of step i: one value per thread, a step ahead.
+    auto column = [&](int i) {
+      const int h = g * p.group + i / per_head, at = (jt + i % per_head) * kTile + r;
+      if (at >= t.len) return half ? 0.0f : INFINITY;  // no row: weights of zero
+      const float x = (half ? p.delta : p.lse)[(int64_t)h * p.tokens + t.lo + at];
+      return half ? x : x * kLog2e;
+    };
+    float next = column(0);
+    // after a wait that ran out the loop goes on without waiting, so that
+    // every warp meets the others' barriers
+    for (int i = 0; i < steps; ++i) {
+      (half ? sm.delta : sm.lse)[i & 1][r] = next;
+      compute_barrier();
+      if (i + 1 < steps) next = column(i + 1);
+      const float *lse = &sm.lse[i & 1][half * 64], *delta = &sm.delta[i & 1][half * 64];
+      const bool diagonal = i % per_head == 0;
+      uint32_t s[64];
+      tc::warp_wait(&sm.s_full, i & 1, abort);
+      tc::fence_after_sync();
+      tc::ld32(tS + mine, *reinterpret_cast<uint32_t(*)[32]>(s));
+      tc::ld32(tS + mine + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+      tc::wait_ld();
+      uint32_t w[32];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (lane + 32 * e < p.D) {
-      p.dk[row * p.D + lane + 32 * e] = __float2bfloat16_rn(dk[e] * p.scale);
-      p.dv[row * p.D + lane + 32 * e] = __float2bfloat16_rn(dv[e]);
+      for (int c = 0; c < 64; c += 4) {
+        const float4 m = *reinterpret_cast<const float4 *>(lse + c);
+        const float mm[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s[c + e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c + e]), p.scale2, -mm[e])));
+      }
+      if (diagonal)
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (half * 64 + c < r) s[c] = 0u;
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        w[c] = pack_bf16(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+      tc::st32(tS + mine, w);
+      tc::wait_st();
+      tc::fence_before_sync();
+      tc::mbar_arrive(&sm.p_ready);
+
+      tc::warp_wait(&sm.dp_full, i & 1, abort);
+      tc::fence_after_sync();
+      uint32_t d[64];
+      tc::ld32(tP + mine, *reinterpret_cast<uint32_t(*)[32]>(d));
+      tc::ld32(tP + mine + 32, *reinterpret_cast<uint32_t(*)[32]>(d + 32));
+      tc::wait_ld();
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        const float4 m = *reinterpret_cast<const float4 *>(delta + c);
+        const float mm[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          d[c + e] = __float_as_uint(__uint_as_float(s[c + e]) *
+                                     (__uint_as_float(d[c + e]) - mm[e]));
+      }
+      if (diagonal)
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (half * 64 + c < r) d[c] = 0u;
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        w[c] = pack_bf16(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1]));
+      tc::st32(tP + mine, w);
+      tc::wait_st();
+      tc::fence_before_sync();
+      tc::mbar_arrive(&sm.ds_ready);
     }
+    if (tc::warp_wait(&sm.done, 0, abort)) {
+      tc::fence_after_sync();
+      const int64_t row = (int64_t)t.lo + jt * kTile + r;
+      bf *out = (half ? p.dk : p.dv) + (row * p.Hk + g) * p.D;
+      write_row<DP>((half ? tK : tV) + ((uint32_t)((warp & 3) * 32) << 16), out, p.D,
+                    half ? p.scale : 1.0f, r < rows);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  settle(sm.abort, p.ws);
+  if (warp == 9) tc::tmem_dealloc(sm.tmem, 512);
+}
+
+template <int DP>
+struct QSmem {
+  alignas(1024) unsigned char q[DP * 256], dout[DP * 256], k[3][DP * 256], v[2][DP * 256];
+  uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[2], v_empty[2];
+  uint64_t s_full[2], dp_full, ds_ready, done;
+  uint32_t tmem;
+  int abort;
+};
+
+// dq: a block per query tile and head, over the key tiles at and before it.
+// In tensor memory: S = Q K^T twice (128 columns each, dS over the one it
+// came from), dP = dO V^T (128), dQ += dS K (DP). Issue order dP(j+1), dQ(j),
+// S(j+2): P(j+1) is formed while dP(j+1) runs, dS(j+1) while dQ(j) and S(j+2)
+// do.
+template <int DP>
+__global__ void __launch_bounds__(320, 1)
+    attention_dq_kernel(const __grid_constant__ CUtensorMap mq,
+                        const __grid_constant__ CUtensorMap mk,
+                        const __grid_constant__ CUtensorMap mv,
+                        const __grid_constant__ CUtensorMap mdo, const BackwardArgs p) {
+  extern __shared__ __align__(1024) unsigned char raw[];
+  QSmem<DP> &sm = *reinterpret_cast<QSmem<DP> *>(raw);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h = blockIdx.x % p.Hq;
+  Tile t;
+  if (!aligned_tiles(raw, p.ws)) return;
+  if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.Hq, lane, t)) return;
+  const int steps = t.first / kTile + 1;
+  const int rows = t.len - t.first < kTile ? t.len - t.first : kTile;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3; ++i) mbar_init(&sm.k_full[i], 1), mbar_init(&sm.k_empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_empty[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+    }
+    for (uint64_t *b : {&sm.q_full, &sm.do_full, &sm.dp_full, &sm.done}) mbar_init(b, 1);
+    mbar_init(&sm.ds_ready, 256);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) tc::tmem_alloc(&sm.tmem, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tS0 = sm.tmem, tP = sm.tmem + 128, tQ = sm.tmem + 256, tS1 = sm.tmem + 384;
+  volatile int *abort = &sm.abort;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      tc::load_tile<DP>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
+      for (int j = 0; j < steps; ++j) {
+        const int row = t.lo + t.first - j * kTile, a = j % 3, b = j & 1;
+        if (j >= 3 && !tc::mbar_wait(&sm.k_empty[a], (j / 3 - 1) & 1, abort)) break;
+        tc::load_tile<DP>(sm.k[a], &mk, &sm.k_full[a], h / p.group, row);
+        if (j == 0) tc::load_tile<DP>(sm.dout, &mdo, &sm.do_full, h, t.lo + t.first);
+        if (j >= 2 && !tc::mbar_wait(&sm.v_empty[b], (j / 2 - 1) & 1, abort)) break;
+        tc::load_tile<DP>(sm.v[b], &mv, &sm.v_full[b], h / p.group, row);
+      }
+    }
+  } else if (warp == 9) {
+    const uint32_t q = tc::smem_addr(sm.q), dout = tc::smem_addr(sm.dout);
+    auto scores = [&](int j) {
+      const int a = j % 3;
+      if (!tc::warp_wait(&sm.k_full[a], (j / 3) & 1, abort)) return false;
+      // keys past the sequence's end meet a dS of zero: they must be finite
+      if (j == 0 && rows < kTile) tc::clear_rows<DP>(sm.k[a], rows, lane);
+      __syncwarp();
+      if (lane == 0) {
+        tc::product_nt<DP>(j & 1 ? tS1 : tS0, q, tc::smem_addr(sm.k[a]));
+        tc::commit(&sm.s_full[j & 1]);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto grads = [&](int j) {
+      const int b = j & 1;
+      if (!tc::warp_wait(&sm.v_full[b], (j / 2) & 1, abort)) return false;
+      if (lane == 0) {
+        tc::product_nt<DP>(tP, dout, tc::smem_addr(sm.v[b]));
+        tc::commit(&sm.dp_full);
+        tc::commit(&sm.v_empty[b]);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = tc::warp_wait(&sm.q_full, 0, abort) && scores(0) &&
+              tc::warp_wait(&sm.do_full, 0, abort) && grads(0) && (steps < 2 || scores(1));
+    for (int j = 0; j < steps && ok; ++j) {
+      ok = tc::warp_wait(&sm.ds_ready, j & 1, abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (j + 1 < steps && !(ok = grads(j + 1))) break;
+      if (lane == 0) {
+        product_halves<DP>(tQ, j & 1 ? tS1 : tS0, tc::smem_addr(sm.k[j % 3]), j > 0);
+        tc::commit(&sm.k_empty[j % 3]);
+        if (j + 1 == steps) tc::commit(&sm.done);
+      }
+      __syncwarp();
+      if (j + 2 < steps) ok = scores(j + 2);
+    }
+  } else {
+    const int r = threadIdx.x & 127, half = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int64_t row = (int64_t)t.lo + t.first + r;
+    float lse = 0.0f, delta = 0.0f;
+    if (r < rows) {
+      lse = p.lse[(int64_t)h * p.tokens + row] * kLog2e;
+      delta = p.delta[(int64_t)h * p.tokens + row];
+    }
+    bool ok = true;
+    for (int j = 0; j < steps && ok; ++j) {
+      const uint32_t at = (j & 1 ? tS1 : tS0) + lanes + half * 64;
+      uint32_t s[64], d[64];
+      ok = tc::warp_wait(&sm.s_full[j & 1], (j / 2) & 1, abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      tc::ld32(at, *reinterpret_cast<uint32_t(*)[32]>(s));
+      tc::ld32(at + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+      tc::wait_ld();
+#pragma unroll
+      for (int c = 0; c < 64; ++c)
+        s[c] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c]), p.scale2, -lse)));
+      ok = tc::warp_wait(&sm.dp_full, j & 1, abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      tc::ld32(tP + lanes + half * 64, *reinterpret_cast<uint32_t(*)[32]>(d));
+      tc::ld32(tP + lanes + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(d + 32));
+      tc::wait_ld();
+#pragma unroll
+      for (int c = 0; c < 64; ++c)
+        d[c] = __float_as_uint(__uint_as_float(s[c]) * (__uint_as_float(d[c]) - delta));
+      if (j == 0)
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (half * 64 + c > r) d[c] = 0u;
+      uint32_t w[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        w[c] = pack_bf16(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1]));
+      tc::st32(at, w);
+      tc::wait_st();
+      tc::fence_before_sync();
+      tc::mbar_arrive(&sm.ds_ready);
+    }
+    if (ok) ok = tc::warp_wait(&sm.done, 0, abort);
+    if (ok && half == 0) {
+      tc::fence_after_sync();
+      write_row<DP>(tQ + lanes, p.dq + (row * p.Hq + h) * p.D, p.D, p.scale, r < rows);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  settle(sm.abort, p.ws);
+  if (warp == 9) tc::tmem_dealloc(sm.tmem, 512);
 }
 
 struct StepArgs {
@@ -480,12 +810,32 @@ cudaError_t launch_forward(const CUtensorMap &mq, const CUtensorMap &mk, const C
                            const ForwardArgs &a, int64_t grid, cudaStream_t st) {
   // at least 76 KB, so that no third block of 64-wide heads waits on an SM
   // for tensor memory that two blocks hold
-  constexpr size_t need = sizeof(ForwardSmem<DP>) + 1024, least = 76 * 1024;
+  constexpr size_t need = sizeof(ForwardSmem<DP>), least = 76 * 1024;
   constexpr size_t smem = need < least ? least : need;
   const cudaError_t e = allow_dynamic_smem<attention_kernel<DP>>(smem);
   if (e != cudaSuccess) return e;
   return launch_ex(attention_kernel<DP>, dim3((unsigned)grid), dim3(192), smem, st, true, mq, mk, mv,
                    a);
+}
+
+template <int DP>
+cudaError_t launch_backward(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                            const CUtensorMap &mdo, const BackwardArgs &a, int64_t tiles,
+                            cudaStream_t st) {
+  // more than half an SM's shared memory, so that one block has the SM (and
+  // its tensor memory) to itself
+  constexpr size_t least = 120 * 1024, kv = sizeof(KvSmem<DP>), q = sizeof(QSmem<DP>);
+  static_assert(kv <= 232448 && q <= 232448, "a block has 227 KB of shared memory at most");
+  constexpr size_t kv_smem = kv < least ? least : kv, q_smem = q < least ? least : q;
+  cudaError_t e = allow_dynamic_smem<attention_dkv_kernel<DP>>(kv_smem);
+  if (e == cudaSuccess) e = allow_dynamic_smem<attention_dq_kernel<DP>>(q_smem);
+  if (e == cudaSuccess)
+    e = launch_ex(attention_dkv_kernel<DP>, dim3((unsigned)(tiles * a.Hk)), dim3(320), kv_smem, st,
+                  true, mq, mk, mv, mdo, a);
+  if (e == cudaSuccess)
+    e = launch_ex(attention_dq_kernel<DP>, dim3((unsigned)(tiles * a.Hq)), dim3(320), q_smem, st,
+                  true, mq, mk, mv, mdo, a);
+  return e;
 }
 
 dim3 row_grid(int64_t rows) { return dim3((unsigned)ceil_div(rows, 4)); }
@@ -581,38 +931,37 @@ rlcs_status rlcs_attention_backward(
   if (outputs_overlap(outs, ins)) return RLCS_ERR_INVALID_ARG;
   if (!scratch || scratch_bytes < rlcs_attention_scratch_bytes(tokens, Hq) || !aligned(scratch, 16))
     return RLCS_ERR_WORKSPACE;
-  AttnArgs a = {};
-  a.dout = static_cast<const bf *>(dout);
-  a.out = static_cast<const bf *>(out);
-  a.q = static_cast<const bf *>(q);
-  a.k = static_cast<const bf *>(k);
-  a.v = static_cast<const bf *>(v);
-  a.qt = q_token_stride;
-  a.qh = q_head_stride;
-  a.kt = k_token_stride;
-  a.kh = k_head_stride;
-  a.vt = v_token_stride;
-  a.vh = v_head_stride;
-  a.cu = cu_seqlens;
-  a.lse = const_cast<float *>(lse);
-  a.delta = reinterpret_cast<float *>(static_cast<char *>(scratch) + 64);
-  a.dq = static_cast<bf *>(dq);
-  a.dk = static_cast<bf *>(dk);
-  a.dv = static_cast<bf *>(dv);
-  a.sequences = sequences;
-  a.tokens = tokens;
-  a.Hq = Hq;
-  a.Hk = Hk;
-  a.D = (int)D;
-  a.group = (int)(Hq / Hk);
-  a.scale = (float)scale;
+  CUtensorMap mq, mk, mv, mdo;
+  if (!tc::make_map(&mq, q, tokens, Hq, D, q_token_stride, q_head_stride) ||
+      !tc::make_map(&mk, k, tokens, Hk, D, k_token_stride, k_head_stride) ||
+      !tc::make_map(&mv, v, tokens, Hk, D, v_token_stride, v_head_stride) ||
+      !tc::make_map(&mdo, dout, tokens, Hq, D, Hq * D, D))
+    return RLCS_ERR_CUDA;
+  float *delta = reinterpret_cast<float *>(static_cast<char *>(scratch) + 64);
+  const BackwardArgs a = {cu_seqlens,
+                          lse,
+                          delta,
+                          static_cast<bf *>(dq),
+                          static_cast<bf *>(dk),
+                          static_cast<bf *>(dv),
+                          static_cast<WsHeader *>(scratch),
+                          sequences,
+                          tokens,
+                          (int)Hq,
+                          (int)Hk,
+                          (int)(Hq / Hk),
+                          (int)D,
+                          (float)scale,
+                          (float)(scale * 1.4426950408889634)};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_ex(attention_delta_kernel, row_grid(tokens * Hq), dim3(128), 0, st, true, a);
-  if (e == cudaSuccess)
-    e = launch_ex(attention_dkv_kernel, row_grid(tokens * Hk), dim3(128), 0, st, true, a);
-  if (e == cudaSuccess)
-    e = launch_ex(attention_dq_kernel, row_grid(tokens * Hq), dim3(128), 0, st, true, a);
-  return launched(e);
+  const cudaError_t e =
+      launch_ex(attention_delta_kernel, dim3((unsigned)ceil_div(tokens * Hq, 16)), dim3(256), 0, st,
+                true, static_cast<const bf *>(dout), static_cast<const bf *>(out), delta, tokens,
+                (int)Hq, (int)D);
+  if (e != cudaSuccess) return launched(e);
+  const int64_t tiles = tile_bound(sequences, tokens);
+  return launched(D <= 64 ? launch_backward<64>(mq, mk, mv, mdo, a, tiles, st)
+                          : launch_backward<128>(mq, mk, mv, mdo, a, tiles, st));
 }
 
 size_t rlcs_attention_step_scratch_bytes(int64_t B, int64_t S, int64_t Hq, int64_t Hk, int64_t D) {

@@ -28,12 +28,11 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p) {
 constexpr uint64_t kWaitNs = 2000000000ull;  // far above any tile's time
 
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t until = globaltimer_ns() + kWaitNs;
-  while (!mbar_try_wait(bar, parity)) {
+  uint64_t until = 0;
+  for (int i = 0; !mbar_try_wait(bar, parity); ++i) {
     if (*abort) return false;
-    if (globaltimer_ns() > until) {
+    if (i == 64) until = globaltimer_ns() + kWaitNs;
+    if (i > 64 && globaltimer_ns() > until) {
       *abort = 1;
       return false;
     }
@@ -100,15 +99,6 @@ __device__ __forceinline__ void st32(uint32_t addr, const uint32_t (&r)[32]) {
       "r"(r[30]), "r"(r[31]), "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void st16(uint32_t addr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
-      : "memory");
-}
-
 // ---------------------------------------------------------------------------
 // Matrix products: D[128 x N] (+)= A[128 x 16] B[16 x N], bf16 in, fp32 out
 // ---------------------------------------------------------------------------
