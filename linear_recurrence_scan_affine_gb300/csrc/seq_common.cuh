@@ -79,6 +79,15 @@ struct Raw<float, 1> {
   __device__ __forceinline__ void clear() { w = 0.0f; }
 };
 template <>
+struct Raw<float, 2> {
+  float2 w;
+  __device__ __forceinline__ void load(const float *p) {
+    w = __ldg(reinterpret_cast<const float2 *>(p));
+  }
+  __device__ __forceinline__ float at(int i) const { return i ? w.y : w.x; }
+  __device__ __forceinline__ void clear() { w = make_float2(0.0f, 0.0f); }
+};
+template <>
 struct Raw<__nv_bfloat16, 1> {
   unsigned short w;
   __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
@@ -104,10 +113,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-template <int V>
-__device__ __forceinline__ void store(float *p, const float (&v)[V]) {
-#pragma unroll
-  for (int i = 0; i < V; ++i) p[i] = v[i];
+__device__ __forceinline__ void store(float *p, const float (&v)[1]) { *p = v[0]; }
+__device__ __forceinline__ void store(float *p, const float (&v)[2]) {
+  *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
 }
 __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[1]) {
   *p = __float2bfloat16_rn(v[0]);

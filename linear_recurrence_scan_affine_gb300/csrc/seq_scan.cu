@@ -7,28 +7,126 @@
 //   mu_t = k_t a_t (dh_t + mu_{t+1}),   L_t = dh_t + mu_{t+1},   mu_T = dh_last
 // so a step's map, (k a, k a dh), needs that step's inputs alone.
 //
-// A block owns CH channels of one batch row and walks the sequence in spans:
-// each thread takes L consecutive steps of its channels into registers,
-// composes their maps, the block joins its warps' maps through shared memory,
-// and each thread replays its steps from the state that reaches them. Every
-// input is read once. A cut's map has m = 0 and composes by selection, so a
-// non-finite state of one episode does not reach the next.
+// A warp walks the sequence for 32 or 64 channels (a row segment of 128 or
+// 256 bytes), with its inputs copied asynchronously into a ring in shared
+// memory a few chunks of steps ahead: each step costs a gate, one fma and a
+// store, and every input is read once. Where a call has too few channels to
+// fill the GPU that way, the warps of a cluster of blocks take consecutive
+// segments of the steps instead: each composes its segment's map, the maps
+// join through shared and distributed shared memory, and each replays its
+// segment from the state that reaches it, its inputs still in the ring or in
+// L2. Nothing passes through global memory and every sum has one fixed order.
+//
+// A cut's map has m = 0 and composes by selection, so a non-finite state of
+// one episode does not reach the next.
+#include <type_traits>
+
 #include "seq_common.cuh"
 
 namespace rlcs {
 namespace seq {
 namespace {
 
-constexpr int kWarps = 8;
-
-__device__ __forceinline__ FPair join(FPair outer, FPair inner) {  // inner applied first
-  if (outer.m == 0.0f) return outer;
-  return {outer.m * inner.m, fmaf(outer.m, inner.c, outer.c)};
+// V channels in float32; pairs use the two-wide fp32 instructions.
+template <int V>
+struct Vf {
+  float e[V];
+};
+template <int V>
+__device__ __forceinline__ Vf<V> fma(Vf<V> a, Vf<V> b, Vf<V> c) {
+  if constexpr (V == 2) {
+    const float2 r = __ffma2_rn(make_float2(a.e[0], a.e[1]), make_float2(b.e[0], b.e[1]),
+                                make_float2(c.e[0], c.e[1]));
+    return {r.x, r.y};
+  } else {
+    return {fmaf(a.e[0], b.e[0], c.e[0])};
+  }
 }
-__device__ __forceinline__ float reach(FPair p, float x) {
-  return p.m == 0.0f ? p.c : fmaf(p.m, x, p.c);
+template <int V>
+__device__ __forceinline__ Vf<V> mul(Vf<V> a, Vf<V> b) {
+  if constexpr (V == 2) {
+    const float2 r = __fmul2_rn(make_float2(a.e[0], a.e[1]), make_float2(b.e[0], b.e[1]));
+    return {r.x, r.y};
+  } else {
+    return {a.e[0] * b.e[0]};
+  }
+}
+template <int V>
+__device__ __forceinline__ Vf<V> add(Vf<V> a, Vf<V> b) {
+  if constexpr (V == 2) {
+    const float2 r = __fadd2_rn(make_float2(a.e[0], a.e[1]), make_float2(b.e[0], b.e[1]));
+    return {r.x, r.y};
+  } else {
+    return {a.e[0] + b.e[0]};
+  }
+}
+template <int V>
+__device__ __forceinline__ Vf<V> all(float x) {
+  Vf<V> r;
+#pragma unroll
+  for (int v = 0; v < V; ++v) r.e[v] = x;
+  return r;
+}
+template <int V>
+__device__ __forceinline__ Vf<V> one_less(Vf<V> x) {  // 1 - x
+  return fma(x, all<V>(-1.0f), all<V>(1.0f));
 }
 
+// The map x -> c + m x of a run of steps, per channel.
+template <int V>
+struct alignas(8 * V) Map {
+  Vf<V> m, c;
+};
+// A cut's map (m = 0) takes nothing of what came before, not even NaN * 0.
+template <int V>
+__device__ __forceinline__ Vf<V> reach(const Map<V> &p, Vf<V> x) {
+  Vf<V> r = fma(p.m, x, p.c);
+#pragma unroll
+  for (int v = 0; v < V; ++v) r.e[v] = p.m.e[v] == 0.0f ? p.c.e[v] : r.e[v];
+  return r;
+}
+template <int V>
+__device__ __forceinline__ Map<V> join(const Map<V> &outer, const Map<V> &inner) {  // inner first
+  return {mul(outer.m, inner.m), reach(outer, inner.c)};
+}
+// 1 - sigmoid(g) = 1 / (1 + e^g), to float32 rounding: no cancellation at
+// either end, and an infinite e^g gives 0.
+template <int V>
+__device__ __forceinline__ Vf<V> keep_out(Vf<V> g) {
+  Vf<V> e = mul(g, all<V>(1.4426950408889634f));
+#pragma unroll
+  for (int v = 0; v < V; ++v) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.e[v]));
+  e = add(e, all<V>(1.0f));
+#pragma unroll
+  for (int v = 0; v < V; ++v) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.e[v]));
+  return e;
+}
+
+// This block's rank and the number of blocks in its cluster.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Write a map to the same shared-memory place of another block of the cluster.
+template <int V>
+__device__ __forceinline__ void put_remote(const Map<V> *place, uint32_t rank, const Map<V> &v) {
+  uint32_t there;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(there)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(place))), "r"(rank));
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there + 4 * k), "f"(v.m.e[k]) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there + 4 * (V + k)), "f"(v.c.e[k])
+                 : "memory");
+  }
+}
 struct ScanArgs {
   const void *x, *gate, *h, *dh;
   const uint8_t *reset;
@@ -37,125 +135,381 @@ struct ScanArgs {
   void *out, *out2;    // h, or dx and dgate
   float *last;         // state after the walk's last step: h_last, or dh0
   int64_t T, D, groups;
+  int segment;  // steps a warp takes at a time (joined walks)
 };
 
+constexpr int kChunkBytes = 4096;  // a chunk of steps, all inputs together
+constexpr int kWarpsMax = 16;      // warps of a block that walk together
+
+// Chunks in a warp's ring: a warp that walks alone keeps three copies in
+// flight, one of 16 that share an SM two, and one that loads through
+// registers writes the next chunk while it reads the last.
+template <int CB, bool JOINED>
+constexpr int ring_chunks() {
+  return CB == 0 ? 2 : (JOINED ? 3 : 4);
+}
+
+template <int CB>
+__device__ __forceinline__ void copy_async(uint32_t dst, uintptr_t src) {
+  if constexpr (CB == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // BACK walks from t = T-1 to 0 (the gradient); step index s counts along the
-// walk, so t = s forward and T-1-s backward.
-template <class E, int V, int L, bool BACK>
-__global__ void __launch_bounds__(kWarps * 32) gated_scan_kernel(const ScanArgs p) {
-  constexpr int CH = 32 * V;
-  constexpr int kSpan = kWarps * L;
-  __shared__ FPair maps[2][kWarps][CH];
+// walk, so t = s forward and T-1-s backward. JOINED: the block's warps and
+// the cluster's blocks share one group of channels; else every warp has its
+// own. CB: bytes per asynchronous copy, or 0 for plain loads (bfloat16 rows
+// that do not start on 4-byte boundaries).
+template <class E, int V, int CB, bool BACK, bool JOINED>
+__global__ void __launch_bounds__(JOINED ? kWarpsMax * 32 : 32)
+    gated_scan_kernel(const ScanArgs p) {
+  constexpr int CH = 32 * V, kRow = CH * (int)sizeof(E), ARRAYS = BACK ? 4 : 2;
+  constexpr int kChunk = kChunkBytes / (ARRAYS * kRow);  // steps
+  constexpr int kStages = ring_chunks<CB, JOINED>();
+  constexpr int kArray = kChunk * kRow;                  // bytes
+  constexpr int kBatch = kChunk < 16 / V ? kChunk : 16 / V;
+  static_assert(kChunk <= 32 && (CB == 0 || kArray % ((CB ? CB : 1) * 32) == 0),
+                "whole rounds of copies");
+  extern __shared__ __align__(128) unsigned char ring_base[];
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t b = blockIdx.x / p.groups, ch = (blockIdx.x % p.groups) * CH + lane * V;
+  const int lane = threadIdx.x & 31;
+  const int warp = JOINED ? __shfl_sync(kFull, threadIdx.x >> 5, 0) : 0;
+  const int warps = JOINED ? (int)blockDim.x >> 5 : 1;
+  const int rank = JOINED ? (int)cluster_rank() : 0, blocks = JOINED ? (int)cluster_size() : 1;
+  const int64_t group = JOINED ? blockIdx.x / blocks : blockIdx.x;
+  const int64_t b = group / p.groups, ch = group % p.groups * CH + lane * V;
   const bool on = ch < p.D;
-  const int64_t base = b * p.T * p.D + ch;
-  const E *x = static_cast<const E *>(p.x) + base, *gate = static_cast<const E *>(p.gate) + base;
-  const E *hs = BACK ? static_cast<const E *>(p.h) + base : nullptr;
-  const E *dh = BACK ? static_cast<const E *>(p.dh) + base : nullptr;
-  E *out = static_cast<E *>(p.out) + base, *out2 = BACK ? static_cast<E *>(p.out2) + base : nullptr;
+  unsigned char *ring = ring_base + warp * kStages * kChunkBytes;
 
-  float carry[V], start[V];
+  // this lane's share of a round of copies
+  constexpr int kPer = CB ? kRow / CB : 1, kRows = CB ? 32 * CB / kRow : 1;
+  const int crow = CB ? lane / kPer : 0;
+  const int64_t cch = group % p.groups * CH + (CB ? lane % kPer * (CB / (int)sizeof(E)) : 0);
+  const bool con = cch < p.D;
+  const uint32_t cdst = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
+                        (CB ? crow * kRow + lane % kPer * CB : 0);
+  const void *const src[4] = {p.gate, BACK ? p.dh : p.x, BACK ? p.x : nullptr, p.h};
+  // Copy steps [s, end) of arrays [0, arrays) into a stage: gate, then x
+  // forward, or dh, x and the state before each step backward.
+  auto copy = [&](int64_t s, int64_t end, int stage, int arrays) {
+    if constexpr (CB != 0) {
+      if (s < end && con) {
+        const int64_t q = s + crow;
+        const int64_t at = ((b * p.T + (BACK ? p.T - 1 - q : q)) * p.D + cch) * (int64_t)sizeof(E);
+        const int64_t next = (BACK ? -p.D : p.D) * (int64_t)(kRows * sizeof(E));
+        const bool whole = s + kChunk <= end && s + kChunk < p.T;  // and none reads before t = 0
+#pragma unroll
+        for (int a = 0; a < ARRAYS; ++a) {
+          if (a >= arrays) break;
+          uintptr_t from = reinterpret_cast<uintptr_t>(src[a]) +
+                           (uintptr_t)(at - (a == 3 ? p.D * (int64_t)sizeof(E) : 0));
+          const uint32_t to = cdst + stage * kChunkBytes + a * kArray;
+#pragma unroll
+          for (int k = 0; k < kChunk / kRows; ++k, from += (uintptr_t)next)
+            if (whole || (q + k * kRows < end && (a != 3 || q + k * kRows < p.T - 1)))
+              copy_async<CB>(to + k * kRows * kRow, from);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  auto place = [&](int stage, int a, int i) {
+    return reinterpret_cast<Raw<E, V> *>(ring + stage * kChunkBytes + a * kArray + i * kRow +
+                                         lane * V * (int)sizeof(E));
+  };
+  auto value = [&](int stage, int a, int i) { return *place(stage, a, i); };
+  // The same through registers (CB = 0): each lane fetches its own column.
+  Raw<E, V> held[CB == 0 ? ARRAYS : 1][CB == 0 ? kChunk : 1];
+  auto fetch = [&](int64_t s, int64_t end, int arrays) {
+    if constexpr (CB == 0) {
+#pragma unroll
+      for (int a = 0; a < ARRAYS; ++a) {
+        if (a >= arrays) break;
+        const int64_t t0 = (BACK ? p.T - 1 - s : s) - (a == 3 ? 1 : 0);
+        const E *from = static_cast<const E *>(src[a]);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+          const int64_t t = BACK ? t0 - i : t0 + i;
+          held[a][i].clear();
+          if (on && s + i < end && t >= 0) held[a][i].load(from + (b * p.T + t) * p.D + ch);
+        }
+      }
+    }
+  };
+  auto put = [&](int stage, int arrays) {
+    if constexpr (CB == 0) {
+#pragma unroll
+      for (int a = 0; a < ARRAYS; ++a) {
+        if (a >= arrays) break;
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) *place(stage, a, i) = held[a][i];
+      }
+    }
+  };
+  // Lane i reads step s + i's reset, a chunk ahead of its use (and compares
+  // it only there, so that nothing waits for the load).
+  auto read_cut = [&](int64_t s, int64_t end) -> uint32_t {
+    const int64_t q = s + lane;
+    uint32_t v = 0;
+    if (p.reset && lane < kChunk && q < end)
+      asm volatile("ld.global.nc.u8 %0, [%1];"
+                   : "=r"(v)
+                   : "l"(p.reset + b * p.T + (BACK ? p.T - 1 - q : q)));
+    return v;
+  };
+  // Run `body` over the chunks of steps [from, end): body(s, n, cut, stage).
+  // `copied`: the ring holds them already.
+  auto walk = [&](int64_t from, int64_t end, int arrays, bool copied, auto body) {
+    if (!copied) {
+#pragma unroll
+      for (int k = 0; k < kStages - 1; ++k) copy(from + k * kChunk, end, k, arrays);
+      fetch(from, end, arrays);
+      put(0, arrays);
+    }
+    uint32_t flag = read_cut(from, end);
+    int stage = 0;
+    for (int64_t s = from; s < end; s += kChunk) {
+      if (CB != 0 && !copied) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncwarp();  // the chunk is here, and every lane is done with the stage refilled next
+        copy(s + (kStages - 1) * kChunk, end, stage == 0 ? kStages - 1 : stage - 1, arrays);
+      }
+      const bool more = CB == 0 && !copied && s + kChunk < end;
+      if (more) fetch(s + kChunk, end, arrays);
+      const uint32_t cut = p.reset ? __ballot_sync(kFull, flag != 0) : 0u;
+      flag = read_cut(s + kChunk, end);
+      body(s, (int)(end - s < kChunk ? end - s : kChunk), cut, stage);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+      if (more) put(stage, arrays);
+    }
+    if (CB != 0 && !copied) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+    }
+  };
+
+  // om = 1 - a comes from the gate; a = 1 - om is off by 2^-24 at most, which
+  // only scales what is carried. PLAIN: a whole chunk without cuts.
+  auto floats = [](const Raw<E, V> &r) {
+    Vf<V> f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) f.e[v] = r.at(v);
+    return f;
+  };
+
+  Vf<V> state = all<V>(0.0f), start = all<V>(0.0f);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    carry[v] = p.first && on ? p.first[b * p.D + ch + v] : 0.0f;
-    start[v] = BACK && p.h0 && on ? p.h0[b * p.D + ch + v] : 0.0f;
+    if (p.first && on) state.e[v] = p.first[b * p.D + ch + v];
+    if (BACK && p.h0 && on) start.e[v] = p.h0[b * p.D + ch + v];
   }
-  int buf = 0;
-  for (int64_t s0 = 0; s0 < p.T; s0 += kSpan, buf ^= 1) {
-    const int64_t s = s0 + warp * L;  // this thread's first step
-    const int n = (int)(p.T - s < L ? (p.T - s > 0 ? p.T - s : 0) : L);
-    Raw<E, V> rx[L], rg[L], rd[BACK ? L : 1], rh[BACK ? L : 1];
+
+  // Replay steps from `state`, writing the results.
+  auto replay = [&](int64_t s, int n, uint32_t cut, int stage) {
+    const int64_t t0 = BACK ? p.T - 1 - s : s, step = BACK ? -p.D : p.D;
+    E *out = static_cast<E *>(p.out) + (b * p.T + t0) * p.D + ch;
+    E *out2 = BACK ? static_cast<E *>(p.out2) + (b * p.T + t0) * p.D + ch : nullptr;
+    auto run = [&](auto plain) {
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-      const int64_t t = BACK ? p.T - 1 - (s + i) : s + i;
-      rx[i].clear();
-      rg[i].clear();
-      if (BACK) rd[i].clear(), rh[i].clear();
-      if (i < n && on) {
-        rx[i].load(x + t * p.D);
-        rg[i].load(gate + t * p.D);
-        if (BACK) {
-          rd[i].load(dh + t * p.D);
-          if (t > 0) rh[i].load(hs + (t - 1) * p.D);
-        }
-      }
-    }
-    uint32_t cut = 0;  // bit i: step i starts an episode
-    if (p.reset) {
-      bool c = false;
-      if (lane < n) c = p.reset[b * p.T + (BACK ? p.T - 1 - (s + lane) : s + lane)] != 0;
-      cut = __ballot_sync(kFull, c);
-    }
-    FPair own[V];
+      for (int i0 = 0; i0 < kChunk; i0 += kBatch) {
+        // a batch's inputs first, then its steps: the stores of one step
+        // would otherwise hold back the next step's reads
+        Vf<V> om[kBatch], y[kBatch];
+        [[maybe_unused]] Vf<V> x[BACK ? kBatch : 1], prev[BACK ? kBatch : 1];
 #pragma unroll
-    for (int v = 0; v < V; ++v) own[v] = {1.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < L; ++i)
-      if (i < n)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const Gate g = gate_of(rg[i].at(v));
-          const float m = cut >> i & 1 ? 0.0f : g.a;
-          const float c = BACK ? m * rd[i].at(v) : g.om * rx[i].at(v);
-          own[v] = join({m, c}, own[v]);
-        }
-#pragma unroll
-    for (int v = 0; v < V; ++v) maps[buf][warp][lane * V + v] = own[v];
-    __syncthreads();
-    float in[V], total[V];  // the state that reaches this thread's steps, and the span's end
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float st = carry[v];
-      in[v] = st;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) in[v] = st;
-        st = reach(maps[buf][w][lane * V + v], st);
-      }
-      total[v] = st;
-    }
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-      if (i < n && on) {
-        const int64_t t = BACK ? p.T - 1 - (s + i) : s + i;
-        float o[V], o2[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const Gate g = gate_of(rg[i].at(v));
-          const bool kept = !(cut >> i & 1);
-          if (BACK) {
-            const float lam = rd[i].at(v) + in[v];
-            const float before = kept ? (t > 0 ? rh[i].at(v) : start[v]) : 0.0f;
-            o[v] = g.om * lam;
-            o2[v] = g.a * o[v] * (before - rx[i].at(v));
-            in[v] = kept ? g.a * lam : 0.0f;
+        for (int i = 0; i < kBatch; ++i) {
+          om[i] = keep_out(floats(value(stage, 0, i0 + i)));
+          y[i] = floats(value(stage, 1, i0 + i));
+          if constexpr (BACK) {
+            x[i] = floats(value(stage, 2, i0 + i));
+            prev[i] = floats(value(stage, 3, i0 + i));
           } else {
-            const float add = g.om * rx[i].at(v);
-            in[v] = kept ? fmaf(g.a, in[v], add) : add;
-            o[v] = in[v];
+            y[i] = mul(om[i], y[i]);
           }
         }
-        store(out + t * p.D, o);
-        if (BACK) store(out2 + t * p.D, o2);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i, out += step, out2 += BACK ? step : 0) {
+          if (!plain && i0 + i >= n) break;
+          const bool kept = plain || !(cut >> (i0 + i) & 1);
+          const Vf<V> a = one_less(om[i]);
+          if constexpr (BACK) {
+            if (!plain) {
+              if (s + i0 + i == p.T - 1) prev[i] = start;
+              if (!kept) prev[i] = all<V>(0.0f);
+            }
+            const Vf<V> lam = add(y[i], state), dx = mul(om[i], lam);
+            const Vf<V> dg = mul(mul(a, dx), fma(x[i], all<V>(-1.0f), prev[i]));
+            state = mul(a, lam);
+            if (!kept) state = all<V>(0.0f);
+            if (on) {
+              store(out, dx.e);
+              store(out2, dg.e);
+            }
+          } else {
+            state = kept ? fma(a, state, y[i]) : y[i];
+            if (on) store(out, state.e);
+          }
+        }
       }
+    };
+    if (n == kChunk && cut == 0 && !(BACK && s + kChunk == p.T)) run(std::true_type{});
+    else run(std::false_type{});
+  };
+
+  if constexpr (!JOINED) {
+    walk(0, p.T, ARRAYS, false, replay);
+    if (p.last && on)
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.last[b * p.D + ch + v] = state.e[v];
+  } else {
+    Map<V>(*maps)[32] = reinterpret_cast<Map<V>(*)[32]>(
+        ring_base + warps * kStages * kChunkBytes);  // [warps][32]
+    Map<V>(*across)[32] = maps + warps;              // [blocks][32]
+    const int64_t span = (int64_t)p.segment * warps * blocks;
+    if (blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    for (int64_t w0 = 0; w0 < p.T; w0 += span) {
+      const int64_t from = w0 + (int64_t)(rank * warps + warp) * p.segment;
+      const int64_t end = from + p.segment < p.T ? from + p.segment : p.T;
+      const bool fits = p.segment <= kStages * kChunk;  // the ring keeps the segment
+      Map<V> own = {all<V>(1.0f), all<V>(0.0f)};
+      walk(from, end, fits ? ARRAYS : 2, false, [&](int64_t s, int n, uint32_t cut, int stage) {
+        auto run = [&](auto plain) {
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) {
+            if (!plain && i >= n) break;
+            const Vf<V> om = keep_out(floats(value(stage, 0, i))), a = one_less(om);
+            const Vf<V> c = mul(BACK ? a : om, floats(value(stage, 1, i)));
+            own.c = fma(a, own.c, c);
+            own.m = mul(own.m, a);
+            if (!plain && (cut >> i & 1)) {
+              own.m = all<V>(0.0f);
+              own.c = BACK ? all<V>(0.0f) : c;
+            }
+          }
+        };
+        if (n == kChunk && cut == 0) run(std::true_type{});
+        else run(std::false_type{});
+      });
+      maps[warp][lane] = own;
+      __syncthreads();
+      if (blocks > 1) {
+        // the peers have started, and have read the last window's maps
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (warp == 0) {
+          Map<V> all_of = maps[0][lane];
+          for (int w = 1; w < warps; ++w) all_of = join(maps[w][lane], all_of);
+          for (int r = 0; r < blocks; ++r) put_remote(&across[rank][lane], r, all_of);
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      }
+      Vf<V> after = state;
+      if (blocks > 1) {
+        for (int r = 0; r < blocks; ++r) {
+          if (r == rank) state = after;
+          after = reach(across[r][lane], after);
+        }
+        if (w0 + span < p.T) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      } else {
+        for (int w = 0; w < warps; ++w) after = reach(maps[w][lane], after);
+      }
+      for (int w = 0; w < warp; ++w) state = reach(maps[w][lane], state);
+      walk(from, end, ARRAYS, fits, replay);
+      if (p.last && on && from < end && end == p.T)
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.last[b * p.D + ch + v] = state.e[v];
+      state = after;
+      __syncthreads();  // every warp has read the block's maps
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = total[v];
-    if (p.last && on && n > 0 && s + n == p.T)
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.last[b * p.D + ch + v] = in[v];
   }
 }
 
-template <class E, int V, bool BACK>
+int sm_count() {
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+    return 152;
+  return v;
+}
+
+// How a call's steps are shared out. Measured on GB300, us forward / gradient:
+//  - a warp walks alone from 5 channel groups per SM on, or where the walk is
+//    short: 64 x 512 x 1024 bf16 45 / 73 against 63 / 80 joined, 128 x 40 x
+//    2048 13 / 23 against 28 / 34; with 128 groups (8 x 4096 x 1024) alone
+//    171 / 276 against 56 / 84 joined;
+//  - joined, the blocks of a cluster are as many as fill the SMs once: 2 x
+//    16384 x 1024 58 / 85 with 4, 82 / 111 with 8 and 89 / 117 with 2;
+//  - up to 8 blocks, or 16 where at most 4 clusters run (16 SMs of one
+//    processing cluster must be free at once): 1 x 30000 x 96 29 / 33 with
+//    16, 44 / 56 with 8; 1 x 131072 x 512 (8 groups) 197 / 271 and 182 / 234;
+//  - segments of 128 steps, which keep the second pass in L2, or 256 where
+//    fewer than half the SMs work: 1 x 131072 x 512 182 / 234 against 203 / 250.
+struct Share {
+  int blocks, warps, steps;  // blocks = 0: every warp alone
+};
+Share share_out(int64_t groups, int64_t T, int chunk) {
+  const int sms = sm_count();
+  if (T <= 128 || groups >= 5 * (int64_t)sms) return {0, 1, 0};
+  int blocks = 1;
+  while (blocks < (groups <= 4 ? 16 : 8) && groups * blocks * 2 <= sms &&
+         T >= (int64_t)blocks * 2 * kWarpsMax * chunk)
+    blocks *= 2;
+  const int64_t warps = ceil_div(T, 32) < kWarpsMax ? ceil_div(T, 32) : kWarpsMax;
+  const int64_t most = groups * blocks * 2 <= sms ? 256 : 128;
+  const int64_t each = ceil_div(ceil_div(T, blocks * warps), chunk) * chunk;
+  return {blocks, (int)warps, (int)(each < most ? each : most)};
+}
+
+template <class E, int V, int CB, bool BACK>
 cudaError_t launch_scan(ScanArgs a, int64_t B, cudaStream_t st) {
-  constexpr int L = 16;
+  constexpr int kRow = 32 * V * (int)sizeof(E), kChunk = kChunkBytes / ((BACK ? 4 : 2) * kRow);
   a.groups = ceil_div(a.D, 32 * V);
-  return launch_ex(gated_scan_kernel<E, V, L, BACK>, dim3((unsigned)(B * a.groups)),
-                   dim3(kWarps * 32), 0, st, true, a);
+  const int64_t groups = B * a.groups;
+  const Share share = share_out(groups, a.T, kChunk);
+  if (share.blocks == 0)
+    return launch_ex(gated_scan_kernel<E, V, CB, BACK, false>, dim3((unsigned)groups), dim3(32),
+                     ring_chunks<CB, false>() * kChunkBytes, st, true, a);
+  a.segment = share.steps;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(groups * share.blocks));
+  cfg.blockDim = dim3((unsigned)share.warps * 32);
+  cfg.dynamicSmemBytes = (size_t)share.warps * ring_chunks<CB, true>() * kChunkBytes +
+                         sizeof(Map<V>) * 32 * (size_t)(share.warps + share.blocks);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)share.blocks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  constexpr auto kernel = gated_scan_kernel<E, V, CB, BACK, true>;
+  cudaError_t e =
+      allow_dynamic_smem<kernel>(kWarpsMax * (3 * kChunkBytes + 2 * sizeof(Map<V>) * 32));
+  if (e == cudaSuccess && share.blocks > 8)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, a) : e;
+}
+
+// Two channels per lane where a pair of them can be loaded and stored
+// together, copies of 16 bytes where every row starts on such a boundary.
+template <bool BACK>
+rlcs_status run_scan(const ScanArgs &a, int64_t B, rlcs_dtype dtype, rlcs_stream_t stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uintptr_t bits = (uintptr_t)(a.D * esize(dtype));
+  for (const void *q : {a.x, a.gate, a.h, a.dh, (const void *)a.out, (const void *)a.out2})
+    bits |= reinterpret_cast<uintptr_t>(q);
+  using bf = __nv_bfloat16;
+  if (dtype == RLCS_F32)
+    return launched(bits % 16 == 0 ? launch_scan<float, 2, 16, BACK>(a, B, st)
+                                   : launch_scan<float, 1, 4, BACK>(a, B, st));
+  return launched(bits % 16 == 0  ? launch_scan<bf, 2, 16, BACK>(a, B, st)
+                  : bits % 4 == 0 ? launch_scan<bf, 2, 4, BACK>(a, B, st)
+                                  : launch_scan<bf, 1, 0, BACK>(a, B, st));
 }
 
 template <class E>
@@ -180,7 +534,7 @@ __global__ void __launch_bounds__(256)
 bool scan_sizes(int64_t B, int64_t T, int64_t D, rlcs_dtype t) {
   // a block per 32 channels at least: the grid's limit in x
   return B > 0 && T > 0 && D > 0 && known(t) && product_fits(B, T, D) &&
-         product_fits(B, ceil_div(D, 32), 1) && B * ceil_div(D, 32) < (int64_t)INT32_MAX;
+         product_fits(B, ceil_div(D, 32), 1) && B * ceil_div(D, 32) * 16 < (int64_t)INT32_MAX;
 }
 
 }  // namespace
@@ -210,11 +564,7 @@ rlcs_status rlcs_gated_scan(const void *x, const void *gate, const uint8_t *rese
   a.last = h_last;
   a.T = T;
   a.D = D;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == RLCS_F32) return launched(launch_scan<float, 1, false>(a, B, st));
-  const bool pairs = D % 2 == 0 && aligned(x, 4) && aligned(gate, 4) && aligned(h, 4);
-  return launched(pairs ? launch_scan<__nv_bfloat16, 2, false>(a, B, st)
-                        : launch_scan<__nv_bfloat16, 1, false>(a, B, st));
+  return run_scan<false>(a, B, dtype, stream);
 }
 
 rlcs_status rlcs_gated_scan_backward(const void *dh, const void *x, const void *gate,
@@ -242,12 +592,7 @@ rlcs_status rlcs_gated_scan_backward(const void *dh, const void *x, const void *
   a.last = dh0;
   a.T = T;
   a.D = D;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == RLCS_F32) return launched(launch_scan<float, 1, true>(a, B, st));
-  const bool pairs = D % 2 == 0 && aligned(x, 4) && aligned(gate, 4) && aligned(h, 4) &&
-                     aligned(dh, 4) && aligned(dx, 4) && aligned(dgate, 4);
-  return launched(pairs ? launch_scan<__nv_bfloat16, 2, true>(a, B, st)
-                        : launch_scan<__nv_bfloat16, 1, true>(a, B, st));
+  return run_scan<true>(a, B, dtype, stream);
 }
 
 rlcs_status rlcs_gated_step(const void *x, const void *gate, const uint8_t *reset,

@@ -83,6 +83,30 @@ def test_gated_scan_and_gradient(rl, B, T, D, dtype, extras):
     close("dh0", dh0, w0)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D", [(1, 6000, 33), (2, 4500, 130), (20, 700, 72), (1000, 130, 40),
+                                   (30, 150, 65), (800, 140, 3)])
+def test_gated_scan_shares(rl, B, T, D, dtype):
+    # walks shared by clusters of 16, 8 and 1 blocks and by single warps, over
+    # channels that fill a warp's columns and ones that do not
+    g, dt = gen(B + T + D), DT[dtype]
+    x, dh = rand(g, B, T, D, dtype=dt), rand(g, B, T, D, dtype=dt)
+    gate = rand(g, B, T, D, scale=2.0, shift=3.0, dtype=dt)
+    reset = torch.rand(B, T, generator=g) < 0.01
+    cx, cg, cr, cd = cuda(x, gate, reset, dh)
+    h, last = rl.rlcs_gated_scan(cx, cg, reset=cr)
+    want = ref.gated_scan(x, gate, reset)
+    close("h", h, want)
+    close("h_last", last, want[:, -1])
+    got = rl.rlcs_gated_scan_backward(cd, cx, cg, h, reset=cr)
+    again = rl.rlcs_gated_scan_backward(cd, cx, cg, h, reset=cr)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    wx, wg, w0, slack = ref.gated_scan_backward(dh, x, gate, reset)
+    close("dx", got[0], wx)
+    close("dgate", got[1], wg, slack if dtype == "bf16" else 0.0)
+    close("dh0", got[2], w0)
+
+
 def test_gated_scan_gradient_against_differences(rl):
     # the directional derivative of sum(h * dh), in float32: the quotient's own
     # rounding is about 2^-24 / eps of the terms' root sum of squares
