@@ -119,6 +119,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float2 pair(const uint32_t *r) {
+  return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // Record a wait that ran out where rlcs_check_status looks for it.
 __device__ __forceinline__ void report_timeout(WsHeader *ws) {
   atomicMax(&ws->status, (uint32_t)RLCS_ERR_TIMEOUT);
@@ -131,18 +135,35 @@ __device__ __forceinline__ void settle(int abort, WsHeader *ws) {
   if (threadIdx.x == 0) report_timeout(ws);
 }
 
-// One row of an fp32 accumulator, times f, to DP bf16 in global memory.
-template <int DP>
-__device__ __forceinline__ void write_row(uint32_t acc, bf *out, int D, float f, bool on) {
+// C[128 x DP] (+)= A B: A's 128 columns in PARTS pieces, each written by its
+// own warps over the start of the 128 / PARTS fp32 columns they had read.
+template <int DP, int PARTS>
+__device__ __forceinline__ void product_parts(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  constexpr int kSteps = 8 / PARTS;  // of 16 columns
 #pragma unroll
-  for (int c = 0; c < DP / 32; ++c) {
+  for (int k = 0; k < 8; ++k)
+    tc::mma_ts(d, a + (k / kSteps) * (128 / PARTS) + (k % kSteps) * 8,
+               tc::operand(b + k * 2048, 16384), tc::instr(DP, true), add || k > 0);
+}
+
+// The two warps of a forward block that share 32 query rows.
+__device__ __forceinline__ void pair_barrier(int quarter) {
+  asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
+}
+
+// COLS columns of one row of an fp32 accumulator, times f, to bf16 in global
+// memory; `left` of them exist.
+template <int COLS>
+__device__ __forceinline__ void write_row(uint32_t acc, bf *out, int left, float f, bool on) {
+#pragma unroll
+  for (int c = 0; c < COLS / 32; ++c) {
     uint32_t a[32];
     tc::ld32(acc + c * 32, a);
     tc::wait_ld();
     if (on)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (c * 32 + i * 8 < D) {
+        if (c * 32 + i * 8 < left) {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -156,8 +177,10 @@ __device__ __forceinline__ void write_row(uint32_t acc, bf *out, int D, float f,
 // ---------------------------------------------------------------------------
 // Forward: a block per query tile and head, two blocks per SM.
 //
-// Warps 0..3 (a query row per thread) turn scores into weights; warp 4 copies
-// tiles in; warp 5 issues the products. Per key tile, in tensor memory:
+// Warps 0..7 turn scores into weights, two threads to a query row (key columns
+// 0..63 and 64..127; they exchange maxima through shared memory): 16 such
+// warps on an SM hide each other's latencies, where 8 that held whole rows
+// spilled registers. Warp 8 copies tiles in; warp 9 issues the products. Per key tile, in tensor memory:
 //   S = Q K^T (128 fp32 columns), P over S (64 columns of bf16 pairs),
 //   O += P V (DP fp32 columns).
 // Products run in the order they are issued, so the next tile's S follows
@@ -179,6 +202,7 @@ __device__ __forceinline__ bool aligned_tiles(const void *raw, WsHeader *ws) {
 template <int DP>
 struct ForwardSmem {
   alignas(1024) unsigned char q[DP * 256], k[DP * 256], v[DP * 256];
+  float row[2][128];  // maxima, and at the end sums, of the two halves of each row
   uint64_t q_full, k_full, k_empty, v_full, v_empty, s_full, p_ready, o_full;
   uint32_t tmem;
   int abort;
@@ -195,7 +219,7 @@ struct ForwardArgs {
 };
 
 template <int DP>
-__global__ void __launch_bounds__(192, 2)
+__global__ void __launch_bounds__(320, 2)
     attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv, const ForwardArgs p) {
   extern __shared__ __align__(1024) unsigned char raw[];
@@ -213,18 +237,18 @@ __global__ void __launch_bounds__(192, 2)
     for (uint64_t *b : {&sm.q_full, &sm.k_full, &sm.k_empty, &sm.v_full, &sm.v_empty, &sm.s_full,
                         &sm.o_full})
       mbar_init(b, 1);
-    mbar_init(&sm.p_ready, 128);
+    mbar_init(&sm.p_ready, 256);
     sm.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 5) tc::tmem_alloc(&sm.tmem, 256);
+  if (warp == 9) tc::tmem_alloc(&sm.tmem, 256);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tS = sm.tmem, tO = sm.tmem + 128;
   volatile int *abort = &sm.abort;
 
-  if (warp == 4) {
+  if (warp == 8) {
     if (lane == 0) {
       tc::load_tile<DP>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
       for (int it = 0; it < steps; ++it) {
@@ -235,7 +259,7 @@ __global__ void __launch_bounds__(192, 2)
         tc::load_tile<DP>(sm.v, &mv, &sm.v_full, h / p.group, row);
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     const uint32_t q = tc::smem_addr(sm.q), k = tc::smem_addr(sm.k), v = tc::smem_addr(sm.v);
     bool ok = tc::warp_wait(&sm.q_full, 0, abort);
     for (int it = 0; it < steps && ok; ++it) {
@@ -256,34 +280,41 @@ __global__ void __launch_bounds__(192, 2)
       if (!ok) break;
       tc::fence_after_sync();
       if (lane == 0) {
-        tc::product_nn<DP>(tO, tS, v, it > 0);
+        product_parts<DP, 2>(tO, tS, v, it > 0);
         tc::commit(&sm.v_empty);
         if (it + 1 == steps) tc::commit(&sm.o_full);
       }
       __syncwarp();
     }
   } else {
-    const int r = threadIdx.x;  // this thread's row of the tile
-    const uint32_t mine = (uint32_t)(warp * 32) << 16;
+    const int r = threadIdx.x & 127, half = warp >> 2;  // this thread's row and half of the keys
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t mine = tS + lanes + half * 64;
+    const float2 k2 = make_float2(p.scale2, p.scale2);
     float m = 0.0f, l = 0.0f;
-    bool ok = true;
+    // after a wait that ran out the loop goes on without waiting, so that
+    // every warp meets its partner's barriers
     for (int it = 0; it < steps; ++it) {
-      ok = tc::warp_wait(&sm.s_full, it & 1, abort);
-      if (!ok) break;
+      tc::warp_wait(&sm.s_full, it & 1, abort);
       tc::fence_after_sync();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tc::ld32(tS + mine + c * 32, s[c]);
+      uint32_t s[64];
+      tc::ld32(mine, *reinterpret_cast<uint32_t(*)[32]>(s));
+      tc::ld32(mine + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
       tc::wait_ld();
       if (it == 0) {  // the diagonal tile
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c > r) s[c / 32][c % 32] = 0xff800000u;
+        for (int c = 0; c < 64; ++c)
+          if (half * 64 + c > r) s[c] = 0xff800000u;
       }
-      float top = -INFINITY;
+      float t4[4];
 #pragma unroll
-      for (int c = 0; c < 128; ++c) top = fmaxf(top, __uint_as_float(s[c / 32][c % 32]));
-      top *= p.scale2;
+      for (int c = 0; c < 4; ++c) t4[c] = __uint_as_float(s[c]);
+#pragma unroll
+      for (int c = 4; c < 64; ++c) t4[c % 4] = fmaxf(t4[c % 4], __uint_as_float(s[c]));
+      const float own = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+      sm.row[half][r] = own;
+      pair_barrier(warp & 3);
+      const float top = fmaxf(own, sm.row[half ^ 1][r]) * p.scale2;
       if (it == 0) {
         m = top == -INFINITY ? 0.0f : top;
       } else {
@@ -292,50 +323,57 @@ __global__ void __launch_bounds__(192, 2)
           const float f = raise ? ex2(m - top) : 1.0f;
           if (raise) m = top;
           l *= f;
-#pragma unroll
-          for (int c = 0; c < DP / 32; ++c) {
-            uint32_t o[32];
-            tc::ld32(tO + mine + c * 32, o);
+          const uint32_t acc = tO + lanes + half * (DP / 2);
+#pragma unroll 1
+          for (int c = 0; c < DP / 2; c += 16) {
+            uint32_t o[16];
+            tc::ld16(acc + c, o);
             tc::wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tc::st32(tO + mine + c * 32, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tc::st16(acc + c, o);
           }
         }
       }
-      float sum[4] = {};
+      const float2 m2 = make_float2(-m, -m);
+      float2 sum[2] = {};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        uint32_t w[32];
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int e = c * 64 + 2 * i;
-          const float a = ex2(fmaf(__uint_as_float(s[e / 32][e % 32]), p.scale2, -m));
-          const float b = ex2(fmaf(__uint_as_float(s[e / 32][e % 32 + 1]), p.scale2, -m));
-          sum[i % 4] += a + b;
-          w[i] = pack_bf16(a, b);
+        for (int i = 0; i < 16; ++i) {
+          float2 a = __ffma2_rn(pair(s + c * 32 + 2 * i), k2, m2);
+          a.x = ex2(a.x);
+          a.y = ex2(a.y);
+          sum[i & 1] = __fadd2_rn(sum[i & 1], a);
+          w[i] = pack_bf16(a.x, a.y);
         }
-        tc::st32(tS + mine + c * 32, w);
+        tc::st16(mine + c * 16, w);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       tc::wait_st();
       tc::fence_before_sync();
       tc::mbar_arrive(&sm.p_ready);
     }
-    if (ok) ok = tc::warp_wait(&sm.o_full, 0, abort);
-    if (ok) {
+    pair_barrier(warp & 3);  // the partner has read the last maximum
+    sm.row[half][r] = l;
+    pair_barrier(warp & 3);
+    l += sm.row[half ^ 1][r];
+    if (tc::warp_wait(&sm.o_full, 0, abort)) {
       tc::fence_after_sync();
-      const float inv = 1.0f / l;
       const int64_t row = (int64_t)t.lo + t.first + r;
-      write_row<DP>(tO + mine, p.o + (row * p.Hq + h) * p.D, p.D, inv, r < rows);
-      if (p.lse && r < rows) p.lse[(int64_t)h * p.tokens + row] = (m + log2f(l)) * kLn2;
+      write_row<DP / 2>(tO + lanes + half * (DP / 2),
+                        p.o + (row * p.Hq + h) * p.D + half * (DP / 2), p.D - half * (DP / 2),
+                        1.0f / l, r < rows);
+      if (p.lse && half == 0 && r < rows)
+        p.lse[(int64_t)h * p.tokens + row] = (m + log2f(l)) * kLn2;
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   settle(sm.abort, p.ws);
-  if (warp == 5) tc::tmem_dealloc(sm.tmem, 256);
+  if (warp == 9) tc::tmem_dealloc(sm.tmem, 256);
 }
 
 // ---------------------------------------------------------------------------
@@ -344,11 +382,11 @@ __global__ void __launch_bounds__(192, 2)
 // tiles. Recomputing costs two of seven products, and buys results without
 // atomics: every sum has one fixed order.
 //
-// Blocks of 320 threads, one per SM (all 512 columns of tensor memory). Warps
-// 0..7 work on the scores, a tensor-memory lane per thread, warps 0..3 on
-// columns 0..63 and 4..7 on 64..127; warp 8 copies tiles; warp 9 issues
-// products. A warpgroup writes its bf16 half over its own fp32 columns, so
-// the halves of an operand start 64 columns apart.
+// Blocks of 576 threads, one per SM (all 512 columns of tensor memory). Warps
+// 0..15 work on the scores, four threads to a row of a tile with 32 columns
+// each; warp 16 copies tiles; warp 17 issues products. A thread's bf16 piece
+// goes over its own fp32 columns, so the pieces of an operand start 32
+// columns apart.
 // ---------------------------------------------------------------------------
 struct BackwardArgs {
   const int32_t *cu;
@@ -384,16 +422,7 @@ __global__ void __launch_bounds__(256)
   if (row < tokens * Hq && d == 0) delta[(row % Hq) * tokens + row / Hq] = t;
 }
 
-// C[128 x DP] (+)= A B with A's two 64-wide halves 64 columns apart.
-template <int DP>
-__device__ __forceinline__ void product_halves(uint32_t d, uint32_t a, uint32_t b, bool add) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    tc::mma_ts(d, a + (k / 4) * 64 + (k % 4) * 8, tc::operand(b + k * 2048, 16384),
-               tc::instr(DP, true), add || k > 0);
-}
-
-__device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
 template <int DP>
 struct KvSmem {
@@ -412,7 +441,7 @@ struct KvSmem {
 // Issue order dV(i), S(i+1), dK(i), dP(i+1): P(i+1) is formed while dK(i) and
 // dP(i+1) run, dS(i+1) while dV(i+1) and S(i+2) run.
 template <int DP>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(576, 1)
     attention_dkv_kernel(const __grid_constant__ CUtensorMap mq,
                          const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mv,
@@ -435,19 +464,19 @@ __global__ void __launch_bounds__(320, 1)
     for (int i = 0; i < 3; ++i) mbar_init(&sm.q_full[i], 1), mbar_init(&sm.q_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.do_full[i], 1), mbar_init(&sm.do_empty[i], 1);
     for (uint64_t *b : {&sm.k_full, &sm.v_full, &sm.s_full, &sm.dp_full, &sm.done}) mbar_init(b, 1);
-    mbar_init(&sm.p_ready, 256);
-    mbar_init(&sm.ds_ready, 256);
+    mbar_init(&sm.p_ready, 512);
+    mbar_init(&sm.ds_ready, 512);
     sm.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) tc::tmem_alloc(&sm.tmem, 512);
+  if (warp == 17) tc::tmem_alloc(&sm.tmem, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tS = sm.tmem, tP = sm.tmem + 128, tV = sm.tmem + 256, tK = sm.tmem + 384;
   volatile int *abort = &sm.abort;
 
-  if (warp == 8) {
+  if (warp == 16) {
     if (lane == 0) {
       tc::load_tile<DP>(sm.k, &mk, &sm.k_full, g, t.lo + jt * kTile);
       tc::load_tile<DP>(sm.v, &mv, &sm.v_full, g, t.lo + jt * kTile);
@@ -460,7 +489,7 @@ __global__ void __launch_bounds__(320, 1)
         tc::load_tile<DP>(sm.dout[b], &mdo, &sm.do_full[b], h, row);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     const uint32_t k = tc::smem_addr(sm.k), v = tc::smem_addr(sm.v);
     // rows past the sequence's end are another sequence's: they meet weights
     // of zero as a second operand, so they must be finite
@@ -495,7 +524,7 @@ __global__ void __launch_bounds__(320, 1)
       if (!ok) break;
       tc::fence_after_sync();
       if (lane == 0) {
-        product_halves<DP>(tV, tS, tc::smem_addr(sm.dout[i & 1]), i > 0);
+        product_parts<DP, 4>(tV, tS, tc::smem_addr(sm.dout[i & 1]), i > 0);
         tc::commit(&sm.do_empty[i & 1]);
       }
       __syncwarp();
@@ -504,7 +533,7 @@ __global__ void __launch_bounds__(320, 1)
       if (!ok) break;
       tc::fence_after_sync();
       if (lane == 0) {
-        product_halves<DP>(tK, tP, tc::smem_addr(sm.q[i % 3]), i > 0);
+        product_parts<DP, 4>(tK, tP, tc::smem_addr(sm.q[i % 3]), i > 0);
         tc::commit(&sm.q_empty[i % 3]);
         if (i + 1 == steps) tc::commit(&sm.done);
       }
@@ -512,74 +541,78 @@ __global__ void __launch_bounds__(320, 1)
       if (i + 1 < steps) ok = grads(i + 1);
     }
   } else {
-    const int r = threadIdx.x & 127, half = warp >> 2;  // this thread's key row, its column half
-    const uint32_t mine = ((uint32_t)((warp & 3) * 32) << 16) + half * 64;
-    // Column statistics of step i: one value per thread, a step ahead.
+    const int r = threadIdx.x & 127, part = warp >> 2;  // this thread's key row, its columns
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, mine = lanes + part * 32;
+    // Column statistics of step i: one value per thread of parts 0 and 1, a
+    // step ahead.
     auto column = [&](int i) {
       const int h = g * p.group + i / per_head, at = (jt + i % per_head) * kTile + r;
-      if (at >= t.len) return half ? 0.0f : INFINITY;  // no row: weights of zero
-      const float x = (half ? p.delta : p.lse)[(int64_t)h * p.tokens + t.lo + at];
-      return half ? x : x * kLog2e;
+      if (part > 1) return 0.0f;
+      if (at >= t.len) return part ? 0.0f : INFINITY;  // no row: weights of zero
+      const float x = (part ? p.delta : p.lse)[(int64_t)h * p.tokens + t.lo + at];
+      return part ? x : x * kLog2e;
     };
     float next = column(0);
+    const float2 k2 = make_float2(p.scale2, p.scale2);
     // after a wait that ran out the loop goes on without waiting, so that
     // every warp meets the others' barriers
     for (int i = 0; i < steps; ++i) {
-      (half ? sm.delta : sm.lse)[i & 1][r] = next;
+      if (part < 2) (part ? sm.delta : sm.lse)[i & 1][r] = next;
       compute_barrier();
       if (i + 1 < steps) next = column(i + 1);
-      const float *lse = &sm.lse[i & 1][half * 64], *delta = &sm.delta[i & 1][half * 64];
+      const float *lse = &sm.lse[i & 1][part * 32], *delta = &sm.delta[i & 1][part * 32];
       const bool diagonal = i % per_head == 0;
-      uint32_t s[64];
+      uint32_t s[32], d[32], w[16];
       tc::warp_wait(&sm.s_full, i & 1, abort);
       tc::fence_after_sync();
-      tc::ld32(tS + mine, *reinterpret_cast<uint32_t(*)[32]>(s));
-      tc::ld32(tS + mine + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+      tc::ld32(tS + mine, s);
       tc::wait_ld();
-      uint32_t w[32];
 #pragma unroll
-      for (int c = 0; c < 64; c += 4) {
+      for (int c = 0; c < 32; c += 4) {
         const float4 m = *reinterpret_cast<const float4 *>(lse + c);
-        const float mm[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[c + e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c + e]), p.scale2, -mm[e])));
+        const float2 a = __ffma2_rn(pair(s + c), k2, make_float2(-m.x, -m.y));
+        const float2 b = __ffma2_rn(pair(s + c + 2), k2, make_float2(-m.z, -m.w));
+        s[c] = __float_as_uint(ex2(a.x));
+        s[c + 1] = __float_as_uint(ex2(a.y));
+        s[c + 2] = __float_as_uint(ex2(b.x));
+        s[c + 3] = __float_as_uint(ex2(b.y));
       }
       if (diagonal)
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (half * 64 + c < r) s[c] = 0u;
+        for (int c = 0; c < 32; ++c)
+          if (part * 32 + c < r) s[c] = 0u;
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
+      for (int c = 0; c < 16; ++c)
         w[c] = pack_bf16(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
-      tc::st32(tS + mine, w);
+      tc::st16(tS + mine, w);
       tc::wait_st();
       tc::fence_before_sync();
       tc::mbar_arrive(&sm.p_ready);
 
       tc::warp_wait(&sm.dp_full, i & 1, abort);
       tc::fence_after_sync();
-      uint32_t d[64];
-      tc::ld32(tP + mine, *reinterpret_cast<uint32_t(*)[32]>(d));
-      tc::ld32(tP + mine + 32, *reinterpret_cast<uint32_t(*)[32]>(d + 32));
+      tc::ld32(tP + mine, d);
       tc::wait_ld();
 #pragma unroll
-      for (int c = 0; c < 64; c += 4) {
+      for (int c = 0; c < 32; c += 4) {
         const float4 m = *reinterpret_cast<const float4 *>(delta + c);
-        const float mm[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          d[c + e] = __float_as_uint(__uint_as_float(s[c + e]) *
-                                     (__uint_as_float(d[c + e]) - mm[e]));
+        const float2 a =
+            __fmul2_rn(pair(s + c), __fadd2_rn(pair(d + c), make_float2(-m.x, -m.y)));
+        const float2 b =
+            __fmul2_rn(pair(s + c + 2), __fadd2_rn(pair(d + c + 2), make_float2(-m.z, -m.w)));
+        d[c] = __float_as_uint(a.x);
+        d[c + 1] = __float_as_uint(a.y);
+        d[c + 2] = __float_as_uint(b.x);
+        d[c + 3] = __float_as_uint(b.y);
       }
       if (diagonal)
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (half * 64 + c < r) d[c] = 0u;
+        for (int c = 0; c < 32; ++c)
+          if (part * 32 + c < r) d[c] = 0u;
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
+      for (int c = 0; c < 16; ++c)
         w[c] = pack_bf16(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1]));
-      tc::st32(tP + mine, w);
+      tc::st16(tP + mine, w);
       tc::wait_st();
       tc::fence_before_sync();
       tc::mbar_arrive(&sm.ds_ready);
@@ -587,16 +620,17 @@ __global__ void __launch_bounds__(320, 1)
     if (tc::warp_wait(&sm.done, 0, abort)) {
       tc::fence_after_sync();
       const int64_t row = (int64_t)t.lo + jt * kTile + r;
-      bf *out = (half ? p.dk : p.dv) + (row * p.Hk + g) * p.D;
-      write_row<DP>((half ? tK : tV) + ((uint32_t)((warp & 3) * 32) << 16), out, p.D,
-                    half ? p.scale : 1.0f, r < rows);
+      const int of = part >> 1, from = (part & 1) * (DP / 2);  // dv or dk, half a row
+      write_row<DP / 2>((of ? tK : tV) + lanes + from,
+                        (of ? p.dk : p.dv) + (row * p.Hk + g) * p.D + from, p.D - from,
+                        of ? p.scale : 1.0f, r < rows);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   settle(sm.abort, p.ws);
-  if (warp == 9) tc::tmem_dealloc(sm.tmem, 512);
+  if (warp == 17) tc::tmem_dealloc(sm.tmem, 512);
 }
 
 template <int DP>
@@ -614,7 +648,7 @@ struct QSmem {
 // S(j+2): P(j+1) is formed while dP(j+1) runs, dS(j+1) while dQ(j) and S(j+2)
 // do.
 template <int DP>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(576, 1)
     attention_dq_kernel(const __grid_constant__ CUtensorMap mq,
                         const __grid_constant__ CUtensorMap mk,
                         const __grid_constant__ CUtensorMap mv,
@@ -638,18 +672,18 @@ __global__ void __launch_bounds__(320, 1)
       mbar_init(&sm.s_full[i], 1);
     }
     for (uint64_t *b : {&sm.q_full, &sm.do_full, &sm.dp_full, &sm.done}) mbar_init(b, 1);
-    mbar_init(&sm.ds_ready, 256);
+    mbar_init(&sm.ds_ready, 512);
     sm.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) tc::tmem_alloc(&sm.tmem, 512);
+  if (warp == 17) tc::tmem_alloc(&sm.tmem, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tS0 = sm.tmem, tP = sm.tmem + 128, tQ = sm.tmem + 256, tS1 = sm.tmem + 384;
   volatile int *abort = &sm.abort;
 
-  if (warp == 8) {
+  if (warp == 16) {
     if (lane == 0) {
       tc::load_tile<DP>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
       for (int j = 0; j < steps; ++j) {
@@ -661,7 +695,7 @@ __global__ void __launch_bounds__(320, 1)
         tc::load_tile<DP>(sm.v[b], &mv, &sm.v_full[b], h / p.group, row);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     const uint32_t q = tc::smem_addr(sm.q), dout = tc::smem_addr(sm.dout);
     auto scores = [&](int j) {
       const int a = j % 3;
@@ -695,7 +729,7 @@ __global__ void __launch_bounds__(320, 1)
       tc::fence_after_sync();
       if (j + 1 < steps && !(ok = grads(j + 1))) break;
       if (lane == 0) {
-        product_halves<DP>(tQ, j & 1 ? tS1 : tS0, tc::smem_addr(sm.k[j % 3]), j > 0);
+        product_parts<DP, 4>(tQ, j & 1 ? tS1 : tS0, tc::smem_addr(sm.k[j % 3]), j > 0);
         tc::commit(&sm.k_empty[j % 3]);
         if (j + 1 == steps) tc::commit(&sm.done);
       }
@@ -703,60 +737,67 @@ __global__ void __launch_bounds__(320, 1)
       if (j + 2 < steps) ok = scores(j + 2);
     }
   } else {
-    const int r = threadIdx.x & 127, half = warp >> 2;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int r = threadIdx.x & 127, part = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, mine = lanes + part * 32;
     const int64_t row = (int64_t)t.lo + t.first + r;
     float lse = 0.0f, delta = 0.0f;
     if (r < rows) {
       lse = p.lse[(int64_t)h * p.tokens + row] * kLog2e;
       delta = p.delta[(int64_t)h * p.tokens + row];
     }
+    const float2 k2 = make_float2(p.scale2, p.scale2), l2 = make_float2(-lse, -lse),
+                 d2 = make_float2(-delta, -delta);
     bool ok = true;
     for (int j = 0; j < steps && ok; ++j) {
-      const uint32_t at = (j & 1 ? tS1 : tS0) + lanes + half * 64;
-      uint32_t s[64], d[64];
+      const uint32_t at = (j & 1 ? tS1 : tS0) + mine;
+      uint32_t s[32], d[32], w[16];
       ok = tc::warp_wait(&sm.s_full[j & 1], (j / 2) & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
-      tc::ld32(at, *reinterpret_cast<uint32_t(*)[32]>(s));
-      tc::ld32(at + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+      tc::ld32(at, s);
       tc::wait_ld();
 #pragma unroll
-      for (int c = 0; c < 64; ++c)
-        s[c] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c]), p.scale2, -lse)));
+      for (int c = 0; c < 32; c += 2) {
+        const float2 a = __ffma2_rn(pair(s + c), k2, l2);
+        s[c] = __float_as_uint(ex2(a.x));
+        s[c + 1] = __float_as_uint(ex2(a.y));
+      }
       ok = tc::warp_wait(&sm.dp_full, j & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
-      tc::ld32(tP + lanes + half * 64, *reinterpret_cast<uint32_t(*)[32]>(d));
-      tc::ld32(tP + lanes + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(d + 32));
+      tc::ld32(tP + mine, d);
       tc::wait_ld();
 #pragma unroll
-      for (int c = 0; c < 64; ++c)
-        d[c] = __float_as_uint(__uint_as_float(s[c]) * (__uint_as_float(d[c]) - delta));
+      for (int c = 0; c < 32; c += 2) {
+        const float2 a = __fmul2_rn(pair(s + c), __fadd2_rn(pair(d + c), d2));
+        d[c] = __float_as_uint(a.x);
+        d[c + 1] = __float_as_uint(a.y);
+      }
       if (j == 0)
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (half * 64 + c > r) d[c] = 0u;
-      uint32_t w[32];
+        for (int c = 0; c < 32; ++c)
+          if (part * 32 + c > r) d[c] = 0u;
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
+      for (int c = 0; c < 16; ++c)
         w[c] = pack_bf16(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1]));
-      tc::st32(at, w);
+      tc::st16(at, w);
       tc::wait_st();
       tc::fence_before_sync();
       tc::mbar_arrive(&sm.ds_ready);
     }
     if (ok) ok = tc::warp_wait(&sm.done, 0, abort);
-    if (ok && half == 0) {
+    if (ok && part < 2) {
       tc::fence_after_sync();
-      write_row<DP>(tQ + lanes, p.dq + (row * p.Hq + h) * p.D, p.D, p.scale, r < rows);
+      const int from = part * (DP / 2);
+      write_row<DP / 2>(tQ + lanes + from, p.dq + (row * p.Hq + h) * p.D + from, p.D - from,
+                        p.scale, r < rows);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   settle(sm.abort, p.ws);
-  if (warp == 9) tc::tmem_dealloc(sm.tmem, 512);
+  if (warp == 17) tc::tmem_dealloc(sm.tmem, 512);
 }
 
 struct StepArgs {
@@ -814,7 +855,7 @@ cudaError_t launch_forward(const CUtensorMap &mq, const CUtensorMap &mk, const C
   constexpr size_t smem = need < least ? least : need;
   const cudaError_t e = allow_dynamic_smem<attention_kernel<DP>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_ex(attention_kernel<DP>, dim3((unsigned)grid), dim3(192), smem, st, true, mq, mk, mv,
+  return launch_ex(attention_kernel<DP>, dim3((unsigned)grid), dim3(320), smem, st, true, mq, mk, mv,
                    a);
 }
 
@@ -830,10 +871,10 @@ cudaError_t launch_backward(const CUtensorMap &mq, const CUtensorMap &mk, const 
   cudaError_t e = allow_dynamic_smem<attention_dkv_kernel<DP>>(kv_smem);
   if (e == cudaSuccess) e = allow_dynamic_smem<attention_dq_kernel<DP>>(q_smem);
   if (e == cudaSuccess)
-    e = launch_ex(attention_dkv_kernel<DP>, dim3((unsigned)(tiles * a.Hk)), dim3(320), kv_smem, st,
+    e = launch_ex(attention_dkv_kernel<DP>, dim3((unsigned)(tiles * a.Hk)), dim3(576), kv_smem, st,
                   true, mq, mk, mv, mdo, a);
   if (e == cudaSuccess)
-    e = launch_ex(attention_dq_kernel<DP>, dim3((unsigned)(tiles * a.Hq)), dim3(320), q_smem, st,
+    e = launch_ex(attention_dq_kernel<DP>, dim3((unsigned)(tiles * a.Hq)), dim3(576), q_smem, st,
                   true, mq, mk, mv, mdo, a);
   return e;
 }

@@ -86,19 +86,25 @@ __device__ __forceinline__ void ld32(uint32_t addr, uint32_t (&r)[32]) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(
-          r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(addr)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Matrix products: D[128 x N] (+)= A[128 x 16] B[16 x N], bf16 in, fp32 out
 // ---------------------------------------------------------------------------
@@ -151,15 +157,6 @@ __device__ __forceinline__ void product_nt(uint32_t d, uint32_t a, uint32_t b) {
     mma_ss(d, operand(a + off, 16), operand(b + off, 16), instr(128, false), k > 0);
   }
 }
-// C[128 x DP] (+)= A[128 x 128] B[128 x DP]: A bf16 in tensor memory (two
-// columns of A per 32-bit column), B's rows contiguous in shared memory.
-template <int DP>
-__device__ __forceinline__ void product_nn(uint32_t d, uint32_t a, uint32_t b, bool add) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    mma_ts(d, a + k * 8, operand(b + k * 2048, 16384), instr(DP, true), add || k > 0);
-}
-
 // ---------------------------------------------------------------------------
 // Tensor-map copies
 // ---------------------------------------------------------------------------
