@@ -135,17 +135,6 @@ __device__ __forceinline__ void settle(int abort, WsHeader *ws) {
   if (threadIdx.x == 0) report_timeout(ws);
 }
 
-// C[128 x DP] (+)= A B: A's 128 columns in PARTS pieces, each written by its
-// own warps over the start of the 128 / PARTS fp32 columns they had read.
-template <int DP, int PARTS>
-__device__ __forceinline__ void product_parts(uint32_t d, uint32_t a, uint32_t b, bool add) {
-  constexpr int kSteps = 8 / PARTS;  // of 16 columns
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    tc::mma_ts(d, a + (k / kSteps) * (128 / PARTS) + (k % kSteps) * 8,
-               tc::operand(b + k * 2048, 16384), tc::instr(DP, true), add || k > 0);
-}
-
 // The two warps of a forward block that share 32 query rows.
 __device__ __forceinline__ void pair_barrier(int quarter) {
   asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
@@ -226,7 +215,7 @@ __global__ void __launch_bounds__(320, 2)
   ForwardSmem<DP> &sm = *reinterpret_cast<ForwardSmem<DP> *>(raw);
   pdl_wait();  // before tensor memory is taken: an earlier grid's blocks may still need it
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   const int h = blockIdx.x % p.Hq;
   Tile t;
   if (!aligned_tiles(raw, p.ws)) return;
@@ -245,8 +234,9 @@ __global__ void __launch_bounds__(320, 2)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tS = sm.tmem, tO = sm.tmem + 128;
+  const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0), tS = tmem, tO = tmem + 128;
   volatile int *abort = &sm.abort;
+  const uint32_t lead = lane == 0;  // the lane that issues products
 
   if (warp == 8) {
     if (lane == 0) {
@@ -265,12 +255,9 @@ __global__ void __launch_bounds__(320, 2)
     for (int it = 0; it < steps && ok; ++it) {
       ok = tc::warp_wait(&sm.k_full, it & 1, abort);
       if (!ok) break;
-      if (lane == 0) {
-        tc::product_nt<DP>(tS, q, k);
-        tc::commit(&sm.k_empty);
-        tc::commit(&sm.s_full);
-      }
-      __syncwarp();
+      tc::product_nt<DP>(lead, tS, q, k);
+      tc::commit(lead, &sm.k_empty);
+      tc::commit(lead, &sm.s_full);
       ok = tc::warp_wait(&sm.v_full, it & 1, abort);
       if (!ok) break;
       // values past the sequence's end meet weights of zero: they must be finite
@@ -279,12 +266,9 @@ __global__ void __launch_bounds__(320, 2)
       ok = tc::warp_wait(&sm.p_ready, it & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
-      if (lane == 0) {
-        product_parts<DP, 2>(tO, tS, v, it > 0);
-        tc::commit(&sm.v_empty);
-        if (it + 1 == steps) tc::commit(&sm.o_full);
-      }
-      __syncwarp();
+      tc::product_parts<DP, 2>(lead, tO, tS, v, it > 0);
+      tc::commit(lead, &sm.v_empty);
+      if (it + 1 == steps) tc::commit(lead, &sm.o_full);
     }
   } else {
     const int r = threadIdx.x & 127, half = warp >> 2;  // this thread's row and half of the keys
@@ -450,7 +434,7 @@ __global__ void __launch_bounds__(576, 1)
   KvSmem<DP> &sm = *reinterpret_cast<KvSmem<DP> *>(raw);
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   const int g = blockIdx.x % p.Hk;
   Tile t;
   if (!aligned_tiles(raw, p.ws)) return;
@@ -473,8 +457,10 @@ __global__ void __launch_bounds__(576, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tS = sm.tmem, tP = sm.tmem + 128, tV = sm.tmem + 256, tK = sm.tmem + 384;
+  const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
+  const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
   volatile int *abort = &sm.abort;
+  const uint32_t lead = lane == 0;  // the lane that issues products
 
   if (warp == 16) {
     if (lane == 0) {
@@ -498,11 +484,8 @@ __global__ void __launch_bounds__(576, 1)
       if (!tc::warp_wait(&sm.q_full[a], (i / 3) & 1, abort)) return false;
       if (i % per_head == per_head - 1 && tail < kTile) tc::clear_rows<DP>(sm.q[a], tail, lane);
       __syncwarp();
-      if (lane == 0) {
-        tc::product_nt<DP>(tS, k, tc::smem_addr(sm.q[a]));
-        tc::commit(&sm.s_full);
-      }
-      __syncwarp();
+      tc::product_nt<DP>(lead, tS, k, tc::smem_addr(sm.q[a]));
+      tc::commit(lead, &sm.s_full);
       return true;
     };
     auto grads = [&](int i) {
@@ -510,11 +493,8 @@ __global__ void __launch_bounds__(576, 1)
       if (!tc::warp_wait(&sm.do_full[b], (i / 2) & 1, abort)) return false;
       if (i % per_head == per_head - 1 && tail < kTile) tc::clear_rows<DP>(sm.dout[b], tail, lane);
       __syncwarp();
-      if (lane == 0) {
-        tc::product_nt<DP>(tP, v, tc::smem_addr(sm.dout[b]));
-        tc::commit(&sm.dp_full);
-      }
-      __syncwarp();
+      tc::product_nt<DP>(lead, tP, v, tc::smem_addr(sm.dout[b]));
+      tc::commit(lead, &sm.dp_full);
       return true;
     };
     bool ok = tc::warp_wait(&sm.k_full, 0, abort) && scores(0) &&
@@ -523,21 +503,15 @@ __global__ void __launch_bounds__(576, 1)
       ok = tc::warp_wait(&sm.p_ready, i & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
-      if (lane == 0) {
-        product_parts<DP, 4>(tV, tS, tc::smem_addr(sm.dout[i & 1]), i > 0);
-        tc::commit(&sm.do_empty[i & 1]);
-      }
-      __syncwarp();
+      tc::product_parts<DP, 4>(lead, tV, tS, tc::smem_addr(sm.dout[i & 1]), i > 0);
+      tc::commit(lead, &sm.do_empty[i & 1]);
       if (i + 1 < steps && !(ok = scores(i + 1))) break;
       ok = tc::warp_wait(&sm.ds_ready, i & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
-      if (lane == 0) {
-        product_parts<DP, 4>(tK, tP, tc::smem_addr(sm.q[i % 3]), i > 0);
-        tc::commit(&sm.q_empty[i % 3]);
-        if (i + 1 == steps) tc::commit(&sm.done);
-      }
-      __syncwarp();
+      tc::product_parts<DP, 4>(lead, tK, tP, tc::smem_addr(sm.q[i % 3]), i > 0);
+      tc::commit(lead, &sm.q_empty[i % 3]);
+      if (i + 1 == steps) tc::commit(lead, &sm.done);
       if (i + 1 < steps) ok = grads(i + 1);
     }
   } else {
@@ -657,7 +631,7 @@ __global__ void __launch_bounds__(576, 1)
   QSmem<DP> &sm = *reinterpret_cast<QSmem<DP> *>(raw);
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   const int h = blockIdx.x % p.Hq;
   Tile t;
   if (!aligned_tiles(raw, p.ws)) return;
@@ -680,8 +654,10 @@ __global__ void __launch_bounds__(576, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tS0 = sm.tmem, tP = sm.tmem + 128, tQ = sm.tmem + 256, tS1 = sm.tmem + 384;
+  const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
+  const uint32_t tS0 = tmem, tP = tmem + 128, tQ = tmem + 256, tS1 = tmem + 384;
   volatile int *abort = &sm.abort;
+  const uint32_t lead = lane == 0;  // the lane that issues products
 
   if (warp == 16) {
     if (lane == 0) {
@@ -703,22 +679,16 @@ __global__ void __launch_bounds__(576, 1)
       // keys past the sequence's end meet a dS of zero: they must be finite
       if (j == 0 && rows < kTile) tc::clear_rows<DP>(sm.k[a], rows, lane);
       __syncwarp();
-      if (lane == 0) {
-        tc::product_nt<DP>(j & 1 ? tS1 : tS0, q, tc::smem_addr(sm.k[a]));
-        tc::commit(&sm.s_full[j & 1]);
-      }
-      __syncwarp();
+      tc::product_nt<DP>(lead, j & 1 ? tS1 : tS0, q, tc::smem_addr(sm.k[a]));
+      tc::commit(lead, &sm.s_full[j & 1]);
       return true;
     };
     auto grads = [&](int j) {
       const int b = j & 1;
       if (!tc::warp_wait(&sm.v_full[b], (j / 2) & 1, abort)) return false;
-      if (lane == 0) {
-        tc::product_nt<DP>(tP, dout, tc::smem_addr(sm.v[b]));
-        tc::commit(&sm.dp_full);
-        tc::commit(&sm.v_empty[b]);
-      }
-      __syncwarp();
+      tc::product_nt<DP>(lead, tP, dout, tc::smem_addr(sm.v[b]));
+      tc::commit(lead, &sm.dp_full);
+      tc::commit(lead, &sm.v_empty[b]);
       return true;
     };
     bool ok = tc::warp_wait(&sm.q_full, 0, abort) && scores(0) &&
@@ -728,12 +698,9 @@ __global__ void __launch_bounds__(576, 1)
       if (!ok) break;
       tc::fence_after_sync();
       if (j + 1 < steps && !(ok = grads(j + 1))) break;
-      if (lane == 0) {
-        product_parts<DP, 4>(tQ, j & 1 ? tS1 : tS0, tc::smem_addr(sm.k[j % 3]), j > 0);
-        tc::commit(&sm.k_empty[j % 3]);
-        if (j + 1 == steps) tc::commit(&sm.done);
-      }
-      __syncwarp();
+      tc::product_parts<DP, 4>(lead, tQ, j & 1 ? tS1 : tS0, tc::smem_addr(sm.k[j % 3]), j > 0);
+      tc::commit(lead, &sm.k_empty[j % 3]);
+      if (j + 1 == steps) tc::commit(lead, &sm.done);
       if (j + 2 < steps) ok = scores(j + 2);
     }
   } else {

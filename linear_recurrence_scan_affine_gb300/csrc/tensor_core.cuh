@@ -115,48 +115,77 @@ constexpr uint32_t instr(int n, bool b_n_contiguous) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_n_contiguous ? 1u : 0u) << 16) |
          ((uint32_t)(n / 8) << 17) | ((128u / 16) << 24);
 }
-// Shared-memory descriptor of a 128-byte-swizzled operand: start address,
-// leading and stride byte offsets in 16-byte units, version 1 (bits 46-47),
-// swizzle code 2 (bits 61-63). With K contiguous the stride offset is the
-// 1024 bytes between groups of 8 rows (leading offset unused). With N
-// contiguous it is the 1024 bytes between groups of 8 k-rows, and the leading
-// offset is the distance between 64-column boxes.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t box_bytes) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(box_bytes >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory descriptor of a 128-byte-swizzled operand. Low word: start
+// address and leading byte offset, in 16-byte units; high word: stride byte
+// offset in 16-byte units, version 1 (bits 46-47), swizzle code 2 (bits
+// 61-63). With K contiguous the stride offset is the 1024 bytes between
+// groups of 8 rows (leading offset unused). With N contiguous it is the 1024
+// bytes between groups of 8 k-rows, and the leading offset is the distance
+// between 64-column boxes.
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t operand_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t operand_n(uint32_t addr) {
+  return (addr >> 4) | ((16384u >> 4) << 16);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
+// Products are issued by one lane, but every lane of its warp runs the code
+// and `lead` predicates the instruction alone: in a branch taken by one lane
+// each descriptor would be built in that lane's registers and moved over, and
+// issuing a tile's products would take longer than running them.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b,
+                                       uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead), "r"(kOperandHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b,
+                                       uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 y, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead), "r"(kOperandHigh)
       : "memory");
 }
-// Arrive on `bar` when every product this thread has issued is complete.
-__device__ __forceinline__ void commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_addr(bar))
-               : "memory");
+// Arrive on `bar` when every product the lead lane has issued is complete.
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar)),
+      "r"(lead)
+      : "memory");
 }
 
 // C[128 x 128] = A[128 x DP] B[128 x DP]^T, both K-contiguous in shared memory.
 template <int DP>
-__device__ __forceinline__ void product_nt(uint32_t d, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void product_nt(uint32_t lead, uint32_t d, uint32_t a, uint32_t b) {
+  const uint32_t x = operand_k(a), y = operand_k(b);
 #pragma unroll
   for (int k = 0; k < DP / 16; ++k) {
-    const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-    mma_ss(d, operand(a + off, 16), operand(b + off, 16), instr(128, false), k > 0);
+    const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
+    mma_ss(lead, d, x + off, y + off, instr(128, false), k > 0);
   }
 }
+// C[128 x DP] (+)= A B, B's rows contiguous in shared memory and A in tensor
+// memory as bf16 pairs (8 columns per 16 of A): its 128 columns in PARTS
+// pieces, each written by its own warps over the start of the 128 / PARTS
+// fp32 columns they had read.
+template <int DP, int PARTS>
+__device__ __forceinline__ void product_parts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b,
+                                              bool add) {
+  constexpr int kSteps = 8 / PARTS;  // of 16 columns
+  const uint32_t y = operand_n(b);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    mma_ts(lead, d, a + (k / kSteps) * (128 / PARTS) + (k % kSteps) * 8, y + k * (2048 >> 4),
+           instr(DP, true), add || k > 0);
+}
+
 // ---------------------------------------------------------------------------
 // Tensor-map copies
 // ---------------------------------------------------------------------------
