@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(320, 2)
     for (uint64_t *b : {&sm.q_full, &sm.k_full, &sm.k_empty, &sm.v_full, &sm.v_empty, &sm.s_full,
                         &sm.o_full})
       mbar_init(b, 1);
-    mbar_init(&sm.p_ready, 256);
+    mbar_init(&sm.p_ready, 8);
     sm.abort = 0;
     fence_mbar_init();
   }
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(320, 2)
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       tc::wait_st();
       tc::fence_before_sync();
-      tc::mbar_arrive(&sm.p_ready);
+      tc::warp_arrive(&sm.p_ready, lead);
     }
     pair_barrier(warp & 3);  // the partner has read the last maximum
     sm.row[half][r] = l;
@@ -448,8 +448,8 @@ __global__ void __launch_bounds__(576, 1)
     for (int i = 0; i < 3; ++i) mbar_init(&sm.q_full[i], 1), mbar_init(&sm.q_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.do_full[i], 1), mbar_init(&sm.do_empty[i], 1);
     for (uint64_t *b : {&sm.k_full, &sm.v_full, &sm.s_full, &sm.dp_full, &sm.done}) mbar_init(b, 1);
-    mbar_init(&sm.p_ready, 512);
-    mbar_init(&sm.ds_ready, 512);
+    mbar_init(&sm.p_ready, 16);
+    mbar_init(&sm.ds_ready, 16);
     sm.abort = 0;
     fence_mbar_init();
   }
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(576, 1)
       tc::st16(tS + mine, w);
       tc::wait_st();
       tc::fence_before_sync();
-      tc::mbar_arrive(&sm.p_ready);
+      tc::warp_arrive(&sm.p_ready, lead);
 
       tc::warp_wait(&sm.dp_full, i & 1, abort);
       tc::fence_after_sync();
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(576, 1)
       tc::st16(tP + mine, w);
       tc::wait_st();
       tc::fence_before_sync();
-      tc::mbar_arrive(&sm.ds_ready);
+      tc::warp_arrive(&sm.ds_ready, lead);
     }
     if (tc::warp_wait(&sm.done, 0, abort)) {
       tc::fence_after_sync();
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(576, 1)
       mbar_init(&sm.s_full[i], 1);
     }
     for (uint64_t *b : {&sm.q_full, &sm.do_full, &sm.dp_full, &sm.done}) mbar_init(b, 1);
-    mbar_init(&sm.ds_ready, 512);
+    mbar_init(&sm.ds_ready, 16);
     sm.abort = 0;
     fence_mbar_init();
   }
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(576, 1)
       tc::st16(at, w);
       tc::wait_st();
       tc::fence_before_sync();
-      tc::mbar_arrive(&sm.ds_ready);
+      tc::warp_arrive(&sm.ds_ready, lead);
     }
     if (ok) ok = tc::warp_wait(&sm.done, 0, abort);
     if (ok && part < 2) {

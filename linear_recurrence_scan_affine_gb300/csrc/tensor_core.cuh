@@ -43,8 +43,11 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
   return __all_sync(kFull, mbar_wait(bar, parity, abort));
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+// One arrival for the whole warp, after what its lanes have done.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, uint32_t lead) {
+  __syncwarp();
+  if (lead)
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // ---------------------------------------------------------------------------
