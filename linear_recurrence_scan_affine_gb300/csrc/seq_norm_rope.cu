@@ -52,6 +52,8 @@ struct HeadArgs {
   float *partial;         // backward: [blocks][2][D]
   int64_t tokens, heads, Hq, max_pos;
   int D, half, inter;
+  bool tables16;  // the tables' rows start on 16-byte boundaries
+  int q_blocks;   // head_pairs_kernel: blocks that take queries
   float eps, inv_d;
 };
 
@@ -140,26 +142,265 @@ __global__ void __launch_bounds__(256) head_any_kernel(const HeadArgs p) {
   }
 }
 
-// Sum the blocks' partial weight gradients, in block order.
+// ---------------------------------------------------------------------------
+// Heads of 8 n elements up to 256: a lane holds 8 of a head's elements as
+// four rotation pairs, so nothing but the mean crosses lanes. A group of D/8
+// lanes takes a few heads of one token at a time, whose cosines and sines it
+// reads once; the first blocks take queries and the rest keys, so a block has
+// one weight vector and, in the gradient, one set of sums.
+// ---------------------------------------------------------------------------
+// Four elements of a head, loaded and stored together.
+template <class E>
+struct Four;
+template <>
+struct Four<float> {
+  float4 w;
+  __device__ __forceinline__ void load(const float *p) {
+    w = __ldg(reinterpret_cast<const float4 *>(p));
+  }
+  __device__ __forceinline__ void get(float (&v)[4]) const {
+    v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+  }
+  static __device__ __forceinline__ void put(float *p, const float (&v)[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  uint2 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    w = __ldg(reinterpret_cast<const uint2 *>(p));
+  }
+  __device__ __forceinline__ void get(float (&v)[4]) const {
+    v[0] = __uint_as_float(w.x << 16);
+    v[1] = __uint_as_float(w.x & 0xffff0000u);
+    v[2] = __uint_as_float(w.y << 16);
+    v[3] = __uint_as_float(w.y & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void put(__nv_bfloat16 *p, const float (&v)[4]) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  }
+};
+
+// A lane's 8 elements: the four first and the four second members of its
+// pairs, each as two two-wide values.
+struct Pairs {
+  float2 a[2], b[2];
+};
+template <bool INTER, class E>
+__device__ __forceinline__ Pairs unpack(const Four<E> &x, const Four<E> &y) {
+  float u[4], v[4];
+  x.get(u);
+  y.get(v);
+  if (INTER)  // (u0, u1), (u2, u3), (v0, v1), (v2, v3)
+    return {{make_float2(u[0], u[2]), make_float2(v[0], v[2])},
+            {make_float2(u[1], u[3]), make_float2(v[1], v[3])}};
+  return {{make_float2(u[0], u[1]), make_float2(u[2], u[3])},
+          {make_float2(v[0], v[1]), make_float2(v[2], v[3])}};
+}
+template <bool INTER, class E>
+__device__ __forceinline__ void write(E *first, E *second, const Pairs &p) {
+  const float u[4] = {p.a[0].x, INTER ? p.b[0].x : p.a[0].y, INTER ? p.a[0].y : p.a[1].x,
+                      INTER ? p.b[0].y : p.a[1].y};
+  const float v[4] = {INTER ? p.a[1].x : p.b[0].x, INTER ? p.b[1].x : p.b[0].y,
+                      INTER ? p.a[1].y : p.b[1].x, p.b[1].y};
+  Four<E>::put(first, u);
+  Four<E>::put(second, v);
+}
+__device__ __forceinline__ float2 neg(float2 x) { return make_float2(-x.x, -x.y); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Sum over the group of lanes that starts at `first`; every lane gets it.
+// LANES: the group's size where it is a power of two, else 0 (`lanes`).
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v, int lanes, int first, int at) {
+  if constexpr (LANES != 0) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+  } else {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float q = __shfl_down_sync(kFull, v, o);
+      if (at < o && at + o < lanes) v += q;
+    }
+    return __shfl_sync(kFull, v, first);
+  }
+}
+
+// Heads a group takes at a time, and blocks per SM the registers are held to.
+// Measured on 32768 tokens, 16 + 4 heads of 128, bf16 (f32: 16384 tokens), us
+// against floors of 50 forward and 75 backward:
+//   forward  4 heads, 4 blocks 56 (f32 63); 4, 3 60 (53); 2, 4 62 (54); 1, 8 82 (61)
+//   gradient 4, 2 97 (82); 2, 3 106 (88); 1, 4 115 (83); 1, 6 214 (163)
+template <class E, bool BACK>
+constexpr int slab_heads() {
+  return BACK || sizeof(E) == 2 ? 4 : 2;
+}
+
+template <class E, bool INTER, int LANES, bool BACK>
+__global__ void __launch_bounds__(256, BACK ? 2 : 4) head_pairs_kernel(const HeadArgs p) {
+  constexpr int kSlab = slab_heads<E, BACK>();
+  extern __shared__ float sums[];  // backward: [groups of a block][D]
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lanes = LANES ? LANES : p.D / 8, per_warp = 32 / lanes;
+  const int gi = lane / lanes, j = lane % lanes, first = gi * lanes;
+  const bool live = gi < per_warp;
+  const int which = (int)blockIdx.x >= p.q_blocks;
+  const int block = which ? (int)blockIdx.x - p.q_blocks : (int)blockIdx.x;
+  const int blocks = which ? (int)gridDim.x - p.q_blocks : p.q_blocks;
+  const int heads = which ? (int)(p.heads - p.Hq) : (int)p.Hq;
+  const int R = 2 * p.half;
+  // this lane's two runs of four elements; its first pair is 4 j
+  const bool turns = 4 * j < p.half;  // (half layout: the whole lane turns or not)
+  const int ea = INTER ? 8 * j : (turns ? 4 * j : R + 8 * (j - R / 8));
+  const int eb = INTER || !turns ? ea + 4 : ea + p.half;
+  Pairs w = {}, g = {};  // weights, and the sums of their gradients
+  if (live) {
+    Four<float> wa, wb;
+    const float *pw = p.w[which];
+    wa.w = make_float4(pw[ea], pw[ea + 1], pw[ea + 2], pw[ea + 3]);
+    wb.w = make_float4(pw[eb], pw[eb + 1], pw[eb + 2], pw[eb + 3]);
+    w = unpack<INTER>(wa, wb);
+  }
+  const int slabs = (heads + kSlab - 1) / kSlab, total = (int)p.tokens * slabs;
+  const int64_t ts = p.ts[which], hs = p.hs[which];
+  const E *px = static_cast<const E *>(p.x[which]);
+  const E *pdy = static_cast<const E *>(p.dy[which]);
+  E *py = static_cast<E *>(p.y[which]);
+  for (int base = (block * 8 + warp) * per_warp; base < total; base += blocks * 8 * per_warp) {
+    const bool on = live && base + gi < total;
+    const int tok = on ? (base + gi) / slabs : 0, h0 = on ? (base + gi) % slabs * kSlab : 0;
+    Four<E> xa[kSlab], xb[kSlab], da[BACK ? kSlab : 1], db[BACK ? kSlab : 1];
+    const E *x0 = px + tok * ts + h0 * hs;
+    const int64_t at = ((int64_t)tok * heads + h0) * p.D;  // in the contiguous arrays
+#pragma unroll
+    for (int u = 0; u < kSlab; ++u)
+      if (on && h0 + u < heads) {
+        xa[u].load(x0 + u * hs + ea);
+        xb[u].load(x0 + u * hs + eb);
+        if constexpr (BACK) {
+          da[u].load(pdy + at + u * p.D + ea);
+          db[u].load(pdy + at + u * p.D + eb);
+        }
+      }
+    float c[4], sn[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = 1.0f, sn[e] = 0.0f;
+    if (on && turns) {
+      const int64_t pos = p.positions[tok];
+      const bool known_pos = pos >= 0 && pos < p.max_pos;
+      const float *ct = p.cos + pos * p.half + 4 * j, *st = p.sin + pos * p.half + 4 * j;
+      if (known_pos && p.tables16) {
+        Four<float> a, b;
+        a.load(ct);
+        b.load(st);
+        a.get(c);
+        b.get(sn);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * j + e < p.half) {
+            c[e] = known_pos ? __ldg(ct + e) : __int_as_float(0x7fffffff);
+            sn[e] = known_pos ? __ldg(st + e) : c[e];
+          }
+      }
+    }
+    const float2 c2[2] = {make_float2(c[0], c[1]), make_float2(c[2], c[3])};
+    const float2 s2[2] = {make_float2(sn[0], sn[1]), make_float2(sn[2], sn[3])};
+#pragma unroll
+    for (int u = 0; u < kSlab; ++u) {
+      const bool use = on && h0 + u < heads;  // (groups of a warp can be at different slabs)
+      const Pairs x = unpack<INTER>(xa[u], xb[u]);
+      float2 q = __fmul2_rn(x.a[0], x.a[0]);
+      q = __ffma2_rn(x.a[1], x.a[1], q);
+      q = __ffma2_rn(x.b[0], x.b[0], q);
+      q = __ffma2_rn(x.b[1], x.b[1], q);
+      const float ss = group_sum<LANES>(use ? q.x + q.y : 0.0f, lanes, first, j);
+      const float r = rsqrtf(ss * p.inv_d + p.eps);
+      Pairs y;
+      if constexpr (!BACK) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 ua = __fmul2_rn(__fmul2_rn(x.a[e], both(r)), w.a[e]);
+          const float2 ub = __fmul2_rn(__fmul2_rn(x.b[e], both(r)), w.b[e]);
+          y.a[e] = __ffma2_rn(neg(ub), s2[e], __fmul2_rn(ua, c2[e]));
+          y.b[e] = __ffma2_rn(ua, s2[e], __fmul2_rn(ub, c2[e]));
+        }
+      } else {
+        const Pairs d = unpack<INTER>(da[u], db[u]);
+        Pairs t;
+        float2 dot = both(0.0f);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 ua = __ffma2_rn(d.b[e], s2[e], __fmul2_rn(d.a[e], c2[e]));
+          const float2 ub = __ffma2_rn(neg(d.a[e]), s2[e], __fmul2_rn(d.b[e], c2[e]));
+          if (use) {
+            g.a[e] = __ffma2_rn(ua, __fmul2_rn(x.a[e], both(r)), g.a[e]);
+            g.b[e] = __ffma2_rn(ub, __fmul2_rn(x.b[e], both(r)), g.b[e]);
+          }
+          t.a[e] = __fmul2_rn(ua, w.a[e]);
+          t.b[e] = __fmul2_rn(ub, w.b[e]);
+          dot = __ffma2_rn(t.a[e], x.a[e], dot);
+          dot = __ffma2_rn(t.b[e], x.b[e], dot);
+        }
+        const float sum = group_sum<LANES>(use ? dot.x + dot.y : 0.0f, lanes, first, j);
+        const float k = sum * r * r * p.inv_d;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          y.a[e] = __fmul2_rn(both(r), __ffma2_rn(x.a[e], both(-k), t.a[e]));
+          y.b[e] = __fmul2_rn(both(r), __ffma2_rn(x.b[e], both(-k), t.b[e]));
+        }
+      }
+      if (use) write<INTER>(py + at + u * p.D + ea, py + at + u * p.D + eb, y);
+    }
+  }
+  if constexpr (BACK) {
+    if (live) {
+      float *mine = sums + (warp * per_warp + gi) * p.D;
+      write<INTER>(mine + ea, mine + eb, g);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.D; i += 256) {
+      float t = 0.0f;
+      for (int k = 0; k < 8 * per_warp; ++k) t += sums[k * p.D + i];
+      p.partial[(int64_t)blockIdx.x * p.D + i] = t;
+    }
+  }
+}
+
+// Sum the blocks' partial weight gradients, in block order: rows [0, split)
+// of `partial` belong to the queries' weight and the rest to the keys', or,
+// with split = 0, the two halves of every 2 D wide row.
 __global__ void __launch_bounds__(1024)
-    weight_sum_kernel(const float *partial, int blocks, int D, float *dq, float *dk) {
+    weight_sum_kernel(const float *partial, int blocks, int split, int D, float *dq, float *dk) {
   __shared__ float part[1024];
   pdl_wait();
   pdl_launch_dependents();
   const int i = blockIdx.x * 32 + (threadIdx.x & 31), row = threadIdx.x >> 5;
+  const int which = i >= D, d = which ? i - D : i;
+  const int64_t width = split ? D : 2 * D, col = split ? d : i;
+  const int from = split && which ? split : 0, to = split && !which ? split : blocks;
   float t = 0.0f;
   if (i < 2 * D)
-    for (int b = row; b < blocks; b += 32) t += partial[(int64_t)b * 2 * D + i];
+    for (int b = from + row; b < to; b += 32) t += partial[b * width + col];
   part[threadIdx.x] = t;
   __syncthreads();
   if (row == 0 && i < 2 * D) {
     for (int k = 1; k < 32; ++k) t += part[k * 32 + threadIdx.x];
-    float *out = i < D ? dq : dk;
-    if (out) out[i < D ? i : i - D] = t;
+    float *out = which ? dk : dq;
+    if (out) out[d] = t;
   }
 }
 
-constexpr int kBlocksMax = 152 * 8;  // blocks that leave partial weight gradients
+// Blocks of a call: the gradient's each leave a row of partial sums, so they
+// are no more than run at once.
+template <bool BACK>
+constexpr int blocks_max() {
+  return 152 * (BACK ? 2 : 8);
+}
 
 bool head_sizes(int64_t tokens, int64_t Hq, int64_t Hk, int64_t D, int64_t R, int64_t max_pos,
                 double eps, rlcs_dtype t) {
@@ -168,8 +409,57 @@ bool head_sizes(int64_t tokens, int64_t Hq, int64_t Hk, int64_t D, int64_t R, in
          product_fits(tokens, Hq + Hk, D) && product_fits(max_pos, D, 1);
 }
 
+// Whether a call can take the paired lanes: whole runs of four elements, each
+// loaded together, that rotation pairs do not straddle.
+template <class E>
+bool pairs_fit(const HeadArgs &a, int Hk) {
+  const int R = 2 * a.half;
+  if (a.D % 8 || a.D > 256 || (!a.inter && R % 8) || a.tokens * a.heads >= (int64_t)INT32_MAX / 2)
+    return false;
+  const uintptr_t run = 4 * sizeof(E);
+  for (int i = 0; i < (Hk > 0 ? 2 : 1); ++i)
+    if (a.ts[i] % 4 || a.hs[i] % 4 || !aligned(a.x[i], run) || !aligned(a.y[i], run) ||
+        !aligned(a.dy[i], run))
+      return false;
+  return true;
+}
+
+// Blocks of the queries' and the keys' heads, each leaving one row of partial
+// weight gradients: as many as their slabs need, within `most` together.
+template <class E, int LANES, bool BACK>
+cudaError_t launch_pairs(HeadArgs &a, int &blocks, cudaStream_t st) {
+  constexpr int kSlab = slab_heads<E, BACK>();
+  const int per_block = 8 * (32 / (a.D / 8)), Hq = (int)a.Hq, Hk = (int)a.heads - Hq;
+  const int64_t nq = ceil_div(a.tokens * ceil_div(Hq, kSlab), per_block);
+  const int64_t nk = ceil_div(a.tokens * ceil_div(Hk, kSlab), per_block);
+  constexpr int kMost = blocks_max<BACK>();
+  if (nq + nk <= kMost) {
+    a.q_blocks = (int)nq;
+    blocks = (int)(nq + nk);
+  } else {
+    int64_t k = nk * kMost / (nq + nk);
+    if (Hk > 0 && k == 0) k = 1;
+    a.q_blocks = (int)(kMost - k);
+    blocks = kMost;
+  }
+  a.tables16 = a.half % 4 == 0 && aligned(a.cos, 16) && aligned(a.sin, 16);
+  const size_t smem = BACK ? (size_t)per_block * a.D * sizeof(float) : 0;  // 8 KB
+  return a.inter ? launch_ex(head_pairs_kernel<E, true, LANES, BACK>, dim3((unsigned)blocks),
+                             dim3(256), smem, st, true, a)
+                 : launch_ex(head_pairs_kernel<E, false, LANES, BACK>, dim3((unsigned)blocks),
+                             dim3(256), smem, st, true, a);
+}
+
 template <class E, bool BACK>
-cudaError_t launch_heads(const HeadArgs &a, int blocks, cudaStream_t st) {
+cudaError_t launch_heads(HeadArgs &a, int &blocks, cudaStream_t st) {
+  a.q_blocks = 0;
+  if (pairs_fit<E>(a, (int)(a.heads - a.Hq))) {
+    if (a.D == 128) return launch_pairs<E, 16, BACK>(a, blocks, st);
+    if (a.D == 64) return launch_pairs<E, 8, BACK>(a, blocks, st);
+    return launch_pairs<E, 0, BACK>(a, blocks, st);
+  }
+  const int64_t want = ceil_div(a.tokens * a.heads, 8);
+  blocks = (int)(want < blocks_max<BACK>() ? want : blocks_max<BACK>());
   const size_t smem = BACK ? (size_t)8 * 2 * a.D * sizeof(float) : 0;
   if (smem > 48 * 1024) {
     const cudaError_t e = allow_dynamic_smem<head_any_kernel<E, BACK>>(64 * 1024);
@@ -216,11 +506,6 @@ bool head_arrays(const HeadArgs &a, int64_t Hk) {
         !product_fits(a.heads, a.hs[i], 1))
       return false;
   return true;
-}
-
-int head_blocks(const HeadArgs &a) {
-  const int64_t want = ceil_div(a.tokens * a.heads, 8);
-  return (int)(want < kBlocksMax ? want : kBlocksMax);
 }
 
 }  // namespace
@@ -286,12 +571,13 @@ rlcs_status rlcs_qk_norm_rope(const void *q, int64_t q_token_stride, int64_t q_h
       range(positions, tokens * 4)};
   if (outputs_overlap(outs, ins)) return RLCS_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return launched(dtype == RLCS_F32 ? launch_heads<float, false>(a, head_blocks(a), st)
-                                    : launch_heads<__nv_bfloat16, false>(a, head_blocks(a), st));
+  int blocks;
+  return launched(dtype == RLCS_F32 ? launch_heads<float, false>(a, blocks, st)
+                                    : launch_heads<__nv_bfloat16, false>(a, blocks, st));
 }
 
 size_t rlcs_qk_norm_rope_scratch_bytes(int64_t D) {
-  return D <= 0 || D > 1024 ? 0 : (size_t)kBlocksMax * 2 * (size_t)D * sizeof(float);
+  return D <= 0 || D > 1024 ? 0 : (size_t)blocks_max<true>() * 2 * (size_t)D * sizeof(float);
 }
 
 rlcs_status rlcs_qk_norm_rope_backward(
@@ -338,13 +624,13 @@ rlcs_status rlcs_qk_norm_rope_backward(
   if (!scratch || scratch_bytes < rlcs_qk_norm_rope_scratch_bytes(D) || !aligned(scratch, 16))
     return RLCS_ERR_WORKSPACE;
   a.partial = static_cast<float *>(scratch);
-  const int blocks = head_blocks(a);
+  int blocks = 0;
   const rlcs_status s =
       launched(dtype == RLCS_F32 ? launch_heads<float, true>(a, blocks, st)
                                  : launch_heads<__nv_bfloat16, true>(a, blocks, st));
   if (s != RLCS_OK) return s;
   return launched(launch_ex(weight_sum_kernel, dim3((unsigned)ceil_div(2 * D, 32)), dim3(1024), 0,
-                            st, true, (const float *)a.partial, blocks, (int)D, dq_weight,
+                            st, true, (const float *)a.partial, blocks, a.q_blocks, (int)D, dq_weight,
                             Hk > 0 ? dk_weight : (float *)nullptr));
 }
 
