@@ -14,59 +14,6 @@ using bf = __nv_bfloat16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float dot_row(const float *s, const bf *r, int D) {
-  float t = 0.0f;
-  for (int d = 0; d < D; d += 8) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(r + d);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      t = fmaf(s[d + 2 * j], __uint_as_float(u[j] << 16), t);
-      t = fmaf(s[d + 2 * j + 1], __uint_as_float(u[j] & 0xffff0000u), t);
-    }
-  }
-  return t;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
-}
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-  return v;
-}
-// acc[e] += w * r[lane + 32 e]
-__device__ __forceinline__ void add_row(float (&acc)[4], float w, const bf *r, int lane, int D) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (lane + 32 * e < D) acc[e] = fmaf(w, __bfloat162float(r[lane + 32 * e]), acc[e]);
-}
-__device__ __forceinline__ void stage(float *s, const bf *r, int lane, int D) {
-  for (int d = lane; d < D; d += 32) s[d] = __bfloat162float(r[d]);
-}
-
-// One warp per query row: keys in steps of 32, a key per lane for the scores.
-__device__ __forceinline__ void attend(const float *qs, const bf *k, int64_t kt, const bf *v,
-                                       int64_t vt, int64_t n, int D, float scale2, int lane,
-                                       float (&acc)[4], float &m, float &l) {
-  m = -INFINITY;
-  l = 0.0f;
-  for (int64_t j0 = 0; j0 < n; j0 += 32) {
-    const bool in = j0 + lane < n;
-    const float s = in ? dot_row(qs, k + (j0 + lane) * kt, D) * scale2 : -INFINITY;
-    const float mn = fmaxf(m, warp_max(s)), ms = mn == -INFINITY ? 0.0f : mn;
-    const float pj = exp2f(s - ms), f = exp2f(m - ms);
-    l = l * f + warp_sum(pj);
-    m = mn;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] *= f;
-    for (int j = 0; j < 32 && j0 + j < n; ++j)
-      add_row(acc, __shfl_sync(kFull, pj, j), v + (j0 + j) * vt, lane, D);
-  }
-}
-
 // ---------------------------------------------------------------------------
 // Tiles of 128 tokens of one sequence
 // ---------------------------------------------------------------------------
@@ -112,6 +59,8 @@ __device__ __forceinline__ bool find_tile(const int32_t *cu, int64_t sequences, 
 int64_t tile_bound(int64_t sequences, int64_t tokens) {
   return tokens / kTile + (sequences < tokens ? sequences : tokens);
 }
+
+__device__ __forceinline__ int64_t ceil_div_dev(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -767,35 +716,308 @@ __global__ void __launch_bounds__(576, 1)
   if (warp == 17) tc::tmem_dealloc(sm.tmem, 512);
 }
 
+// ---------------------------------------------------------------------------
+// One new token per sequence. Bound by reading the cache once.
+//
+// Work items are (sequence, key/value head, chunk of positions), taken in
+// turn by as many blocks as run at once, so long and short caches share the
+// GPU evenly. A warp takes 32 positions at a time, straight from global
+// memory into the operands of two small products: the order of the summed
+// index is free, so each lane loads 16 contiguous bytes of a key row, and the
+// order of the output index is free, so each lane loads 16 contiguous bytes of
+// the value rows and pairs them up itself.
+//   S^T[16 positions x 8 rows] = K Q^T,  O^T[16 elements x 8 rows] += V^T P^T
+// (rows: the query heads that share the key/value head, 8 or 16 to an item).
+// Chunks of one sequence are joined by a second kernel, in chunk order.
+// ---------------------------------------------------------------------------
 struct StepArgs {
   const bf *q, *k, *v;
   int64_t kb, kt, kh, vb, vt, vh;
   const int32_t *lengths;
   bf *o;
-  int64_t B, S, Hq, Hk;
-  int D, group;
-  float scale;
+  float *partial;  // [B, Hq, chunks, D + 2]: o, running maximum, sum
+  int64_t B, S;
+  int Hq, Hk, D, group, row_blocks, chunk, chunks;
+  float scale2;
 };
+constexpr int kStepWarps = 4;
+constexpr int kChunksMax = 256;
+constexpr int step_blocks(int row_blocks) { return row_blocks == 1 ? 3 : 2; }  // per SM
 
-__global__ void __launch_bounds__(128) attention_step_kernel(const StepArgs p) {
-  __shared__ float qs[4][128];
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {  // an 8 x 8 matrix over the warp
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint4 load16(const bf *p, bool on) {
+  return on ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ int64_t cache_length(const StepArgs &p, int64_t b) {
+  const int64_t n = p.lengths[b];
+  return n < 0 ? 0 : (n > p.S ? p.S : n);
+}
+
+template <int DP, int NR>
+__global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
+    attention_step_kernel(const StepArgs p) {
+  constexpr int KC = DP / 32;  // 16-byte pieces of a key row per lane
+  constexpr int VC = DP / 64;  // of a value row
+  constexpr int MT = DP / 16;  // output tiles
+  __shared__ float so[kStepWarps][NR * 8][DP + 4];
+  __shared__ float sm[kStepWarps][NR * 8], sl[kStepWarps][NR * 8];
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = (int64_t)blockIdx.x * 4 + warp, b = row / p.Hq, h = row % p.Hq;
-  if (b >= p.B) return;
-  int64_t n = p.lengths[b];
-  n = n < 0 ? 0 : (n > p.S ? p.S : n);
-  stage(qs[warp], p.q + row * p.D, lane, p.D);
-  __syncwarp();
-  const int64_t g = h / p.group;
-  float acc[4] = {}, m, l;
-  attend(qs[warp], p.k + b * p.kb + g * p.kh, p.kt, p.v + b * p.vb + g * p.vh, p.vt, n, p.D,
-         p.scale * kLog2e, lane, acc, m, l);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = lane >> 2, c = lane & 3;
+  int64_t b = 0, before = 0;  // the sequence that holds this block's item, items of earlier ones
+  for (int64_t item = blockIdx.x;; item += gridDim.x) {
+    // items of sequence b: its chunks x heads x row blocks
+    int64_t n = 0, items = 0;
+    for (;; ++b, before += items) {
+      if (b >= p.B) return;
+      if (p.B - b >= 32) {  // skip 32 sequences at a time
+        int64_t own = ceil_div_dev(cache_length(p, b + lane), p.chunk) * p.Hk * p.row_blocks;
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (lane + 32 * e < p.D)
-      p.o[row * p.D + lane + 32 * e] = __float2bfloat16_rn(n > 0 ? acc[e] / l : 0.0f);
+        for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(kFull, own, o);
+        if (item >= before + own) {
+          items = own;
+          b += 31;
+          continue;
+        }
+      }
+      n = cache_length(p, b);
+      items = ceil_div_dev(n, p.chunk) * p.Hk * p.row_blocks;
+      if (item < before + items) break;
+    }
+    const int at = (int)(item - before);
+    const int per = p.Hk * p.row_blocks, which = at / per, rest = at % per;
+    const int g = rest / p.row_blocks, r0 = rest % p.row_blocks * (NR * 8);
+    const int64_t from = (int64_t)which * p.chunk;
+    const int64_t to = from + p.chunk < n ? from + p.chunk : n;
+
+    // queries: row e of each block of 8, as the second operand
+    uint4 q[NR][KC];
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int m = 0; m < KC; ++m) {
+        const int row = r0 + r * 8 + e, col = (m * 4 + c) * 8;
+        q[r][m] = load16(p.q + ((int64_t)b * p.Hq + g * p.group + row) * p.D + col,
+                         row < p.group && col < p.D);
+      }
+    const bf *k = p.k + b * p.kb + g * p.kh, *v = p.v + b * p.vb + g * p.vh;
+    float acc[NR][MT][4] = {};
+    float top[NR][2], sum[NR][2];
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) top[r][i] = -INFINITY, sum[r][i] = 0.0f;
+    for (int64_t pos = from + warp * 32; pos < to; pos += kStepWarps * 32) {
+      // keys: rows e and e + 8 of two runs of 16 positions
+      uint4 kk[2][2][KC];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int64_t x = pos + t * 16 + i * 8 + e;
+#pragma unroll
+          for (int m = 0; m < KC; ++m)
+            kk[t][i][m] = load16(k + x * p.kt + (m * 4 + c) * 8, x < to && (m * 4 + c) * 8 < p.D);
+        }
+      // values: rows 2c, 2c + 1 (and + 8) of each run, pieces e (and e + 8)
+      uint4 vv[2][4][VC];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t x = pos + t * 16 + (i >> 1) * 8 + 2 * c + (i & 1);
+#pragma unroll
+          for (int m = 0; m < VC; ++m)
+            vv[t][i][m] = load16(v + x * p.vt + (m * 8 + e) * 8, x < to && (m * 8 + e) * 8 < p.D);
+        }
+      float s[NR][2][4];
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[r][t][i] = 0.0f;
+#pragma unroll
+          for (int m = 0; m < KC; ++m) {
+            const uint4 a = kk[t][0][m], d = kk[t][1][m], w = q[r][m];
+            mma16816(s[r][t], a.x, d.x, a.y, d.y, w.x, w.y);
+            mma16816(s[r][t], a.z, d.z, a.w, d.w, w.z, w.w);
+          }
+        }
+      // weights: rows 2c and 2c + 1, positions e and e + 8 of each run
+      uint32_t w[NR][2][2];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        float hi[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[r][t][i] = pos + t * 16 + (i >> 1) * 8 + e < to ? s[r][t][i] * p.scale2 : -INFINITY;
+            hi[i & 1] = fmaxf(hi[i & 1], s[r][t][i]);
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) hi[i] = fmaxf(hi[i], __shfl_xor_sync(kFull, hi[i], o));
+          hi[i] = fmaxf(hi[i], top[r][i]);
+        }
+        if (__any_sync(kFull, hi[0] > top[r][0] || hi[1] > top[r][1])) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float f = hi[i] == -INFINITY ? 1.0f : ex2(top[r][i] - hi[i]);
+            top[r][i] = hi[i];
+            sum[r][i] *= f;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[r][m][i] *= f, acc[r][m][2 + i] *= f;
+          }
+        }
+        const float z[2] = {top[r][0] == -INFINITY ? 0.0f : top[r][0],
+                            top[r][1] == -INFINITY ? 0.0f : top[r][1]};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float x = ex2(s[r][t][2 * i] - z[0]), y = ex2(s[r][t][2 * i + 1] - z[1]);
+            sum[r][0] += x;
+            sum[r][1] += y;
+            w[r][t][i] = transposed(pack_bf16(x, y));
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        auto word = [&](int i, int m, int k) {
+          const uint4 x = vv[t][i][m];
+          return k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w;
+        };
+        auto couple = [&](int i, int m, int d) {  // element d of rows i and i + 1
+          return __byte_perm(word(i, m, d >> 1), word(i + 1, m, d >> 1), d & 1 ? 0x7632 : 0x5410);
+        };
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          // tile m: element m of each piece, and of the second pieces (64-wide
+          // heads: elements m and m + 4)
+          const int d0 = m, d1 = VC == 2 ? m : m + 4, p1 = VC == 2 ? 1 : 0;
+          const uint32_t a0 = couple(0, 0, d0), a1 = couple(0, p1, d1), a2 = couple(2, 0, d0),
+                         a3 = couple(2, p1, d1);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) mma16816(acc[r][m], a0, a1, a2, a3, w[r][t][0], w[r][t][1]);
+        }
+      }
+    }
+    // join the warps: rows 2c and 2c + 1 of each block
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) sum[r][i] += __shfl_xor_sync(kFull, sum[r][i], o);
+        if (e == 0) {
+          sm[warp][r * 8 + 2 * c + i] = top[r][i];
+          sl[warp][r * 8 + 2 * c + i] = sum[r][i];
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int d = VC == 2 ? (i >> 1) * 64 + e * 8 + m : e * 8 + m + (i >> 1) * 4;
+          so[warp][r * 8 + 2 * c + (i & 1)][d] = acc[r][m][i];
+        }
+    }
+    __syncthreads();
+    const bool only = n <= p.chunk;
+    for (int x = threadIdx.x; x < NR * 8 * DP; x += kStepWarps * 32) {
+      const int row = x / DP, d = x % DP;
+      if (r0 + row >= p.group || d >= p.D) continue;
+      float m = sm[0][row];
+#pragma unroll
+      for (int y = 1; y < kStepWarps; ++y) m = fmaxf(m, sm[y][row]);
+      float l = 0.0f, o = 0.0f;
+#pragma unroll
+      for (int y = 0; y < kStepWarps; ++y) {
+        const float f = sm[y][row] == -INFINITY ? 0.0f : ex2(sm[y][row] - m);
+        l = fmaf(f, sl[y][row], l);
+        if (f != 0.0f) o = fmaf(f, so[y][row][d], o);
+      }
+      const int64_t head = b * p.Hq + g * p.group + r0 + row;
+      if (only) {
+        p.o[head * p.D + d] = __float2bfloat16_rn(o / l);
+      } else {
+        float *out = p.partial + (head * p.chunks + which) * (p.D + 2);
+        out[d] = o;
+        if (d == 0) out[p.D] = m, out[p.D + 1] = l;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Join the chunks of each sequence, a block per query head; zero where the
+// cache is empty.
+__global__ void __launch_bounds__(128) attention_step_join_kernel(const StepArgs p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t head = blockIdx.x;
+  const int64_t n = cache_length(p, head / p.Hq);
+  const int chunks = (int)ceil_div_dev(n, p.chunk), d = threadIdx.x;
+  __shared__ float weight[kChunksMax], high[4];
+  if (chunks == 1) return;  // its one item wrote the result
+  const float *in = p.partial + head * p.chunks * (p.D + 2);
+  float m = -INFINITY;
+  for (int i = threadIdx.x; i < chunks; i += 128) {
+    weight[i] = in[i * (p.D + 2) + p.D];
+    m = fmaxf(m, weight[i]);
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+  if ((threadIdx.x & 31) == 0) high[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
+  float l = 0.0f, o = 0.0f;
+  if (d < p.D)
+#pragma unroll 8
+    for (int i = 0; i < chunks; ++i) {
+      const float f = ex2(weight[i] - m);
+      l = fmaf(f, in[i * (p.D + 2) + p.D + 1], l);
+      o = fmaf(f, in[i * (p.D + 2) + d], o);
+    }
+  if (d >= p.D) return;
+  p.o[head * p.D + d] = __float2bfloat16_rn(chunks ? o / l : 0.0f);
+}
+
+// Positions of a work item: some 16 items per SM at full caches, of at least
+// 128 positions, and at most kChunksMax to a sequence.
+int64_t step_chunk(int64_t B, int64_t S, int64_t Hk) {
+  const double even = (double)B * (double)Hk * (double)S / (152 * 16);
+  int64_t chunk = 128;
+  while (chunk < even || chunk * kChunksMax < S) chunk *= 2;
+  return chunk;
+}
+
+template <int DP, int NR>
+cudaError_t launch_step(StepArgs &a, cudaStream_t st) {
+  a.row_blocks = (a.group + NR * 8 - 1) / (NR * 8);
+  const int64_t items = a.B * a.chunks * a.Hk * a.row_blocks, most = 152 * step_blocks(NR);
+  const cudaError_t e =
+      items > 0 ? launch_ex(attention_step_kernel<DP, NR>, dim3((unsigned)(items < most ? items : most)),
+                            dim3(kStepWarps * 32), 0, st, true, a)
+                : cudaSuccess;
+  if (e != cudaSuccess) return e;
+  return launch_ex(attention_step_join_kernel, dim3((unsigned)(a.B * a.Hq)), dim3(128), 0, st, true,
+                   a);
 }
 
 // Token and head strides that 16-byte loads can use.
@@ -845,8 +1067,6 @@ cudaError_t launch_backward(const CUtensorMap &mq, const CUtensorMap &mk, const 
                   true, mq, mk, mv, mdo, a);
   return e;
 }
-
-dim3 row_grid(int64_t rows) { return dim3((unsigned)ceil_div(rows, 4)); }
 
 }  // namespace
 }  // namespace seq
@@ -973,9 +1193,10 @@ rlcs_status rlcs_attention_backward(
 }
 
 size_t rlcs_attention_step_scratch_bytes(int64_t B, int64_t S, int64_t Hq, int64_t Hk, int64_t D) {
-  (void)S;
-  (void)Hk;
-  return B <= 0 || Hq <= 0 || D <= 0 ? 0 : 16;
+  if (B <= 0 || S <= 0 || Hq <= 0 || Hk <= 0 || D <= 0) return 16;
+  const int64_t chunks = ceil_div(S, step_chunk(B, S, Hk));
+  if (!product_fits(B, Hq, chunks, (D + 2) * 4)) return 0;
+  return (size_t)(B * Hq * chunks * (D + 2) * 4);
 }
 
 rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_batch_stride,
@@ -985,7 +1206,8 @@ rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_ba
                                 const int32_t *lengths, void *out, int64_t B, int64_t S,
                                 int64_t Hq, int64_t Hk, int64_t D, double scale, rlcs_dtype dtype,
                                 void *scratch, size_t scratch_bytes, rlcs_stream_t stream) {
-  if (B < 0 || S < 0 || !attn_sizes(0, B, Hq, Hk, D, scale, dtype) ||
+  if (B < 0 || S < 0 || S >= (int64_t)1 << 40 || !attn_sizes(0, B, Hq, Hk, D, scale, dtype) ||
+      B * Hq >= (int64_t)INT32_MAX ||
       !product_fits(B, k_batch_stride < 0 ? 0 : k_batch_stride, 1) ||
       !product_fits(B, v_batch_stride < 0 ? 0 : v_batch_stride, 1) || k_batch_stride < 0 ||
       v_batch_stride < 0)
@@ -1025,13 +1247,21 @@ rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_ba
   a.o = static_cast<bf *>(out);
   a.B = B;
   a.S = S;
-  a.Hq = Hq;
-  a.Hk = Hk;
+  a.Hq = (int)Hq;
+  a.Hk = (int)Hk;
   a.D = (int)D;
   a.group = (int)(Hq / Hk);
-  a.scale = (float)scale;
-  return launched(launch_ex(attention_step_kernel, row_grid(B * Hq), dim3(128), 0,
-                            reinterpret_cast<cudaStream_t>(stream), true, a));
+  a.chunk = (int)step_chunk(B, S, Hk);
+  a.chunks = (int)ceil_div(S, a.chunk);
+  if (!product_fits(a.chunks, Hk, a.group, 1) ||
+      (int64_t)a.chunks * Hk * a.group >= (int64_t)INT32_MAX)
+    return RLCS_ERR_INVALID_ARG;
+  a.partial = static_cast<float *>(scratch);
+  a.scale2 = (float)(scale * 1.4426950408889634);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (a.group <= 8)
+    return launched(D <= 64 ? launch_step<64, 1>(a, st) : launch_step<128, 1>(a, st));
+  return launched(D <= 64 ? launch_step<64, 2>(a, st) : launch_step<128, 2>(a, st));
 }
 
 }  // extern "C"
