@@ -319,7 +319,9 @@ __global__ void __launch_bounds__(320, 2)
 // 0..15 work on the scores, four threads to a row of a tile with 32 columns
 // each; warp 16 copies tiles; warp 17 issues products. A thread's bf16 piece
 // goes over its own fp32 columns, so the pieces of an operand start 32
-// columns apart.
+// columns apart. dS is rounded to bf16 for its product, as P is; on the
+// diagonal tile, whose short rows carry most of the gradient, the rounding's
+// remainder goes into the other half of those columns and is multiplied too.
 // ---------------------------------------------------------------------------
 struct BackwardArgs {
   const int32_t *cu;
@@ -328,6 +330,7 @@ struct BackwardArgs {
   WsHeader *ws;
   int64_t sequences, tokens;
   int Hq, Hk, group, D;
+  int split;            // dk, dv: blocks (a cluster) that share a group's query heads
   float scale, scale2;  // scale2 = scale * log2 e
 };
 
@@ -355,6 +358,36 @@ __global__ void __launch_bounds__(256)
   if (row < tokens * Hq && d == 0) delta[(row % Hq) * tokens + row / Hq] = t;
 }
 
+// 32 values as bf16 pairs over the first 16 of their columns and, where
+// `rest`, what the rounding took away over the other 16.
+__device__ __forceinline__ void store_bf16(uint32_t at, const uint32_t (&d)[32], bool rest) {
+  uint32_t w[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    w[c] = pack_bf16(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1]));
+  tc::st16(at, w);
+  if (rest) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      w[c] = pack_bf16(__uint_as_float(d[2 * c]) - __uint_as_float(w[c] << 16),
+                       __uint_as_float(d[2 * c + 1]) - __uint_as_float(w[c] & 0xffff0000u));
+    tc::st16(at + 16, w);
+  }
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Four words to the shared memory of another block of the cluster.
+__device__ __forceinline__ void put_remote4(uint32_t place, uint32_t rank, const uint32_t *x) {
+  uint32_t there;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(place), "r"(rank));
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(there), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3])
+               : "memory");
+}
+
 __device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
 template <int DP>
@@ -373,6 +406,9 @@ struct KvSmem {
 //   dV += P^T dO and dK += dS^T Q (DP columns each).
 // Issue order dV(i), S(i+1), dK(i), dP(i+1): P(i+1) is formed while dK(i) and
 // dP(i+1) run, dS(i+1) while dV(i+1) and S(i+2) run.
+// Where key tiles and heads alone would leave SMs idle, a cluster of blocks
+// shares the group's query heads and adds its sums up through distributed
+// shared memory, in rank order, each block the columns of its own.
 template <int DP>
 __global__ void __launch_bounds__(576, 1)
     attention_dkv_kernel(const __grid_constant__ CUtensorMap mq,
@@ -384,13 +420,14 @@ __global__ void __launch_bounds__(576, 1)
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
-  const int g = blockIdx.x % p.Hk;
+  const int rank = blockIdx.x % p.split, g = blockIdx.x / p.split % p.Hk;
+  const int heads = p.group / p.split, head0 = g * p.group + rank * heads;
   Tile t;
   if (!aligned_tiles(raw, p.ws)) return;
-  if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.Hk, lane, t)) return;
+  if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.split / p.Hk, lane, t)) return;
   const int tiles = (t.len + kTile - 1) / kTile;
   const int jt = tiles - 1 - t.first / kTile;  // the first key tile has the most query tiles
-  const int per_head = tiles - jt, steps = per_head * p.group;
+  const int per_head = tiles - jt, steps = per_head * heads;
   const int rows = t.len - jt * kTile < kTile ? t.len - jt * kTile : kTile;
   const int tail = t.len - (tiles - 1) * kTile;  // rows of the sequence's last tile
   if (threadIdx.x == 0) {
@@ -416,7 +453,7 @@ __global__ void __launch_bounds__(576, 1)
       tc::load_tile<DP>(sm.k, &mk, &sm.k_full, g, t.lo + jt * kTile);
       tc::load_tile<DP>(sm.v, &mv, &sm.v_full, g, t.lo + jt * kTile);
       for (int i = 0; i < steps; ++i) {
-        const int h = g * p.group + i / per_head, row = t.lo + (jt + i % per_head) * kTile;
+        const int h = head0 + i / per_head, row = t.lo + (jt + i % per_head) * kTile;
         const int a = i % 3, b = i & 1;
         if (i >= 3 && !tc::mbar_wait(&sm.q_empty[a], (i / 3 - 1) & 1, abort)) break;
         tc::load_tile<DP>(sm.q[a], &mq, &sm.q_full[a], h, row);
@@ -459,6 +496,8 @@ __global__ void __launch_bounds__(576, 1)
       if (!ok) break;
       tc::fence_after_sync();
       tc::product_parts<DP, 4>(lead, tK, tP, tc::smem_addr(sm.q[i % 3]), i > 0);
+      if (i % per_head == 0)
+        tc::product_parts<DP, 4>(lead, tK, tP + 16, tc::smem_addr(sm.q[i % 3]), true);
       tc::commit(lead, &sm.q_empty[i % 3]);
       if (i + 1 == steps) tc::commit(lead, &sm.done);
       if (i + 1 < steps) ok = grads(i + 1);
@@ -469,7 +508,7 @@ __global__ void __launch_bounds__(576, 1)
     // Column statistics of step i: one value per thread of parts 0 and 1, a
     // step ahead.
     auto column = [&](int i) {
-      const int h = g * p.group + i / per_head, at = (jt + i % per_head) * kTile + r;
+      const int h = head0 + i / per_head, at = (jt + i % per_head) * kTile + r;
       if (part > 1) return 0.0f;
       if (at >= t.len) return part ? 0.0f : INFINITY;  // no row: weights of zero
       const float x = (part ? p.delta : p.lse)[(int64_t)h * p.tokens + t.lo + at];
@@ -485,7 +524,7 @@ __global__ void __launch_bounds__(576, 1)
       if (i + 1 < steps) next = column(i + 1);
       const float *lse = &sm.lse[i & 1][part * 32], *delta = &sm.delta[i & 1][part * 32];
       const bool diagonal = i % per_head == 0;
-      uint32_t s[32], d[32], w[16];
+      uint32_t s[32], d[32];
       tc::warp_wait(&sm.s_full, i & 1, abort);
       tc::fence_after_sync();
       tc::ld32(tS + mine, s);
@@ -504,10 +543,7 @@ __global__ void __launch_bounds__(576, 1)
 #pragma unroll
         for (int c = 0; c < 32; ++c)
           if (part * 32 + c < r) s[c] = 0u;
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        w[c] = pack_bf16(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
-      tc::st16(tS + mine, w);
+      store_bf16(tS + mine, s, false);
       tc::wait_st();
       tc::fence_before_sync();
       tc::warp_arrive(&sm.p_ready, lead);
@@ -532,21 +568,62 @@ __global__ void __launch_bounds__(576, 1)
 #pragma unroll
         for (int c = 0; c < 32; ++c)
           if (part * 32 + c < r) d[c] = 0u;
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        w[c] = pack_bf16(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1]));
-      tc::st16(tP + mine, w);
+      store_bf16(tP + mine, d, diagonal);
       tc::wait_st();
       tc::fence_before_sync();
       tc::warp_arrive(&sm.ds_ready, lead);
     }
-    if (tc::warp_wait(&sm.done, 0, abort)) {
+    if (tc::warp_wait(&sm.done, 0, abort) && p.split == 1) {
       tc::fence_after_sync();
       const int64_t row = (int64_t)t.lo + jt * kTile + r;
       const int of = part >> 1, from = (part & 1) * (DP / 2);  // dv or dk, half a row
       write_row<DP / 2>((of ? tK : tV) + lanes + from,
                         (of ? p.dk : p.dv) + (row * p.Hk + g) * p.D + from, p.D - from,
                         of ? p.scale : 1.0f, r < rows);
+    }
+  }
+  if (p.split > 1) {
+    __syncwarp();
+    tc::fence_before_sync();
+    cluster_barrier();  // every block is done with its tiles: their memory takes the sums
+    tc::fence_after_sync();
+    const int r = threadIdx.x & 127, part = warp >> 2;
+    const int fours = 2 * DP / 4 / p.split;  // of the 2 DP columns (dv, dk), a block's own
+    // [source][own columns, by fours][row], 16 bytes each
+    if (part < 4) {
+      const uint32_t acc = (part < 2 ? tV : tK) + ((uint32_t)((warp & 3) * 32) << 16) +
+                           (part & 1) * (DP / 2);
+      const uint32_t here = tc::smem_addr(raw) + (rank * fours * 128 + r) * 16;
+#pragma unroll
+      for (int c = 0; c < DP / 2; c += 16) {
+        uint32_t x[16];
+        tc::ld16(acc + c, x);
+        tc::wait_ld();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int four = (part * (DP / 2) + c) / 4 + k;
+          put_remote4(here + four % fours * 2048, four / fours, x + 4 * k);
+        }
+      }
+    }
+    tc::fence_before_sync();
+    cluster_barrier();
+    tc::fence_after_sync();
+    if (part < 4 && r < rows) {
+      const float4 *sums = reinterpret_cast<const float4 *>(raw);
+      const int64_t row = ((int64_t)t.lo + jt * kTile + r) * p.Hk + g;
+      for (int four = part; four < fours; four += 4) {
+        float4 x = sums[four * 128 + r];
+        for (int k = 1; k < p.split; ++k) {
+          const float4 y = sums[(k * fours + four) * 128 + r];
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        const int col = (rank * fours + four) * 4, of = col >= DP, d = col - of * DP;
+        const float f = of ? p.scale : 1.0f;
+        if (d < p.D)
+          *reinterpret_cast<uint2 *>((of ? p.dk : p.dv) + row * p.D + d) =
+              make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
+      }
     }
   }
   tc::fence_before_sync();
@@ -648,6 +725,7 @@ __global__ void __launch_bounds__(576, 1)
       tc::fence_after_sync();
       if (j + 1 < steps && !(ok = grads(j + 1))) break;
       tc::product_parts<DP, 4>(lead, tQ, j & 1 ? tS1 : tS0, tc::smem_addr(sm.k[j % 3]), j > 0);
+      if (j == 0) tc::product_parts<DP, 4>(lead, tQ, tS0 + 16, tc::smem_addr(sm.k[0]), true);
       tc::commit(lead, &sm.k_empty[j % 3]);
       if (j + 1 == steps) tc::commit(lead, &sm.done);
       if (j + 2 < steps) ok = scores(j + 2);
@@ -666,7 +744,7 @@ __global__ void __launch_bounds__(576, 1)
     bool ok = true;
     for (int j = 0; j < steps && ok; ++j) {
       const uint32_t at = (j & 1 ? tS1 : tS0) + mine;
-      uint32_t s[32], d[32], w[16];
+      uint32_t s[32], d[32];
       ok = tc::warp_wait(&sm.s_full[j & 1], (j / 2) & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
@@ -693,10 +771,7 @@ __global__ void __launch_bounds__(576, 1)
 #pragma unroll
         for (int c = 0; c < 32; ++c)
           if (part * 32 + c > r) d[c] = 0u;
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        w[c] = pack_bf16(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1]));
-      tc::st16(at, w);
+      store_bf16(at, d, j == 0);
       tc::wait_st();
       tc::fence_before_sync();
       tc::warp_arrive(&sm.ds_ready, lead);
@@ -1048,6 +1123,14 @@ cudaError_t launch_forward(const CUtensorMap &mq, const CUtensorMap &mk, const C
                    a);
 }
 
+// Blocks that share a group's query heads: the fewest, of the powers of two
+// that divide the group, that make up a block per SM.
+int group_split(int64_t blocks, int group) {
+  int split = 1;
+  while (split < 8 && group % (2 * split) == 0 && blocks * split < 152) split *= 2;
+  return split;
+}
+
 template <int DP>
 cudaError_t launch_backward(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                             const CUtensorMap &mdo, const BackwardArgs &a, int64_t tiles,
@@ -1059,9 +1142,21 @@ cudaError_t launch_backward(const CUtensorMap &mq, const CUtensorMap &mk, const 
   constexpr size_t kv_smem = kv < least ? least : kv, q_smem = q < least ? least : q;
   cudaError_t e = allow_dynamic_smem<attention_dkv_kernel<DP>>(kv_smem);
   if (e == cudaSuccess) e = allow_dynamic_smem<attention_dq_kernel<DP>>(q_smem);
-  if (e == cudaSuccess)
-    e = launch_ex(attention_dkv_kernel<DP>, dim3((unsigned)(tiles * a.Hk)), dim3(576), kv_smem, st,
-                  true, mq, mk, mv, mdo, a);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * a.Hk * a.split));
+  cfg.blockDim = dim3(576);
+  cfg.dynamicSmemBytes = kv_smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.split > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, attention_dkv_kernel<DP>, mq, mk, mv, mdo, a);
   if (e == cudaSuccess)
     e = launch_ex(attention_dq_kernel<DP>, dim3((unsigned)(tiles * a.Hq)), dim3(576), q_smem, st,
                   true, mq, mk, mv, mdo, a);
@@ -1179,6 +1274,7 @@ rlcs_status rlcs_attention_backward(
                           (int)Hk,
                           (int)(Hq / Hk),
                           (int)D,
+                          group_split(tile_bound(sequences, tokens) * Hk, (int)(Hq / Hk)),
                           (float)scale,
                           (float)(scale * 1.4426950408889634)};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

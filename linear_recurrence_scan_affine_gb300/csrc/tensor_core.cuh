@@ -126,9 +126,13 @@ constexpr uint32_t instr(int n, bool b_n_contiguous) {
 // bytes between groups of 8 k-rows, and the leading offset is the distance
 // between 64-column boxes.
 constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t operand_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+// (In a cluster a shared-memory address carries the block's rank above its
+// 18 bits of offset.)
+__device__ __forceinline__ uint32_t operand_k(uint32_t addr) {
+  return ((addr & 0x3ffff) >> 4) | (1u << 16);
+}
 __device__ __forceinline__ uint32_t operand_n(uint32_t addr) {
-  return (addr >> 4) | ((16384u >> 4) << 16);
+  return ((addr & 0x3ffff) >> 4) | ((16384u >> 4) << 16);
 }
 // Products are issued by one lane, but every lane of its warp runs the code
 // and `lead` predicates the instruction alone: in a branch taken by one lane
