@@ -171,13 +171,17 @@ __global__ void __launch_bounds__(320, 2)
   if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.Hq, lane, t)) return;
   const int steps = t.first / kTile + 1;
   const int rows = t.len - t.first < kTile ? t.len - t.first : kTile;
-  if (threadIdx.x == 0) {
+  // the copying lane sets the barriers up and starts the first copies at once
+  if (warp == 8 && lane == 0) {
     for (uint64_t *b : {&sm.q_full, &sm.k_full, &sm.k_empty, &sm.v_full, &sm.v_empty, &sm.s_full,
                         &sm.o_full})
       mbar_init(b, 1);
     mbar_init(&sm.p_ready, 8);
     sm.abort = 0;
     fence_mbar_init();
+    tc::load_tile<DP>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
+    tc::load_tile<DP>(sm.k, &mk, &sm.k_full, h / p.group, t.lo + t.first);
+    tc::load_tile<DP>(sm.v, &mv, &sm.v_full, h / p.group, t.lo + t.first);
   }
   if (warp == 9) tc::tmem_alloc(&sm.tmem, 256);
   tc::fence_before_sync();
@@ -189,12 +193,11 @@ __global__ void __launch_bounds__(320, 2)
 
   if (warp == 8) {
     if (lane == 0) {
-      tc::load_tile<DP>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
-      for (int it = 0; it < steps; ++it) {
+      for (int it = 1; it < steps; ++it) {
         const int row = t.lo + t.first - it * kTile;
-        if (it > 0 && !tc::mbar_wait(&sm.k_empty, (it - 1) & 1, abort)) break;
+        if (!tc::mbar_wait(&sm.k_empty, (it - 1) & 1, abort)) break;
         tc::load_tile<DP>(sm.k, &mk, &sm.k_full, h / p.group, row);
-        if (it > 0 && !tc::mbar_wait(&sm.v_empty, (it - 1) & 1, abort)) break;
+        if (!tc::mbar_wait(&sm.v_empty, (it - 1) & 1, abort)) break;
         tc::load_tile<DP>(sm.v, &mv, &sm.v_full, h / p.group, row);
       }
     }
@@ -430,7 +433,15 @@ __global__ void __launch_bounds__(576, 1)
   const int per_head = tiles - jt, steps = per_head * heads;
   const int rows = t.len - jt * kTile < kTile ? t.len - jt * kTile : kTile;
   const int tail = t.len - (tiles - 1) * kTile;  // rows of the sequence's last tile
-  if (threadIdx.x == 0) {
+  auto load_q = [&](int i) {
+    tc::load_tile<DP>(sm.q[i % 3], &mq, &sm.q_full[i % 3], head0 + i / per_head,
+                      t.lo + (jt + i % per_head) * kTile);
+  };
+  auto load_dout = [&](int i) {
+    tc::load_tile<DP>(sm.dout[i & 1], &mdo, &sm.do_full[i & 1], head0 + i / per_head,
+                      t.lo + (jt + i % per_head) * kTile);
+  };
+  if (warp == 16 && lane == 0) {
     for (int i = 0; i < 3; ++i) mbar_init(&sm.q_full[i], 1), mbar_init(&sm.q_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.do_full[i], 1), mbar_init(&sm.do_empty[i], 1);
     for (uint64_t *b : {&sm.k_full, &sm.v_full, &sm.s_full, &sm.dp_full, &sm.done}) mbar_init(b, 1);
@@ -438,6 +449,10 @@ __global__ void __launch_bounds__(576, 1)
     mbar_init(&sm.ds_ready, 16);
     sm.abort = 0;
     fence_mbar_init();
+    tc::load_tile<DP>(sm.k, &mk, &sm.k_full, g, t.lo + jt * kTile);
+    load_q(0);
+    tc::load_tile<DP>(sm.v, &mv, &sm.v_full, g, t.lo + jt * kTile);
+    load_dout(0);
   }
   if (warp == 17) tc::tmem_alloc(&sm.tmem, 512);
   tc::fence_before_sync();
@@ -450,15 +465,11 @@ __global__ void __launch_bounds__(576, 1)
 
   if (warp == 16) {
     if (lane == 0) {
-      tc::load_tile<DP>(sm.k, &mk, &sm.k_full, g, t.lo + jt * kTile);
-      tc::load_tile<DP>(sm.v, &mv, &sm.v_full, g, t.lo + jt * kTile);
-      for (int i = 0; i < steps; ++i) {
-        const int h = head0 + i / per_head, row = t.lo + (jt + i % per_head) * kTile;
-        const int a = i % 3, b = i & 1;
-        if (i >= 3 && !tc::mbar_wait(&sm.q_empty[a], (i / 3 - 1) & 1, abort)) break;
-        tc::load_tile<DP>(sm.q[a], &mq, &sm.q_full[a], h, row);
-        if (i >= 2 && !tc::mbar_wait(&sm.do_empty[b], (i / 2 - 1) & 1, abort)) break;
-        tc::load_tile<DP>(sm.dout[b], &mdo, &sm.do_full[b], h, row);
+      for (int i = 1; i < steps; ++i) {
+        if (i >= 3 && !tc::mbar_wait(&sm.q_empty[i % 3], (i / 3 - 1) & 1, abort)) break;
+        load_q(i);
+        if (i >= 2 && !tc::mbar_wait(&sm.do_empty[i & 1], (i / 2 - 1) & 1, abort)) break;
+        load_dout(i);
       }
     }
   } else if (warp == 17) {
@@ -664,7 +675,15 @@ __global__ void __launch_bounds__(576, 1)
   if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.Hq, lane, t)) return;
   const int steps = t.first / kTile + 1;
   const int rows = t.len - t.first < kTile ? t.len - t.first : kTile;
-  if (threadIdx.x == 0) {
+  auto load_k = [&](int j) {
+    tc::load_tile<DP>(sm.k[j % 3], &mk, &sm.k_full[j % 3], h / p.group,
+                      t.lo + t.first - j * kTile);
+  };
+  auto load_v = [&](int j) {
+    tc::load_tile<DP>(sm.v[j & 1], &mv, &sm.v_full[j & 1], h / p.group,
+                      t.lo + t.first - j * kTile);
+  };
+  if (warp == 16 && lane == 0) {
     for (int i = 0; i < 3; ++i) mbar_init(&sm.k_full[i], 1), mbar_init(&sm.k_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.v_full[i], 1);
@@ -675,6 +694,10 @@ __global__ void __launch_bounds__(576, 1)
     mbar_init(&sm.ds_ready, 16);
     sm.abort = 0;
     fence_mbar_init();
+    tc::load_tile<DP>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
+    load_k(0);
+    tc::load_tile<DP>(sm.dout, &mdo, &sm.do_full, h, t.lo + t.first);
+    load_v(0);
   }
   if (warp == 17) tc::tmem_alloc(&sm.tmem, 512);
   tc::fence_before_sync();
@@ -687,14 +710,11 @@ __global__ void __launch_bounds__(576, 1)
 
   if (warp == 16) {
     if (lane == 0) {
-      tc::load_tile<DP>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
-      for (int j = 0; j < steps; ++j) {
-        const int row = t.lo + t.first - j * kTile, a = j % 3, b = j & 1;
-        if (j >= 3 && !tc::mbar_wait(&sm.k_empty[a], (j / 3 - 1) & 1, abort)) break;
-        tc::load_tile<DP>(sm.k[a], &mk, &sm.k_full[a], h / p.group, row);
-        if (j == 0) tc::load_tile<DP>(sm.dout, &mdo, &sm.do_full, h, t.lo + t.first);
-        if (j >= 2 && !tc::mbar_wait(&sm.v_empty[b], (j / 2 - 1) & 1, abort)) break;
-        tc::load_tile<DP>(sm.v[b], &mv, &sm.v_full[b], h / p.group, row);
+      for (int j = 1; j < steps; ++j) {
+        if (j >= 3 && !tc::mbar_wait(&sm.k_empty[j % 3], (j / 3 - 1) & 1, abort)) break;
+        load_k(j);
+        if (j >= 2 && !tc::mbar_wait(&sm.v_empty[j & 1], (j / 2 - 1) & 1, abort)) break;
+        load_v(j);
       }
     }
   } else if (warp == 17) {
@@ -1076,7 +1096,7 @@ __global__ void __launch_bounds__(128) attention_step_join_kernel(const StepArgs
 // Positions of a work item: some 16 items per SM at full caches, of at least
 // 128 positions, and at most kChunksMax to a sequence.
 int64_t step_chunk(int64_t B, int64_t S, int64_t Hk) {
-  const double even = (double)B * (double)Hk * (double)S / (152 * 16);
+  const double even = (double)B * (double)Hk * (double)S / (kSms * 16);
   int64_t chunk = 128;
   while (chunk < even || chunk * kChunksMax < S) chunk *= 2;
   return chunk;
@@ -1085,7 +1105,7 @@ int64_t step_chunk(int64_t B, int64_t S, int64_t Hk) {
 template <int DP, int NR>
 cudaError_t launch_step(StepArgs &a, cudaStream_t st) {
   a.row_blocks = (a.group + NR * 8 - 1) / (NR * 8);
-  const int64_t items = a.B * a.chunks * a.Hk * a.row_blocks, most = 152 * step_blocks(NR);
+  const int64_t items = a.B * a.chunks * a.Hk * a.row_blocks, most = kSms * step_blocks(NR);
   const cudaError_t e =
       items > 0 ? launch_ex(attention_step_kernel<DP, NR>, dim3((unsigned)(items < most ? items : most)),
                             dim3(kStepWarps * 32), 0, st, true, a)
@@ -1127,7 +1147,7 @@ cudaError_t launch_forward(const CUtensorMap &mq, const CUtensorMap &mk, const C
 // that divide the group, that make up a block per SM.
 int group_split(int64_t blocks, int group) {
   int split = 1;
-  while (split < 8 && group % (2 * split) == 0 && blocks * split < 152) split *= 2;
+  while (split < 8 && group % (2 * split) == 0 && blocks * split < kSms) split *= 2;
   return split;
 }
 

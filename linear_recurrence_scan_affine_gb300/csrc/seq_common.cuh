@@ -13,6 +13,7 @@
 namespace rlcs {
 namespace seq {
 
+constexpr int kSms = 152;  // GB300: what grids are sized for (a different count stays correct)
 constexpr int64_t kMaxElems = (int64_t)1 << 60;  // element counts stay far below 2^63
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(1024)
 // are no more than run at once.
 template <bool BACK>
 constexpr int blocks_max() {
-  return 152 * (BACK ? 2 : 8);
+  return kSms * (BACK ? 2 : 8);
 }
 
 bool head_sizes(int64_t tokens, int64_t Hq, int64_t Hk, int64_t D, int64_t R, int64_t max_pos,

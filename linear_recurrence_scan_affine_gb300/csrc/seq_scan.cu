@@ -427,14 +427,6 @@ __global__ void __launch_bounds__(JOINED ? kWarpsMax * 32 : 32)
   }
 }
 
-int sm_count() {
-  int dev = 0, v = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
-    return 152;
-  return v;
-}
-
 // How a call's steps are shared out. Measured on GB300, us forward / gradient:
 //  - a warp walks alone from 5 channel groups per SM on, or where the walk is
 //    short: 64 x 512 x 1024 bf16 45 / 73 against 63 / 80 joined, 128 x 40 x
@@ -451,14 +443,13 @@ struct Share {
   int blocks, warps, steps;  // blocks = 0: every warp alone
 };
 Share share_out(int64_t groups, int64_t T, int chunk) {
-  const int sms = sm_count();
-  if (T <= 128 || groups >= 5 * (int64_t)sms) return {0, 1, 0};
+  if (T <= 128 || groups >= 5 * (int64_t)kSms) return {0, 1, 0};
   int blocks = 1;
-  while (blocks < (groups <= 4 ? 16 : 8) && groups * blocks * 2 <= sms &&
+  while (blocks < (groups <= 4 ? 16 : 8) && groups * blocks * 2 <= kSms &&
          T >= (int64_t)blocks * 2 * kWarpsMax * chunk)
     blocks *= 2;
   const int64_t warps = ceil_div(T, 32) < kWarpsMax ? ceil_div(T, 32) : kWarpsMax;
-  const int64_t most = groups * blocks * 2 <= sms ? 256 : 128;
+  const int64_t most = groups * blocks * 2 <= kSms ? 256 : 128;
   const int64_t each = ceil_div(ceil_div(T, blocks * warps), chunk) * chunk;
   return {blocks, (int)warps, (int)(each < most ? each : most)};
 }
