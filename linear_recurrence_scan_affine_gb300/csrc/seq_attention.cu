@@ -328,7 +328,9 @@ __global__ void __launch_bounds__(320, 2)
 // ---------------------------------------------------------------------------
 struct BackwardArgs {
   const int32_t *cu;
-  const float *lse, *delta;  // [Hq, tokens]
+  const bf *dout, *out;
+  const float *lse;  // [Hq, tokens]
+  float *delta;      // the same
   bf *dq, *dk, *dv;
   WsHeader *ws;
   int64_t sequences, tokens;
@@ -337,28 +339,46 @@ struct BackwardArgs {
   float scale, scale2;  // scale2 = scale * log2 e
 };
 
-// 8 elements per lane, 16 lanes per row.
+// Eight products of bf16, summed in fp32.
+__device__ __forceinline__ float dot8(const uint4 &u, const uint4 &v) {
+  const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
+  float t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), t);
+    t = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), t);
+  }
+  return t;
+}
+
+// delta: DP/8 lanes to a row, 8 elements to a lane, four rows at a time.
+template <int DP>
 __global__ void __launch_bounds__(256)
     attention_delta_kernel(const bf *dout, const bf *out, float *delta, int64_t tokens, int Hq,
                            int D) {
+  constexpr int kLanes = DP / 8, kRows = 256 / kLanes;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int d = (threadIdx.x & 15) * 8;
-  float t = 0.0f;
-  if (row < tokens * Hq && d < D) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(dout + row * D + d);
-    const uint4 b = *reinterpret_cast<const uint4 *>(out + row * D + d);
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  const int d = threadIdx.x % kLanes * 8;
+  const int64_t first = (int64_t)blockIdx.x * 4 * kRows + threadIdx.x / kLanes, end = tokens * Hq;
+  uint4 a[4], b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      t = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), t);
-      t = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), t);
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = first + i * kRows;
+    a[i] = b[i] = make_uint4(0, 0, 0, 0);
+    if (row < end && d < D) {
+      a[i] = __ldg(reinterpret_cast<const uint4 *>(dout + row * D + d));
+      b[i] = __ldg(reinterpret_cast<const uint4 *>(out + row * D + d));
     }
   }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
-  if (row < tokens * Hq && d == 0) delta[(row % Hq) * tokens + row / Hq] = t;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = first + i * kRows;
+    float t = dot8(a[i], b[i]);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
+    if (row < end && d == 0) delta[row % Hq * tokens + row / Hq] = t;
+  }
 }
 
 // 32 values as bf16 pairs over the first 16 of their columns and, where
@@ -516,14 +536,14 @@ __global__ void __launch_bounds__(576, 1)
   } else {
     const int r = threadIdx.x & 127, part = warp >> 2;  // this thread's key row, its columns
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, mine = lanes + part * 32;
-    // Column statistics of step i: one value per thread of parts 0 and 1, a
-    // step ahead.
+    // Column statistics of step i, negated: one value per thread of parts 0
+    // and 1, a step ahead.
     auto column = [&](int i) {
       const int h = head0 + i / per_head, at = (jt + i % per_head) * kTile + r;
       if (part > 1) return 0.0f;
-      if (at >= t.len) return part ? 0.0f : INFINITY;  // no row: weights of zero
+      if (at >= t.len) return part ? 0.0f : -INFINITY;  // no row: weights of zero
       const float x = (part ? p.delta : p.lse)[(int64_t)h * p.tokens + t.lo + at];
-      return part ? x : x * kLog2e;
+      return part ? -x : -x * kLog2e;
     };
     float next = column(0);
     const float2 k2 = make_float2(p.scale2, p.scale2);
@@ -543,8 +563,8 @@ __global__ void __launch_bounds__(576, 1)
 #pragma unroll
       for (int c = 0; c < 32; c += 4) {
         const float4 m = *reinterpret_cast<const float4 *>(lse + c);
-        const float2 a = __ffma2_rn(pair(s + c), k2, make_float2(-m.x, -m.y));
-        const float2 b = __ffma2_rn(pair(s + c + 2), k2, make_float2(-m.z, -m.w));
+        const float2 a = __ffma2_rn(pair(s + c), k2, make_float2(m.x, m.y));
+        const float2 b = __ffma2_rn(pair(s + c + 2), k2, make_float2(m.z, m.w));
         s[c] = __float_as_uint(ex2(a.x));
         s[c + 1] = __float_as_uint(ex2(a.y));
         s[c + 2] = __float_as_uint(ex2(b.x));
@@ -567,9 +587,9 @@ __global__ void __launch_bounds__(576, 1)
       for (int c = 0; c < 32; c += 4) {
         const float4 m = *reinterpret_cast<const float4 *>(delta + c);
         const float2 a =
-            __fmul2_rn(pair(s + c), __fadd2_rn(pair(d + c), make_float2(-m.x, -m.y)));
+            __fmul2_rn(pair(s + c), __fadd2_rn(pair(d + c), make_float2(m.x, m.y)));
         const float2 b =
-            __fmul2_rn(pair(s + c + 2), __fadd2_rn(pair(d + c + 2), make_float2(-m.z, -m.w)));
+            __fmul2_rn(pair(s + c + 2), __fadd2_rn(pair(d + c + 2), make_float2(m.z, m.w)));
         d[c] = __float_as_uint(a.x);
         d[c + 1] = __float_as_uint(a.y);
         d[c + 2] = __float_as_uint(b.x);
@@ -1157,10 +1177,15 @@ cudaError_t launch_backward(const CUtensorMap &mq, const CUtensorMap &mk, const 
                             cudaStream_t st) {
   // more than half an SM's shared memory, so that one block has the SM (and
   // its tensor memory) to itself
+  constexpr int kRows = 4 * 256 / (DP / 8);  // of delta, to a block
+  cudaError_t e = launch_ex(attention_delta_kernel<DP>,
+                            dim3((unsigned)ceil_div(a.tokens * a.Hq, kRows)), dim3(256), 0, st, true,
+                            a.dout, a.out, a.delta, a.tokens, a.Hq, a.D);
+  if (e != cudaSuccess) return e;
   constexpr size_t least = 120 * 1024, kv = sizeof(KvSmem<DP>), q = sizeof(QSmem<DP>);
   static_assert(kv <= 232448 && q <= 232448, "a block has 227 KB of shared memory at most");
   constexpr size_t kv_smem = kv < least ? least : kv, q_smem = q < least ? least : q;
-  cudaError_t e = allow_dynamic_smem<attention_dkv_kernel<DP>>(kv_smem);
+  e = allow_dynamic_smem<attention_dkv_kernel<DP>>(kv_smem);
   if (e == cudaSuccess) e = allow_dynamic_smem<attention_dq_kernel<DP>>(q_smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1282,6 +1307,8 @@ rlcs_status rlcs_attention_backward(
     return RLCS_ERR_CUDA;
   float *delta = reinterpret_cast<float *>(static_cast<char *>(scratch) + 64);
   const BackwardArgs a = {cu_seqlens,
+                          static_cast<const bf *>(dout),
+                          static_cast<const bf *>(out),
                           lse,
                           delta,
                           static_cast<bf *>(dq),
@@ -1298,11 +1325,6 @@ rlcs_status rlcs_attention_backward(
                           (float)scale,
                           (float)(scale * 1.4426950408889634)};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      launch_ex(attention_delta_kernel, dim3((unsigned)ceil_div(tokens * Hq, 16)), dim3(256), 0, st,
-                true, static_cast<const bf *>(dout), static_cast<const bf *>(out), delta, tokens,
-                (int)Hq, (int)D);
-  if (e != cudaSuccess) return launched(e);
   const int64_t tiles = tile_bound(sequences, tokens);
   return launched(D <= 64 ? launch_backward<64>(mq, mk, mv, mdo, a, tiles, st)
                           : launch_backward<128>(mq, mk, mv, mdo, a, tiles, st));
