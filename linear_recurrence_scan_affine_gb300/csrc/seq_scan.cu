@@ -431,25 +431,28 @@ __global__ void __launch_bounds__(JOINED ? kWarpsMax * 32 : 32)
 //  - a warp walks alone from 5 channel groups per SM on, or where the walk is
 //    short: 64 x 512 x 1024 bf16 45 / 73 against 63 / 80 joined, 128 x 40 x
 //    2048 13 / 23 against 28 / 34; with 128 groups (8 x 4096 x 1024) alone
-//    171 / 276 against 56 / 84 joined;
+//    171 / 276 against 53 / 74 joined;
 //  - joined, the blocks of a cluster are as many as fill the SMs once: 2 x
-//    16384 x 1024 58 / 85 with 4, 82 / 111 with 8 and 89 / 117 with 2;
-//  - up to 8 blocks, or 16 where at most 4 clusters run (16 SMs of one
-//    processing cluster must be free at once): 1 x 30000 x 96 29 / 33 with
-//    16, 44 / 56 with 8; 1 x 131072 x 512 (8 groups) 197 / 271 and 182 / 234;
-//  - segments of 128 steps, which keep the second pass in L2, or 256 where
-//    fewer than half the SMs work: 1 x 131072 x 512 182 / 234 against 203 / 250.
+//    16384 x 1024 54 / 77 with 4, 75 / 108 with 8 and 82 / 111 with 2;
+//  - a cluster's blocks must find their SMs in one processing cluster: up to 8
+//    blocks, 12 for at most 8 clusters and 16 for at most 4. 1 x 131072 x 512
+//    (8) 132 / 189 with 12, 183 / 262 with 16, 166 / 222 with 8; 1 x 30000 x
+//    96 (2) 27 / 32 with 16, 30 / 40 with 12;
+//  - segments of 256 steps, or, where most SMs work, 128 forward and 64 in the
+//    gradient, which keep the second pass in L2: 8 x 4096 x 1024 53 / 74
+//    against 56 / 87.
 struct Share {
   int blocks, warps, steps;  // blocks = 0: every warp alone
 };
-Share share_out(int64_t groups, int64_t T, int chunk) {
+Share share_out(int64_t groups, int64_t T, int chunk, bool back) {
   if (T <= 128 || groups >= 5 * (int64_t)kSms) return {0, 1, 0};
   int blocks = 1;
-  while (blocks < (groups <= 4 ? 16 : 8) && groups * blocks * 2 <= kSms &&
-         T >= (int64_t)blocks * 2 * kWarpsMax * chunk)
-    blocks *= 2;
+  for (int wider : {2, 4, 8, 12, 16})
+    if (groups <= (wider > 12 ? 4 : wider > 8 ? 8 : kSms / wider) &&
+        T >= (int64_t)wider * kWarpsMax * chunk)
+      blocks = wider;
   const int64_t warps = ceil_div(T, 32) < kWarpsMax ? ceil_div(T, 32) : kWarpsMax;
-  const int64_t most = groups * blocks * 2 <= kSms ? 256 : 128;
+  const int64_t most = groups * blocks <= 2 * kSms / 3 ? 256 : (back ? 64 : 128);
   const int64_t each = ceil_div(ceil_div(T, blocks * warps), chunk) * chunk;
   return {blocks, (int)warps, (int)(each < most ? each : most)};
 }
@@ -459,7 +462,7 @@ cudaError_t launch_scan(ScanArgs a, int64_t B, cudaStream_t st) {
   constexpr int kRow = 32 * V * (int)sizeof(E), kChunk = kChunkBytes / ((BACK ? 4 : 2) * kRow);
   a.groups = ceil_div(a.D, 32 * V);
   const int64_t groups = B * a.groups;
-  const Share share = share_out(groups, a.T, kChunk);
+  const Share share = share_out(groups, a.T, kChunk, BACK);
   if (share.blocks == 0)
     return launch_ex(gated_scan_kernel<E, V, CB, BACK, false>, dim3((unsigned)groups), dim3(32),
                      ring_chunks<CB, false>() * kChunkBytes, st, true, a);
