@@ -96,14 +96,15 @@ def base_name(est):
 
 
 def kernel_source_hash():
-    """Short hash of the CUDA sources, to tell whether stored ncu counters
-    still describe the kernels being timed."""
+    """Short hash of the estimators' CUDA sources, to tell whether stored ncu
+    counters still describe the kernels being timed."""
     import glob
     import hashlib
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "linear_recurrence_scan_affine_gb300", "csrc")
     for f in sorted(glob.glob(os.path.join(csrc, "*.cu*"))):
-        if os.path.basename(f) == "diag.cu":  # the diagnostic, not an estimator kernel
+        # the diagnostic and the sequence operators are no estimator kernels
+        if os.path.basename(f).startswith(("diag.cu", "seq_", "tensor_core.cuh")):
             continue
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:
