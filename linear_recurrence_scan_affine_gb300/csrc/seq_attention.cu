@@ -19,6 +19,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;
 
+// Rows of the tiles a block walks over: with heads up to 64 wide half as many,
+// so that two or three blocks share an SM's tensor memory and hide each
+// other's waits, which short sequences are made of.
+template <int DP>
+constexpr int inner() {
+  return DP == 64 ? 64 : 128;
+}
+
 // Tile `index` in the order of sequences, longest rows first within each
 // (its last tile first): the sequence's bounds and the tile's number, or
 // false past the last tile. One warp; every lane gets the result.
@@ -139,9 +147,12 @@ __device__ __forceinline__ bool aligned_tiles(const void *raw, WsHeader *ws) {
 
 template <int DP>
 struct ForwardSmem {
-  alignas(1024) unsigned char q[DP * 256], k[DP * 256], v[DP * 256];
+  static constexpr int kStages = DP == 64 ? 2 : 1;  // of keys and values
+  alignas(1024) unsigned char q[DP * 256], k[kStages][DP * inner<DP>() * 2],
+      v[kStages][DP * inner<DP>() * 2];
   float row[2][128];  // maxima, and at the end sums, of the two halves of each row
-  uint64_t q_full, k_full, k_empty, v_full, v_empty, s_full, p_ready, o_full;
+  uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t s_full, p_ready, o_full;
   uint32_t tmem;
   int abort;
 };
@@ -157,7 +168,7 @@ struct ForwardArgs {
 };
 
 template <int DP>
-__global__ void __launch_bounds__(320, 2)
+__global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
     attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv, const ForwardArgs p) {
   extern __shared__ __align__(1024) unsigned char raw[];
@@ -169,97 +180,109 @@ __global__ void __launch_bounds__(320, 2)
   Tile t;
   if (!aligned_tiles(raw, p.ws)) return;
   if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.Hq, lane, t)) return;
-  const int steps = t.first / kTile + 1;
+  constexpr int IT = inner<DP>(), kStages = ForwardSmem<DP>::kStages;
   const int rows = t.len - t.first < kTile ? t.len - t.first : kTile;
+  const int steps = (t.first + rows + IT - 1) / IT;  // key tiles, the last one first
+  auto first_key = [&](int it) { return (steps - 1 - it) * IT; };
+  auto load_k = [&](int it) {
+    tc::load_tile<DP, IT>(sm.k[it % kStages], &mk, &sm.k_full[it % kStages], h / p.group,
+                          t.lo + first_key(it));
+  };
+  auto load_v = [&](int it) {
+    tc::load_tile<DP, IT>(sm.v[it % kStages], &mv, &sm.v_full[it % kStages], h / p.group,
+                          t.lo + first_key(it));
+  };
   // the copying lane sets the barriers up and starts the first copies at once
   if (warp == 8 && lane == 0) {
-    for (uint64_t *b : {&sm.q_full, &sm.k_full, &sm.k_empty, &sm.v_full, &sm.v_empty, &sm.s_full,
-                        &sm.o_full})
-      mbar_init(b, 1);
+    for (int i = 0; i < kStages; ++i)
+      for (uint64_t *b : {&sm.k_full[i], &sm.k_empty[i], &sm.v_full[i], &sm.v_empty[i]})
+        mbar_init(b, 1);
+    for (uint64_t *b : {&sm.q_full, &sm.s_full, &sm.o_full}) mbar_init(b, 1);
     mbar_init(&sm.p_ready, 8);
     sm.abort = 0;
     fence_mbar_init();
-    tc::load_tile<DP>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
-    tc::load_tile<DP>(sm.k, &mk, &sm.k_full, h / p.group, t.lo + t.first);
-    tc::load_tile<DP>(sm.v, &mv, &sm.v_full, h / p.group, t.lo + t.first);
+    tc::load_tile<DP, kTile>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
+    load_k(0);
+    load_v(0);
   }
-  if (warp == 9) tc::tmem_alloc(&sm.tmem, 256);
+  if (warp == 9) tc::tmem_alloc(&sm.tmem, IT + DP);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0), tS = tmem, tO = tmem + 128;
+  const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0), tS = tmem, tO = tmem + IT;
   volatile int *abort = &sm.abort;
   const uint32_t lead = lane == 0;  // the lane that issues products
 
   if (warp == 8) {
     if (lane == 0) {
       for (int it = 1; it < steps; ++it) {
-        const int row = t.lo + t.first - it * kTile;
-        if (!tc::mbar_wait(&sm.k_empty, (it - 1) & 1, abort)) break;
-        tc::load_tile<DP>(sm.k, &mk, &sm.k_full, h / p.group, row);
-        if (!tc::mbar_wait(&sm.v_empty, (it - 1) & 1, abort)) break;
-        tc::load_tile<DP>(sm.v, &mv, &sm.v_full, h / p.group, row);
+        const int st = it % kStages, use = it / kStages;
+        if (use > 0 && !tc::mbar_wait(&sm.k_empty[st], (use - 1) & 1, abort)) break;
+        load_k(it);
+        if (use > 0 && !tc::mbar_wait(&sm.v_empty[st], (use - 1) & 1, abort)) break;
+        load_v(it);
       }
     }
   } else if (warp == 9) {
-    const uint32_t q = tc::smem_addr(sm.q), k = tc::smem_addr(sm.k), v = tc::smem_addr(sm.v);
     bool ok = tc::warp_wait(&sm.q_full, 0, abort);
     for (int it = 0; it < steps && ok; ++it) {
-      ok = tc::warp_wait(&sm.k_full, it & 1, abort);
+      const int st = it % kStages, use = it / kStages;
+      ok = tc::warp_wait(&sm.k_full[st], use & 1, abort);
       if (!ok) break;
-      tc::product_nt<DP>(lead, tS, q, k);
-      tc::commit(lead, &sm.k_empty);
+      tc::product_nt<DP, IT>(lead, tS, tc::smem_addr(sm.q), tc::smem_addr(sm.k[st]));
+      tc::commit(lead, &sm.k_empty[st]);
       tc::commit(lead, &sm.s_full);
-      ok = tc::warp_wait(&sm.v_full, it & 1, abort);
+      ok = tc::warp_wait(&sm.v_full[st], use & 1, abort);
       if (!ok) break;
       // values past the sequence's end meet weights of zero: they must be finite
-      if (it == 0 && rows < kTile) tc::clear_rows<DP>(sm.v, rows, lane);
+      if (it == 0 && first_key(0) + IT > t.len)
+        tc::clear_rows<DP, IT>(sm.v[st], t.len - first_key(0), lane);
       __syncwarp();
       ok = tc::warp_wait(&sm.p_ready, it & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
-      tc::product_parts<DP, 2>(lead, tO, tS, v, it > 0);
-      tc::commit(lead, &sm.v_empty);
+      tc::product_parts<DP, IT, 2>(lead, tO, tS, tc::smem_addr(sm.v[st]), it > 0);
+      tc::commit(lead, &sm.v_empty[st]);
       if (it + 1 == steps) tc::commit(lead, &sm.o_full);
     }
   } else {
+    constexpr int HC = IT / 2;  // key columns of a thread
     const int r = threadIdx.x & 127, half = warp >> 2;  // this thread's row and half of the keys
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t mine = tS + lanes + half * 64;
+    const uint32_t mine = tS + lanes + half * HC;
     const float2 k2 = make_float2(p.scale2, p.scale2);
-    float m = 0.0f, l = 0.0f;
+    float m = -INFINITY, l = 0.0f;
     // after a wait that ran out the loop goes on without waiting, so that
     // every warp meets its partner's barriers
     for (int it = 0; it < steps; ++it) {
       tc::warp_wait(&sm.s_full, it & 1, abort);
       tc::fence_after_sync();
-      uint32_t s[64];
-      tc::ld32(mine, *reinterpret_cast<uint32_t(*)[32]>(s));
-      tc::ld32(mine + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-      tc::wait_ld();
-      if (it == 0) {  // the diagonal tile
+      uint32_t s[HC];
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (half * 64 + c > r) s[c] = 0xff800000u;
+      for (int c = 0; c < HC; c += 32) tc::ld32(mine + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
+      tc::wait_ld();
+      const int last = t.first + r - first_key(it) - half * HC;  // the last column this row sees
+      if (first_key(it) + IT > t.first + 1) {
+#pragma unroll
+        for (int c = 0; c < HC; ++c)
+          if (c > last) s[c] = 0xff800000u;
       }
       float t4[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) t4[c] = __uint_as_float(s[c]);
 #pragma unroll
-      for (int c = 4; c < 64; ++c) t4[c % 4] = fmaxf(t4[c % 4], __uint_as_float(s[c]));
+      for (int c = 4; c < HC; ++c) t4[c % 4] = fmaxf(t4[c % 4], __uint_as_float(s[c]));
       const float own = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
       sm.row[half][r] = own;
       pair_barrier(warp & 3);
       const float top = fmaxf(own, sm.row[half ^ 1][r]) * p.scale2;
-      if (it == 0) {
-        m = top == -INFINITY ? 0.0f : top;
-      } else {
-        const bool raise = top > m + 8.0f;
-        if (__any_sync(kFull, raise)) {
-          const float f = raise ? ex2(m - top) : 1.0f;
-          if (raise) m = top;
-          l *= f;
-          const uint32_t acc = tO + lanes + half * (DP / 2);
+      const bool raise = top > m + 8.0f;  // from the start (m = -inf) too
+      if (__any_sync(kFull, raise)) {
+        const float f = raise ? ex2(m - top) : 1.0f;
+        if (raise) m = top;
+        l *= f;
+        const uint32_t acc = tO + lanes + half * (DP / 2);
+        if (it > 0)
 #pragma unroll 1
           for (int c = 0; c < DP / 2; c += 16) {
             uint32_t o[16];
@@ -269,12 +292,12 @@ __global__ void __launch_bounds__(320, 2)
             for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
             tc::st16(acc + c, o);
           }
-        }
       }
-      const float2 m2 = make_float2(-m, -m);
+      const float zero = m == -INFINITY ? 0.0f : -m;  // (a row that has seen no key yet)
+      const float2 m2 = make_float2(zero, zero);
       float2 sum[2] = {};
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < HC / 32; ++c) {
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -309,7 +332,7 @@ __global__ void __launch_bounds__(320, 2)
   __syncthreads();
   tc::fence_after_sync();
   settle(sm.abort, p.ws);
-  if (warp == 9) tc::tmem_dealloc(sm.tmem, 256);
+  if (warp == 9) tc::tmem_dealloc(sm.tmem, IT + DP);
 }
 
 // ---------------------------------------------------------------------------
@@ -411,11 +434,22 @@ __device__ __forceinline__ void put_remote4(uint32_t place, uint32_t rank, const
                : "memory");
 }
 
-__device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+// Four score warps to 32 columns of the inner tile, one that copies and one
+// that issues.
+template <int DP>
+constexpr int backward_threads() {
+  return (4 * inner<DP>() / 32 + 2) * 32;
+}
+
+template <int DP>
+__device__ __forceinline__ void compute_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(backward_threads<DP>() - 64) : "memory");
+}
 
 template <int DP>
 struct KvSmem {
-  alignas(1024) unsigned char k[DP * 256], v[DP * 256], q[3][DP * 256], dout[2][DP * 256];
+  alignas(1024) unsigned char k[DP * 256], v[DP * 256], q[3][DP * inner<DP>() * 2],
+      dout[2][DP * inner<DP>() * 2];
   float lse[2][128], delta[2][128];
   uint64_t k_full, v_full, q_full[3], q_empty[3], do_full[2], do_empty[2];
   uint64_t s_full, dp_full, p_ready, ds_ready, done;
@@ -433,7 +467,7 @@ struct KvSmem {
 // shares the group's query heads and adds its sums up through distributed
 // shared memory, in rank order, each block the columns of its own.
 template <int DP>
-__global__ void __launch_bounds__(576, 1)
+__global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
     attention_dkv_kernel(const __grid_constant__ CUtensorMap mq,
                          const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mv,
@@ -448,42 +482,45 @@ __global__ void __launch_bounds__(576, 1)
   Tile t;
   if (!aligned_tiles(raw, p.ws)) return;
   if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.split / p.Hk, lane, t)) return;
-  const int tiles = (t.len + kTile - 1) / kTile;
-  const int jt = tiles - 1 - t.first / kTile;  // the first key tile has the most query tiles
-  const int per_head = tiles - jt, steps = per_head * heads;
-  const int rows = t.len - jt * kTile < kTile ? t.len - jt * kTile : kTile;
-  const int tail = t.len - (tiles - 1) * kTile;  // rows of the sequence's last tile
+  constexpr int IT = inner<DP>(), PARTS = IT / 32, kCopy = 4 * PARTS, kIssue = kCopy + 1;
+  constexpr int kSubs = kTile / IT;  // query tiles that meet the diagonal
+  // the first key tile has the most query tiles: turn the order round
+  const int key0 = ((t.len + kTile - 1) / kTile - 1) * kTile - t.first;
+  const int tiles = (t.len + IT - 1) / IT, per_head = tiles - key0 / IT, steps = per_head * heads;
+  const int rows = t.len - key0 < kTile ? t.len - key0 : kTile;
+  const int tail = t.len - (tiles - 1) * IT;  // rows of the sequence's last query tile
+  auto first_row = [&](int i) { return key0 + i % per_head * IT; };
   auto load_q = [&](int i) {
-    tc::load_tile<DP>(sm.q[i % 3], &mq, &sm.q_full[i % 3], head0 + i / per_head,
-                      t.lo + (jt + i % per_head) * kTile);
+    tc::load_tile<DP, IT>(sm.q[i % 3], &mq, &sm.q_full[i % 3], head0 + i / per_head,
+                          t.lo + first_row(i));
   };
   auto load_dout = [&](int i) {
-    tc::load_tile<DP>(sm.dout[i & 1], &mdo, &sm.do_full[i & 1], head0 + i / per_head,
-                      t.lo + (jt + i % per_head) * kTile);
+    tc::load_tile<DP, IT>(sm.dout[i & 1], &mdo, &sm.do_full[i & 1], head0 + i / per_head,
+                          t.lo + first_row(i));
   };
-  if (warp == 16 && lane == 0) {
+  if (warp == kCopy && lane == 0) {
     for (int i = 0; i < 3; ++i) mbar_init(&sm.q_full[i], 1), mbar_init(&sm.q_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.do_full[i], 1), mbar_init(&sm.do_empty[i], 1);
     for (uint64_t *b : {&sm.k_full, &sm.v_full, &sm.s_full, &sm.dp_full, &sm.done}) mbar_init(b, 1);
-    mbar_init(&sm.p_ready, 16);
-    mbar_init(&sm.ds_ready, 16);
+    mbar_init(&sm.p_ready, 4 * PARTS);
+    mbar_init(&sm.ds_ready, 4 * PARTS);
     sm.abort = 0;
     fence_mbar_init();
-    tc::load_tile<DP>(sm.k, &mk, &sm.k_full, g, t.lo + jt * kTile);
+    tc::load_tile<DP, kTile>(sm.k, &mk, &sm.k_full, g, t.lo + key0);
     load_q(0);
-    tc::load_tile<DP>(sm.v, &mv, &sm.v_full, g, t.lo + jt * kTile);
+    tc::load_tile<DP, kTile>(sm.v, &mv, &sm.v_full, g, t.lo + key0);
     load_dout(0);
   }
-  if (warp == 17) tc::tmem_alloc(&sm.tmem, 512);
+  if (warp == kIssue) tc::tmem_alloc(&sm.tmem, 2 * IT + 2 * DP);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
-  const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
+  const uint32_t tS = tmem, tP = tS + IT, tV = tP + IT, tK = tV + DP;
   volatile int *abort = &sm.abort;
   const uint32_t lead = lane == 0;  // the lane that issues products
 
-  if (warp == 16) {
+  if (warp == kCopy) {
     if (lane == 0) {
       for (int i = 1; i < steps; ++i) {
         if (i >= 3 && !tc::mbar_wait(&sm.q_empty[i % 3], (i / 3 - 1) & 1, abort)) break;
@@ -492,25 +529,25 @@ __global__ void __launch_bounds__(576, 1)
         load_dout(i);
       }
     }
-  } else if (warp == 17) {
+  } else if (warp == kIssue) {
     const uint32_t k = tc::smem_addr(sm.k), v = tc::smem_addr(sm.v);
     // rows past the sequence's end are another sequence's: they meet weights
     // of zero as a second operand, so they must be finite
     auto scores = [&](int i) {
       const int a = i % 3;
       if (!tc::warp_wait(&sm.q_full[a], (i / 3) & 1, abort)) return false;
-      if (i % per_head == per_head - 1 && tail < kTile) tc::clear_rows<DP>(sm.q[a], tail, lane);
+      if (i % per_head == per_head - 1 && tail < IT) tc::clear_rows<DP, IT>(sm.q[a], tail, lane);
       __syncwarp();
-      tc::product_nt<DP>(lead, tS, k, tc::smem_addr(sm.q[a]));
+      tc::product_nt<DP, IT>(lead, tS, k, tc::smem_addr(sm.q[a]));
       tc::commit(lead, &sm.s_full);
       return true;
     };
     auto grads = [&](int i) {
       const int b = i & 1;
       if (!tc::warp_wait(&sm.do_full[b], (i / 2) & 1, abort)) return false;
-      if (i % per_head == per_head - 1 && tail < kTile) tc::clear_rows<DP>(sm.dout[b], tail, lane);
+      if (i % per_head == per_head - 1 && tail < IT) tc::clear_rows<DP, IT>(sm.dout[b], tail, lane);
       __syncwarp();
-      tc::product_nt<DP>(lead, tP, v, tc::smem_addr(sm.dout[b]));
+      tc::product_nt<DP, IT>(lead, tP, v, tc::smem_addr(sm.dout[b]));
       tc::commit(lead, &sm.dp_full);
       return true;
     };
@@ -520,15 +557,15 @@ __global__ void __launch_bounds__(576, 1)
       ok = tc::warp_wait(&sm.p_ready, i & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
-      tc::product_parts<DP, 4>(lead, tV, tS, tc::smem_addr(sm.dout[i & 1]), i > 0);
+      tc::product_parts<DP, IT, PARTS>(lead, tV, tS, tc::smem_addr(sm.dout[i & 1]), i > 0);
       tc::commit(lead, &sm.do_empty[i & 1]);
       if (i + 1 < steps && !(ok = scores(i + 1))) break;
       ok = tc::warp_wait(&sm.ds_ready, i & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
-      tc::product_parts<DP, 4>(lead, tK, tP, tc::smem_addr(sm.q[i % 3]), i > 0);
-      if (i % per_head == 0)
-        tc::product_parts<DP, 4>(lead, tK, tP + 16, tc::smem_addr(sm.q[i % 3]), true);
+      tc::product_parts<DP, IT, PARTS>(lead, tK, tP, tc::smem_addr(sm.q[i % 3]), i > 0);
+      if (i % per_head < kSubs)
+        tc::product_parts<DP, IT, PARTS>(lead, tK, tP + 16, tc::smem_addr(sm.q[i % 3]), true);
       tc::commit(lead, &sm.q_empty[i % 3]);
       if (i + 1 == steps) tc::commit(lead, &sm.done);
       if (i + 1 < steps) ok = grads(i + 1);
@@ -539,8 +576,8 @@ __global__ void __launch_bounds__(576, 1)
     // Column statistics of step i, negated: one value per thread of parts 0
     // and 1, a step ahead.
     auto column = [&](int i) {
-      const int h = head0 + i / per_head, at = (jt + i % per_head) * kTile + r;
-      if (part > 1) return 0.0f;
+      const int h = head0 + i / per_head, at = first_row(i) + r;
+      if (part > 1 || r >= IT) return 0.0f;
       if (at >= t.len) return part ? 0.0f : -INFINITY;  // no row: weights of zero
       const float x = (part ? p.delta : p.lse)[(int64_t)h * p.tokens + t.lo + at];
       return part ? -x : -x * kLog2e;
@@ -550,11 +587,13 @@ __global__ void __launch_bounds__(576, 1)
     // after a wait that ran out the loop goes on without waiting, so that
     // every warp meets the others' barriers
     for (int i = 0; i < steps; ++i) {
-      if (part < 2) (part ? sm.delta : sm.lse)[i & 1][r] = next;
-      compute_barrier();
+      if (part < 2 && r < IT) (part ? sm.delta : sm.lse)[i & 1][r] = next;
+      compute_barrier<DP>();
       if (i + 1 < steps) next = column(i + 1);
       const float *lse = &sm.lse[i & 1][part * 32], *delta = &sm.delta[i & 1][part * 32];
-      const bool diagonal = i % per_head == 0;
+      const bool diagonal = i % per_head < kSubs;
+      // (masked: columns before this key's own row)
+      const int own = key0 + r - first_row(i) - part * 32;
       uint32_t s[32], d[32];
       tc::warp_wait(&sm.s_full, i & 1, abort);
       tc::fence_after_sync();
@@ -573,7 +612,7 @@ __global__ void __launch_bounds__(576, 1)
       if (diagonal)
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-          if (part * 32 + c < r) s[c] = 0u;
+          if (c < own) s[c] = 0u;
       store_bf16(tS + mine, s, false);
       tc::wait_st();
       tc::fence_before_sync();
@@ -598,7 +637,7 @@ __global__ void __launch_bounds__(576, 1)
       if (diagonal)
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-          if (part * 32 + c < r) d[c] = 0u;
+          if (c < own) d[c] = 0u;
       store_bf16(tP + mine, d, diagonal);
       tc::wait_st();
       tc::fence_before_sync();
@@ -606,11 +645,11 @@ __global__ void __launch_bounds__(576, 1)
     }
     if (tc::warp_wait(&sm.done, 0, abort) && p.split == 1) {
       tc::fence_after_sync();
-      const int64_t row = (int64_t)t.lo + jt * kTile + r;
-      const int of = part >> 1, from = (part & 1) * (DP / 2);  // dv or dk, half a row
-      write_row<DP / 2>((of ? tK : tV) + lanes + from,
-                        (of ? p.dk : p.dv) + (row * p.Hk + g) * p.D + from, p.D - from,
-                        of ? p.scale : 1.0f, r < rows);
+      const int64_t row = (int64_t)t.lo + key0 + r;
+      const int of = part * 64 / DP, from = part * 64 % DP;  // dv or dk, 64 columns
+      write_row<64>((of ? tK : tV) + lanes + from,
+                    (of ? p.dk : p.dv) + (row * p.Hk + g) * p.D + from, p.D - from,
+                    of ? p.scale : 1.0f, r < rows);
     }
   }
   if (p.split > 1) {
@@ -621,18 +660,18 @@ __global__ void __launch_bounds__(576, 1)
     const int r = threadIdx.x & 127, part = warp >> 2;
     const int fours = 2 * DP / 4 / p.split;  // of the 2 DP columns (dv, dk), a block's own
     // [source][own columns, by fours][row], 16 bytes each
-    if (part < 4) {
-      const uint32_t acc = (part < 2 ? tV : tK) + ((uint32_t)((warp & 3) * 32) << 16) +
-                           (part & 1) * (DP / 2);
+    if (part < PARTS) {
+      const uint32_t acc = (part * 64 < DP ? tV : tK) + ((uint32_t)((warp & 3) * 32) << 16) +
+                           part * 64 % DP;
       const uint32_t here = tc::smem_addr(raw) + (rank * fours * 128 + r) * 16;
 #pragma unroll
-      for (int c = 0; c < DP / 2; c += 16) {
+      for (int c = 0; c < 64; c += 16) {
         uint32_t x[16];
         tc::ld16(acc + c, x);
         tc::wait_ld();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int four = (part * (DP / 2) + c) / 4 + k;
+          const int four = (part * 64 + c) / 4 + k;
           put_remote4(here + four % fours * 2048, four / fours, x + 4 * k);
         }
       }
@@ -640,10 +679,10 @@ __global__ void __launch_bounds__(576, 1)
     tc::fence_before_sync();
     cluster_barrier();
     tc::fence_after_sync();
-    if (part < 4 && r < rows) {
+    if (part < PARTS && r < rows) {
       const float4 *sums = reinterpret_cast<const float4 *>(raw);
-      const int64_t row = ((int64_t)t.lo + jt * kTile + r) * p.Hk + g;
-      for (int four = part; four < fours; four += 4) {
+      const int64_t row = ((int64_t)t.lo + key0 + r) * p.Hk + g;
+      for (int four = part; four < fours; four += PARTS) {
         float4 x = sums[four * 128 + r];
         for (int k = 1; k < p.split; ++k) {
           const float4 y = sums[(k * fours + four) * 128 + r];
@@ -661,12 +700,13 @@ __global__ void __launch_bounds__(576, 1)
   __syncthreads();
   tc::fence_after_sync();
   settle(sm.abort, p.ws);
-  if (warp == 17) tc::tmem_dealloc(sm.tmem, 512);
+  if (warp == kIssue) tc::tmem_dealloc(sm.tmem, 2 * IT + 2 * DP);
 }
 
 template <int DP>
 struct QSmem {
-  alignas(1024) unsigned char q[DP * 256], dout[DP * 256], k[3][DP * 256], v[2][DP * 256];
+  alignas(1024) unsigned char q[DP * 256], dout[DP * 256], k[3][DP * inner<DP>() * 2],
+      v[2][DP * inner<DP>() * 2];
   uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[2], v_empty[2];
   uint64_t s_full[2], dp_full, ds_ready, done;
   uint32_t tmem;
@@ -679,7 +719,7 @@ struct QSmem {
 // S(j+2): P(j+1) is formed while dP(j+1) runs, dS(j+1) while dQ(j) and S(j+2)
 // do.
 template <int DP>
-__global__ void __launch_bounds__(576, 1)
+__global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
     attention_dq_kernel(const __grid_constant__ CUtensorMap mq,
                         const __grid_constant__ CUtensorMap mk,
                         const __grid_constant__ CUtensorMap mv,
@@ -693,17 +733,18 @@ __global__ void __launch_bounds__(576, 1)
   Tile t;
   if (!aligned_tiles(raw, p.ws)) return;
   if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.Hq, lane, t)) return;
-  const int steps = t.first / kTile + 1;
+  constexpr int IT = inner<DP>(), PARTS = IT / 32, kCopy = 4 * PARTS, kIssue = kCopy + 1;
   const int rows = t.len - t.first < kTile ? t.len - t.first : kTile;
+  const int steps = (t.first + rows + IT - 1) / IT;  // key tiles, the last one first
+  auto first_key = [&](int j) { return (steps - 1 - j) * IT; };
+  auto diagonal = [&](int j) { return first_key(j) + IT > t.first; };
   auto load_k = [&](int j) {
-    tc::load_tile<DP>(sm.k[j % 3], &mk, &sm.k_full[j % 3], h / p.group,
-                      t.lo + t.first - j * kTile);
+    tc::load_tile<DP, IT>(sm.k[j % 3], &mk, &sm.k_full[j % 3], h / p.group, t.lo + first_key(j));
   };
   auto load_v = [&](int j) {
-    tc::load_tile<DP>(sm.v[j & 1], &mv, &sm.v_full[j & 1], h / p.group,
-                      t.lo + t.first - j * kTile);
+    tc::load_tile<DP, IT>(sm.v[j & 1], &mv, &sm.v_full[j & 1], h / p.group, t.lo + first_key(j));
   };
-  if (warp == 16 && lane == 0) {
+  if (warp == kCopy && lane == 0) {
     for (int i = 0; i < 3; ++i) mbar_init(&sm.k_full[i], 1), mbar_init(&sm.k_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.v_full[i], 1);
@@ -711,24 +752,24 @@ __global__ void __launch_bounds__(576, 1)
       mbar_init(&sm.s_full[i], 1);
     }
     for (uint64_t *b : {&sm.q_full, &sm.do_full, &sm.dp_full, &sm.done}) mbar_init(b, 1);
-    mbar_init(&sm.ds_ready, 16);
+    mbar_init(&sm.ds_ready, 4 * PARTS);
     sm.abort = 0;
     fence_mbar_init();
-    tc::load_tile<DP>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
+    tc::load_tile<DP, kTile>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
     load_k(0);
-    tc::load_tile<DP>(sm.dout, &mdo, &sm.do_full, h, t.lo + t.first);
+    tc::load_tile<DP, kTile>(sm.dout, &mdo, &sm.do_full, h, t.lo + t.first);
     load_v(0);
   }
-  if (warp == 17) tc::tmem_alloc(&sm.tmem, 512);
+  if (warp == kIssue) tc::tmem_alloc(&sm.tmem, 3 * IT + DP);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
-  const uint32_t tS0 = tmem, tP = tmem + 128, tQ = tmem + 256, tS1 = tmem + 384;
+  const uint32_t tS0 = tmem, tP = tS0 + IT, tQ = tP + IT, tS1 = tQ + DP;
   volatile int *abort = &sm.abort;
   const uint32_t lead = lane == 0;  // the lane that issues products
 
-  if (warp == 16) {
+  if (warp == kCopy) {
     if (lane == 0) {
       for (int j = 1; j < steps; ++j) {
         if (j >= 3 && !tc::mbar_wait(&sm.k_empty[j % 3], (j / 3 - 1) & 1, abort)) break;
@@ -737,22 +778,23 @@ __global__ void __launch_bounds__(576, 1)
         load_v(j);
       }
     }
-  } else if (warp == 17) {
+  } else if (warp == kIssue) {
     const uint32_t q = tc::smem_addr(sm.q), dout = tc::smem_addr(sm.dout);
     auto scores = [&](int j) {
       const int a = j % 3;
       if (!tc::warp_wait(&sm.k_full[a], (j / 3) & 1, abort)) return false;
       // keys past the sequence's end meet a dS of zero: they must be finite
-      if (j == 0 && rows < kTile) tc::clear_rows<DP>(sm.k[a], rows, lane);
+      if (j == 0 && first_key(0) + IT > t.len)
+        tc::clear_rows<DP, IT>(sm.k[a], t.len - first_key(0), lane);
       __syncwarp();
-      tc::product_nt<DP>(lead, j & 1 ? tS1 : tS0, q, tc::smem_addr(sm.k[a]));
+      tc::product_nt<DP, IT>(lead, j & 1 ? tS1 : tS0, q, tc::smem_addr(sm.k[a]));
       tc::commit(lead, &sm.s_full[j & 1]);
       return true;
     };
     auto grads = [&](int j) {
       const int b = j & 1;
       if (!tc::warp_wait(&sm.v_full[b], (j / 2) & 1, abort)) return false;
-      tc::product_nt<DP>(lead, tP, dout, tc::smem_addr(sm.v[b]));
+      tc::product_nt<DP, IT>(lead, tP, dout, tc::smem_addr(sm.v[b]));
       tc::commit(lead, &sm.dp_full);
       tc::commit(lead, &sm.v_empty[b]);
       return true;
@@ -764,8 +806,9 @@ __global__ void __launch_bounds__(576, 1)
       if (!ok) break;
       tc::fence_after_sync();
       if (j + 1 < steps && !(ok = grads(j + 1))) break;
-      tc::product_parts<DP, 4>(lead, tQ, j & 1 ? tS1 : tS0, tc::smem_addr(sm.k[j % 3]), j > 0);
-      if (j == 0) tc::product_parts<DP, 4>(lead, tQ, tS0 + 16, tc::smem_addr(sm.k[0]), true);
+      const uint32_t ds = j & 1 ? tS1 : tS0, k = tc::smem_addr(sm.k[j % 3]);
+      tc::product_parts<DP, IT, PARTS>(lead, tQ, ds, k, j > 0);
+      if (diagonal(j)) tc::product_parts<DP, IT, PARTS>(lead, tQ, ds + 16, k, true);
       tc::commit(lead, &sm.k_empty[j % 3]);
       if (j + 1 == steps) tc::commit(lead, &sm.done);
       if (j + 2 < steps) ok = scores(j + 2);
@@ -807,28 +850,29 @@ __global__ void __launch_bounds__(576, 1)
         d[c] = __float_as_uint(a.x);
         d[c + 1] = __float_as_uint(a.y);
       }
-      if (j == 0)
+      const int last = t.first + r - first_key(j) - part * 32;  // the last column this row sees
+      if (diagonal(j))
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-          if (part * 32 + c > r) d[c] = 0u;
-      store_bf16(at, d, j == 0);
+          if (c > last) d[c] = 0u;
+      store_bf16(at, d, diagonal(j));
       tc::wait_st();
       tc::fence_before_sync();
       tc::warp_arrive(&sm.ds_ready, lead);
     }
     if (ok) ok = tc::warp_wait(&sm.done, 0, abort);
-    if (ok && part < 2) {
+    if (ok) {
       tc::fence_after_sync();
-      const int from = part * (DP / 2);
-      write_row<DP / 2>(tQ + lanes + from, p.dq + (row * p.Hq + h) * p.D + from, p.D - from,
-                        p.scale, r < rows);
+      const int from = part * 32;  // (DP is 32 PARTS)
+      write_row<32>(tQ + lanes + from, p.dq + (row * p.Hq + h) * p.D + from, p.D - from, p.scale,
+                    r < rows);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   settle(sm.abort, p.ws);
-  if (warp == 17) tc::tmem_dealloc(sm.tmem, 512);
+  if (warp == kIssue) tc::tmem_dealloc(sm.tmem, 3 * IT + DP);
 }
 
 // ---------------------------------------------------------------------------
@@ -1153,10 +1197,7 @@ bool attn_sizes(int64_t sequences, int64_t tokens, int64_t Hq, int64_t Hk, int64
 template <int DP>
 cudaError_t launch_forward(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                            const ForwardArgs &a, int64_t grid, cudaStream_t st) {
-  // at least 76 KB, so that no third block of 64-wide heads waits on an SM
-  // for tensor memory that two blocks hold
-  constexpr size_t need = sizeof(ForwardSmem<DP>), least = 76 * 1024;
-  constexpr size_t smem = need < least ? least : need;
+  constexpr size_t smem = sizeof(ForwardSmem<DP>);
   const cudaError_t e = allow_dynamic_smem<attention_kernel<DP>>(smem);
   if (e != cudaSuccess) return e;
   return launch_ex(attention_kernel<DP>, dim3((unsigned)grid), dim3(320), smem, st, true, mq, mk, mv,
@@ -1171,26 +1212,26 @@ int group_split(int64_t blocks, int group) {
   return split;
 }
 
+struct BackwardMaps {
+  CUtensorMap q, k, v, dout;
+};
+
 template <int DP>
-cudaError_t launch_backward(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
-                            const CUtensorMap &mdo, const BackwardArgs &a, int64_t tiles,
-                            cudaStream_t st) {
-  // more than half an SM's shared memory, so that one block has the SM (and
-  // its tensor memory) to itself
+cudaError_t launch_backward(const BackwardMaps &stay, const BackwardMaps &walk,
+                            const BackwardArgs &a, int64_t tiles, cudaStream_t st) {
   constexpr int kRows = 4 * 256 / (DP / 8);  // of delta, to a block
   cudaError_t e = launch_ex(attention_delta_kernel<DP>,
                             dim3((unsigned)ceil_div(a.tokens * a.Hq, kRows)), dim3(256), 0, st, true,
                             a.dout, a.out, a.delta, a.tokens, a.Hq, a.D);
   if (e != cudaSuccess) return e;
-  constexpr size_t least = 120 * 1024, kv = sizeof(KvSmem<DP>), q = sizeof(QSmem<DP>);
-  static_assert(kv <= 232448 && q <= 232448, "a block has 227 KB of shared memory at most");
-  constexpr size_t kv_smem = kv < least ? least : kv, q_smem = q < least ? least : q;
+  constexpr size_t kv_smem = sizeof(KvSmem<DP>), q_smem = sizeof(QSmem<DP>);
+  static_assert(kv_smem <= 232448 && q_smem <= 232448, "a block has 227 KB of shared memory");
   e = allow_dynamic_smem<attention_dkv_kernel<DP>>(kv_smem);
   if (e == cudaSuccess) e = allow_dynamic_smem<attention_dq_kernel<DP>>(q_smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * a.Hk * a.split));
-  cfg.blockDim = dim3(576);
+  cfg.blockDim = dim3(backward_threads<DP>());
   cfg.dynamicSmemBytes = kv_smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -1201,10 +1242,10 @@ cudaError_t launch_backward(const CUtensorMap &mq, const CUtensorMap &mk, const 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.split > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, attention_dkv_kernel<DP>, mq, mk, mv, mdo, a);
+  e = cudaLaunchKernelEx(&cfg, attention_dkv_kernel<DP>, walk.q, stay.k, stay.v, walk.dout, a);
   if (e == cudaSuccess)
-    e = launch_ex(attention_dq_kernel<DP>, dim3((unsigned)(tiles * a.Hq)), dim3(576), q_smem, st,
-                  true, mq, mk, mv, mdo, a);
+    e = launch_ex(attention_dq_kernel<DP>, dim3((unsigned)(tiles * a.Hq)), dim3(backward_threads<DP>()), q_smem, st,
+                  true, stay.q, walk.k, walk.v, stay.dout, a);
   return e;
 }
 
@@ -1248,9 +1289,10 @@ rlcs_status rlcs_attention(const void *q, int64_t q_token_stride, int64_t q_head
   if (!scratch || scratch_bytes < rlcs_attention_scratch_bytes(tokens, Hq) || !aligned(scratch, 16))
     return RLCS_ERR_WORKSPACE;
   CUtensorMap mq, mk, mv;
-  if (!tc::make_map(&mq, q, tokens, Hq, D, q_token_stride, q_head_stride) ||
-      !tc::make_map(&mk, k, tokens, Hk, D, k_token_stride, k_head_stride) ||
-      !tc::make_map(&mv, v, tokens, Hk, D, v_token_stride, v_head_stride))
+  const int it = D <= 64 ? inner<64>() : inner<128>();
+  if (!tc::make_map(&mq, q, tokens, Hq, D, q_token_stride, q_head_stride, kTile) ||
+      !tc::make_map(&mk, k, tokens, Hk, D, k_token_stride, k_head_stride, it) ||
+      !tc::make_map(&mv, v, tokens, Hk, D, v_token_stride, v_head_stride, it))
     return RLCS_ERR_CUDA;
   const ForwardArgs a = {cu_seqlens,
                          static_cast<bf *>(out),
@@ -1299,12 +1341,17 @@ rlcs_status rlcs_attention_backward(
   if (outputs_overlap(outs, ins)) return RLCS_ERR_INVALID_ARG;
   if (!scratch || scratch_bytes < rlcs_attention_scratch_bytes(tokens, Hq) || !aligned(scratch, 16))
     return RLCS_ERR_WORKSPACE;
-  CUtensorMap mq, mk, mv, mdo;
-  if (!tc::make_map(&mq, q, tokens, Hq, D, q_token_stride, q_head_stride) ||
-      !tc::make_map(&mk, k, tokens, Hk, D, k_token_stride, k_head_stride) ||
-      !tc::make_map(&mv, v, tokens, Hk, D, v_token_stride, v_head_stride) ||
-      !tc::make_map(&mdo, dout, tokens, Hq, D, Hq * D, D))
-    return RLCS_ERR_CUDA;
+  // tiles that stay (128 rows) and tiles a block walks over, of each array
+  BackwardMaps stay, walk;
+  for (int w = 0; w < 2; ++w) {
+    BackwardMaps &m = w ? walk : stay;
+    const int rows = w && D <= 64 ? inner<64>() : kTile;
+    if (!tc::make_map(&m.q, q, tokens, Hq, D, q_token_stride, q_head_stride, rows) ||
+        !tc::make_map(&m.k, k, tokens, Hk, D, k_token_stride, k_head_stride, rows) ||
+        !tc::make_map(&m.v, v, tokens, Hk, D, v_token_stride, v_head_stride, rows) ||
+        !tc::make_map(&m.dout, dout, tokens, Hq, D, Hq * D, D, rows))
+      return RLCS_ERR_CUDA;
+  }
   float *delta = reinterpret_cast<float *>(static_cast<char *>(scratch) + 64);
   const BackwardArgs a = {cu_seqlens,
                           static_cast<const bf *>(dout),
@@ -1326,8 +1373,8 @@ rlcs_status rlcs_attention_backward(
                           (float)(scale * 1.4426950408889634)};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t tiles = tile_bound(sequences, tokens);
-  return launched(D <= 64 ? launch_backward<64>(mq, mk, mv, mdo, a, tiles, st)
-                          : launch_backward<128>(mq, mk, mv, mdo, a, tiles, st));
+  return launched(D <= 64 ? launch_backward<64>(stay, walk, a, tiles, st)
+                          : launch_backward<128>(stay, walk, a, tiles, st));
 }
 
 size_t rlcs_attention_step_scratch_bytes(int64_t B, int64_t S, int64_t Hq, int64_t Hk, int64_t D) {

@@ -131,8 +131,9 @@ constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t operand_k(uint32_t addr) {
   return ((addr & 0x3ffff) >> 4) | (1u << 16);
 }
+template <int ROWS>
 __device__ __forceinline__ uint32_t operand_n(uint32_t addr) {
-  return ((addr & 0x3ffff) >> 4) | ((16384u >> 4) << 16);
+  return ((addr & 0x3ffff) >> 4) | ((ROWS * 128u >> 4) << 16);
 }
 // Products are issued by one lane, but every lane of its warp runs the code
 // and `lead` predicates the instruction alone: in a branch taken by one lane
@@ -168,28 +169,27 @@ __device__ __forceinline__ void commit(uint32_t lead, uint64_t *bar) {
       : "memory");
 }
 
-// C[128 x 128] = A[128 x DP] B[128 x DP]^T, both K-contiguous in shared memory.
-template <int DP>
+// C[128 x N] = A[128 x DP] B[N x DP]^T, both K-contiguous in shared memory.
+template <int DP, int N>
 __device__ __forceinline__ void product_nt(uint32_t lead, uint32_t d, uint32_t a, uint32_t b) {
   const uint32_t x = operand_k(a), y = operand_k(b);
 #pragma unroll
-  for (int k = 0; k < DP / 16; ++k) {
-    const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
-    mma_ss(lead, d, x + off, y + off, instr(128, false), k > 0);
-  }
+  for (int k = 0; k < DP / 16; ++k)
+    mma_ss(lead, d, x + (((k / 4) * 16384 + (k % 4) * 32) >> 4),
+           y + (((k / 4) * N * 128 + (k % 4) * 32) >> 4), instr(N, false), k > 0);
 }
-// C[128 x DP] (+)= A B, B's rows contiguous in shared memory and A in tensor
-// memory as bf16 pairs (8 columns per 16 of A): its 128 columns in PARTS
-// pieces, each written by its own warps over the start of the 128 / PARTS
-// fp32 columns they had read.
-template <int DP, int PARTS>
+// C[128 x DP] (+)= A[128 x K] B[K x DP], B's rows contiguous in shared memory
+// and A in tensor memory as bf16 pairs (8 columns per 16 of A): its K columns
+// in PARTS pieces, each written by its own warps over the start of the K /
+// PARTS fp32 columns they had read.
+template <int DP, int K, int PARTS>
 __device__ __forceinline__ void product_parts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b,
                                               bool add) {
-  constexpr int kSteps = 8 / PARTS;  // of 16 columns
-  const uint32_t y = operand_n(b);
+  constexpr int kSteps = K / 16 / PARTS;
+  const uint32_t y = operand_n<K>(b);
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    mma_ts(lead, d, a + (k / kSteps) * (128 / PARTS) + (k % kSteps) * 8, y + k * (2048 >> 4),
+  for (int k = 0; k < K / 16; ++k)
+    mma_ts(lead, d, a + (k / kSteps) * (K / PARTS) + (k % kSteps) * 8, y + k * (2048 >> 4),
            instr(DP, true), add || k > 0);
 }
 
@@ -204,29 +204,29 @@ __device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, uint
       "l"(map), "r"(smem_addr(bar)), "r"(col), "r"(head), "r"(token)
       : "memory");
 }
-// A 128-token by DP-column tile: DP/64 boxes; columns past the array's width
-// and tokens past its end read as zero.
-template <int DP>
+// A tile of ROWS tokens by DP columns: DP/64 boxes; columns past the array's
+// width and tokens past its end read as zero.
+template <int DP, int ROWS>
 __device__ __forceinline__ void load_tile(unsigned char *dst, const CUtensorMap *map, uint64_t *bar,
                                           int head, int token) {
-  mbar_arrive_expect_tx(bar, DP * 256);
+  mbar_arrive_expect_tx(bar, DP * ROWS * 2);
 #pragma unroll
-  for (int c = 0; c < DP / 64; ++c) load_box(dst + c * 16384, map, bar, c * 64, head, token);
+  for (int c = 0; c < DP / 64; ++c) load_box(dst + c * ROWS * 128, map, bar, c * 64, head, token);
 }
-// Zero rows [from, 128) of a tile that a copy has filled, by one warp.
-template <int DP>
+// Zero rows [from, ROWS) of a tile that a copy has filled, by one warp.
+template <int DP, int ROWS>
 __device__ __forceinline__ void clear_rows(unsigned char *tile, int from, int lane) {
 #pragma unroll
   for (int c = 0; c < DP / 64; ++c)
-    for (int i = from * 8 + lane; i < 1024; i += 32)
-      reinterpret_cast<uint4 *>(tile + c * 16384)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = from * 8 + lane; i < ROWS * 8; i += 32)
+      reinterpret_cast<uint4 *>(tile + c * ROWS * 128)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_shared();
 }
 
-// Host: the map of a [tokens, heads, D] bf16 view, in 64-column boxes of 128
-// tokens of one head.
+// Host: the map of a [tokens, heads, D] bf16 view, in 64-column boxes of
+// `rows` tokens of one head.
 inline bool make_map(CUtensorMap *map, const void *base, int64_t tokens, int64_t heads, int64_t D,
-                     int64_t token_stride, int64_t head_stride) {
+                     int64_t token_stride, int64_t head_stride, int rows) {
   using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                               const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
                               const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -243,7 +243,7 @@ inline bool make_map(CUtensorMap *map, const void *base, int64_t tokens, int64_t
   if (!encode) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)token_stride * 2};
-  const cuuint32_t box[3] = {64, 1, 128}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, one[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
                 box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
