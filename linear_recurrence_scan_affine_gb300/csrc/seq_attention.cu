@@ -489,14 +489,20 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
   const int tiles = (t.len + IT - 1) / IT, per_head = tiles - key0 / IT, steps = per_head * heads;
   const int rows = t.len - key0 < kTile ? t.len - key0 : kTile;
   const int tail = t.len - (tiles - 1) * IT;  // rows of the sequence's last query tile
-  auto first_row = [&](int i) { return key0 + i % per_head * IT; };
-  auto load_q = [&](int i) {
-    tc::load_tile<DP, IT>(sm.q[i % 3], &mq, &sm.q_full[i % 3], head0 + i / per_head,
-                          t.lo + first_row(i));
+  // Step i is query tile `sub` of head `head`, counted up by each role.
+  struct Step {
+    int head, sub;
   };
-  auto load_dout = [&](int i) {
-    tc::load_tile<DP, IT>(sm.dout[i & 1], &mdo, &sm.do_full[i & 1], head0 + i / per_head,
-                          t.lo + first_row(i));
+  auto after = [&](Step x) {
+    return x.sub + 1 < per_head ? Step{x.head, x.sub + 1} : Step{x.head + 1, 0};
+  };
+  const Step begin = {head0, 0};
+  auto first_row = [&](Step x) { return key0 + x.sub * IT; };
+  auto load_q = [&](int i, Step x) {
+    tc::load_tile<DP, IT>(sm.q[i % 3], &mq, &sm.q_full[i % 3], x.head, t.lo + first_row(x));
+  };
+  auto load_dout = [&](int i, Step x) {
+    tc::load_tile<DP, IT>(sm.dout[i & 1], &mdo, &sm.do_full[i & 1], x.head, t.lo + first_row(x));
   };
   if (warp == kCopy && lane == 0) {
     for (int i = 0; i < 3; ++i) mbar_init(&sm.q_full[i], 1), mbar_init(&sm.q_empty[i], 1);
@@ -507,9 +513,9 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
     sm.abort = 0;
     fence_mbar_init();
     tc::load_tile<DP, kTile>(sm.k, &mk, &sm.k_full, g, t.lo + key0);
-    load_q(0);
+    load_q(0, begin);
     tc::load_tile<DP, kTile>(sm.v, &mv, &sm.v_full, g, t.lo + key0);
-    load_dout(0);
+    load_dout(0, begin);
   }
   if (warp == kIssue) tc::tmem_alloc(&sm.tmem, 2 * IT + 2 * DP);
   tc::fence_before_sync();
@@ -522,78 +528,85 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
 
   if (warp == kCopy) {
     if (lane == 0) {
+      Step x = begin;
       for (int i = 1; i < steps; ++i) {
+        x = after(x);
         if (i >= 3 && !tc::mbar_wait(&sm.q_empty[i % 3], (i / 3 - 1) & 1, abort)) break;
-        load_q(i);
+        load_q(i, x);
         if (i >= 2 && !tc::mbar_wait(&sm.do_empty[i & 1], (i / 2 - 1) & 1, abort)) break;
-        load_dout(i);
+        load_dout(i, x);
       }
     }
   } else if (warp == kIssue) {
     const uint32_t k = tc::smem_addr(sm.k), v = tc::smem_addr(sm.v);
     // rows past the sequence's end are another sequence's: they meet weights
     // of zero as a second operand, so they must be finite
-    auto scores = [&](int i) {
+    auto scores = [&](int i, Step x) {
       const int a = i % 3;
       if (!tc::warp_wait(&sm.q_full[a], (i / 3) & 1, abort)) return false;
-      if (i % per_head == per_head - 1 && tail < IT) tc::clear_rows<DP, IT>(sm.q[a], tail, lane);
+      if (x.sub == per_head - 1 && tail < IT) tc::clear_rows<DP, IT>(sm.q[a], tail, lane);
       __syncwarp();
       tc::product_nt<DP, IT>(lead, tS, k, tc::smem_addr(sm.q[a]));
       tc::commit(lead, &sm.s_full);
       return true;
     };
-    auto grads = [&](int i) {
+    auto grads = [&](int i, Step x) {
       const int b = i & 1;
       if (!tc::warp_wait(&sm.do_full[b], (i / 2) & 1, abort)) return false;
-      if (i % per_head == per_head - 1 && tail < IT) tc::clear_rows<DP, IT>(sm.dout[b], tail, lane);
+      if (x.sub == per_head - 1 && tail < IT) tc::clear_rows<DP, IT>(sm.dout[b], tail, lane);
       __syncwarp();
       tc::product_nt<DP, IT>(lead, tP, v, tc::smem_addr(sm.dout[b]));
       tc::commit(lead, &sm.dp_full);
       return true;
     };
-    bool ok = tc::warp_wait(&sm.k_full, 0, abort) && scores(0) &&
-              tc::warp_wait(&sm.v_full, 0, abort) && grads(0);
+    Step x = begin;
+    bool ok = tc::warp_wait(&sm.k_full, 0, abort) && scores(0, x) &&
+              tc::warp_wait(&sm.v_full, 0, abort) && grads(0, x);
     for (int i = 0; i < steps && ok; ++i) {
+      const bool diagonal = x.sub < kSubs;
+      x = after(x);
       ok = tc::warp_wait(&sm.p_ready, i & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
       tc::product_parts<DP, IT, PARTS>(lead, tV, tS, tc::smem_addr(sm.dout[i & 1]), i > 0);
       tc::commit(lead, &sm.do_empty[i & 1]);
-      if (i + 1 < steps && !(ok = scores(i + 1))) break;
+      if (i + 1 < steps && !(ok = scores(i + 1, x))) break;
       ok = tc::warp_wait(&sm.ds_ready, i & 1, abort);
       if (!ok) break;
       tc::fence_after_sync();
       tc::product_parts<DP, IT, PARTS>(lead, tK, tP, tc::smem_addr(sm.q[i % 3]), i > 0);
-      if (i % per_head < kSubs)
+      if (diagonal)
         tc::product_parts<DP, IT, PARTS>(lead, tK, tP + 16, tc::smem_addr(sm.q[i % 3]), true);
       tc::commit(lead, &sm.q_empty[i % 3]);
       if (i + 1 == steps) tc::commit(lead, &sm.done);
-      if (i + 1 < steps) ok = grads(i + 1);
+      if (i + 1 < steps) ok = grads(i + 1, x);
     }
   } else {
     const int r = threadIdx.x & 127, part = warp >> 2;  // this thread's key row, its columns
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, mine = lanes + part * 32;
     // Column statistics of step i, negated: one value per thread of parts 0
     // and 1, a step ahead.
-    auto column = [&](int i) {
-      const int h = head0 + i / per_head, at = first_row(i) + r;
+    auto column = [&](Step y) {
+      const int at = first_row(y) + r;
       if (part > 1 || r >= IT) return 0.0f;
       if (at >= t.len) return part ? 0.0f : -INFINITY;  // no row: weights of zero
-      const float x = (part ? p.delta : p.lse)[(int64_t)h * p.tokens + t.lo + at];
+      const float x = (part ? p.delta : p.lse)[(int64_t)y.head * p.tokens + t.lo + at];
       return part ? -x : -x * kLog2e;
     };
-    float next = column(0);
+    Step x = begin;
+    float next = column(x);
     const float2 k2 = make_float2(p.scale2, p.scale2);
     // after a wait that ran out the loop goes on without waiting, so that
     // every warp meets the others' barriers
     for (int i = 0; i < steps; ++i) {
       if (part < 2 && r < IT) (part ? sm.delta : sm.lse)[i & 1][r] = next;
       compute_barrier<DP>();
-      if (i + 1 < steps) next = column(i + 1);
+      const int row0 = first_row(x);
+      const bool diagonal = x.sub < kSubs;
+      x = after(x);
+      if (i + 1 < steps) next = column(x);
       const float *lse = &sm.lse[i & 1][part * 32], *delta = &sm.delta[i & 1][part * 32];
-      const bool diagonal = i % per_head < kSubs;
-      // (masked: columns before this key's own row)
-      const int own = key0 + r - first_row(i) - part * 32;
+      const int own = key0 + r - row0 - part * 32;  // columns before this key's own row: masked
       uint32_t s[32], d[32];
       tc::warp_wait(&sm.s_full, i & 1, abort);
       tc::fence_after_sync();
