@@ -148,14 +148,17 @@ rlcs_status rlcs_qk_norm_rope_backward(
  * arrays; token i attends to tokens j <= i of its own sequence:
  *   P_ij = softmax_j(scale * q_i . k_j),  o_i = sum_j P_ij v_j
  *   lse_i = log sum_j exp(scale * q_i . k_j)            (natural logarithm)
- * for scale > 0. Query head h reads key/value head h / (Hq/Hk); Hq is a
- * multiple of Hk. q
- * [tokens, Hq, D], k and v [tokens, Hk, D], with token and head strides that
- * are multiples of 8 and 16-byte aligned bases (RLCS_ERR_MISALIGNED
- * otherwise). D is a multiple of 8 up to 128. cu_seqlens [sequences + 1]
- * int32 in device memory, nondecreasing from 0; bounds outside [0, tokens]
- * are clamped, and tokens that no sequence holds are not written. out
- * [tokens, Hq, D] contiguous; lse [Hq, tokens] float32 may be NULL.
+ * for 1e-30 <= scale <= 1e30. Query head h reads key/value head h / (Hq/Hk);
+ * Hq is a multiple of Hk.
+ * q [tokens, Hq, D], k and v [tokens, Hk, D], with positive token and head
+ * strides that are multiples of 8 and 16-byte aligned bases
+ * (RLCS_ERR_MISALIGNED otherwise). D is a multiple of 8 up to 128.
+ * cu_seqlens [sequences + 1] int32 in device memory, nondecreasing from 0;
+ * bounds outside [0, tokens] are clamped, and tokens that no sequence holds
+ * are not written. out [tokens, Hq, D] contiguous; lse [Hq, tokens] float32
+ * may be NULL.
+ * Keys and values that a row does not see never change it, infinities and
+ * NaN included.
  * `scratch`: rlcs_attention_scratch_bytes(...) bytes, 16-byte aligned; its
  * first 64 bytes are zeroed once before the first use (rlcs_workspace_init)
  * and hold the device-side status that rlcs_check_status reads. */
@@ -174,7 +177,9 @@ rlcs_status rlcs_attention(const void *q, int64_t q_token_stride, int64_t q_head
  *   dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i,
  * dk and dv summed over the query heads that share the head. dq [tokens, Hq,
  * D], dk, dv [tokens, Hk, D] contiguous. The same scratch as the forward
- * call's size. */
+ * call's size. An element that is not finite makes gradients of its own
+ * sequence so, and in its own tile of 128 tokens those of every token; other
+ * sequences stay as they are. */
 rlcs_status rlcs_attention_backward(
     const void *dout, const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
     int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,

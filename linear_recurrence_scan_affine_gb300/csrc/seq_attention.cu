@@ -155,10 +155,13 @@ struct ForwardSmem {
   uint64_t s_full, p_ready, o_full;
   uint32_t tmem;
   int abort;
+  int special;  // an infinity or NaN among the diagonal's values
 };
 
 struct ForwardArgs {
   const int32_t *cu;
+  const bf *v;
+  int64_t v_token, v_head;  // strides
   bf *o;
   float *lse;
   WsHeader *ws;
@@ -166,6 +169,28 @@ struct ForwardArgs {
   int Hq, group, D;
   float scale2;  // scale * log2 e
 };
+
+// Values that are not finite, on the diagonal: a weight of zero does not take
+// them out of a product, so the product sees zeros in their place, and the
+// rows whose mask lets them through get them here. One row of the tile, half
+// of its columns; rare, and not made fast.
+template <int DP>
+__device__ __noinline__ void add_special(const ForwardArgs &p, const Tile &t, int h, int r,
+                                         int half) {
+  const int64_t first = (int64_t)t.lo + t.first;
+  const bf *v = p.v + first * p.v_token + h / p.group * p.v_head;
+  bf *o = p.o + ((first + r) * p.Hq + h) * p.D;
+  for (int d = half * (DP / 2); d < (half + 1) * (DP / 2) && d < p.D; d += 8)
+    for (int j = 0; j <= r; ++j) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4 *>(v + j * p.v_token + d));
+      if (!tc::special(x)) continue;
+      const bf *e = reinterpret_cast<const bf *>(&x);
+      for (int i = 0; i < 8; ++i) {
+        const float f = __bfloat162float(e[i]);
+        if (!(fabsf(f) < INFINITY)) o[d + i] = __float2bfloat16_rn(__bfloat162float(o[d + i]) + f);
+      }
+    }
+}
 
 template <int DP>
 __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
@@ -184,6 +209,7 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
   const int rows = t.len - t.first < kTile ? t.len - t.first : kTile;
   const int steps = (t.first + rows + IT - 1) / IT;  // key tiles, the last one first
   auto first_key = [&](int it) { return (steps - 1 - it) * IT; };
+  auto diagonal = [&](int it) { return first_key(it) >= t.first; };  // at most kStages tiles
   auto load_k = [&](int it) {
     tc::load_tile<DP, IT>(sm.k[it % kStages], &mk, &sm.k_full[it % kStages], h / p.group,
                           t.lo + first_key(it));
@@ -199,7 +225,7 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
         mbar_init(b, 1);
     for (uint64_t *b : {&sm.q_full, &sm.s_full, &sm.o_full}) mbar_init(b, 1);
     mbar_init(&sm.p_ready, 8);
-    sm.abort = 0;
+    sm.abort = sm.special = 0;
     fence_mbar_init();
     tc::load_tile<DP, kTile>(sm.q, &mq, &sm.q_full, h, t.lo + t.first);
     load_k(0);
@@ -210,7 +236,7 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0), tS = tmem, tO = tmem + IT;
-  volatile int *abort = &sm.abort;
+  volatile int *abort = &sm.abort, *special = &sm.special;
   const uint32_t lead = lane == 0;  // the lane that issues products
 
   if (warp == 8) {
@@ -240,6 +266,7 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
       __syncwarp();
       ok = tc::warp_wait(&sm.p_ready, it & 1, abort);
       if (!ok) break;
+      if (diagonal(it) && *special) tc::clear_special<DP, IT>(sm.v[st], lane);
       tc::fence_after_sync();
       tc::product_parts<DP, IT, 2>(lead, tO, tS, tc::smem_addr(sm.v[st]), it > 0);
       tc::commit(lead, &sm.v_empty[st]);
@@ -255,6 +282,14 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
     // after a wait that ran out the loop goes on without waiting, so that
     // every warp meets its partner's barriers
     for (int it = 0; it < steps; ++it) {
+      if (diagonal(it)) {  // look its values over while its scores are formed
+        uint32_t found = 0;
+        tc::warp_wait(&sm.v_full[it], 0, abort);
+#pragma unroll
+        for (int i = 0; i < DP * IT / 8; i += 256)
+          found |= tc::special(reinterpret_cast<const uint4 *>(sm.v[it])[i + threadIdx.x]);
+        if (found) *special = 1;
+      }
       tc::warp_wait(&sm.s_full, it & 1, abort);
       tc::fence_after_sync();
       uint32_t s[HC];
@@ -262,7 +297,7 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
       for (int c = 0; c < HC; c += 32) tc::ld32(mine + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
       tc::wait_ld();
       const int last = t.first + r - first_key(it) - half * HC;  // the last column this row sees
-      if (first_key(it) + IT > t.first + 1) {
+      if (diagonal(it)) {
 #pragma unroll
         for (int c = 0; c < HC; ++c)
           if (c > last) s[c] = 0xff800000u;
@@ -332,6 +367,8 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
   __syncthreads();
   tc::fence_after_sync();
   settle(sm.abort, p.ws);
+  if (*special && warp < 8 && (threadIdx.x & 127) < rows && !*abort)
+    add_special<DP>(p, t, h, threadIdx.x & 127, warp >> 2);
   if (warp == 9) tc::tmem_dealloc(sm.tmem, IT + DP);
 }
 
@@ -1203,7 +1240,8 @@ bool attn_sizes(int64_t sequences, int64_t tokens, int64_t Hq, int64_t Hk, int64
                 rlcs_dtype t) {
   return sequences >= 0 && tokens >= 0 && tokens <= INT32_MAX && sequences < INT32_MAX && Hq > 0 &&
          Hk > 0 && Hq % Hk == 0 && D > 0 && D <= 128 && D % 8 == 0 && t == RLCS_BF16 &&
-         scale > 0.0 && scale <= 3.0e38 && product_fits(tokens, Hq, D) && tile_bound(sequences, tokens) * Hq < (int64_t)INT32_MAX &&
+         scale >= 1e-30 && scale <= 1e30 && product_fits(tokens, Hq, D) &&
+         tile_bound(sequences, tokens) * Hq < (int64_t)INT32_MAX &&
          tokens * Hq < (int64_t)4 * INT32_MAX;
 }
 
@@ -1308,6 +1346,9 @@ rlcs_status rlcs_attention(const void *q, int64_t q_token_stride, int64_t q_head
       !tc::make_map(&mv, v, tokens, Hk, D, v_token_stride, v_head_stride, it))
     return RLCS_ERR_CUDA;
   const ForwardArgs a = {cu_seqlens,
+                         static_cast<const bf *>(v),
+                         v_token_stride,
+                         v_head_stride,
                          static_cast<bf *>(out),
                          lse,
                          static_cast<WsHeader *>(scratch),

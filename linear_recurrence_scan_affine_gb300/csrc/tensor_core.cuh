@@ -222,6 +222,23 @@ __device__ __forceinline__ void clear_rows(unsigned char *tile, int from, int la
       reinterpret_cast<uint4 *>(tile + c * ROWS * 128)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_shared();
 }
+// Nonzero where one of eight bf16 values is infinite or NaN: its exponent's
+// eight ones carry into the sign's place.
+__device__ __forceinline__ uint32_t special(const uint4 &x) {
+  auto carry = [](uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; };
+  return (carry(x.x) | carry(x.y) | carry(x.z) | carry(x.w)) & 0x80008000u;
+}
+// Zeros in place of such values of a tile, by one warp.
+template <int DP, int ROWS>
+__device__ __noinline__ void clear_special(unsigned char *tile, int lane) {
+  uint32_t *w = reinterpret_cast<uint32_t *>(tile);
+  for (int i = lane; i < DP * ROWS / 2; i += 32) {
+    const uint32_t s = ((w[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    if (s) w[i] &= (s & 0x8000u ? 0u : 0xffffu) | (s & 0x80000000u ? 0u : 0xffff0000u);
+  }
+  __syncwarp();
+  fence_proxy_async_shared();
+}
 
 // Host: the map of a [tokens, heads, D] bf16 view, in 64-column boxes of
 // `rows` tokens of one head.

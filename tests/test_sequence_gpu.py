@@ -523,3 +523,31 @@ def test_calls_on_another_stream_and_in_a_graph(rl):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(kept, everything()))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("at", [0, 1, 63, 64, 100, 127, 128, 250, 299])
+def test_attention_later_tokens_stay_masked(rl, D, at):
+    # keys and values of a later token, whatever they hold, change no bit of
+    # an earlier row; one infinite element reaches its own column alone, in
+    # the rows that see it
+    g = gen(31 + at)
+    n, Hq, Hk, bf = 300, 4, 2, torch.bfloat16
+    q, k, v = (rand(g, n, h, D, dtype=bf).cuda() for h in (Hq, Hk, Hk))
+    cu = bounds([n]).cuda()
+    out, lse = rl.rlcs_attention(q, k, v, cu, return_lse=True)
+    for bad in (math.nan, math.inf):
+        k2, v2 = k.clone(), v.clone()
+        k2[at:], v2[at:] = bad, -bad
+        got, glse = rl.rlcs_attention(q, k2, v2, cu, return_lse=True)
+        assert torch.equal(got[:at], out[:at]) and torch.equal(glse[:, :at], lse[:, :at])
+        assert torch.isnan(got[at:]).all()
+    v2 = v.clone()
+    v2[at, 0, 3], v2[at, 1, D - 1] = math.inf, -math.inf
+    want = out.clone()
+    want[at:, :2, 3], want[at:, 2:, D - 1] = math.inf, -math.inf
+    assert torch.equal(rl.rlcs_attention(q, k, v2, cu), want)
+    v2[n - 1, 0, 3] = -math.inf
+    got = rl.rlcs_attention(q, k, v2, cu)
+    assert torch.equal(got[:n - 1], want[:n - 1])
+    assert torch.isnan(got[n - 1, :2, 3]).all() or at == n - 1

@@ -190,3 +190,10 @@ def test_binding_refuses_host_tensors_and_wrong_kinds():
             call()
     with pytest.raises(ValueError):
         sequence.rlcs_rope_table(4, 4, scaling="none such")
+
+
+def test_attention_scale_range():
+    # scale * log2(e) is held in float32: outside this range it would be zero,
+    # subnormal or infinite
+    for scale in (0.0, -0.125, 1e-31, 1e-320, 1e31, 3e38, float("inf"), float("nan")):
+        assert attn(scale=scale) == INVALID, scale
