@@ -52,8 +52,9 @@ def _declare():
 
 _declare()
 
+
 def _call(name, *args):
-    """Call the library; tensors are passed by address and None as NULL."""
+    """Call the library with addresses and numbers; raise on any other status."""
     st = _fn[name](*args)
     if st:
         raise _b.RlcsError(st, name)
@@ -192,7 +193,7 @@ def rlcs_gated_scan(x, gate, reset=None, h0=None, out=None):
     last = torch.empty((B, D), dtype=torch.float32, device=x.device)
     _call("rlcs_gated_scan", x.data_ptr(), gate.data_ptr(), _at(reset), _at(h0), h.data_ptr(),
           last.data_ptr(), B, T, D, _DTYPES[x.dtype], _raw_stream(dev))
-    return h.view(x.shape), last
+    return (h if out is None else h.view(x.shape)), last
 
 
 @_streamed
@@ -339,7 +340,7 @@ def rlcs_attention(q, k, v, cu_seqlens, scale=None, return_lse=False):
     """Causal attention over packed sequences: q [tokens, Hq, D], k and v
     [tokens, Hk, D] bfloat16, D a multiple of 8 up to 128, Hq a multiple of
     Hk; sequence s holds tokens cu_seqlens[s] to cu_seqlens[s+1] (int32).
-    `scale` (> 0) defaults to D ** -0.5. Views whose strides are multiples of
+    `scale` (positive) defaults to D ** -0.5. Views whose strides are multiples of
     8 elements on a 16-byte boundary are read in place, others copied. Returns
     out [tokens, Hq, D], or (out, lse [Hq, tokens] float32) with
     `return_lse`. Tokens that no sequence holds are left unwritten."""
@@ -423,4 +424,4 @@ def rlcs_attention_step(q, k_cache, v_cache, lengths, scale=None, out=None):
     _call("rlcs_attention_step", q.data_ptr(), *ks, *vs, lengths.data_ptr(), o.data_ptr(), B, S,
           Hq, Hk, D, D ** -0.5 if scale is None else scale, _DTYPES[q.dtype], ws + 64, wsb - 64,
           stream)
-    return o.view(q.shape)
+    return o if out is None else o.view(q.shape)
