@@ -928,29 +928,38 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
 // ---------------------------------------------------------------------------
 // One new token per sequence. Bound by reading the cache once.
 //
-// Work items are (sequence, key/value head, chunk of positions), taken in
-// turn by as many blocks as run at once, so long and short caches share the
-// GPU evenly. A warp takes 32 positions at a time, straight from global
-// memory into the operands of two small products: the order of the summed
-// index is free, so each lane loads 16 contiguous bytes of a key row, and the
-// order of the output index is free, so each lane loads 16 contiguous bytes of
-// the value rows and pairs them up itself.
+// A unit of work is kUnit positions of one sequence's cache for one key/value
+// head. All units stand in a row (sequence, head, position), which is cut into
+// equal runs, one to each of the blocks that run at once: short and long
+// caches share the GPU evenly, and a block leaves at most two heads
+// unfinished, at its run's ends. A second kernel joins those, in run order.
+// A warp takes 32 positions at a time, straight from global memory into the
+// operands of two small products: the order of the summed index is free, so
+// each lane loads 16 contiguous bytes of a key row, and the order of the
+// output index is free, so each lane loads 16 contiguous bytes of the value
+// rows and pairs them up itself.
 //   S^T[16 positions x 8 rows] = K Q^T,  O^T[16 elements x 8 rows] += V^T P^T
-// (rows: the query heads that share the key/value head, 8 or 16 to an item).
-// Chunks of one sequence are joined by a second kernel, in chunk order.
+// (rows: the query heads that share the key/value head, 8 or 16 at a time).
 // ---------------------------------------------------------------------------
+// A head that starts in one block's run and ends in a later one's; kept by
+// the block after the one it starts in.
+struct Unfinished {
+  int b, head, last;  // key/value head x row block; the block it ends in, 0 for none
+};
 struct StepArgs {
   const bf *q, *k, *v;
   int64_t kb, kt, kh, vb, vt, vh;
   const int32_t *lengths;
   bf *o;
-  float *partial;  // [B, Hq, chunks, D + 2]: o, running maximum, sum
+  Unfinished *list;  // [blocks]
+  float *partial;    // [blocks][2: first, last][rows][D + 2]: o, running maximum, sum
   int64_t B, S;
-  int Hq, Hk, D, group, row_blocks, chunk, chunks;
+  int Hq, Hk, D, group, row_blocks, blocks;
   float scale2;
 };
 constexpr int kStepWarps = 4;
-constexpr int kChunksMax = 256;
+constexpr int kUnit = kStepWarps * 32;
+constexpr size_t kListBytes = 16384;  // of the scratch, for the list of unfinished heads
 constexpr int step_blocks(int row_blocks) { return row_blocks == 1 ? 3 : 2; }  // per SM
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -973,6 +982,7 @@ __device__ __forceinline__ int64_t cache_length(const StepArgs &p, int64_t b) {
   const int64_t n = p.lengths[b];
   return n < 0 ? 0 : (n > p.S ? p.S : n);
 }
+__device__ __forceinline__ int units_of(int64_t n) { return (int)((n + kUnit - 1) / kUnit); }
 
 template <int DP, int NR>
 __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
@@ -982,34 +992,58 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
   constexpr int MT = DP / 16;  // output tiles
   __shared__ float so[kStepWarps][NR * 8][DP + 4];
   __shared__ float sm[kStepWarps][NR * 8], sl[kStepWarps][NR * 8];
+  __shared__ int run[2], upto[kStepWarps];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = lane >> 2, c = lane & 3;
-  int64_t b = 0, before = 0;  // the sequence that holds this block's item, items of earlier ones
-  for (int64_t item = blockIdx.x;; item += gridDim.x) {
-    // items of sequence b: its chunks x heads x row blocks
-    int64_t n = 0, items = 0;
-    for (;; ++b, before += items) {
-      if (b >= p.B) return;
-      if (p.B - b >= 32) {  // skip 32 sequences at a time
-        int64_t own = ceil_div_dev(cache_length(p, b + lane), p.chunk) * p.Hk * p.row_blocks;
+  const int per = p.Hk * p.row_blocks;  // heads of a sequence
+  // count the units, a slice of the sequences to a thread, and find the
+  // sequence in which this block's run starts
+  const int slice = (int)(p.B * threadIdx.x / kUnit);
+  const int slice_end = (int)(p.B * (threadIdx.x + 1) / kUnit);
+  int own = 0, sum_to;
+  for (int x = slice; x < slice_end; ++x) own += units_of(cache_length(p, x)) * per;
+  sum_to = own;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(kFull, own, o);
-        if (item >= before + own) {
-          items = own;
-          b += 31;
-          continue;
-        }
-      }
-      n = cache_length(p, b);
-      items = ceil_div_dev(n, p.chunk) * p.Hk * p.row_blocks;
-      if (item < before + items) break;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, sum_to, o);
+    if (lane >= o) sum_to += y;
+  }
+  if (lane == 31) upto[warp] = sum_to;
+  __syncthreads();
+  int units = 0;
+#pragma unroll
+  for (int w = 0; w < kStepWarps; ++w) {
+    if (w < warp) sum_to += upto[w];
+    units += upto[w];
+  }
+  const int block = blockIdx.x, blocks = units < p.blocks ? units : p.blocks;  // that have a run
+  auto run_start = [&](int i) { return (int)((int64_t)units * i / blocks); };
+  const int start = block < blocks ? run_start(block) : units;
+  if (start >= sum_to - own && start < sum_to) run[0] = slice, run[1] = sum_to - own;
+  if (threadIdx.x == 0) p.list[block].last = 0;
+  // nothing cached: zeros
+  for (int64_t x = block; x < p.B; x += p.blocks)
+    if (cache_length(p, x) == 0)
+      for (int y = threadIdx.x; y < p.Hq * p.D; y += kUnit)
+        p.o[x * p.Hq * p.D + y] = __float2bfloat16_rn(0.0f);
+  __syncthreads();
+  if (block >= blocks) return;
+  const int end = run_start(block + 1);
+  int b = run[0], before = run[1];  // the sequence a unit is in, units of those before it
+  for (int unit = start; unit < end;) {
+    const int64_t n = cache_length(p, b);
+    const int of_head = units_of(n);
+    if (unit >= before + of_head * per) {
+      before += of_head * per;
+      ++b;
+      continue;
     }
-    const int at = (int)(item - before);
-    const int per = p.Hk * p.row_blocks, which = at / per, rest = at % per;
-    const int g = rest / p.row_blocks, r0 = rest % p.row_blocks * (NR * 8);
-    const int64_t from = (int64_t)which * p.chunk;
-    const int64_t to = from + p.chunk < n ? from + p.chunk : n;
+    const int head = (unit - before) / of_head, t0 = (unit - before) % of_head;
+    const int t1 = t0 + (end - unit) < of_head ? t0 + (end - unit) : of_head;
+    unit += t1 - t0;
+    const int g = head / p.row_blocks, r0 = head % p.row_blocks * (NR * 8);
+    const int64_t from = (int64_t)t0 * kUnit, to = (int64_t)t1 * kUnit < n ? (int64_t)t1 * kUnit : n;
 
     // queries: row e of each block of 8, as the second operand
     uint4 q[NR][KC];
@@ -1147,7 +1181,13 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
         }
     }
     __syncthreads();
-    const bool only = n <= p.chunk;
+    const bool whole = t0 == 0 && t1 == of_head;
+    if (t0 > 0 && threadIdx.x == 0) {
+      // t0 > 0 at the run's start alone; unit x is in run ((x + 1) * blocks - 1) / units
+      const int head0 = before + head * of_head;
+      if (run_start(block - 1) <= head0)
+        p.list[block] = {b, head, (int)(((int64_t)(head0 + of_head) * blocks - 1) / units)};
+    }
     for (int x = threadIdx.x; x < NR * 8 * DP; x += kStepWarps * 32) {
       const int row = x / DP, d = x % DP;
       if (r0 + row >= p.group || d >= p.D) continue;
@@ -1161,11 +1201,11 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
         l = fmaf(f, sl[y][row], l);
         if (f != 0.0f) o = fmaf(f, so[y][row][d], o);
       }
-      const int64_t head = b * p.Hq + g * p.group + r0 + row;
-      if (only) {
-        p.o[head * p.D + d] = __float2bfloat16_rn(o / l);
+      const int64_t at = b * p.Hq + g * p.group + r0 + row;
+      if (whole) {
+        p.o[at * p.D + d] = __float2bfloat16_rn(o / l);
       } else {
-        float *out = p.partial + (head * p.chunks + which) * (p.D + 2);
+        float *out = p.partial + ((int64_t)(2 * block + (t0 == 0)) * (NR * 8) + row) * (p.D + 2);
         out[d] = o;
         if (d == 0) out[p.D] = m, out[p.D + 1] = l;
       }
@@ -1174,59 +1214,79 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
   }
 }
 
-// Join the chunks of each sequence, a block per query head; zero where the
-// cache is empty.
-__global__ void __launch_bounds__(128) attention_step_join_kernel(const StepArgs p) {
+// Join the heads that no block finished: block i the one that starts in run
+// i - 1 and goes on in run i, rows blockIdx.y, blockIdx.y + gridDim.y, ...
+// Four groups of threads take every fourth run.
+__global__ void __launch_bounds__(512) attention_step_join_kernel(const StepArgs p, int rows) {
+  __shared__ float part[4][128][3];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t head = blockIdx.x;
-  const int64_t n = cache_length(p, head / p.Hq);
-  const int chunks = (int)ceil_div_dev(n, p.chunk), d = threadIdx.x;
-  __shared__ float weight[kChunksMax], high[4];
-  if (chunks == 1) return;  // its one item wrote the result
-  const float *in = p.partial + head * p.chunks * (p.D + 2);
-  float m = -INFINITY;
-  for (int i = threadIdx.x; i < chunks; i += 128) {
-    weight[i] = in[i * (p.D + 2) + p.D];
-    m = fmaxf(m, weight[i]);
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
-  if ((threadIdx.x & 31) == 0) high[threadIdx.x >> 5] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
-  float l = 0.0f, o = 0.0f;
-  if (d < p.D)
-#pragma unroll 8
-    for (int i = 0; i < chunks; ++i) {
-      const float f = ex2(weight[i] - m);
-      l = fmaf(f, in[i * (p.D + 2) + p.D + 1], l);
-      o = fmaf(f, in[i * (p.D + 2) + d], o);
+  const int i = blockIdx.x + 1;
+  const Unfinished u = p.list[i];
+  if (u.last == 0) return;
+  const int d = threadIdx.x & 127, set = threadIdx.x >> 7, runs = u.last - i + 2;
+  const int g = u.head / p.row_blocks, r0 = u.head % p.row_blocks * rows;
+  // the first run's last place, then the others' first
+  auto place = [&](int k, int row) {
+    return p.partial + ((int64_t)(2 * (i - 1 + k) + (k == 0)) * rows + row) * (p.D + 2);
+  };
+  for (int row = blockIdx.y; row < rows && r0 + row < p.group; row += gridDim.y) {
+    float m = -INFINITY, l = 0.0f, o = 0.0f;
+#pragma unroll 4
+    for (int k = set; k < runs; k += 4) {
+      const float *in = place(k, row);
+      const float x = d < p.D ? in[d] : 0.0f, top = in[p.D], sum = in[p.D + 1];
+      const float high = fmaxf(m, top), z = high == -INFINITY ? 0.0f : high;
+      const float f = ex2(m - z), h = ex2(top - z);
+      l = fmaf(l, f, sum * h);
+      o = fmaf(o, f, x * h);
+      m = high;
     }
-  if (d >= p.D) return;
-  p.o[head * p.D + d] = __float2bfloat16_rn(chunks ? o / l : 0.0f);
+    part[set][d][0] = m, part[set][d][1] = l, part[set][d][2] = o;
+    __syncthreads();
+    if (set == 0 && d < p.D) {
+#pragma unroll
+      for (int k = 1; k < 4; ++k) m = fmaxf(m, part[k][d][0]);
+      const float z = m == -INFINITY ? 0.0f : m;
+      l = o = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = ex2(part[k][d][0] - z);
+        l = fmaf(part[k][d][1], f, l);
+        o = fmaf(part[k][d][2], f, o);
+      }
+      p.o[((int64_t)u.b * p.Hq + g * p.group + r0 + row) * p.D + d] = __float2bfloat16_rn(o / l);
+    }
+    __syncthreads();
+  }
 }
 
-// Positions of a work item: some 16 items per SM at full caches, of at least
-// 128 positions, and at most kChunksMax to a sequence.
-int64_t step_chunk(int64_t B, int64_t S, int64_t Hk) {
-  const double even = (double)B * (double)Hk * (double)S / (kSms * 16);
-  int64_t chunk = 128;
-  while (chunk < even || chunk * kChunksMax < S) chunk *= 2;
-  return chunk;
+// Query heads to a row block, and blocks of a call: no more than run at once.
+int step_rows(int64_t group) { return group <= 8 ? 8 : 16; }
+int64_t step_heads(int64_t B, int64_t Hq, int64_t Hk) {
+  const int64_t group = Hq / Hk;
+  return B * Hk * ceil_div(group, step_rows(group));
+}
+bool step_fits(int64_t B, int64_t S, int64_t Hq, int64_t Hk) {  // units are counted in 32 bits
+  return product_fits(B, Hq, S / kUnit + 1) &&
+         step_heads(B, Hq, Hk) * ceil_div(S, kUnit) < (int64_t)INT32_MAX;
+}
+int step_grid(int64_t B, int64_t S, int64_t Hq, int64_t Hk) {
+  const int64_t most = kSms * step_blocks(step_rows(Hq / Hk) / 8);
+  const int64_t units = step_heads(B, Hq, Hk) * ceil_div(S, kUnit);
+  return (int)(units < 1 ? 1 : units < most ? units : most);
 }
 
 template <int DP, int NR>
-cudaError_t launch_step(StepArgs &a, cudaStream_t st) {
-  a.row_blocks = (a.group + NR * 8 - 1) / (NR * 8);
-  const int64_t items = a.B * a.chunks * a.Hk * a.row_blocks, most = kSms * step_blocks(NR);
-  const cudaError_t e =
-      items > 0 ? launch_ex(attention_step_kernel<DP, NR>, dim3((unsigned)(items < most ? items : most)),
-                            dim3(kStepWarps * 32), 0, st, true, a)
-                : cudaSuccess;
-  if (e != cudaSuccess) return e;
-  return launch_ex(attention_step_join_kernel, dim3((unsigned)(a.B * a.Hq)), dim3(128), 0, st, true,
-                   a);
+cudaError_t launch_step(const StepArgs &a, cudaStream_t st) {
+  const cudaError_t e = launch_ex(attention_step_kernel<DP, NR>, dim3((unsigned)a.blocks),
+                                  dim3(kUnit), 0, st, true, a);
+  if (e != cudaSuccess || a.blocks == 1) return e;
+  // few heads over many blocks: a block to each of a head's rows
+  const bool wide = a.B * a.Hk * a.row_blocks * 8 <= a.blocks;
+  return launch_ex(attention_step_join_kernel,
+                   dim3((unsigned)a.blocks - 1, wide ? (unsigned)NR * 8 : 1u), dim3(512), 0, st, true,
+                   a, NR * 8);
 }
 
 // Token and head strides that 16-byte loads can use.
@@ -1432,10 +1492,11 @@ rlcs_status rlcs_attention_backward(
 }
 
 size_t rlcs_attention_step_scratch_bytes(int64_t B, int64_t S, int64_t Hq, int64_t Hk, int64_t D) {
-  if (B <= 0 || S <= 0 || Hq <= 0 || Hk <= 0 || D <= 0) return 16;
-  const int64_t chunks = ceil_div(S, step_chunk(B, S, Hk));
-  if (!product_fits(B, Hq, chunks, (D + 2) * 4)) return 0;
-  return (size_t)(B * Hq * chunks * (D + 2) * 4);
+  if (B <= 0 || S < 0 || Hq <= 0 || Hk <= 0 || Hk > Hq || D <= 0 || D > 128 ||
+      !step_fits(B, S, Hq, Hk))
+    return 16;
+  const size_t rows = (size_t)step_grid(B, S, Hq, Hk) * 2 * step_rows(Hq / Hk);
+  return kListBytes + rows * (size_t)(D + 2) * 4;
 }
 
 rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_batch_stride,
@@ -1445,12 +1506,13 @@ rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_ba
                                 const int32_t *lengths, void *out, int64_t B, int64_t S,
                                 int64_t Hq, int64_t Hk, int64_t D, double scale, rlcs_dtype dtype,
                                 void *scratch, size_t scratch_bytes, rlcs_stream_t stream) {
-  if (B < 0 || S < 0 || S >= (int64_t)1 << 40 || !attn_sizes(0, B, Hq, Hk, D, scale, dtype) ||
-      B * Hq >= (int64_t)INT32_MAX ||
+  if (B < 0 || S < 0 || !attn_sizes(0, B, Hq, Hk, D, scale, dtype) ||
+      B * Hq >= (int64_t)INT32_MAX || !step_fits(B, S, Hq, Hk) ||
       !product_fits(B, k_batch_stride < 0 ? 0 : k_batch_stride, 1) ||
       !product_fits(B, v_batch_stride < 0 ? 0 : v_batch_stride, 1) || k_batch_stride < 0 ||
       v_batch_stride < 0)
     return RLCS_ERR_INVALID_ARG;
+  static_assert(kSms * 3 * sizeof(Unfinished) <= kListBytes, "an entry to each block");
   if (B == 0) return RLCS_OK;
   if (!q || !lengths || !out || (S > 0 && (!k_cache || !v_cache))) return RLCS_ERR_INVALID_ARG;
   const rlcs_status su[] = {strides_usable(k_cache, k_position_stride, k_head_stride, S, Hk),
@@ -1490,12 +1552,10 @@ rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_ba
   a.Hk = (int)Hk;
   a.D = (int)D;
   a.group = (int)(Hq / Hk);
-  a.chunk = (int)step_chunk(B, S, Hk);
-  a.chunks = (int)ceil_div(S, a.chunk);
-  if (!product_fits(a.chunks, Hk, a.group, 1) ||
-      (int64_t)a.chunks * Hk * a.group >= (int64_t)INT32_MAX)
-    return RLCS_ERR_INVALID_ARG;
-  a.partial = static_cast<float *>(scratch);
+  a.row_blocks = (int)ceil_div(a.group, step_rows(a.group));
+  a.blocks = step_grid(B, S, Hq, Hk);
+  a.list = static_cast<Unfinished *>(scratch);
+  a.partial = reinterpret_cast<float *>(static_cast<char *>(scratch) + kListBytes);
   a.scale2 = (float)(scale * 1.4426950408889634);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (a.group <= 8)
