@@ -27,48 +27,74 @@ constexpr int inner() {
   return DP == 64 ? 64 : 128;
 }
 
-// Tile `index` in the order of sequences, longest rows first within each
-// (its last tile first): the sequence's bounds and the tile's number, or
-// false past the last tile. One warp; every lane gets the result.
+// Tile `index` in the order of sequences, longest rows first within each (its
+// last tile first): the sequence's bounds and the tile's number. One warp
+// looks, a slice of the sequences to a lane; past kWarpSearch sequences the
+// whole block does, so that many short episodes cost a block one round of
+// loads.
 struct Tile {
   int lo, len, first;  // the sequence's first token and length; the tile's first row in it
 };
-__device__ __forceinline__ bool find_tile(const int32_t *cu, int64_t sequences, int64_t tokens,
-                                          int64_t index, int lane, Tile &t) {
-  for (int64_t s0 = 0; s0 < sequences; s0 += 32) {
-    int lo = 0, len = 0;
-    if (s0 + lane < sequences) {
-      const int64_t a = cu[s0 + lane] < 0 ? 0 : cu[s0 + lane];
-      const int64_t b = cu[s0 + lane + 1] < tokens ? cu[s0 + lane + 1] : tokens;
-      lo = (int)a;
-      len = b > a ? (int)(b - a) : 0;
-    }
-    const int tiles = (len + kTile - 1) / kTile;
-    int upto = tiles;  // tiles of this group's sequences up to this one
+struct TileSearch {
+  int64_t upto[18];  // tiles of each warp's sequences
+  Tile tile;
+  int found;
+};
+constexpr int kWarpSearch = 128;
+
+__device__ __forceinline__ Tile sequence(const int32_t *cu, int s, int tokens) {
+  const int a = cu[s] < 0 ? 0 : cu[s], b = cu[s + 1] < tokens ? cu[s + 1] : tokens;
+  return {a, b > a ? b - a : 0, 0};
+}
+__device__ __forceinline__ int tiles_of(const Tile &t) { return (t.len + kTile - 1) / kTile; }
+// The whole block calls this; `searcher` is the warp that goes on with the
+// result at once, the others read it after the block's next barrier.
+__device__ __forceinline__ void find_tile(const int32_t *cu, int sequences, int tokens, int index,
+                                          int searcher, TileSearch &sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool few = sequences <= kWarpSearch;
+  if (few && warp != searcher) return;
+  const int slice = few ? (sequences + 31) / 32 : (int)((sequences + blockDim.x - 1) / blockDim.x);
+  const int at = slice * (few ? lane : (int)threadIdx.x);
+  const int end = at < sequences - slice ? at + slice : sequences;
+  if (warp == searcher && lane == 0) sm.found = 0;
+  int64_t own = 0;
+#pragma unroll 4
+  for (int s = at; s < end; ++s) own += tiles_of(sequence(cu, s, tokens));
+  int64_t upto = own;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(kFull, upto, o);
-      if (lane >= o) upto += n;
-    }
-    const unsigned hit = __ballot_sync(kFull, index < upto);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      t.lo = __shfl_sync(kFull, lo, src);
-      t.len = __shfl_sync(kFull, len, src);
-      t.first = (__shfl_sync(kFull, upto, src) - 1 - (int)index) * kTile;
-      return true;
-    }
-    index -= __shfl_sync(kFull, upto, 31);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t n = __shfl_up_sync(kFull, upto, o);
+    if (lane >= o) upto += n;
   }
-  return false;
+  if (!few) {
+    if (lane == 31) sm.upto[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) upto += sm.upto[w];
+  } else {
+    __syncwarp();
+  }
+  int64_t left = index - (upto - own);
+  if (left >= 0 && left < own)
+    for (int s = at; s < end; ++s) {
+      Tile x = sequence(cu, s, tokens);
+      const int tiles = tiles_of(x);
+      if (left < tiles) {
+        x.first = (tiles - 1 - (int)left) * kTile;
+        sm.tile = x;
+        sm.found = 1;
+        break;
+      }
+      left -= tiles;
+    }
+  if (few) __syncwarp();
+  else __syncthreads();
 }
 
 // Tiles that well-formed bounds can need.
 int64_t tile_bound(int64_t sequences, int64_t tokens) {
   return tokens / kTile + (sequences < tokens ? sequences : tokens);
 }
-
-__device__ __forceinline__ int64_t ceil_div_dev(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -153,6 +179,7 @@ struct ForwardSmem {
   float row[2][128];  // maxima, and at the end sums, of the two halves of each row
   uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t s_full, p_ready, o_full;
+  TileSearch search;
   uint32_t tmem;
   int abort;
   int special;  // an infinity or NaN among the diagonal's values
@@ -202,12 +229,22 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   const int h = blockIdx.x % p.Hq;
-  Tile t;
-  if (!aligned_tiles(raw, p.ws)) return;
-  if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.Hq, lane, t)) return;
   constexpr int IT = inner<DP>(), kStages = ForwardSmem<DP>::kStages;
-  const int rows = t.len - t.first < kTile ? t.len - t.first : kTile;
-  const int steps = (t.first + rows + IT - 1) / IT;  // key tiles, the last one first
+  if (!aligned_tiles(raw, p.ws)) return;
+  // An SM starts its next block only when the last has taken its tensor memory
+  // and given up the right to more: that comes before anything slow. (400
+  // episodes of 60 steps, 12 heads on 4 of 64, with one warp looking for the
+  // tile: forward 161 -> 84 us, dk and dv 76 -> 61, dq 147 -> 92. 40 of 600 are
+  // 2% slower: their blocks now start together rather than in turn.)
+  if (warp == 9) tc::tmem_alloc(&sm.tmem, IT + DP);
+  find_tile(p.cu, (int)p.sequences, (int)p.tokens, blockIdx.x / p.Hq, 8, sm.search);
+  Tile t;
+  int rows, steps;  // steps: key tiles, the last one first
+  auto take_tile = [&] {
+    t = sm.search.tile;
+    rows = t.len - t.first < kTile ? t.len - t.first : kTile;
+    steps = (t.first + rows + IT - 1) / IT;
+  };
   auto first_key = [&](int it) { return (steps - 1 - it) * IT; };
   auto diagonal = [&](int it) { return first_key(it) >= t.first; };  // at most kStages tiles
   auto load_k = [&](int it) {
@@ -219,7 +256,8 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
                           t.lo + first_key(it));
   };
   // the copying lane sets the barriers up and starts the first copies at once
-  if (warp == 8 && lane == 0) {
+  if (warp == 8 && lane == 0 && sm.search.found) {
+    take_tile();
     for (int i = 0; i < kStages; ++i)
       for (uint64_t *b : {&sm.k_full[i], &sm.k_empty[i], &sm.v_full[i], &sm.v_empty[i]})
         mbar_init(b, 1);
@@ -231,10 +269,14 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
     load_k(0);
     load_v(0);
   }
-  if (warp == 9) tc::tmem_alloc(&sm.tmem, IT + DP);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  if (!sm.search.found) {
+    if (warp == 9) tc::tmem_dealloc(sm.tmem, IT + DP);
+    return;
+  }
+  take_tile();
   const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0), tS = tmem, tO = tmem + IT;
   volatile int *abort = &sm.abort, *special = &sm.special;
   const uint32_t lead = lane == 0;  // the lane that issues products
@@ -490,6 +532,7 @@ struct KvSmem {
   float lse[2][128], delta[2][128];
   uint64_t k_full, v_full, q_full[3], q_empty[3], do_full[2], do_empty[2];
   uint64_t s_full, dp_full, p_ready, ds_ready, done;
+  TileSearch search;
   uint32_t tmem;
   int abort;
 };
@@ -516,16 +559,24 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   const int rank = blockIdx.x % p.split, g = blockIdx.x / p.split % p.Hk;
   const int heads = p.group / p.split, head0 = g * p.group + rank * heads;
-  Tile t;
-  if (!aligned_tiles(raw, p.ws)) return;
-  if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.split / p.Hk, lane, t)) return;
   constexpr int IT = inner<DP>(), PARTS = IT / 32, kCopy = 4 * PARTS, kIssue = kCopy + 1;
+  if (!aligned_tiles(raw, p.ws)) return;
+  if (warp == kIssue) tc::tmem_alloc(&sm.tmem, 2 * IT + 2 * DP);
+  find_tile(p.cu, (int)p.sequences, (int)p.tokens, blockIdx.x / p.split / p.Hk, kCopy, sm.search);
   constexpr int kSubs = kTile / IT;  // query tiles that meet the diagonal
-  // the first key tile has the most query tiles: turn the order round
-  const int key0 = ((t.len + kTile - 1) / kTile - 1) * kTile - t.first;
-  const int tiles = (t.len + IT - 1) / IT, per_head = tiles - key0 / IT, steps = per_head * heads;
-  const int rows = t.len - key0 < kTile ? t.len - key0 : kTile;
-  const int tail = t.len - (tiles - 1) * IT;  // rows of the sequence's last query tile
+  Tile t;
+  int key0, per_head, steps, rows;
+  int tail;  // rows of the sequence's last query tile
+  auto take_tile = [&] {
+    t = sm.search.tile;
+    // the first key tile has the most query tiles: turn the order round
+    key0 = ((t.len + kTile - 1) / kTile - 1) * kTile - t.first;
+    const int tiles = (t.len + IT - 1) / IT;
+    per_head = tiles - key0 / IT;
+    steps = per_head * heads;
+    rows = t.len - key0 < kTile ? t.len - key0 : kTile;
+    tail = t.len - (tiles - 1) * IT;
+  };
   // Step i is query tile `sub` of head `head`, counted up by each role.
   struct Step {
     int head, sub;
@@ -541,7 +592,8 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
   auto load_dout = [&](int i, Step x) {
     tc::load_tile<DP, IT>(sm.dout[i & 1], &mdo, &sm.do_full[i & 1], x.head, t.lo + first_row(x));
   };
-  if (warp == kCopy && lane == 0) {
+  if (warp == kCopy && lane == 0 && sm.search.found) {
+    take_tile();
     for (int i = 0; i < 3; ++i) mbar_init(&sm.q_full[i], 1), mbar_init(&sm.q_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.do_full[i], 1), mbar_init(&sm.do_empty[i], 1);
     for (uint64_t *b : {&sm.k_full, &sm.v_full, &sm.s_full, &sm.dp_full, &sm.done}) mbar_init(b, 1);
@@ -554,10 +606,14 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
     tc::load_tile<DP, kTile>(sm.v, &mv, &sm.v_full, g, t.lo + key0);
     load_dout(0, begin);
   }
-  if (warp == kIssue) tc::tmem_alloc(&sm.tmem, 2 * IT + 2 * DP);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  if (!sm.search.found) {
+    if (warp == kIssue) tc::tmem_dealloc(sm.tmem, 2 * IT + 2 * DP);
+    return;
+  }
+  take_tile();
   const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
   const uint32_t tS = tmem, tP = tS + IT, tV = tP + IT, tK = tV + DP;
   volatile int *abort = &sm.abort;
@@ -759,6 +815,7 @@ struct QSmem {
       v[2][DP * inner<DP>() * 2];
   uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[2], v_empty[2];
   uint64_t s_full[2], dp_full, ds_ready, done;
+  TileSearch search;
   uint32_t tmem;
   int abort;
 };
@@ -780,12 +837,17 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   const int h = blockIdx.x % p.Hq;
-  Tile t;
-  if (!aligned_tiles(raw, p.ws)) return;
-  if (!find_tile(p.cu, p.sequences, p.tokens, blockIdx.x / p.Hq, lane, t)) return;
   constexpr int IT = inner<DP>(), PARTS = IT / 32, kCopy = 4 * PARTS, kIssue = kCopy + 1;
-  const int rows = t.len - t.first < kTile ? t.len - t.first : kTile;
-  const int steps = (t.first + rows + IT - 1) / IT;  // key tiles, the last one first
+  if (!aligned_tiles(raw, p.ws)) return;
+  if (warp == kIssue) tc::tmem_alloc(&sm.tmem, 3 * IT + DP);
+  find_tile(p.cu, (int)p.sequences, (int)p.tokens, blockIdx.x / p.Hq, kCopy, sm.search);
+  Tile t;
+  int rows, steps;  // steps: key tiles, the last one first
+  auto take_tile = [&] {
+    t = sm.search.tile;
+    rows = t.len - t.first < kTile ? t.len - t.first : kTile;
+    steps = (t.first + rows + IT - 1) / IT;
+  };
   auto first_key = [&](int j) { return (steps - 1 - j) * IT; };
   auto diagonal = [&](int j) { return first_key(j) + IT > t.first; };
   auto load_k = [&](int j) {
@@ -794,7 +856,8 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
   auto load_v = [&](int j) {
     tc::load_tile<DP, IT>(sm.v[j & 1], &mv, &sm.v_full[j & 1], h / p.group, t.lo + first_key(j));
   };
-  if (warp == kCopy && lane == 0) {
+  if (warp == kCopy && lane == 0 && sm.search.found) {
+    take_tile();
     for (int i = 0; i < 3; ++i) mbar_init(&sm.k_full[i], 1), mbar_init(&sm.k_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.v_full[i], 1);
@@ -810,10 +873,14 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
     tc::load_tile<DP, kTile>(sm.dout, &mdo, &sm.do_full, h, t.lo + t.first);
     load_v(0);
   }
-  if (warp == kIssue) tc::tmem_alloc(&sm.tmem, 3 * IT + DP);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  if (!sm.search.found) {
+    if (warp == kIssue) tc::tmem_dealloc(sm.tmem, 3 * IT + DP);
+    return;
+  }
+  take_tile();
   const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
   const uint32_t tS0 = tmem, tP = tS0 + IT, tQ = tP + IT, tS1 = tQ + DP;
   volatile int *abort = &sm.abort;
@@ -1298,7 +1365,7 @@ rlcs_status strides_usable(const void *p, int64_t ts, int64_t hs, int64_t tokens
 
 bool attn_sizes(int64_t sequences, int64_t tokens, int64_t Hq, int64_t Hk, int64_t D, double scale,
                 rlcs_dtype t) {
-  return sequences >= 0 && tokens >= 0 && tokens <= INT32_MAX && sequences < INT32_MAX && Hq > 0 &&
+  return sequences >= 0 && tokens >= 0 && tokens <= INT32_MAX && sequences < INT32_MAX - 1024 && Hq > 0 &&
          Hk > 0 && Hq % Hk == 0 && D > 0 && D <= 128 && D % 8 == 0 && t == RLCS_BF16 &&
          scale >= 1e-30 && scale <= 1e30 && product_fits(tokens, Hq, D) &&
          tile_bound(sequences, tokens) * Hq < (int64_t)INT32_MAX &&
