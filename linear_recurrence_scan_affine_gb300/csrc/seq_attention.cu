@@ -1281,16 +1281,28 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
   }
 }
 
-// Join the heads that no block finished: block i the one that starts in run
-// i - 1 and goes on in run i, rows blockIdx.y, blockIdx.y + gridDim.y, ...
-// Four groups of threads take every fourth run.
+// Join the heads that no block finished, blockIdx.x counting them in the list's
+// order: that of block i starts in run i - 1 and goes on in run i. Rows
+// blockIdx.y, blockIdx.y + gridDim.y, ...; four groups of threads take every
+// fourth run.
 __global__ void __launch_bounds__(512) attention_step_join_kernel(const StepArgs p, int rows) {
   __shared__ float part[4][128][3];
+  __shared__ int upto[16], entry;
   pdl_wait();
   pdl_launch_dependents();
-  const int i = blockIdx.x + 1;
+  const int mine = threadIdx.x + 1;  // (a list has at most 3 * kSms entries)
+  const bool set_here = mine < p.blocks && p.list[mine].last != 0;
+  const unsigned ballot = __ballot_sync(kFull, set_here);
+  if ((threadIdx.x & 31) == 0) upto[threadIdx.x >> 5] = __popc(ballot);
+  if (threadIdx.x == 0) entry = 0;
+  __syncthreads();
+  int before = __popc(ballot & ((1u << (threadIdx.x & 31)) - 1));
+  for (int w = 0; w < (int)threadIdx.x >> 5; ++w) before += upto[w];
+  if (set_here && before == (int)blockIdx.x) entry = mine;
+  __syncthreads();
+  const int i = entry;
+  if (i == 0) return;
   const Unfinished u = p.list[i];
-  if (u.last == 0) return;
   const int d = threadIdx.x & 127, set = threadIdx.x >> 7, runs = u.last - i + 2;
   const int g = u.head / p.row_blocks, r0 = u.head % p.row_blocks * rows;
   // the first run's last place, then the others' first
@@ -1350,10 +1362,11 @@ cudaError_t launch_step(const StepArgs &a, cudaStream_t st) {
                                   dim3(kUnit), 0, st, true, a);
   if (e != cudaSuccess || a.blocks == 1) return e;
   // few heads over many blocks: a block to each of a head's rows
-  const bool wide = a.B * a.Hk * a.row_blocks * 8 <= a.blocks;
+  const int64_t heads = a.B * a.Hk * a.row_blocks, most = a.blocks - 1;
+  const bool wide = heads * 8 <= a.blocks;
   return launch_ex(attention_step_join_kernel,
-                   dim3((unsigned)a.blocks - 1, wide ? (unsigned)NR * 8 : 1u), dim3(512), 0, st, true,
-                   a, NR * 8);
+                   dim3((unsigned)(heads < most ? heads : most), wide ? (unsigned)NR * 8 : 1u),
+                   dim3(512), 0, st, true, a, NR * 8);
 }
 
 // Token and head strides that 16-byte loads can use.
@@ -1579,7 +1592,8 @@ rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_ba
       !product_fits(B, v_batch_stride < 0 ? 0 : v_batch_stride, 1) || k_batch_stride < 0 ||
       v_batch_stride < 0)
     return RLCS_ERR_INVALID_ARG;
-  static_assert(kSms * 3 * sizeof(Unfinished) <= kListBytes, "an entry to each block");
+  static_assert(kSms * 3 <= 512 && kSms * 3 * sizeof(Unfinished) <= kListBytes,
+                "an entry to each block, a thread of the join to each entry");
   if (B == 0) return RLCS_OK;
   if (!q || !lengths || !out || (S > 0 && (!k_cache || !v_cache))) return RLCS_ERR_INVALID_ARG;
   const rlcs_status su[] = {strides_usable(k_cache, k_position_stride, k_head_stride, S, Hk),
