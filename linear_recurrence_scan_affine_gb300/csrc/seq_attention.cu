@@ -1000,13 +1000,13 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
 // equal runs, one to each of the blocks that run at once: short and long
 // caches share the GPU evenly, and a block leaves at most two heads
 // unfinished, at its run's ends. A second kernel joins those, in run order.
-// A warp takes 32 positions at a time, straight from global memory into the
-// operands of two small products: the order of the summed index is free, so
-// each lane loads 16 contiguous bytes of a key row, and the order of the
-// output index is free, so each lane loads 16 contiguous bytes of the value
-// rows and pairs them up itself.
+// A warp takes 16 positions at a time, copied asynchronously into its own ring
+// in shared memory, as the operands of two small products:
 //   S^T[16 positions x 8 rows] = K Q^T,  O^T[16 elements x 8 rows] += V^T P^T
 // (rows: the query heads that share the key/value head, 8 or 16 at a time).
+// Loads straight from global memory into the operands' registers leave memory
+// idle while a warp computes, and their values must be paired up: 115 us where
+// this takes 106 (64 caches of up to 8192, 16 heads on 4 of 128, 5.9 TB/s).
 // ---------------------------------------------------------------------------
 // A head that starts in one block's run and ends in a later one's; kept by
 // the block after the one it starts in.
@@ -1025,9 +1025,13 @@ struct StepArgs {
   float scale2;
 };
 constexpr int kStepWarps = 4;
+constexpr int kStepThreads = kStepWarps * 32;
 constexpr int kUnit = kStepWarps * 32;
 constexpr size_t kListBytes = 16384;  // of the scratch, for the list of unfinished heads
-constexpr int step_blocks(int row_blocks) { return row_blocks == 1 ? 3 : 2; }  // per SM
+// Blocks per SM. Eight rows: 3 with rings of 16 KB (64 caches of 8192, 16 heads
+// on 4 of 128: 91 us; 128 of 512, 8 on 8: 33) against 2 with 24 KB (91; 36).
+// Sixteen: 2 (32 of 16384, 16 on 1: 37 us) against 3, whose sums spill (58).
+constexpr int step_blocks(int eights) { return eights == 1 ? 3 : 2; }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -1042,8 +1046,25 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {  // an 8 x 8 matrix
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint4 load16(const bf *p, bool on) {
-  return on ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
+// Four 8 x 8 matrices of shared memory, the row addresses of matrix i in lanes
+// 8 i to 8 i + 7, as they are or transposed.
+template <bool TRANS>
+__device__ __forceinline__ void matrices(uint32_t at, uint32_t (&x)[4]) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(at)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(at)
+                 : "memory");
+}
+// 16 bytes to shared memory, or zeros (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const bf *src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
 }
 __device__ __forceinline__ int64_t cache_length(const StepArgs &p, int64_t b) {
   const int64_t n = p.lengths[b];
@@ -1051,23 +1072,41 @@ __device__ __forceinline__ int64_t cache_length(const StepArgs &p, int64_t b) {
 }
 __device__ __forceinline__ int units_of(int64_t n) { return (int)((n + kUnit - 1) / kUnit); }
 
+constexpr int kRingBytes = 16384;  // of a warp
+
 template <int DP, int NR>
-__global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
+__global__ void __launch_bounds__(kStepThreads, step_blocks(NR))
     attention_step_kernel(const StepArgs p) {
-  constexpr int KC = DP / 32;  // 16-byte pieces of a key row per lane
-  constexpr int VC = DP / 64;  // of a value row
-  constexpr int MT = DP / 16;  // output tiles
-  __shared__ float so[kStepWarps][NR * 8][DP + 4];
+  constexpr int CH = DP / 8;            // 16-byte pieces of a row
+  constexpr int kHalf = 16 * DP * 2;    // bytes of a stage's keys, or values
+  constexpr int kStages = kRingBytes / (2 * kHalf);
+  constexpr int MT = DP / 16;           // 16 columns at a time
+  extern __shared__ __align__(128) unsigned char rings[];
   __shared__ float sm[kStepWarps][NR * 8], sl[kStepWarps][NR * 8];
   __shared__ int run[2], upto[kStepWarps];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = lane >> 2, c = lane & 3;
   const int per = p.Hk * p.row_blocks;  // heads of a sequence
+  // A lane's part in copies, and the rows and pieces it addresses for the
+  // matrices. Piece x of row y is kept at place x ^ (y & 7) of its row, so that
+  // neither meets bank conflicts.
+  constexpr int kRows = 32 / CH;  // of a copy
+  const int crow = lane / CH, cpiece = lane % CH;
+  const uint32_t cswizzle = (cpiece ^ crow) * 16;
+  const uint32_t krow = ((lane & 7) + (lane >> 3 & 1) * 8) * DP * 2;
+  const uint32_t vrow = ((lane & 7) + (lane >> 4) * 8) * DP * 2 + kHalf;
+  const uint32_t kpiece = ((lane >> 4) ^ (lane & 7)) * 16, vpiece = ((lane >> 3 & 1) ^ (lane & 7)) * 16;
+  const uint32_t ring = tc::smem_addr(rings) + warp * kRingBytes;
+  // a run's sums, in the ring once it is empty
+  static_assert(NR * 8 * (DP + 4) * 4 <= kRingBytes, "the sums fit the ring");
+  auto so = [&](int w, int row, int d) -> float & {
+    return reinterpret_cast<float *>(rings + w * kRingBytes)[row * (DP + 4) + d];
+  };
   // count the units, a slice of the sequences to a thread, and find the
   // sequence in which this block's run starts
-  const int slice = (int)(p.B * threadIdx.x / kUnit);
-  const int slice_end = (int)(p.B * (threadIdx.x + 1) / kUnit);
+  const int slice = (int)(p.B * threadIdx.x / kStepThreads);
+  const int slice_end = (int)(p.B * (threadIdx.x + 1) / kStepThreads);
   int own = 0, sum_to;
   for (int x = slice; x < slice_end; ++x) own += units_of(cache_length(p, x)) * per;
   sum_to = own;
@@ -1092,7 +1131,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
   // nothing cached: zeros
   for (int64_t x = block; x < p.B; x += p.blocks)
     if (cache_length(p, x) == 0)
-      for (int y = threadIdx.x; y < p.Hq * p.D; y += kUnit)
+      for (int y = threadIdx.x; y < p.Hq * p.D; y += kStepThreads)
         p.o[x * p.Hq * p.D + y] = __float2bfloat16_rn(0.0f);
   __syncthreads();
   if (block >= blocks) return;
@@ -1113,80 +1152,73 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
     const int64_t from = (int64_t)t0 * kUnit, to = (int64_t)t1 * kUnit < n ? (int64_t)t1 * kUnit : n;
 
     // queries: row e of each block of 8, as the second operand
-    uint4 q[NR][KC];
+    uint32_t q[NR][MT][2];
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
-      for (int m = 0; m < KC; ++m) {
-        const int row = r0 + r * 8 + e, col = (m * 4 + c) * 8;
-        q[r][m] = load16(p.q + ((int64_t)b * p.Hq + g * p.group + row) * p.D + col,
-                         row < p.group && col < p.D);
-      }
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = r0 + r * 8 + e, col = m * 16 + i * 8 + c * 2;
+          const bf *at = p.q + ((int64_t)b * p.Hq + g * p.group + row) * p.D + col;
+          q[r][m][i] = row < p.group && col < p.D ? __ldg(reinterpret_cast<const uint32_t *>(at)) : 0u;
+        }
     const bf *k = p.k + b * p.kb + g * p.kh, *v = p.v + b * p.vb + g * p.vh;
+    // copy 16 positions; rows past the end and columns past D are zeros
+    auto fetch = [&](int64_t pos, int stage) {
+      if (pos < to) {
+        const int left = cpiece * 8 < p.D ? (int)(to - pos < 16 ? to - pos : 16) - crow : 0;
+        const bf *kp = k + (pos + crow) * p.kt + cpiece * 8;
+        const bf *vp = v + (pos + crow) * p.vt + cpiece * 8;
+        const uint32_t at = ring + stage * 2 * kHalf + crow * DP * 2;
+#pragma unroll
+        for (int j = 0; j < 16; j += kRows, kp += kRows * p.kt, vp += kRows * p.vt) {
+          const uint32_t dst = at + j * DP * 2 + (cswizzle ^ ((j & 7) * 16));
+          copy16(dst, j < left ? kp : k, j < left);
+          copy16(dst + kHalf, j < left ? vp : v, j < left);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     float acc[NR][MT][4] = {};
     float top[NR][2], sum[NR][2];
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
       for (int i = 0; i < 2; ++i) top[r][i] = -INFINITY, sum[r][i] = 0.0f;
-    for (int64_t pos = from + warp * 32; pos < to; pos += kStepWarps * 32) {
-      // keys: rows e and e + 8 of two runs of 16 positions
-      uint4 kk[2][2][KC];
+    constexpr int kStride = kStepWarps * 16;
+    int stage = 0;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int i = 0; i < kStages - 1; ++i) fetch(from + warp * 16 + i * kStride, i);
+    for (int64_t pos = from + warp * 16; pos < to; pos += kStride) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();  // these 16 are here, and every lane is done with the stage filled next
+      fetch(pos + (kStages - 1) * kStride, stage == 0 ? kStages - 1 : stage - 1);
+      const uint32_t keys = ring + stage * 2 * kHalf + krow, values = ring + stage * 2 * kHalf + vrow;
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+      float s[NR][4] = {};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int64_t x = pos + t * 16 + i * 8 + e;
+      for (int m = 0; m < MT; ++m) {
+        uint32_t x[4];
+        matrices<false>(keys + (kpiece ^ (m * 32)), x);
 #pragma unroll
-          for (int m = 0; m < KC; ++m)
-            kk[t][i][m] = load16(k + x * p.kt + (m * 4 + c) * 8, x < to && (m * 4 + c) * 8 < p.D);
-        }
-      // values: rows 2c, 2c + 1 (and + 8) of each run, pieces e (and e + 8)
-      uint4 vv[2][4][VC];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t x = pos + t * 16 + (i >> 1) * 8 + 2 * c + (i & 1);
-#pragma unroll
-          for (int m = 0; m < VC; ++m)
-            vv[t][i][m] = load16(v + x * p.vt + (m * 8 + e) * 8, x < to && (m * 8 + e) * 8 < p.D);
-        }
-      float s[NR][2][4];
-#pragma unroll
-      for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[r][t][i] = 0.0f;
-#pragma unroll
-          for (int m = 0; m < KC; ++m) {
-            const uint4 a = kk[t][0][m], d = kk[t][1][m], w = q[r][m];
-            mma16816(s[r][t], a.x, d.x, a.y, d.y, w.x, w.y);
-            mma16816(s[r][t], a.z, d.z, a.w, d.w, w.z, w.w);
-          }
-        }
-      // weights: rows 2c and 2c + 1, positions e and e + 8 of each run
-      uint32_t w[NR][2][2];
+        for (int r = 0; r < NR; ++r) mma16816(s[r], x[0], x[1], x[2], x[3], q[r][m][0], q[r][m][1]);
+      }
+      // weights: rows 2c and 2c + 1, positions e and e + 8. The maximum is
+      // raised only when a score passes it by 2^8 (or is the first).
+      uint32_t w[NR][2];
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        float hi[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[r][t][i] = pos + t * 16 + (i >> 1) * 8 + e < to ? s[r][t][i] * p.scale2 : -INFINITY;
-            hi[i & 1] = fmaxf(hi[i & 1], s[r][t][i]);
-          }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) hi[i] = fmaxf(hi[i], __shfl_xor_sync(kFull, hi[i], o));
-          hi[i] = fmaxf(hi[i], top[r][i]);
-        }
-        if (__any_sync(kFull, hi[0] > top[r][0] || hi[1] > top[r][1])) {
+        for (int i = 0; i < 4; ++i)
+          s[r][i] = pos + (i >> 1) * 8 + e < to ? s[r][i] * p.scale2 : -INFINITY;
+        float hi[2] = {fmaxf(s[r][0], s[r][2]), fmaxf(s[r][1], s[r][3])};
+        if (__any_sync(kFull, hi[0] > top[r][0] + 8.0f || hi[1] > top[r][1] + 8.0f)) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) hi[i] = fmaxf(hi[i], __shfl_xor_sync(kFull, hi[i], o));
+            hi[i] = fmaxf(hi[i], top[r][i]);
             const float f = hi[i] == -INFINITY ? 1.0f : ex2(top[r][i] - hi[i]);
             top[r][i] = hi[i];
             sum[r][i] *= f;
@@ -1197,36 +1229,23 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
         const float z[2] = {top[r][0] == -INFINITY ? 0.0f : top[r][0],
                             top[r][1] == -INFINITY ? 0.0f : top[r][1]};
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float x = ex2(s[r][t][2 * i] - z[0]), y = ex2(s[r][t][2 * i + 1] - z[1]);
-            sum[r][0] += x;
-            sum[r][1] += y;
-            w[r][t][i] = transposed(pack_bf16(x, y));
-          }
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        auto word = [&](int i, int m, int k) {
-          const uint4 x = vv[t][i][m];
-          return k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w;
-        };
-        auto couple = [&](int i, int m, int d) {  // element d of rows i and i + 1
-          return __byte_perm(word(i, m, d >> 1), word(i + 1, m, d >> 1), d & 1 ? 0x7632 : 0x5410);
-        };
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          // tile m: element m of each piece, and of the second pieces (64-wide
-          // heads: elements m and m + 4)
-          const int d0 = m, d1 = VC == 2 ? m : m + 4, p1 = VC == 2 ? 1 : 0;
-          const uint32_t a0 = couple(0, 0, d0), a1 = couple(0, p1, d1), a2 = couple(2, 0, d0),
-                         a3 = couple(2, p1, d1);
-#pragma unroll
-          for (int r = 0; r < NR; ++r) mma16816(acc[r][m], a0, a1, a2, a3, w[r][t][0], w[r][t][1]);
+        for (int i = 0; i < 2; ++i) {
+          const float x = ex2(s[r][2 * i] - z[0]), y = ex2(s[r][2 * i + 1] - z[1]);
+          sum[r][0] += x;
+          sum[r][1] += y;
+          w[r][i] = transposed(pack_bf16(x, y));
         }
       }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint32_t x[4];
+        matrices<true>(values + (vpiece ^ (m * 32)), x);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) mma16816(acc[r][m], x[0], x[1], x[2], x[3], w[r][0], w[r][1]);
+      }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
     // join the warps: rows 2c and 2c + 1 of each block
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -1243,8 +1262,8 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int d = VC == 2 ? (i >> 1) * 64 + e * 8 + m : e * 8 + m + (i >> 1) * 4;
-          so[warp][r * 8 + 2 * c + (i & 1)][d] = acc[r][m][i];
+          const int d = m * 16 + (i >> 1) * 8 + e;
+          so(warp, r * 8 + 2 * c + (i & 1), d) = acc[r][m][i];
         }
     }
     __syncthreads();
@@ -1255,7 +1274,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
       if (run_start(block - 1) <= head0)
         p.list[block] = {b, head, (int)(((int64_t)(head0 + of_head) * blocks - 1) / units)};
     }
-    for (int x = threadIdx.x; x < NR * 8 * DP; x += kStepWarps * 32) {
+    for (int x = threadIdx.x; x < NR * 8 * DP; x += kStepThreads) {
       const int row = x / DP, d = x % DP;
       if (r0 + row >= p.group || d >= p.D) continue;
       float m = sm[0][row];
@@ -1266,7 +1285,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
       for (int y = 0; y < kStepWarps; ++y) {
         const float f = sm[y][row] == -INFINITY ? 0.0f : ex2(sm[y][row] - m);
         l = fmaf(f, sl[y][row], l);
-        if (f != 0.0f) o = fmaf(f, so[y][row][d], o);
+        if (f != 0.0f) o = fmaf(f, so(y, row, d), o);
       }
       const int64_t at = b * p.Hq + g * p.group + r0 + row;
       if (whole) {
@@ -1282,62 +1301,97 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(NR))
 }
 
 // Join the heads that no block finished, blockIdx.x counting them in the list's
-// order: that of block i starts in run i - 1 and goes on in run i. Rows
-// blockIdx.y, blockIdx.y + gridDim.y, ...; four groups of threads take every
-// fourth run.
-__global__ void __launch_bounds__(512) attention_step_join_kernel(const StepArgs p, int rows) {
-  __shared__ float part[4][128][3];
-  __shared__ int upto[16], entry;
+// order: that of block i starts in run i - 1 and goes on in run i. SPLIT warps
+// share a row's runs; a lane has columns 2 lane, 2 lane + 1 and those + 64.
+constexpr int kJoinWarps = 8;
+template <int SPLIT>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    attention_step_join_kernel(const StepArgs p, int rows) {
+  __shared__ int upto[kJoinWarps], entry;
   pdl_wait();
   pdl_launch_dependents();
-  const int mine = threadIdx.x + 1;  // (a list has at most 3 * kSms entries)
-  const bool set_here = mine < p.blocks && p.list[mine].last != 0;
-  const unsigned ballot = __ballot_sync(kFull, set_here);
-  if ((threadIdx.x & 31) == 0) upto[threadIdx.x >> 5] = __popc(ballot);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // two entries of the list to a thread
+  const int mine = 2 * threadIdx.x + 1;
+  const bool a = mine < p.blocks && p.list[mine].last != 0;
+  const bool b = mine + 1 < p.blocks && p.list[mine + 1].last != 0;
+  const unsigned as = __ballot_sync(kFull, a), bs = __ballot_sync(kFull, b);
+  if (lane == 0) upto[warp] = __popc(as) + __popc(bs);
   if (threadIdx.x == 0) entry = 0;
   __syncthreads();
-  int before = __popc(ballot & ((1u << (threadIdx.x & 31)) - 1));
-  for (int w = 0; w < (int)threadIdx.x >> 5; ++w) before += upto[w];
-  if (set_here && before == (int)blockIdx.x) entry = mine;
+  const unsigned below = (1u << lane) - 1;
+  int before = __popc(as & below) + __popc(bs & below);
+  for (int w = 0; w < warp; ++w) before += upto[w];
+  if (a && before == (int)blockIdx.x) entry = mine;
+  if (b && before + a == (int)blockIdx.x) entry = mine + 1;
   __syncthreads();
   const int i = entry;
   if (i == 0) return;
   const Unfinished u = p.list[i];
-  const int d = threadIdx.x & 127, set = threadIdx.x >> 7, runs = u.last - i + 2;
-  const int g = u.head / p.row_blocks, r0 = u.head % p.row_blocks * rows;
-  // the first run's last place, then the others' first
-  auto place = [&](int k, int row) {
-    return p.partial + ((int64_t)(2 * (i - 1 + k) + (k == 0)) * rows + row) * (p.D + 2);
-  };
-  for (int row = blockIdx.y; row < rows && r0 + row < p.group; row += gridDim.y) {
-    float m = -INFINITY, l = 0.0f, o = 0.0f;
-#pragma unroll 4
-    for (int k = set; k < runs; k += 4) {
-      const float *in = place(k, row);
-      const float x = d < p.D ? in[d] : 0.0f, top = in[p.D], sum = in[p.D + 1];
-      const float high = fmaxf(m, top), z = high == -INFINITY ? 0.0f : high;
-      const float f = ex2(m - z), h = ex2(top - z);
-      l = fmaf(l, f, sum * h);
-      o = fmaf(o, f, x * h);
-      m = high;
-    }
-    part[set][d][0] = m, part[set][d][1] = l, part[set][d][2] = o;
-    __syncthreads();
-    if (set == 0 && d < p.D) {
+  const int runs = u.last - i + 2, g = u.head / p.row_blocks;
+  const int row = blockIdx.y * (kJoinWarps / SPLIT) + warp / SPLIT;
+  const int at = u.head % p.row_blocks * rows + row;  // of the group's query heads
+  const bool on = at < p.group;
+  float m = -INFINITY, l = 0.0f, o[4] = {};
+  // 32 runs at a time: their weights, one to a lane, then their sums
+  for (int k0 = warp % SPLIT; on && k0 < runs; k0 += 32 * SPLIT) {
+    // the first run's last place, then the others' first
+    auto place = [&](int k) {
+      return p.partial + ((int64_t)(2 * (i - 1 + k) + (k == 0)) * rows + row) * (p.D + 2);
+    };
+    const int k = k0 + lane * SPLIT;
+    const float2 own = k < runs ? *reinterpret_cast<const float2 *>(place(k) + p.D)
+                                : make_float2(-INFINITY, 0.0f);
+    float high = own.x;
 #pragma unroll
-      for (int k = 1; k < 4; ++k) m = fmaxf(m, part[k][d][0]);
-      const float z = m == -INFINITY ? 0.0f : m;
-      l = o = 0.0f;
+    for (int x = 16; x > 0; x >>= 1) high = fmaxf(high, __shfl_xor_sync(kFull, high, x));
+    high = fmaxf(high, m);
+    const float z = high == -INFINITY ? 0.0f : high, f = ex2(m - z), w = ex2(own.x - z);
+    m = high;
+    float t = own.y * w;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float f = ex2(part[k][d][0] - z);
-        l = fmaf(part[k][d][1], f, l);
-        o = fmaf(part[k][d][2], f, o);
-      }
-      p.o[((int64_t)u.b * p.Hq + g * p.group + r0 + row) * p.D + d] = __float2bfloat16_rn(o / l);
+    for (int x = 16; x > 0; x >>= 1) t += __shfl_xor_sync(kFull, t, x);
+    l = fmaf(l, f, t);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] *= f;
+    const int n = (runs - k0 + SPLIT - 1) / SPLIT < 32 ? (runs - k0 + SPLIT - 1) / SPLIT : 32;
+#pragma unroll 8
+    for (int y = 0; y < n; ++y) {
+      const float h = __shfl_sync(kFull, w, y);
+      const float *in = place(k0 + y * SPLIT);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (x * 64 + 2 * lane < p.D) {
+          const float2 q = *reinterpret_cast<const float2 *>(in + x * 64 + 2 * lane);
+          o[2 * x] = fmaf(h, q.x, o[2 * x]);
+          o[2 * x + 1] = fmaf(h, q.y, o[2 * x + 1]);
+        }
     }
-    __syncthreads();
   }
+  if constexpr (SPLIT > 1) {  // the row's warps, in order
+    static_assert(SPLIT == kJoinWarps, "a block has one row");
+    __shared__ float parts[SPLIT][32][4], stats[SPLIT][2];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) parts[warp][lane][x] = o[x];
+    if (lane == 0) stats[warp][0] = m, stats[warp][1] = l;
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 1; w < SPLIT; ++w) m = fmaxf(m, stats[w][0]);
+    const float z = m == -INFINITY ? 0.0f : m;
+    l = o[0] = o[1] = o[2] = o[3] = 0.0f;
+    for (int w = 0; w < SPLIT; ++w) {
+      const float f = ex2(stats[w][0] - z);
+      l = fmaf(f, stats[w][1], l);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] = fmaf(f, parts[w][lane][x], o[x]);
+    }
+  }
+  bf *out = p.o + ((int64_t)u.b * p.Hq + g * p.group + at) * p.D;
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    if (on && x * 64 + 2 * lane < p.D)
+      *reinterpret_cast<uint32_t *>(out + x * 64 + 2 * lane) =
+          pack_bf16(o[2 * x] / l, o[2 * x + 1] / l);
 }
 
 // Query heads to a row block, and blocks of a call: no more than run at once.
@@ -1358,15 +1412,24 @@ int step_grid(int64_t B, int64_t S, int64_t Hq, int64_t Hk) {
 
 template <int DP, int NR>
 cudaError_t launch_step(const StepArgs &a, cudaStream_t st) {
-  const cudaError_t e = launch_ex(attention_step_kernel<DP, NR>, dim3((unsigned)a.blocks),
-                                  dim3(kUnit), 0, st, true, a);
+  constexpr size_t smem = (size_t)kStepWarps * kRingBytes;
+  cudaError_t e = allow_dynamic_smem<attention_step_kernel<DP, NR>>(smem);
+  if (e == cudaSuccess)
+    e = launch_ex(attention_step_kernel<DP, NR>, dim3((unsigned)a.blocks),
+                  dim3(kStepThreads), smem, st,
+                  true, a);
   if (e != cudaSuccess || a.blocks == 1) return e;
-  // few heads over many blocks: a block to each of a head's rows
+  // A warp to each of a head's rows, or, where a head is left in more than 8
+  // runs, a block: with 4 caches of 65536, 16 heads on 1 (76 runs to a row) 11
+  // us, and 22 by four warps; with 32 of 16384, 24 on 2 (5 runs) warps take 9
+  // us and one block that goes over the rows 28.
   const int64_t heads = a.B * a.Hk * a.row_blocks, most = a.blocks - 1;
-  const bool wide = heads * 8 <= a.blocks;
-  return launch_ex(attention_step_join_kernel,
-                   dim3((unsigned)(heads < most ? heads : most), wide ? (unsigned)NR * 8 : 1u),
-                   dim3(512), 0, st, true, a, NR * 8);
+  const unsigned x = (unsigned)(heads < most ? heads : most);
+  const dim3 threads(kJoinWarps * 32);
+  return heads * 8 < a.blocks
+             ? launch_ex(attention_step_join_kernel<kJoinWarps>, dim3(x, NR * 8), threads, 0, st, true,
+                         a, NR * 8)
+             : launch_ex(attention_step_join_kernel<1>, dim3(x, NR), threads, 0, st, true, a, NR * 8);
 }
 
 // Token and head strides that 16-byte loads can use.
@@ -1592,8 +1655,8 @@ rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_ba
       !product_fits(B, v_batch_stride < 0 ? 0 : v_batch_stride, 1) || k_batch_stride < 0 ||
       v_batch_stride < 0)
     return RLCS_ERR_INVALID_ARG;
-  static_assert(kSms * 3 <= 512 && kSms * 3 * sizeof(Unfinished) <= kListBytes,
-                "an entry to each block, a thread of the join to each entry");
+  static_assert(kSms * 3 <= 2 * kJoinWarps * 32 && kSms * 3 * sizeof(Unfinished) <= kListBytes,
+                "an entry to each block, a thread of the join to two");
   if (B == 0) return RLCS_OK;
   if (!q || !lengths || !out || (S > 0 && (!k_cache || !v_cache))) return RLCS_ERR_INVALID_ARG;
   const rlcs_status su[] = {strides_usable(k_cache, k_position_stride, k_head_stride, S, Hk),
