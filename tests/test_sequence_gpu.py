@@ -551,3 +551,54 @@ def test_attention_later_tokens_stay_masked(rl, D, at):
     got = rl.rlcs_attention(q, k, v2, cu)
     assert torch.equal(got[:n - 1], want[:n - 1])
     assert torch.isnan(got[n - 1, :2, 3]).all() or at == n - 1
+
+
+@pytest.mark.parametrize("count,longest,D", [(128, 3, 64), (129, 200, 64), (700, 5, 128),
+                                             (1500, 2, 64)])
+def test_attention_many_sequences(rl, count, longest, D):
+    # more sequences than a warp, and than a block, has lanes; many are empty
+    g = gen(count)
+    lens = [int(x) for x in torch.randint(0, longest + 1, (count,), generator=g)]
+    n, Hq, Hk, bf = sum(lens), 2, 1, torch.bfloat16
+    q, k, v, dout = (rand(g, n, h, D, dtype=bf) for h in (Hq, Hk, Hk, Hq))
+    cu, scale = bounds(lens).cuda(), D ** -0.5
+    out, lse = rl.rlcs_attention(*cuda(q, k, v), cu, return_lse=True)
+    want, wlse, slack = ref.attention(q, k, v, lens, scale)
+    close("out", out, want, slack)
+    close("lse", lse, wlse)
+    got = rl.rlcs_attention_backward(dout.cuda(), *cuda(q, k, v), out, lse, cu)
+    grads, slacks = ref.attention_backward(dout, q, k, v, lens, scale)
+    for name, a, b, s in zip(("dq", "dk", "dv"), got, grads, slacks):
+        close(name, a, b, s)
+
+
+@pytest.mark.parametrize("B,S,Hq,Hk,D", [(1, 20000, 16, 1, 128), (3, 9000, 24, 1, 72),
+                                         (300, 260, 4, 2, 64), (40, 700, 8, 8, 128),
+                                         (600, 3, 2, 1, 64)])
+def test_attention_step_runs(rl, B, S, Hq, Hk, D):
+    # heads cut into a few runs and into many, several heads to a run, and
+    # more sequences than threads, some without entries
+    g = gen(B + S)
+    bf = torch.bfloat16
+    q, kc, vc = (rand(g, *shape, dtype=bf) for shape in ((B, Hq, D), (B, S, Hk, D), (B, S, Hk, D)))
+    lengths = torch.randint(0, S + 1, (B,), generator=g, dtype=torch.int32)
+    lengths[0] = S
+    lengths[B // 2 + 1:B // 2 + 4] = 0
+    want, slack = ref.attention_step(q, kc, vc, lengths, D ** -0.5)
+    out = rl.rlcs_attention_step(*cuda(q, kc, vc, lengths))
+    close("out", out, want, slack)
+    assert torch.equal(out, rl.rlcs_attention_step(*cuda(q, kc, vc, lengths)))
+
+
+def test_attention_step_large_scores(rl):
+    # one entry far ahead of the rest, anywhere in the cache: the running
+    # maximum moves by hundreds within a run and between runs
+    B, S, Hq, D = 1, 3000, 4, 64
+    for hot in (0, 17, 1500, 2999):
+        q = torch.full((B, Hq, D), 4.0, dtype=torch.bfloat16)
+        kc = torch.full((B, S, 1, D), -4.0, dtype=torch.bfloat16)
+        kc[:, hot] = 4.0
+        vc = rand(gen(hot), B, S, 1, D, dtype=torch.bfloat16)
+        lengths = torch.tensor([S], dtype=torch.int32)
+        want, slack = ref.attention_step(q, kc, vc, lengths, D ** -0.5)
+        close("out", rl.rlcs_attention_step(*cuda(q, kc, vc, lengths)), want, slack)
