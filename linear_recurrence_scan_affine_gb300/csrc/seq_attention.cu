@@ -21,7 +21,10 @@ constexpr int kTile = 128;
 
 // Rows of the tiles a block walks over: with heads up to 64 wide half as many,
 // so that two or three blocks share an SM's tensor memory and hide each
-// other's waits, which short sequences are made of.
+// other's waits, which short sequences are made of (packed episodes of up to
+// 1024 steps, 12 heads of 64 on 4, forward and gradient: 273 us against 304
+// with 128). Wider heads keep 128 (one sequence of 16384, 8 heads of 128 on 1,
+// forward: 414 us against 514 with 64).
 template <int DP>
 constexpr int inner() {
   return DP == 64 ? 64 : 128;
@@ -147,14 +150,18 @@ __device__ __forceinline__ void write_row(uint32_t acc, bf *out, int left, float
 }
 
 // ---------------------------------------------------------------------------
-// Forward: a block per query tile and head, two blocks per SM.
+// Forward: a block per query tile and head, two blocks per SM (three with heads
+// up to 64 wide).
 //
-// Warps 0..7 turn scores into weights, two threads to a query row (key columns
-// 0..63 and 64..127; they exchange maxima through shared memory): 16 such
-// warps on an SM hide each other's latencies, where 8 that held whole rows
-// spilled registers. Warp 8 copies tiles in; warp 9 issues the products. Per key tile, in tensor memory:
-//   S = Q K^T (128 fp32 columns), P over S (64 columns of bf16 pairs),
+// Warps 0..7 turn scores into weights, two threads to a query row (the lower
+// and the upper half of the key columns; they exchange maxima through shared
+// memory): 16 such warps on an SM hide each other's latencies, where 8 that
+// held whole rows spilled registers. Warp 8 copies tiles in; warp 9 issues the
+// products. Per key tile, in tensor memory:
+//   S = Q K^T (128 or 64 fp32 columns), P over S (bf16 pairs),
 //   O += P V (DP fp32 columns).
+// P is rounded to bf16, the type the product takes; its sum is of the unrounded
+// weights in fp32.
 // Products run in the order they are issued, so the next tile's S follows
 // the product that reads P. While one block's weights are formed the other
 // block's products keep the tensor cores busy. Key tiles run from the
@@ -162,6 +169,12 @@ __device__ __forceinline__ void write_row(uint32_t acc, bf *out, int left, float
 // raised only when it grows by more than 2^8 (weights then stay within fp32
 // and bf16 range, and the final division removes the common factor), so O is
 // rarely rescaled.
+//
+// One sequence of 16384, 8 heads of 128 on 1: 414 us, 1.33 PFLOP/s (a library
+// matrix product reaches 1.95), the tensor pipe busy 61% of the time: bound by
+// the chain from a tile's scores to its weights and on to the product, which
+// two blocks cover only in part. 40 x 600, 12 heads of 64 on 4: 75 us, most of
+// it starting and ending blocks of two to ten key tiles.
 // ---------------------------------------------------------------------------
 // The swizzle of tiles in shared memory counts from 1024-byte boundaries;
 // `raw` is declared on one. A block that finds it elsewhere does nothing.
@@ -336,7 +349,8 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
       tc::fence_after_sync();
       uint32_t s[HC];
 #pragma unroll
-      for (int c = 0; c < HC; c += 32) tc::ld32(mine + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
+      for (int c = 0; c < HC; c += 32)
+        tc::ld32(mine + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
       tc::wait_ld();
       const int last = t.first + r - first_key(it) - half * HC;  // the last column this row sees
       if (diagonal(it)) {
@@ -420,13 +434,19 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
 // tiles. Recomputing costs two of seven products, and buys results without
 // atomics: every sum has one fixed order.
 //
-// Blocks of 576 threads, one per SM (all 512 columns of tensor memory). Warps
-// 0..15 work on the scores, four threads to a row of a tile with 32 columns
-// each; warp 16 copies tiles; warp 17 issues products. A thread's bf16 piece
-// goes over its own fp32 columns, so the pieces of an operand start 32
-// columns apart. dS is rounded to bf16 for its product, as P is; on the
-// diagonal tile, whose short rows carry most of the gradient, the rounding's
-// remainder goes into the other half of those columns and is multiplied too.
+// Blocks of 576 threads, one per SM (all 512 columns of tensor memory); heads
+// up to 64 wide, 320 threads, two per SM. Four warps to 32 columns of a tile
+// work on the scores, a row and 32 columns to a thread; one more warp copies
+// tiles and one issues products. A thread's bf16 piece goes over its own fp32
+// columns, so the pieces of an operand start 32 columns apart. dS is rounded to
+// bf16 for its product, as P is; on the diagonal tile, whose short rows carry
+// most of the gradient, the rounding's remainder goes into the other half of
+// those columns and is multiplied too.
+//
+// 2 x 4096, 16 heads of 128 on 4: delta 14 us (4.7 TB/s), dk and dv 198 us (1.39
+// PFLOP/s with the recomputed product, the tensor pipe busy 68%), dq 167 us
+// (1.24, 57%). Both are bound by the chain scores, weights, product within a
+// step, of which products of the steps before and after cover part.
 // ---------------------------------------------------------------------------
 struct BackwardArgs {
   const int32_t *cu;
@@ -1063,7 +1083,8 @@ __device__ __forceinline__ void matrices(uint32_t at, uint32_t (&x)[4]) {
 }
 // 16 bytes to shared memory, or zeros (nothing is read then).
 __device__ __forceinline__ void copy16(uint32_t dst, const bf *src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(on ? 16 : 0)
                : "memory");
 }
 __device__ __forceinline__ int64_t cache_length(const StepArgs &p, int64_t b) {
@@ -1096,7 +1117,8 @@ __global__ void __launch_bounds__(kStepThreads, step_blocks(NR))
   const uint32_t cswizzle = (cpiece ^ crow) * 16;
   const uint32_t krow = ((lane & 7) + (lane >> 3 & 1) * 8) * DP * 2;
   const uint32_t vrow = ((lane & 7) + (lane >> 4) * 8) * DP * 2 + kHalf;
-  const uint32_t kpiece = ((lane >> 4) ^ (lane & 7)) * 16, vpiece = ((lane >> 3 & 1) ^ (lane & 7)) * 16;
+  const uint32_t kpiece = ((lane >> 4) ^ (lane & 7)) * 16;
+  const uint32_t vpiece = ((lane >> 3 & 1) ^ (lane & 7)) * 16;
   const uint32_t ring = tc::smem_addr(rings) + warp * kRingBytes;
   // a run's sums, in the ring once it is empty
   static_assert(NR * 8 * (DP + 4) * 4 <= kRingBytes, "the sums fit the ring");
@@ -1149,7 +1171,8 @@ __global__ void __launch_bounds__(kStepThreads, step_blocks(NR))
     const int t1 = t0 + (end - unit) < of_head ? t0 + (end - unit) : of_head;
     unit += t1 - t0;
     const int g = head / p.row_blocks, r0 = head % p.row_blocks * (NR * 8);
-    const int64_t from = (int64_t)t0 * kUnit, to = (int64_t)t1 * kUnit < n ? (int64_t)t1 * kUnit : n;
+    const int64_t from = (int64_t)t0 * kUnit;
+    const int64_t to = (int64_t)t1 * kUnit < n ? (int64_t)t1 * kUnit : n;
 
     // queries: row e of each block of 8, as the second operand
     uint32_t q[NR][MT][2];
@@ -1161,7 +1184,8 @@ __global__ void __launch_bounds__(kStepThreads, step_blocks(NR))
         for (int i = 0; i < 2; ++i) {
           const int row = r0 + r * 8 + e, col = m * 16 + i * 8 + c * 2;
           const bf *at = p.q + ((int64_t)b * p.Hq + g * p.group + row) * p.D + col;
-          q[r][m][i] = row < p.group && col < p.D ? __ldg(reinterpret_cast<const uint32_t *>(at)) : 0u;
+          q[r][m][i] =
+              row < p.group && col < p.D ? __ldg(reinterpret_cast<const uint32_t *>(at)) : 0u;
         }
     const bf *k = p.k + b * p.kb + g * p.kh, *v = p.v + b * p.vb + g * p.vh;
     // copy 16 positions; rows past the end and columns past D are zeros
@@ -1194,7 +1218,8 @@ __global__ void __launch_bounds__(kStepThreads, step_blocks(NR))
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();  // these 16 are here, and every lane is done with the stage filled next
       fetch(pos + (kStages - 1) * kStride, stage == 0 ? kStages - 1 : stage - 1);
-      const uint32_t keys = ring + stage * 2 * kHalf + krow, values = ring + stage * 2 * kHalf + vrow;
+      const uint32_t keys = ring + stage * 2 * kHalf + krow;
+      const uint32_t values = ring + stage * 2 * kHalf + vrow;
       stage = stage == kStages - 1 ? 0 : stage + 1;
       float s[NR][4] = {};
 #pragma unroll
@@ -1427,9 +1452,10 @@ cudaError_t launch_step(const StepArgs &a, cudaStream_t st) {
   const unsigned x = (unsigned)(heads < most ? heads : most);
   const dim3 threads(kJoinWarps * 32);
   return heads * 8 < a.blocks
-             ? launch_ex(attention_step_join_kernel<kJoinWarps>, dim3(x, NR * 8), threads, 0, st, true,
-                         a, NR * 8)
-             : launch_ex(attention_step_join_kernel<1>, dim3(x, NR), threads, 0, st, true, a, NR * 8);
+             ? launch_ex(attention_step_join_kernel<kJoinWarps>, dim3(x, NR * 8), threads, 0, st,
+                         true, a, NR * 8)
+             : launch_ex(attention_step_join_kernel<1>, dim3(x, NR), threads, 0, st, true, a,
+                         NR * 8);
 }
 
 // Token and head strides that 16-byte loads can use.
@@ -1441,8 +1467,8 @@ rlcs_status strides_usable(const void *p, int64_t ts, int64_t hs, int64_t tokens
 
 bool attn_sizes(int64_t sequences, int64_t tokens, int64_t Hq, int64_t Hk, int64_t D, double scale,
                 rlcs_dtype t) {
-  return sequences >= 0 && tokens >= 0 && tokens <= INT32_MAX && sequences < INT32_MAX - 1024 && Hq > 0 &&
-         Hk > 0 && Hq % Hk == 0 && D > 0 && D <= 128 && D % 8 == 0 && t == RLCS_BF16 &&
+  return sequences >= 0 && tokens >= 0 && tokens <= INT32_MAX &&
+         sequences < INT32_MAX - 1024 && Hq > 0 && Hk > 0 && Hq % Hk == 0 && D > 0 && D <= 128 && D % 8 == 0 && t == RLCS_BF16 &&
          scale >= 1e-30 && scale <= 1e30 && product_fits(tokens, Hq, D) &&
          tile_bound(sequences, tokens) * Hq < (int64_t)INT32_MAX &&
          tokens * Hq < (int64_t)4 * INT32_MAX;
@@ -1454,12 +1480,14 @@ cudaError_t launch_forward(const CUtensorMap &mq, const CUtensorMap &mk, const C
   constexpr size_t smem = sizeof(ForwardSmem<DP>);
   const cudaError_t e = allow_dynamic_smem<attention_kernel<DP>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_ex(attention_kernel<DP>, dim3((unsigned)grid), dim3(320), smem, st, true, mq, mk, mv,
-                   a);
+  return launch_ex(attention_kernel<DP>, dim3((unsigned)grid), dim3(320), smem, st, true, mq, mk,
+                   mv, a);
 }
 
 // Blocks that share a group's query heads: the fewest, of the powers of two
-// that divide the group, that make up a block per SM.
+// that divide the group, that make up a block per SM. (8192 tokens, 8 heads on 1
+// of 128, 64 key tiles: 306 us with 4 to a tile, 1117 with one; 2 x 4096, 16 on
+// 4, 256 tiles: 222 with one against 289 with 4.)
 int group_split(int64_t blocks, int group) {
   int split = 1;
   while (split < 8 && group % (2 * split) == 0 && blocks * split < kSms) split *= 2;

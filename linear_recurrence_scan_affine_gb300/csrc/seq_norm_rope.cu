@@ -63,8 +63,11 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Any head width: a warp per head, lanes over rotation pairs, then over the
-// elements past the rotated ones.
+// Any head width, stride and alignment: a warp per head, lanes over rotation
+// pairs, then over the elements past the rotated ones. Its loads are of single
+// elements and the head is read twice: 32768 tokens, 16 + 4 heads of 128, bf16,
+// forward and gradient took 643 us through a kernel of this shape, 147 through
+// the paired lanes below.
 template <class E, bool BACK>
 __global__ void __launch_bounds__(256) head_any_kernel(const HeadArgs p) {
   extern __shared__ float sums[];  // backward: [8 warps][2][D]
@@ -147,7 +150,9 @@ __global__ void __launch_bounds__(256) head_any_kernel(const HeadArgs p) {
 // four rotation pairs, so nothing but the mean crosses lanes. A group of D/8
 // lanes takes a few heads of one token at a time, whose cosines and sines it
 // reads once; the first blocks take queries and the rest keys, so a block has
-// one weight vector and, in the gradient, one set of sums.
+// one weight vector and, in the gradient, one set of sums. Bound by memory: one
+// read and one write of every head; 32768 tokens, 16 + 4 heads of 128, bf16,
+// forward and gradient 147 us for 840 MB, 5.7 TB/s (a copy reaches 6.7).
 // ---------------------------------------------------------------------------
 // Four elements of a head, loaded and stored together.
 template <class E>
@@ -371,7 +376,8 @@ __global__ void __launch_bounds__(256, BACK ? 2 : 4) head_pairs_kernel(const Hea
   }
 }
 
-// Sum the blocks' partial weight gradients, in block order: rows [0, split)
+// Sum the blocks' partial weight gradients in one fixed order, for the same bits
+// every time: 3 us for 304 blocks and D = 128. Rows [0, split)
 // of `partial` belong to the queries' weight and the rest to the keys', or,
 // with split = 0, the two halves of every 2 D wide row.
 __global__ void __launch_bounds__(1024)
