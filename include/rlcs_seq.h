@@ -26,8 +26,10 @@
  *            the last dimension is contiguous, so a head tensor can be a view
  *            of a fused projection. Arrays without strides are contiguous.
  * Masks.     uint8, set when nonzero.
- * Empty.     A call on zero tokens or zero sequences does nothing and returns
- *            RLCS_OK; negative sizes are RLCS_ERR_INVALID_ARG.
+ * Empty.     Norm and attention on zero tokens or zero sequences do nothing and
+ *            return RLCS_OK (weight gradients become zero); the recurrence needs
+ *            at least one sequence, step and channel. Negative sizes are
+ *            RLCS_ERR_INVALID_ARG.
  * Aliasing.  Outputs must not overlap any input or each other (inputs may
  *            overlap inputs), but rlcs_gated_step's new_state may be state.
  * Order.     No result depends on the order of atomics: repeated calls on
