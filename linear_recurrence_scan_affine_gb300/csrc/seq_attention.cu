@@ -171,10 +171,13 @@ __device__ __forceinline__ void write_row(uint32_t acc, bf *out, int left, float
 // rarely rescaled.
 //
 // One sequence of 16384, 8 heads of 128 on 1: 414 us, 1.33 PFLOP/s (a library
-// matrix product reaches 1.95), the tensor pipe busy 61% of the time: bound by
-// the chain from a tile's scores to its weights and on to the product, which
-// two blocks cover only in part. 40 x 600, 12 heads of 64 on 4: 75 us, most of
-// it starting and ending blocks of two to ten key tiles.
+// matrix product reaches 1.95), the tensor pipe busy 61% of the time. S takes
+// 830 clocks where PV takes 510: both its operands come from shared memory, 128
+// bytes a clock at full rate, which is all that an SM can read, while copies
+// come in. The rest is the chain from a tile's scores to its weights (1100
+// clocks) and on to the product, which two blocks cover only in part. 40 x 600,
+// 12 heads of 64 on 4: 75 us, most of it starting and ending blocks of two to
+// ten key tiles.
 // ---------------------------------------------------------------------------
 // The swizzle of tiles in shared memory counts from 1024-byte boundaries;
 // `raw` is declared on one. A block that finds it elsewhere does nothing.
