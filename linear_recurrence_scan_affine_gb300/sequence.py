@@ -71,15 +71,23 @@ _scratch_cache = {}
 
 
 def _scratch(need, dev, stream):
+    """Address and size of the buffer, of `need` bytes at least."""
     key = (dev, stream)
-    with _b._ws_lock:
-        ws = _scratch_cache.get(key)
-        if ws is None or ws.numel() < need:
-            # on the current stream, which is the one that will use it
-            ws = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device="cuda:%d" % dev)
-            ws[:64].zero_()
-            _scratch_cache[key] = ws
-    return ws.data_ptr(), ws.numel()
+    entry = _scratch_cache.get(key)
+    if entry is None or entry[2] < need:
+        with _b._ws_lock:
+            entry = _scratch_cache.get(key)
+            if entry is None or entry[2] < need:
+                # on the current stream, which is the one that will use it
+                ws = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device="cuda:%d" % dev)
+                ws[:64].zero_()
+                entry = _scratch_cache[key] = (ws, ws.data_ptr(), ws.numel())
+    return entry[1], entry[2]
+
+
+@functools.lru_cache(maxsize=256)
+def _scratch_bytes(name, *sizes):
+    return _fn[name](*sizes)
 
 
 def check_scratch():
@@ -87,7 +95,7 @@ def check_scratch():
     with _b._ws_lock:
         items = list(_scratch_cache.values())
     for ws in items:
-        _b._check(_lib.rlcs_check_status(_b._ptr(ws), None), "rlcs_check_status")
+        _b._check(_lib.rlcs_check_status(_b._ptr(ws[0]), None), "rlcs_check_status")
 
 
 def _streamed(f):
@@ -308,7 +316,7 @@ def rlcs_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, si
     dqw = torch.empty(D, dtype=torch.float32, device=q.device)
     dkw = torch.empty(D, dtype=torch.float32, device=q.device)
     stream = _raw_stream(dev)
-    ws, wsb = _scratch(_fn["rlcs_qk_norm_rope_scratch_bytes"](D) + 64, dev, stream)
+    ws, wsb = _scratch(_scratch_bytes("rlcs_qk_norm_rope_scratch_bytes", D) + 64, dev, stream)
     _call("rlcs_qk_norm_rope_backward", dq_out.data_ptr(), dk_out.data_ptr(), *arrays,
           dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), *sizes,
           1 if interleaved else 0, eps, _DTYPES[q.dtype], ws + 64, wsb - 64, stream)
@@ -349,7 +357,7 @@ def rlcs_attention(q, k, v, cu_seqlens, scale=None, return_lse=False):
     out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
     lse = torch.empty((Hq, n), dtype=torch.float32, device=q.device) if return_lse else None
     stream = _raw_stream(dev)
-    ws, wsb = _scratch(_fn["rlcs_attention_scratch_bytes"](n, Hq), dev, stream)
+    ws, wsb = _scratch(_scratch_bytes("rlcs_attention_scratch_bytes", n, Hq), dev, stream)
     _call("rlcs_attention", *arrays, keep[3].data_ptr(), out.data_ptr(), _at(lse), *sizes,
           D ** -0.5 if scale is None else scale, _DTYPES[q.dtype], ws, wsb, stream)
     return (out, lse) if return_lse else out
@@ -370,7 +378,7 @@ def rlcs_attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=None):
     dk = torch.empty((n, Hk, D), dtype=q.dtype, device=q.device)
     dv = torch.empty((n, Hk, D), dtype=q.dtype, device=q.device)
     stream = _raw_stream(dev)
-    ws, wsb = _scratch(_fn["rlcs_attention_scratch_bytes"](n, Hq), dev, stream)
+    ws, wsb = _scratch(_scratch_bytes("rlcs_attention_scratch_bytes", n, Hq), dev, stream)
     _call("rlcs_attention_backward", dout.data_ptr(), *arrays, out.data_ptr(), lse.data_ptr(),
           keep[3].data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *sizes,
           D ** -0.5 if scale is None else scale, _DTYPES[q.dtype], ws, wsb, stream)
@@ -381,13 +389,14 @@ def _cache(t, name, B, D, dev):
     _need(t, name, 4, (torch.bfloat16,))
     if t.get_device() != dev:
         raise ValueError("%s must be on cuda:%d, got %s" % (name, dev, t.device))
-    if t.shape[0] != B or t.shape[3] != D:
+    batch, positions, heads, width = t.shape
+    if batch != B or width != D:
         raise ValueError("%s must have shape (%d, positions, heads, %d)" % (name, B, D))
     b, s, h, d = t.stride()
     # a dimension of one element has no stride to speak of
-    if t.shape[2] == 1:
+    if heads == 1:
         h = 8
-    if t.shape[1] <= 1:
+    if positions <= 1:
         s = 8
     if B <= 1:
         b = 8
@@ -420,7 +429,8 @@ def rlcs_attention_step(q, k_cache, v_cache, lengths, scale=None, out=None):
     lengths = _like(lengths, "lengths", (B,), torch.int32, dev)
     o = torch.empty_like(q) if out is None else _b._out(out, "out", q)
     stream = _raw_stream(dev)
-    ws, wsb = _scratch(_fn["rlcs_attention_step_scratch_bytes"](B, S, Hq, Hk, D) + 64, dev, stream)
+    need = _scratch_bytes("rlcs_attention_step_scratch_bytes", B, S, Hq, Hk, D) + 64
+    ws, wsb = _scratch(need, dev, stream)
     _call("rlcs_attention_step", q.data_ptr(), *ks, *vs, lengths.data_ptr(), o.data_ptr(), B, S,
           Hq, Hk, D, D ** -0.5 if scale is None else scale, _DTYPES[q.dtype], ws + 64, wsb - 64,
           stream)
