@@ -39,21 +39,25 @@ struct Tile {
   int lo, len, first;  // the sequence's first token and length; the tile's first row in it
 };
 struct TileSearch {
-  int64_t upto[18];  // tiles of each warp's sequences
+  unsigned upto[18];  // tiles of each warp's sequences
   Tile tile;
   int found;
 };
 constexpr int kWarpSearch = 128;
 
-__device__ __forceinline__ Tile sequence(const int32_t *cu, int s, int tokens) {
-  const int a = cu[s] < 0 ? 0 : cu[s], b = cu[s + 1] < tokens ? cu[s + 1] : tokens;
+// The sequence between two bounds.
+__device__ __forceinline__ Tile between(int a, int b, int tokens) {
+  a = a < 0 ? 0 : a;
+  b = b < tokens ? b : tokens;
   return {a, b > a ? b - a : 0, 0};
 }
-__device__ __forceinline__ int tiles_of(const Tile &t) { return (t.len + kTile - 1) / kTile; }
+__device__ __forceinline__ unsigned tiles_of(const Tile &t) { return (t.len + kTile - 1) / kTile; }
 // The whole block calls this; `searcher` is the warp that goes on with the
-// result at once, the others read it after the block's next barrier.
-__device__ __forceinline__ void find_tile(const int32_t *cu, int sequences, int tokens, int index,
-                                          int searcher, TileSearch &sm) {
+// result at once, the others read it after the block's next barrier. (Tiles of
+// bounds that are not in order may be counted past 32 bits: what is found then
+// is still a tile inside the arrays.)
+__device__ __forceinline__ void find_tile(const int32_t *cu, int sequences, int tokens,
+                                          unsigned index, int searcher, TileSearch &sm) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool few = sequences <= kWarpSearch;
   if (few && warp != searcher) return;
@@ -61,13 +65,21 @@ __device__ __forceinline__ void find_tile(const int32_t *cu, int sequences, int 
   const int at = slice * (few ? lane : (int)threadIdx.x);
   const int end = at < sequences - slice ? at + slice : sequences;
   if (warp == searcher && lane == 0) sm.found = 0;
-  int64_t own = 0;
-#pragma unroll 4
-  for (int s = at; s < end; ++s) own += tiles_of(sequence(cu, s, tokens));
-  int64_t upto = own;
+  constexpr int kOwn = kWarpSearch / 32;
+  int bound[kOwn + 1];  // one round of loads
+  unsigned own = 0;
+  if (few) {
+#pragma unroll
+    for (int j = 0; j <= kOwn; ++j) bound[j] = cu[at + j < end ? at + j : end];
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) own += tiles_of(between(bound[j], bound[j + 1], tokens));
+  } else {
+    for (int s = at; s < end; ++s) own += tiles_of(between(cu[s], cu[s + 1], tokens));
+  }
+  unsigned upto = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t n = __shfl_up_sync(kFull, upto, o);
+    const unsigned n = __shfl_up_sync(kFull, upto, o);
     if (lane >= o) upto += n;
   }
   if (!few) {
@@ -77,19 +89,28 @@ __device__ __forceinline__ void find_tile(const int32_t *cu, int sequences, int 
   } else {
     __syncwarp();
   }
-  int64_t left = index - (upto - own);
-  if (left >= 0 && left < own)
-    for (int s = at; s < end; ++s) {
-      Tile x = sequence(cu, s, tokens);
-      const int tiles = tiles_of(x);
-      if (left < tiles) {
-        x.first = (tiles - 1 - (int)left) * kTile;
-        sm.tile = x;
-        sm.found = 1;
-        break;
-      }
-      left -= tiles;
+  unsigned left = index - (upto - own);
+  auto take = [&](const Tile &x) {  // whether the tile is this sequence's
+    const unsigned tiles = tiles_of(x);
+    if (left < tiles) {
+      sm.tile = {x.lo, x.len, (int)(tiles - 1 - left) * kTile};
+      sm.found = 1;
+      return true;
     }
+    left -= tiles;
+    return false;
+  };
+  if (left < own) {
+    if (few) {
+      bool done = false;
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j)
+        if (!done) done = take(between(bound[j], bound[j + 1], tokens));
+    } else {
+      for (int s = at; s < end; ++s)
+        if (take(between(cu[s], cu[s + 1], tokens))) break;
+    }
+  }
   if (few) __syncwarp();
   else __syncthreads();
 }
