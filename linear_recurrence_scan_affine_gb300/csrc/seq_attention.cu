@@ -454,9 +454,12 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
 
 // ---------------------------------------------------------------------------
 // Gradient. delta_i = sum_d dout_id out_id first, then two kernels that each
-// form P and dS again from q, k, lse: dk and dv by key tiles, dq by query
+// form P and dS again from q, k, lse: dq by query tiles, dk and dv by key
 // tiles. Recomputing costs two of seven products, and buys results without
-// atomics: every sum has one fixed order.
+// atomics: every sum has one fixed order. The output that delta is made from
+// is rounded to bf16; rows short enough to have all their keys in one tile get
+// it from P and dP instead, in the dq kernel (59 episodes of up to 3 steps: dq
+// and dk within 1.7e-3 of 64 bits, the rounding of the result, 3.3e-3 before).
 //
 // Blocks of 576 threads, one per SM (all 512 columns of tensor memory); heads
 // up to 64 wide, 320 threads, two per SM. Four warps to 32 columns of a tile
@@ -857,12 +860,19 @@ template <int DP>
 struct QSmem {
   alignas(1024) unsigned char q[DP * 256], dout[DP * 256], k[3][DP * inner<DP>() * 2],
       v[2][DP * inner<DP>() * 2];
+  float sum[4][128];  // of weights times dP, by the threads of a row
   uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[2], v_empty[2];
   uint64_t s_full[2], dp_full, ds_ready, done;
   TileSearch search;
   uint32_t tmem;
   int abort;
 };
+
+// The warps of a dq block that share 32 query rows.
+template <int PARTS>
+__device__ __forceinline__ void row_barrier(int quarter) {
+  asm volatile("bar.sync %0, %1;" ::"r"(quarter + 1), "n"(PARTS * 32) : "memory");
+}
 
 // dq: a block per query tile and head, over the key tiles at and before it.
 // In tensor memory: S = Q K^T twice (128 columns each, dS over the one it
@@ -983,14 +993,14 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
       lse = p.lse[(int64_t)h * p.tokens + row] * kLog2e;
       delta = p.delta[(int64_t)h * p.tokens + row];
     }
-    const float2 k2 = make_float2(p.scale2, p.scale2), l2 = make_float2(-lse, -lse),
-                 d2 = make_float2(-delta, -delta);
-    bool ok = true;
-    for (int j = 0; j < steps && ok; ++j) {
+    const float2 k2 = make_float2(p.scale2, p.scale2), l2 = make_float2(-lse, -lse);
+    float2 d2 = make_float2(-delta, -delta);
+    // after a wait that ran out the loop goes on without waiting, so that
+    // every warp meets the others' barriers
+    for (int j = 0; j < steps; ++j) {
       const uint32_t at = (j & 1 ? tS1 : tS0) + mine;
       uint32_t s[32], d[32];
-      ok = tc::warp_wait(&sm.s_full[j & 1], (j / 2) & 1, abort);
-      if (!ok) break;
+      tc::warp_wait(&sm.s_full[j & 1], (j / 2) & 1, abort);
       tc::fence_after_sync();
       tc::ld32(at, s);
       tc::wait_ld();
@@ -1000,18 +1010,34 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
         s[c] = __float_as_uint(ex2(a.x));
         s[c + 1] = __float_as_uint(ex2(a.y));
       }
-      ok = tc::warp_wait(&sm.dp_full, j & 1, abort);
-      if (!ok) break;
+      tc::warp_wait(&sm.dp_full, j & 1, abort);
       tc::fence_after_sync();
       tc::ld32(tP + mine, d);
       tc::wait_ld();
+      const int last = t.first + r - first_key(j) - part * 32;  // the last column this row sees
+      if (t.first == 0 && first_key(j) == 0) {
+        // rows whose keys all are in this tile: delta = sum_j P_ij dP_ij, without
+        // the rounding of the output, which the few weights of a short row feel
+        float own = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c <= last) own = fmaf(__uint_as_float(s[c]), __uint_as_float(d[c]), own);
+        sm.sum[part][r] = own;
+        row_barrier<PARTS>(warp & 3);
+        own = 0.0f;
+#pragma unroll
+        for (int c = 0; c < PARTS; ++c) own += sm.sum[c][r];
+        if (r < IT && r < rows) {
+          d2 = make_float2(-own, -own);
+          if (part == 0) p.delta[(int64_t)h * p.tokens + row] = own;  // for dk
+        }
+      }
 #pragma unroll
       for (int c = 0; c < 32; c += 2) {
         const float2 a = __fmul2_rn(pair(s + c), __fadd2_rn(pair(d + c), d2));
         d[c] = __float_as_uint(a.x);
         d[c + 1] = __float_as_uint(a.y);
       }
-      const int last = t.first + r - first_key(j) - part * 32;  // the last column this row sees
       if (diagonal(j))
 #pragma unroll
         for (int c = 0; c < 32; ++c)
@@ -1021,8 +1047,7 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
       tc::fence_before_sync();
       tc::warp_arrive(&sm.ds_ready, lead);
     }
-    if (ok) ok = tc::warp_wait(&sm.done, 0, abort);
-    if (ok) {
+    if (tc::warp_wait(&sm.done, 0, abort)) {
       tc::fence_after_sync();
       const int from = part * 32;  // (DP is 32 PARTS)
       write_row<32>(tQ + lanes + from, p.dq + (row * p.Hq + h) * p.D + from, p.D - from, p.scale,
@@ -1535,6 +1560,10 @@ cudaError_t launch_backward(const BackwardMaps &stay, const BackwardMaps &walk,
   e = allow_dynamic_smem<attention_dkv_kernel<DP>>(kv_smem);
   if (e == cudaSuccess) e = allow_dynamic_smem<attention_dq_kernel<DP>>(q_smem);
   if (e != cudaSuccess) return e;
+  // dq first: it leaves delta without the output's rounding for short rows
+  e = launch_ex(attention_dq_kernel<DP>, dim3((unsigned)(tiles * a.Hq)),
+                dim3(backward_threads<DP>()), q_smem, st, true, stay.q, walk.k, walk.v, stay.dout, a);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * a.Hk * a.split));
   cfg.blockDim = dim3(backward_threads<DP>());
@@ -1548,11 +1577,7 @@ cudaError_t launch_backward(const BackwardMaps &stay, const BackwardMaps &walk,
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.split > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, attention_dkv_kernel<DP>, walk.q, stay.k, stay.v, walk.dout, a);
-  if (e == cudaSuccess)
-    e = launch_ex(attention_dq_kernel<DP>, dim3((unsigned)(tiles * a.Hq)), dim3(backward_threads<DP>()), q_smem, st,
-                  true, stay.q, walk.k, walk.v, stay.dout, a);
-  return e;
+  return cudaLaunchKernelEx(&cfg, attention_dkv_kernel<DP>, walk.q, stay.k, stay.v, walk.dout, a);
 }
 
 }  // namespace

@@ -602,3 +602,22 @@ def test_attention_step_large_scores(rl):
         lengths = torch.tensor([S], dtype=torch.int32)
         want, slack = ref.attention_step(q, kc, vc, lengths, D ** -0.5)
         close("out", rl.rlcs_attention_step(*cuda(q, kc, vc, lengths)), want, slack)
+
+
+@pytest.mark.parametrize("longest,D", [(2, 64), (3, 128), (17, 64), (60, 128), (64, 64), (128, 128)])
+def test_attention_gradient_of_short_rows(rl, longest, D):
+    # rows with all their keys in one tile take delta from P and dP, not from
+    # the rounded output, and dS as two bfloat16 terms: dq and dk carry the
+    # rounding of the result alone (2^-9 of each element at most) and that of
+    # float32 sums
+    g = gen(longest + D)
+    lens = [int(x) for x in torch.randint(1, longest + 1, (40,), generator=g)] + [longest]
+    n, Hq, Hk, bf = sum(lens), 6, 3, torch.bfloat16
+    q, k, v, dout = (rand(g, n, h, D, dtype=bf) for h in (Hq, Hk, Hk, Hq))
+    cu, scale = bounds(lens).cuda(), D ** -0.5
+    out, lse = rl.rlcs_attention(*cuda(q, k, v), cu, return_lse=True)
+    dq, dk, _ = rl.rlcs_attention_backward(dout.cuda(), *cuda(q, k, v), out, lse, cu)
+    (wq, wk, _), _ = ref.attention_backward(dout, q, k, v, lens, scale)
+    for name, a, w in (("dq", dq, wq), ("dk", dk, wk)):
+        off = float((a.cpu().double() - w).norm() / w.norm())
+        assert off < 2.0 ** -9 + 1e-4, (name, off)
