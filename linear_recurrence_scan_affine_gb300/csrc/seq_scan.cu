@@ -25,6 +25,7 @@
 //
 // A cut's map has m = 0 and composes by selection, so a non-finite state of
 // one episode does not reach the next.
+#include <atomic>
 #include <type_traits>
 
 #include "seq_common.cuh"
@@ -439,24 +440,29 @@ __global__ void __launch_bounds__(JOINED ? kWarpsMax * 32 : 32)
 //    short: 64 x 512 x 1024 bf16 45 / 73 against 63 / 80 joined, 128 x 40 x
 //    2048 13 / 23 against 28 / 34; with 128 groups (8 x 4096 x 1024) alone
 //    171 / 276 against 53 / 74 joined;
-//  - joined, the blocks of a cluster are as many as fill the SMs once: 2 x
-//    16384 x 1024 54 / 77 with 4, 75 / 108 with 8 and 82 / 111 with 2;
-//  - a cluster's blocks must find their SMs in one processing cluster: up to 8
-//    blocks, 12 for at most 8 clusters and 16 for at most 4. 1 x 131072 x 512
-//    (8) 132 / 189 with 12, 183 / 262 with 16, 166 / 222 with 8; 1 x 30000 x
-//    96 (2) 27 / 32 with 16, 30 / 40 with 12;
+//  - joined, the blocks of a cluster are as many as let every group of channels
+//    have its cluster at once, which depends on how many SMs each of the
+//    device's processing clusters has: the runtime is asked. (8 clusters of 12
+//    fit, 7 of 13 to 16: 1 x 131072 x 512 (8 groups) 132 / 189 with 12, 183 /
+//    262 with 16, 166 / 222 with 8; 1 x 131072 x 832 (13) 178 / 251 with 10, 191
+//    / 286 with 8; 1 x 65536 x 1088 (17) 141 / 192 with 6, 189 / 279 with 8; 2 x
+//    16384 x 1024 (32) 54 / 77 with 4, 75 / 108 with 8 and 82 / 111 with 2.)
+//    Sizes are not tried where a smaller one did as well: 26 groups take 4 (96 /
+//    140) rather than 5 (113 / 133).
 //  - segments of 256 steps, or, where most SMs work, 128 forward and 64 in the
 //    gradient, which keep the second pass in L2: 8 x 4096 x 1024 53 / 74
 //    against 56 / 87.
 struct Share {
   int blocks, warps, steps;  // blocks = 0: every warp alone
 };
-Share share_out(int64_t groups, int64_t T, int chunk, bool back) {
+// at_once(n): clusters of n blocks that the device runs at the same time.
+template <class AtOnce>
+Share share_out(int64_t groups, int64_t T, int chunk, bool back, AtOnce at_once) {
   if (T <= 128 || groups >= 5 * (int64_t)kSms) return {0, 1, 0};
   int blocks = 1;
-  for (int wider : {2, 4, 8, 12, 16})
-    if (groups <= (wider > 12 ? 4 : wider > 8 ? 8 : kSms / wider) &&
-        T >= (int64_t)wider * kWarpsMax * chunk)
+  for (int wider : {2, 3, 4, 6, 8, 9, 10, 12, 16})
+    if (groups * wider <= kSms && T >= (int64_t)wider * kWarpsMax * chunk &&
+        groups <= at_once(wider))
       blocks = wider;
   const int64_t warps = ceil_div(T, 32) < kWarpsMax ? ceil_div(T, 32) : kWarpsMax;
   const int64_t most = groups * blocks <= 2 * kSms / 3 ? 256 : (back ? 64 : 128);
@@ -464,15 +470,53 @@ Share share_out(int64_t groups, int64_t T, int chunk, bool back) {
   return {blocks, (int)warps, (int)(each < most ? each : most)};
 }
 
+// Clusters of `size` blocks of a kernel, each with an SM to itself, that the
+// current device runs at once; asked once per device and size. The kernel may
+// be launched with any size that was asked for.
+template <auto Kernel>
+int clusters_at_once(int size, size_t smem) {
+  static std::atomic<int> known[64][17];  // the answer + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::atomic<int> *k = dev < 64 ? &known[dev][size] : nullptr;
+  if (k && k->load(std::memory_order_relaxed)) return k->load(std::memory_order_relaxed) - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(size * kSms));
+  cfg.blockDim = dim3(kWarpsMax * 32);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)size;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (allow_dynamic_smem<Kernel>(smem) != cudaSuccess ||
+      cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  if (k) k->store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 template <class E, int V, int CB, bool BACK>
 cudaError_t launch_scan(ScanArgs a, int64_t B, cudaStream_t st) {
   constexpr int kRow = 32 * V * (int)sizeof(E), kChunk = kChunkBytes / ((BACK ? 4 : 2) * kRow);
   a.groups = ceil_div(a.D, 32 * V);
   const int64_t groups = B * a.groups;
-  const Share share = share_out(groups, a.T, kChunk, BACK);
+  constexpr auto kernel = gated_scan_kernel<E, V, CB, BACK, true>;
+  constexpr size_t most =
+      kWarpsMax * (ring_chunks<CB, true>() * kChunkBytes + 2 * sizeof(Map<V>) * 32);
+  const Share share = share_out(groups, a.T, kChunk, BACK,
+                                [](int size) { return clusters_at_once<kernel>(size, most); });
   if (share.blocks == 0)
     return launch_ex(gated_scan_kernel<E, V, CB, BACK, false>, dim3((unsigned)groups), dim3(32),
                      ring_chunks<CB, false>() * kChunkBytes, st, true, a);
+  const cudaError_t e = allow_dynamic_smem<kernel>(most);
+  if (e != cudaSuccess) return e;
   a.segment = share.steps;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * share.blocks));
@@ -488,12 +532,7 @@ cudaError_t launch_scan(ScanArgs a, int64_t B, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  constexpr auto kernel = gated_scan_kernel<E, V, CB, BACK, true>;
-  cudaError_t e =
-      allow_dynamic_smem<kernel>(kWarpsMax * (3 * kChunkBytes + 2 * sizeof(Map<V>) * 32));
-  if (e == cudaSuccess && share.blocks > 8)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, a) : e;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 // Two channels per lane where a pair of them can be loaded and stored

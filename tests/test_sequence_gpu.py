@@ -621,3 +621,12 @@ def test_attention_gradient_of_short_rows(rl, longest, D):
     for name, a, w in (("dq", dq, wq), ("dk", dk, wk)):
         off = float((a.cpu().double() - w).norm() / w.norm())
         assert off < 2.0 ** -9 + 1e-4, (name, off)
+
+
+# channel groups (of 64) by steps that take clusters of each size: 16, 10, 9,
+# 6, 4, 3 and 2 blocks where the device has the room that was measured
+@pytest.mark.parametrize("B,T,D", [(1, 4200, 384), (1, 2700, 832), (1, 2500, 960), (2, 1700, 704),
+                                   (5, 1100, 448), (10, 900, 256), (37, 600, 100)])
+def test_gated_scan_over_clusters(rl, B, T, D):
+    for dtype in ("bf16", "f32"):
+        test_gated_scan_and_gradient(rl, B, T, D, dtype, True)
