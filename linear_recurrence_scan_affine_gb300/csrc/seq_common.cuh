@@ -125,8 +125,9 @@ __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[2]) {
   *reinterpret_cast<uint32_t *>(p) = pack_bf16(v[0], v[1]);
 }
 
-// sigmoid(g) and 1 - sigmoid(g), each to float32 rounding: both come from
-// e = exp(-|g|) <= 1, so neither overflows nor cancels.
+// sigmoid(g) and 1 - sigmoid(g): both come from e = exp(-|g|) <= 1, so neither
+// overflows nor cancels. The smaller one's relative error grows with |g|, as
+// the exponent is rounded before its power is taken.
 struct Gate {
   float a, om;
 };

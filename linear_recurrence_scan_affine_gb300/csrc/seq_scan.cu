@@ -96,17 +96,29 @@ template <int V>
 __device__ __forceinline__ Map<V> join(const Map<V> &outer, const Map<V> &inner) {  // inner first
   return {mul(outer.m, inner.m), reach(outer, inner.c)};
 }
-// 1 - sigmoid(g) = 1 / (1 + e^g), to float32 rounding: no cancellation at
-// either end, and an infinite e^g gives 0.
+// a = sigmoid(g) and om = 1 - a = 1 / (1 + e^g), neither by cancellation: a =
+// e^g om for a closed gate (g < 0), whose a is small, else 1 - om. Relative
+// error up to (2 |g| + 8) 2^-24: the exponent g log2 e is rounded, to 2^-24 of
+// itself, before its power is taken. An infinite e^g gives om = 0, a = 1.
 template <int V>
-__device__ __forceinline__ Vf<V> keep_out(Vf<V> g) {
+struct Gates {
+  Vf<V> a, om;
+};
+template <int V>
+__device__ __forceinline__ Gates<V> gates_of(Vf<V> g) {
   Vf<V> e = mul(g, all<V>(1.4426950408889634f));
 #pragma unroll
   for (int v = 0; v < V; ++v) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.e[v]));
-  e = add(e, all<V>(1.0f));
+  Vf<V> om = add(e, all<V>(1.0f));
 #pragma unroll
-  for (int v = 0; v < V; ++v) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.e[v]));
-  return e;
+  for (int v = 0; v < V; ++v) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(om.e[v]));
+  Vf<V> a = one_less(om);
+#pragma unroll
+  for (int v = 0; v < V; ++v)  // (one instruction less than a product and a selection)
+    asm("{\n\t.reg .pred p;\n\tsetp.lt.f32 p, %1, 0f00000000;\n\t@p mul.f32 %0, %2, %3;\n\t}"
+        : "+f"(a.e[v])
+        : "f"(g.e[v]), "f"(e.e[v]), "f"(om.e[v]));
+  return {a, om};
 }
 
 // This block's rank and the number of blocks in its cluster.
@@ -299,8 +311,6 @@ __global__ void __launch_bounds__(JOINED ? kWarpsMax * 32 : 32)
     }
   };
 
-  // om = 1 - a comes from the gate; a = 1 - om is off by 2^-24 at most, which
-  // only scales what is carried. PLAIN: a whole chunk without cuts.
   auto floats = [](const Raw<E, V> &r) {
     Vf<V> f;
 #pragma unroll
@@ -325,39 +335,41 @@ __global__ void __launch_bounds__(JOINED ? kWarpsMax * 32 : 32)
       for (int i0 = 0; i0 < kChunk; i0 += kBatch) {
         // a batch's inputs first, then its steps: the stores of one step
         // would otherwise hold back the next step's reads
-        Vf<V> om[kBatch], y[kBatch];
-        [[maybe_unused]] Vf<V> x[BACK ? kBatch : 1], prev[BACK ? kBatch : 1];
+        Vf<V> a[kBatch], y[kBatch];  // y: (1 - a) x, or dh
+        // 1 - a, and a (keep h - x), which is dgate but for dx
+        [[maybe_unused]] Vf<V> om[BACK ? kBatch : 1], slope[BACK ? kBatch : 1];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          om[i] = keep_out(floats(value(stage, 0, i0 + i)));
+          const Gates<V> g = gates_of(floats(value(stage, 0, i0 + i)));
+          a[i] = g.a;
           y[i] = floats(value(stage, 1, i0 + i));
           if constexpr (BACK) {
-            x[i] = floats(value(stage, 2, i0 + i));
-            prev[i] = floats(value(stage, 3, i0 + i));
+            om[i] = g.om;
+            Vf<V> prev = floats(value(stage, 3, i0 + i));
+            if (!plain) {
+              if (s + i0 + i == p.T - 1) prev = start;
+              if (cut >> (i0 + i) & 1) prev = all<V>(0.0f);
+            }
+            slope[i] = mul(g.a, fma(floats(value(stage, 2, i0 + i)), all<V>(-1.0f), prev));
           } else {
-            y[i] = mul(om[i], y[i]);
+            y[i] = mul(g.om, y[i]);
           }
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i, out += step, out2 += BACK ? step : 0) {
           if (!plain && i0 + i >= n) break;
           const bool kept = plain || !(cut >> (i0 + i) & 1);
-          const Vf<V> a = one_less(om[i]);
           if constexpr (BACK) {
-            if (!plain) {
-              if (s + i0 + i == p.T - 1) prev[i] = start;
-              if (!kept) prev[i] = all<V>(0.0f);
-            }
             const Vf<V> lam = add(y[i], state), dx = mul(om[i], lam);
-            const Vf<V> dg = mul(mul(a, dx), fma(x[i], all<V>(-1.0f), prev[i]));
-            state = mul(a, lam);
+            const Vf<V> dg = mul(dx, slope[i]);
+            state = mul(a[i], lam);
             if (!kept) state = all<V>(0.0f);
             if (on) {
               store(out, dx.e);
               store(out2, dg.e);
             }
           } else {
-            state = kept ? fma(a, state, y[i]) : y[i];
+            state = kept ? fma(a[i], state, y[i]) : y[i];
             if (on) store(out, state.e);
           }
         }
@@ -388,10 +400,10 @@ __global__ void __launch_bounds__(JOINED ? kWarpsMax * 32 : 32)
 #pragma unroll
           for (int i = 0; i < kChunk; ++i) {
             if (!plain && i >= n) break;
-            const Vf<V> om = keep_out(floats(value(stage, 0, i))), a = one_less(om);
-            const Vf<V> c = mul(BACK ? a : om, floats(value(stage, 1, i)));
-            own.c = fma(a, own.c, c);
-            own.m = mul(own.m, a);
+            const Gates<V> g = gates_of(floats(value(stage, 0, i)));
+            const Vf<V> c = mul(BACK ? g.a : g.om, floats(value(stage, 1, i)));
+            own.c = fma(g.a, own.c, c);
+            own.m = mul(own.m, g.a);
             if (!plain && (cut >> i & 1)) {
               own.m = all<V>(0.0f);
               own.c = BACK ? all<V>(0.0f) : c;
