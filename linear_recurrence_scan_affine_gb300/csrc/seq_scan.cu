@@ -23,8 +23,9 @@
 // MB, 3.1 TB/s: the gates are worked out in both passes, on the 96 SMs that
 // clusters of 12 can take, with 59% of the issue slots busy.
 //
-// A cut's map has m = 0 and composes by selection, so a non-finite state of
-// one episode does not reach the next.
+// A cut's map has m = -0, which no product of gates is, and composes by
+// selection: a state that is not finite does not pass a cut, and passes
+// everything else, however small the product of the gates on its way.
 #include <atomic>
 #include <type_traits>
 
@@ -84,17 +85,30 @@ template <int V>
 struct alignas(8 * V) Map {
   Vf<V> m, c;
 };
-// A cut's map (m = 0) takes nothing of what came before, not even NaN * 0.
+// The mark of a cut. Further gates, none below zero, keep its sign; a product
+// of gates that has become too small for float32 is +0.
+__device__ __forceinline__ float cut_mark() { return -0.0f; }
+__device__ __forceinline__ bool is_cut(float m) { return __float_as_uint(m) == 0x80000000u; }
+// A cut takes nothing of what came before, not even NaN * 0. A product of
+// gates that has become +0 stands for a positive one: it leaves an infinity as
+// it is, as the steps one by one would.
 template <int V>
 __device__ __forceinline__ Vf<V> reach(const Map<V> &p, Vf<V> x) {
-  Vf<V> r = fma(p.m, x, p.c);
+  Vf<V> r;
 #pragma unroll
-  for (int v = 0; v < V; ++v) r.e[v] = p.m.e[v] == 0.0f ? p.c.e[v] : r.e[v];
+  for (int v = 0; v < V; ++v) {
+    const float m = p.m.e[v] == 0.0f && fabsf(x.e[v]) == INFINITY ? 1.0f : p.m.e[v];
+    r.e[v] = is_cut(p.m.e[v]) ? p.c.e[v] : fmaf(m, x.e[v], p.c.e[v]);
+  }
   return r;
 }
 template <int V>
 __device__ __forceinline__ Map<V> join(const Map<V> &outer, const Map<V> &inner) {  // inner first
-  return {mul(outer.m, inner.m), reach(outer, inner.c)};
+  Map<V> r = {mul(outer.m, inner.m), reach(outer, inner.c)};
+#pragma unroll
+  for (int v = 0; v < V; ++v)  // (the product of two marks is +0)
+    if (is_cut(outer.m.e[v])) r.m.e[v] = cut_mark();
+  return r;
 }
 // a = sigmoid(g) and om = 1 - a = 1 / (1 + e^g), neither by cancellation: a =
 // e^g om for a closed gate (g < 0), whose a is small, else 1 - om. Relative
@@ -405,7 +419,7 @@ __global__ void __launch_bounds__(JOINED ? kWarpsMax * 32 : 32)
             own.c = fma(g.a, own.c, c);
             own.m = mul(own.m, g.a);
             if (!plain && (cut >> i & 1)) {
-              own.m = all<V>(0.0f);
+              own.m = all<V>(cut_mark());
               own.c = BACK ? all<V>(0.0f) : c;
             }
           }
