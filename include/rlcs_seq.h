@@ -155,10 +155,11 @@ rlcs_status rlcs_qk_norm_rope_backward(
  * q [tokens, Hq, D], k and v [tokens, Hk, D], with positive token and head
  * strides that are multiples of 8 and 16-byte aligned bases
  * (RLCS_ERR_MISALIGNED otherwise). D is a multiple of 8 up to 128.
- * cu_seqlens [sequences + 1] int32 in device memory, nondecreasing from 0;
- * bounds outside [0, tokens] are clamped, and tokens that no sequence holds
- * are not written. out [tokens, Hq, D] contiguous; lse [Hq, tokens] float32
- * may be NULL.
+ * cu_seqlens [sequences + 1] int32 in device memory, nondecreasing; bounds
+ * outside [0, tokens] are clamped. Tokens that no sequence holds (before the
+ * first bound, from the last on) get rows of zeros, and -inf in lse. out
+ * [tokens, Hq, D] contiguous; lse [Hq, tokens] float32 may be NULL. With no
+ * sequences at all (0, no bounds to read) nothing is written.
  * Keys and values that a row does not see never change it, infinities and
  * NaN included.
  * `scratch`: rlcs_attention_scratch_bytes(...) bytes, 16-byte aligned; its
@@ -178,8 +179,8 @@ rlcs_status rlcs_attention(const void *q, int64_t q_token_stride, int64_t q_head
  *   dv_j = sum_i P_ij dout_i,   dS_ij = P_ij (dout_i . v_j - delta_i),
  *   dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i,
  * dk and dv summed over the query heads that share the head. dq [tokens, Hq,
- * D], dk, dv [tokens, Hk, D] contiguous. The same scratch as the forward
- * call's size. An element that is not finite makes gradients of its own
+ * D], dk, dv [tokens, Hk, D] contiguous, zeros for tokens that no sequence
+ * holds. The same scratch as the forward call's size. An element that is not finite makes gradients of its own
  * sequence so, and in its own tile of 128 tokens those of every token; other
  * sequences stay as they are. */
 rlcs_status rlcs_attention_backward(

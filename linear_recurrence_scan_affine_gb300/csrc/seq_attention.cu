@@ -130,6 +130,41 @@ __device__ __forceinline__ float2 pair(const uint32_t *r) {
   return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// Tokens that no sequence holds: those before the first bound and from the
+// last on. Their rows of a result are zeros, each block of the grid taking a
+// share of them, and their log sums are -inf (of nothing). The warps that wait
+// for a block's first scores do it, so that the two loads cost a call without
+// such tokens nothing.
+struct Unheld {
+  int lo, hi;  // [0, lo) and [hi, tokens)
+};
+__device__ __forceinline__ Unheld unheld(const int32_t *cu, int sequences, int tokens) {
+  int lo = __ldg(cu), hi = __ldg(cu + sequences);
+  lo = lo < 0 ? 0 : (lo < tokens ? lo : tokens);
+  hi = hi < lo ? lo : (hi < tokens ? hi : tokens);
+  return {lo, hi};
+}
+__device__ __noinline__ void zero_unheld(bf *x, int width, Unheld u, int tokens, int thread,
+                                         int threads) {
+  const int eights = width / 8;
+  const int64_t n = (int64_t)(u.lo + tokens - u.hi) * eights;
+  for (int64_t i = (int64_t)blockIdx.x * threads + thread; i < n;
+       i += (int64_t)gridDim.x * threads) {
+    const int64_t row = i / eights;
+    reinterpret_cast<uint4 *>(x + (row < u.lo ? row : row - u.lo + u.hi) * width)[i % eights] =
+        make_uint4(0, 0, 0, 0);
+  }
+}
+__device__ __noinline__ void empty_unheld(float *lse, int heads, Unheld u, int tokens, int thread,
+                                          int threads) {
+  const int rows = u.lo + tokens - u.hi;
+  for (int64_t i = (int64_t)blockIdx.x * threads + thread; i < (int64_t)rows * heads;
+       i += (int64_t)gridDim.x * threads) {
+    const int row = (int)(i % rows);
+    lse[i / rows * tokens + (row < u.lo ? row : row - u.lo + u.hi)] = -INFINITY;
+  }
+}
+
 // Record a wait that ran out where rlcs_check_status looks for it.
 __device__ __forceinline__ void report_timeout(WsHeader *ws) {
   atomicMax(&ws->status, (uint32_t)RLCS_ERR_TIMEOUT);
@@ -309,7 +344,14 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  auto clear_unheld = [&] {
+    const Unheld u = unheld(p.cu, (int)p.sequences, (int)p.tokens);
+    if (u.lo == 0 && u.hi == (int)p.tokens) return;
+    zero_unheld(p.o, p.Hq * p.D, u, (int)p.tokens, threadIdx.x, 256);
+    if (p.lse) empty_unheld(p.lse, p.Hq, u, (int)p.tokens, threadIdx.x, 256);
+  };
   if (!sm.search.found) {
+    if (warp < 8) clear_unheld();
     if (warp == 9) tc::tmem_dealloc(sm.tmem, IT + DP);
     return;
   }
@@ -358,6 +400,7 @@ __global__ void __launch_bounds__(320, DP == 64 ? 3 : 2)
     const uint32_t mine = tS + lanes + half * HC;
     const float2 k2 = make_float2(p.scale2, p.scale2);
     float m = -INFINITY, l = 0.0f;
+    clear_unheld();
     // after a wait that ran out the loop goes on without waiting, so that
     // every warp meets its partner's barriers
     for (int it = 0; it < steps; ++it) {
@@ -656,7 +699,15 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  auto clear_unheld = [&] {
+    constexpr int kThreads = backward_threads<DP>() - 64;
+    const Unheld u = unheld(p.cu, (int)p.sequences, (int)p.tokens);
+    if (u.lo == 0 && u.hi == (int)p.tokens) return;
+    zero_unheld(p.dk, p.Hk * p.D, u, (int)p.tokens, threadIdx.x, kThreads);
+    zero_unheld(p.dv, p.Hk * p.D, u, (int)p.tokens, threadIdx.x, kThreads);
+  };
   if (!sm.search.found) {
+    if (warp < kCopy) clear_unheld();
     if (warp == kIssue) tc::tmem_dealloc(sm.tmem, 2 * IT + 2 * DP);
     return;
   }
@@ -735,6 +786,7 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
     };
     Step x = begin;
     float next = column(x);
+    clear_unheld();
     const float2 k2 = make_float2(p.scale2, p.scale2);
     // after a wait that ran out the loop goes on without waiting, so that
     // every warp meets the others' barriers
@@ -930,7 +982,13 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  auto clear_unheld = [&] {
+    const Unheld u = unheld(p.cu, (int)p.sequences, (int)p.tokens);
+    if (u.lo == 0 && u.hi == (int)p.tokens) return;
+    zero_unheld(p.dq, p.Hq * p.D, u, (int)p.tokens, threadIdx.x, backward_threads<DP>() - 64);
+  };
   if (!sm.search.found) {
+    if (warp < kCopy) clear_unheld();
     if (warp == kIssue) tc::tmem_dealloc(sm.tmem, 3 * IT + DP);
     return;
   }
@@ -995,6 +1053,7 @@ __global__ void __launch_bounds__(backward_threads<DP>(), DP == 64 ? 2 : 1)
     }
     const float2 k2 = make_float2(p.scale2, p.scale2), l2 = make_float2(-lse, -lse);
     float2 d2 = make_float2(-delta, -delta);
+    clear_unheld();
     // after a wait that ran out the loop goes on without waiting, so that
     // every warp meets the others' barriers
     for (int j = 0; j < steps; ++j) {

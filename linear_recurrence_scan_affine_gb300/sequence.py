@@ -343,6 +343,12 @@ def _attention_args(q, k, v, cu_seqlens):
     return dev, (cu.numel() - 1, n, Hq, Hk, D), arrays, (q, k, v, cu)
 
 
+def _rows_out(sequences, shape, like):
+    """An array the library writes whole, where there are sequences at all."""
+    make = torch.empty if sequences else torch.zeros
+    return make(shape, dtype=like.dtype, device=like.device)
+
+
 @_streamed
 def rlcs_attention(q, k, v, cu_seqlens, scale=None, return_lse=False):
     """Causal attention over packed sequences: q [tokens, Hq, D], k and v
@@ -351,11 +357,14 @@ def rlcs_attention(q, k, v, cu_seqlens, scale=None, return_lse=False):
     `scale` (positive) defaults to D ** -0.5. Views whose strides are multiples of
     8 elements on a 16-byte boundary are read in place, others copied. Returns
     out [tokens, Hq, D], or (out, lse [Hq, tokens] float32) with
-    `return_lse`. Tokens that no sequence holds are left unwritten."""
+    `return_lse`. Tokens that no sequence holds (before the first bound, from
+    the last on) get zeros, and -inf in lse."""
     dev, sizes, arrays, keep = _attention_args(q, k, v, cu_seqlens)
-    _, n, Hq, _, D = sizes
-    out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
+    sequences, n, Hq, _, D = sizes
+    out = _rows_out(sequences, (n, Hq, D), q)
     lse = torch.empty((Hq, n), dtype=torch.float32, device=q.device) if return_lse else None
+    if return_lse and sequences == 0:
+        lse.fill_(-float("inf"))
     stream = _raw_stream(dev)
     ws, wsb = _scratch(_scratch_bytes("rlcs_attention_scratch_bytes", n, Hq), dev, stream)
     _call("rlcs_attention", *arrays, keep[3].data_ptr(), out.data_ptr(), _at(lse), *sizes,
@@ -367,16 +376,16 @@ def rlcs_attention(q, k, v, cu_seqlens, scale=None, return_lse=False):
 def rlcs_attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=None):
     """Gradients (dq, dk, dv) of rlcs_attention from the gradient of its
     output; `out` and `lse` are the forward call's. The gradients of a shared
-    key/value head sum over its query heads."""
+    key/value head sum over its query heads; those of tokens that no sequence
+    holds are zeros."""
     dev, sizes, arrays, keep = _attention_args(q, k, v, cu_seqlens)
-    _, n, Hq, Hk, D = sizes
+    sequences, n, Hq, Hk, D = sizes
     dout = _like(dout, "dout", (n, Hq, D), q.dtype, dev)
     out = _like(out, "out", (n, Hq, D), q.dtype, dev)
     dout, out = (t.clone() if t.data_ptr() % 16 else t for t in (dout, out))
     lse = _like(lse, "lse", (Hq, n), torch.float32, dev)
-    dq = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
-    dk = torch.empty((n, Hk, D), dtype=q.dtype, device=q.device)
-    dv = torch.empty((n, Hk, D), dtype=q.dtype, device=q.device)
+    dq = _rows_out(sequences, (n, Hq, D), q)
+    dk, dv = (_rows_out(sequences, (n, Hk, D), q) for _ in range(2))
     stream = _raw_stream(dev)
     ws, wsb = _scratch(_scratch_bytes("rlcs_attention_scratch_bytes", n, Hq), dev, stream)
     _call("rlcs_attention_backward", dout.data_ptr(), *arrays, out.data_ptr(), lse.data_ptr(),
