@@ -128,7 +128,7 @@ rlcs_status rlcs_qk_norm_rope(const void *q, int64_t q_token_stride, int64_t q_h
 /* Gradient of rlcs_qk_norm_rope. dq_out [tokens, Hq, D] and dk_out
  * [tokens, Hk, D] (contiguous) are the gradients of its outputs; dq, dk
  * (contiguous) and the weights' gradients dq_weight, dk_weight [D] float32
- * are written. With R the rotation (its transpose turns back),
+ * are written (with Hk = 0 dk_weight is zeros, or NULL). With R the rotation (its transpose turns back),
  *   du = R^T dy,  dw = sum over tokens and heads of du * x * r,
  *   dx = r * (w du - x r^2 mean(w du x)),   r = (mean(x^2) + eps)^(-1/2).
  * Each weight gradient is summed per block, then over blocks in a fixed

@@ -600,7 +600,7 @@ rlcs_status rlcs_qk_norm_rope_backward(
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (tokens == 0) {  // no rows: the weights' gradients are zero
     cudaError_t e = cudaMemsetAsync(dq_weight, 0, (size_t)D * 4, st);
-    if (e == cudaSuccess && Hk > 0) e = cudaMemsetAsync(dk_weight, 0, (size_t)D * 4, st);
+    if (e == cudaSuccess && dk_weight) e = cudaMemsetAsync(dk_weight, 0, (size_t)D * 4, st);
     return launched(e);
   }
   HeadArgs a = head_args(q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride,
@@ -615,7 +615,7 @@ rlcs_status rlcs_qk_norm_rope_backward(
   const Range none = range(nullptr, 0);
   const Range work = range(scratch, (int64_t)scratch_bytes);
   const Range outs[] = {range(dq, nq), Hk ? range(dk, nk) : none, range(dq_weight, D * 4),
-                        Hk ? range(dk_weight, D * 4) : none, work};
+                        range(dk_weight, D * 4), work};
   const Range ins[] = {
       range(dq_out, nq),
       Hk ? range(dk_out, nk) : none,
@@ -637,7 +637,7 @@ rlcs_status rlcs_qk_norm_rope_backward(
   if (s != RLCS_OK) return s;
   return launched(launch_ex(weight_sum_kernel, dim3((unsigned)ceil_div(2 * D, 32)), dim3(1024), 0,
                             st, true, (const float *)a.partial, blocks, a.q_blocks, (int)D, dq_weight,
-                            Hk > 0 ? dk_weight : (float *)nullptr));
+                            dk_weight));
 }
 
 }  // extern "C"

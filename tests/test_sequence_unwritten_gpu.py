@@ -54,3 +54,16 @@ def test_attention_rows_no_sequence_holds(rl, poisoned, cu, n, Hq, Hk, D):
     for a, b in zip(grads, rl.rlcs_attention_backward(part[3], *part[:3], o2, l2, inner)):
         # (a group's query heads may be shared by more blocks: another order of sums)
         assert torch.allclose(a[held].float(), b.float(), rtol=2.0 ** -7, atol=2.0 ** -12)
+
+
+@pytest.mark.parametrize("D", [64, 7])
+@pytest.mark.parametrize("n", [0, 5])
+def test_norm_gradient_without_key_heads(rl, poisoned, n, D):
+    g = torch.Generator().manual_seed(1)
+    q, dq = (torch.randn(n, 3, D, generator=g).cuda() for _ in range(2))
+    k, w = torch.zeros(n, 0, D).cuda(), torch.ones(D).cuda()
+    cos = sin = torch.ones(4, 0).cuda()
+    pos = torch.zeros(n, dtype=torch.int32).cuda()
+    got = rl.rlcs_qk_norm_rope_backward(dq, k, q, k, w, w, cos, sin, pos)
+    assert float(got[3].abs().sum()) == 0.0
+    assert torch.isfinite(got[0]).all() and torch.isfinite(got[2]).all()
