@@ -343,6 +343,10 @@ def _attention_args(q, k, v, cu_seqlens):
     return dev, (cu.numel() - 1, n, Hq, Hk, D), arrays, (q, k, v, cu)
 
 
+def _scale(scale, D):
+    return max(D, 1) ** -0.5 if scale is None else scale  # (the library refuses D = 0)
+
+
 def _rows_out(sequences, shape, like):
     """An array the library writes whole, where there are sequences at all."""
     make = torch.empty if sequences else torch.zeros
@@ -368,7 +372,7 @@ def rlcs_attention(q, k, v, cu_seqlens, scale=None, return_lse=False):
     stream = _raw_stream(dev)
     ws, wsb = _scratch(_scratch_bytes("rlcs_attention_scratch_bytes", n, Hq), dev, stream)
     _call("rlcs_attention", *arrays, keep[3].data_ptr(), out.data_ptr(), _at(lse), *sizes,
-          D ** -0.5 if scale is None else scale, _DTYPES[q.dtype], ws, wsb, stream)
+          _scale(scale, D), _DTYPES[q.dtype], ws, wsb, stream)
     return (out, lse) if return_lse else out
 
 
@@ -390,7 +394,7 @@ def rlcs_attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=None):
     ws, wsb = _scratch(_scratch_bytes("rlcs_attention_scratch_bytes", n, Hq), dev, stream)
     _call("rlcs_attention_backward", dout.data_ptr(), *arrays, out.data_ptr(), lse.data_ptr(),
           keep[3].data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *sizes,
-          D ** -0.5 if scale is None else scale, _DTYPES[q.dtype], ws, wsb, stream)
+          _scale(scale, D), _DTYPES[q.dtype], ws, wsb, stream)
     return dq, dk, dv
 
 
@@ -441,6 +445,6 @@ def rlcs_attention_step(q, k_cache, v_cache, lengths, scale=None, out=None):
     need = _scratch_bytes("rlcs_attention_step_scratch_bytes", B, S, Hq, Hk, D) + 64
     ws, wsb = _scratch(need, dev, stream)
     _call("rlcs_attention_step", q.data_ptr(), *ks, *vs, lengths.data_ptr(), o.data_ptr(), B, S,
-          Hq, Hk, D, D ** -0.5 if scale is None else scale, _DTYPES[q.dtype], ws + 64, wsb - 64,
+          Hq, Hk, D, _scale(scale, D), _DTYPES[q.dtype], ws + 64, wsb - 64,
           stream)
     return o if out is None else o.view(q.shape)
