@@ -91,9 +91,12 @@ def _scratch_bytes(name, *sizes):
 
 
 def check_scratch():
-    """Synchronise and check the status word of every scratch buffer."""
+    """Wait for every stream of the devices that have scratch buffers, then
+    check each buffer's status word."""
     with _b._ws_lock:
         items = list(_scratch_cache.values())
+    for dev in {ws[0].device for ws in items}:
+        torch.cuda.synchronize(dev)  # streams do not wait for one another
     for ws in items:
         _b._check(_lib.rlcs_check_status(_b._ptr(ws[0]), None), "rlcs_check_status")
 
