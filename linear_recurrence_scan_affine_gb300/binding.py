@@ -711,8 +711,11 @@ def rlcs_workspace_bytes(N, T):
 
 
 def check_all_workspaces():
-    """Synchronise and check the status word of every cached workspace."""
+    """Wait for every stream of the devices that have cached workspaces, then
+    check each workspace's status word."""
     with _ws_lock:
         items = list(_ws_cache.values())
+    for dev in {ws.device for ws in items}:
+        torch.cuda.synchronize(dev)  # streams do not wait for one another
     for ws in items:
         _check(_lib.rlcs_check_status(_ptr(ws), None), "rlcs_check_status")

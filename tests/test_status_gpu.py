@@ -28,3 +28,19 @@ def test_check_scratch_waits_for_other_streams(rl):
     assert not done.query()
     rl.check_scratch()
     assert done.query()
+
+
+def test_check_all_workspaces_waits_for_other_streams(rl):
+    r = torch.zeros(2, 40000, device="cuda")
+    big = torch.zeros(1 << 28, device="cuda")
+    side = torch.cuda.Stream()
+    rl.rlcs_gae(r, r, r, stream=side)  # loads the kernel
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(100):
+            big.add_(1.0)
+        rl.rlcs_gae(r, r, r)
+        done = side.record_event()
+    assert not done.query()
+    rl.check_all_workspaces()
+    assert done.query()
