@@ -164,7 +164,12 @@ rlcs_status rlcs_qk_norm_rope_backward(
  * NaN included.
  * `scratch`: rlcs_attention_scratch_bytes(...) bytes, 16-byte aligned; its
  * first 64 bytes are zeroed once before the first use (rlcs_workspace_init)
- * and hold the device-side status that rlcs_check_status reads. */
+ * and hold the device-side status that rlcs_check_status reads. A caller that
+ * reads rlcs_attention_status instead need not zero them, or keep them.
+ * rlcs_attention_backward, rlcs_attention_step and rlcs_qk_norm_rope_backward
+ * are several launches that pass values through their scratch: calls that
+ * share one are issued one whole call after another, on one stream, and a
+ * captured graph that uses one counts as a call at each of its replays. */
 size_t rlcs_attention_scratch_bytes(int64_t tokens, int64_t Hq);
 rlcs_status rlcs_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
                            const void *k, int64_t k_token_stride, int64_t k_head_stride,
@@ -173,6 +178,12 @@ rlcs_status rlcs_attention(const void *q, int64_t q_token_stride, int64_t q_head
                            int64_t tokens, int64_t Hq, int64_t Hk, int64_t D, double scale,
                            rlcs_dtype dtype, void *scratch, size_t scratch_bytes,
                            rlcs_stream_t stream);
+
+/* What attention calls on the current device have recorded since this was
+ * last asked, whatever scratch they had: waits for the device, returns the
+ * highest code (RLCS_OK, or RLCS_ERR_TIMEOUT where a bounded wait ran out) and
+ * clears it. */
+rlcs_status rlcs_attention_status(void);
 
 /* Gradient of rlcs_attention: dout [tokens, Hq, D] contiguous; out and lse
  * as the forward call wrote them. With delta_i = sum_d dout_id out_id,

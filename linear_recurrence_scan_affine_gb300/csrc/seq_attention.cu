@@ -165,16 +165,22 @@ __device__ __noinline__ void empty_unheld(float *lse, int heads, Unheld u, int t
   }
 }
 
-// Record a wait that ran out where rlcs_check_status looks for it.
-__device__ __forceinline__ void report_timeout(WsHeader *ws) {
-  atomicMax(&ws->status, (uint32_t)RLCS_ERR_TIMEOUT);
+// The highest code that any attention call has recorded on this device, for
+// callers whose scratch does not outlive a call.
+__device__ uint32_t device_status;
+
+// Record what went wrong where rlcs_check_status and rlcs_attention_status
+// look for it.
+__device__ __forceinline__ void report(WsHeader *ws, rlcs_status code) {
+  atomicMax(&ws->status, (uint32_t)code);
+  atomicMax(&device_status, (uint32_t)code);
 }
 
 // A wait that ran out: let copies in flight land, then record it.
 __device__ __forceinline__ void settle(int abort, WsHeader *ws) {
   if (!abort) return;
   for (int i = 0; i < 1000; ++i) __nanosleep(2000);
-  if (threadIdx.x == 0) report_timeout(ws);
+  if (threadIdx.x == 0) report(ws, RLCS_ERR_TIMEOUT);
 }
 
 // The two warps of a forward block that share 32 query rows.
@@ -239,7 +245,7 @@ __device__ __forceinline__ void write_row(uint32_t acc, bf *out, int left, float
 // `raw` is declared on one. A block that finds it elsewhere does nothing.
 __device__ __forceinline__ bool aligned_tiles(const void *raw, WsHeader *ws) {
   if ((tc::smem_addr(raw) & 1023) == 0) return true;
-  if (threadIdx.x == 0) atomicMax(&ws->status, (uint32_t)RLCS_ERR_CUDA);
+  if (threadIdx.x == 0) report(ws, RLCS_ERR_CUDA);
   return false;
 }
 
@@ -1647,6 +1653,18 @@ using namespace rlcs;
 using namespace rlcs::seq;
 
 extern "C" {
+
+rlcs_status rlcs_attention_status(void) {
+  uint32_t code = 0;
+  const uint32_t none = 0;
+  if (cudaDeviceSynchronize() != cudaSuccess ||
+      cudaMemcpyFromSymbol(&code, device_status, sizeof(code)) != cudaSuccess ||
+      (code && cudaMemcpyToSymbol(device_status, &none, sizeof(none)) != cudaSuccess)) {
+    cudaGetLastError();
+    return RLCS_ERR_CUDA;
+  }
+  return static_cast<rlcs_status>(code);
+}
 
 size_t rlcs_attention_scratch_bytes(int64_t tokens, int64_t Hq) {
   if (tokens < 0 || Hq <= 0 || !product_fits(tokens, Hq, 4)) return 0;

@@ -20,8 +20,8 @@ _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
 EXPORTED = ("rlcs_gated_scan", "rlcs_gated_scan_backward", "rlcs_gated_step", "rlcs_rope_table",
             "rlcs_qk_norm_rope", "rlcs_qk_norm_rope_scratch_bytes", "rlcs_qk_norm_rope_backward",
-            "rlcs_attention_scratch_bytes", "rlcs_attention", "rlcs_attention_backward",
-            "rlcs_attention_step_scratch_bytes", "rlcs_attention_step")
+            "rlcs_attention_status", "rlcs_attention_scratch_bytes", "rlcs_attention",
+            "rlcs_attention_backward", "rlcs_attention_step_scratch_bytes", "rlcs_attention_step")
 
 
 def _declare():
@@ -37,6 +37,7 @@ def _declare():
         "rlcs_qk_norm_rope_scratch_bytes": ([I64], SZ),
         "rlcs_qk_norm_rope_backward": ([P, P] + view * 2 + [P] * 9 + [I64] * 6
                                        + [I, F, I, P, SZ, P], I),
+        "rlcs_attention_status": ([], I),
         "rlcs_attention_scratch_bytes": ([I64, I64], SZ),
         "rlcs_attention": (view * 3 + [P] * 3 + [I64] * 5 + [F, I, P, SZ, P], I),
         "rlcs_attention_backward": ([P] + view * 3 + [P] * 6 + [I64] * 5 + [F, I, P, SZ, P], I),
@@ -63,26 +64,14 @@ def _call(name, *args):
 _fn = {name: getattr(_lib, name) for name in EXPORTED}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
-# One scratch buffer per (device, stream), apart from the estimators'
-# workspaces: these operators leave sums in it, which would break the chunk
-# records a look-back relies on. Its first 64 bytes hold a status word and are
-# zeroed when it is made.
-_scratch_cache = {}
-
-
-def _scratch(need, dev, stream):
-    """Address and size of the buffer, of `need` bytes at least."""
-    key = (dev, stream)
-    entry = _scratch_cache.get(key)
-    if entry is None or entry[2] < need:
-        with _b._ws_lock:
-            entry = _scratch_cache.get(key)
-            if entry is None or entry[2] < need:
-                # on the current stream, which is the one that will use it
-                ws = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device="cuda:%d" % dev)
-                ws[:64].zero_()
-                entry = _scratch_cache[key] = (ws, ws.data_ptr(), ws.numel())
-    return entry[1], entry[2]
+# Some calls are several launches that pass values through a scratch, and the
+# interpreter lock is released while one is issued. So a scratch is the call's
+# own: taken from PyTorch's allocator (in a capture, from the graph's memory)
+# and given back once the launches are issued, since what the allocator hands
+# it to next on this stream runs after them.
+_alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
+_free = torch._C._cuda_cudaCachingAllocator_raw_delete
+_attended = set()  # devices with attention calls
 
 
 @functools.lru_cache(maxsize=256)
@@ -90,15 +79,21 @@ def _scratch_bytes(name, *sizes):
     return _fn[name](*sizes)
 
 
+def _call_with_scratch(name, need, stream, *args):
+    """_call with `need` bytes of scratch and the stream as last arguments."""
+    ws = _alloc(need, stream)
+    try:
+        _call(name, *args, ws, need, stream)
+    finally:
+        _free(ws)
+
+
 def check_scratch():
-    """Wait for every stream of the devices that have scratch buffers, then
-    check each buffer's status word."""
-    with _b._ws_lock:
-        items = list(_scratch_cache.values())
-    for dev in {ws[0].device for ws in items}:
-        torch.cuda.synchronize(dev)  # streams do not wait for one another
-    for ws in items:
-        _b._check(_lib.rlcs_check_status(_b._ptr(ws[0]), None), "rlcs_check_status")
+    """Wait for every device with attention calls, and raise what they recorded
+    there since the last check."""
+    for dev in sorted(_attended):
+        with torch.cuda.device(dev):
+            _b._check(_fn["rlcs_attention_status"](), "rlcs_attention_status")
 
 
 def _streamed(f):
@@ -318,11 +313,11 @@ def rlcs_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, si
     dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
     dqw = torch.empty(D, dtype=torch.float32, device=q.device)
     dkw = torch.empty(D, dtype=torch.float32, device=q.device)
-    stream = _raw_stream(dev)
-    ws, wsb = _scratch(_scratch_bytes("rlcs_qk_norm_rope_scratch_bytes", D) + 64, dev, stream)
-    _call("rlcs_qk_norm_rope_backward", dq_out.data_ptr(), dk_out.data_ptr(), *arrays,
-          dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), *sizes,
-          1 if interleaved else 0, eps, _DTYPES[q.dtype], ws + 64, wsb - 64, stream)
+    _call_with_scratch("rlcs_qk_norm_rope_backward",
+                       _scratch_bytes("rlcs_qk_norm_rope_scratch_bytes", D), _raw_stream(dev),
+                       dq_out.data_ptr(), dk_out.data_ptr(), *arrays, dq.data_ptr(), dk.data_ptr(),
+                       dqw.data_ptr(), dkw.data_ptr(), *sizes, 1 if interleaved else 0, eps,
+                       _DTYPES[q.dtype])
     return dq, dk, dqw, dkw
 
 
@@ -372,10 +367,10 @@ def rlcs_attention(q, k, v, cu_seqlens, scale=None, return_lse=False):
     lse = torch.empty((Hq, n), dtype=torch.float32, device=q.device) if return_lse else None
     if return_lse and sequences == 0:
         lse.fill_(-float("inf"))
-    stream = _raw_stream(dev)
-    ws, wsb = _scratch(_scratch_bytes("rlcs_attention_scratch_bytes", n, Hq), dev, stream)
-    _call("rlcs_attention", *arrays, keep[3].data_ptr(), out.data_ptr(), _at(lse), *sizes,
-          _scale(scale, D), _DTYPES[q.dtype], ws, wsb, stream)
+    _attended.add(dev)
+    _call_with_scratch("rlcs_attention", _scratch_bytes("rlcs_attention_scratch_bytes", n, Hq),
+                       _raw_stream(dev), *arrays, keep[3].data_ptr(), out.data_ptr(), _at(lse),
+                       *sizes, _scale(scale, D), _DTYPES[q.dtype])
     return (out, lse) if return_lse else out
 
 
@@ -393,11 +388,12 @@ def rlcs_attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=None):
     lse = _like(lse, "lse", (Hq, n), torch.float32, dev)
     dq = _rows_out(sequences, (n, Hq, D), q)
     dk, dv = (_rows_out(sequences, (n, Hk, D), q) for _ in range(2))
-    stream = _raw_stream(dev)
-    ws, wsb = _scratch(_scratch_bytes("rlcs_attention_scratch_bytes", n, Hq), dev, stream)
-    _call("rlcs_attention_backward", dout.data_ptr(), *arrays, out.data_ptr(), lse.data_ptr(),
-          keep[3].data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *sizes,
-          _scale(scale, D), _DTYPES[q.dtype], ws, wsb, stream)
+    _attended.add(dev)
+    _call_with_scratch("rlcs_attention_backward",
+                       _scratch_bytes("rlcs_attention_scratch_bytes", n, Hq), _raw_stream(dev),
+                       dout.data_ptr(), *arrays, out.data_ptr(), lse.data_ptr(),
+                       keep[3].data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *sizes,
+                       _scale(scale, D), _DTYPES[q.dtype])
     return dq, dk, dv
 
 
@@ -444,10 +440,8 @@ def rlcs_attention_step(q, k_cache, v_cache, lengths, scale=None, out=None):
                          % (Hq, Hk))
     lengths = _like(lengths, "lengths", (B,), torch.int32, dev)
     o = torch.empty_like(q) if out is None else _b._out(out, "out", q)
-    stream = _raw_stream(dev)
-    need = _scratch_bytes("rlcs_attention_step_scratch_bytes", B, S, Hq, Hk, D) + 64
-    ws, wsb = _scratch(need, dev, stream)
-    _call("rlcs_attention_step", q.data_ptr(), *ks, *vs, lengths.data_ptr(), o.data_ptr(), B, S,
-          Hq, Hk, D, _scale(scale, D), _DTYPES[q.dtype], ws + 64, wsb - 64,
-          stream)
+    _call_with_scratch("rlcs_attention_step",
+                       _scratch_bytes("rlcs_attention_step_scratch_bytes", B, S, Hq, Hk, D),
+                       _raw_stream(dev), q.data_ptr(), *ks, *vs, lengths.data_ptr(), o.data_ptr(),
+                       B, S, Hq, Hk, D, _scale(scale, D), _DTYPES[q.dtype])
     return o if out is None else o.view(q.shape)
