@@ -105,9 +105,12 @@ def _stream(stream):
 
 
 # One zeroed workspace per (device, stream), grown on demand. A workspace is
-# reused only by calls on its own stream, which the stream orders.
+# reused only by calls on its own stream, which the stream orders. One that was
+# outgrown is kept: a graph captured with it writes to it at every replay. (It
+# grows to twice its size at least, so all that are kept are smaller together.)
 _ws_lock = threading.Lock()
 _ws_cache = {}
+_ws_outgrown = []
 
 
 def workspace_for(N, T, device, stream=None, need=None):
@@ -125,8 +128,12 @@ def workspace_for(N, T, device, stream=None, need=None):
         if ws is None or ws.numel() < need:
             # zeroed on the stream that will use it, so the fill is ordered
             # before the first call (and the memory belongs to that stream)
+            size = max(need, 1 << 16)
+            if ws is not None:
+                _ws_outgrown.append(ws)
+                size = max(size, 2 * ws.numel())
             with torch.cuda.stream(s):
-                ws = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
+                ws = torch.zeros(size, dtype=torch.uint8, device=device)
             _ws_cache[key] = ws
     return ws, ws.numel()
 
@@ -714,7 +721,7 @@ def check_all_workspaces():
     """Wait for every stream of the devices that have cached workspaces, then
     check each workspace's status word."""
     with _ws_lock:
-        items = list(_ws_cache.values())
+        items = list(_ws_cache.values()) + _ws_outgrown
     for dev in {ws.device for ws in items}:
         torch.cuda.synchronize(dev)  # streams do not wait for one another
     for ws in items:
