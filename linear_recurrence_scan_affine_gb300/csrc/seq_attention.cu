@@ -232,8 +232,8 @@ __device__ __forceinline__ void write_row(uint32_t acc, bf *out, int left, float
 // and bf16 range, and the final division removes the common factor), so O is
 // rarely rescaled.
 //
-// One sequence of 16384, 8 heads of 128 on 1: 414 us, 1.33 PFLOP/s (a library
-// matrix product reaches 1.95), the tensor pipe busy 61% of the time. S takes
+// One sequence of 16384, 8 heads of 128 on 1: 420 us, 1.31 PFLOP/s (a library
+// matrix product reaches 1.95), the tensor pipe busy 60% of the time. S takes
 // 830 clocks where PV takes 510: both its operands come from shared memory, 128
 // bytes a clock at full rate, which is all that an SM can read, while copies
 // come in. The rest is the chain from a tile's scores to its weights (1100

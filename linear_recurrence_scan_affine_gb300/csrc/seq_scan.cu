@@ -17,11 +17,11 @@
 // segment from the state that reaches it, its inputs still in the ring or in
 // L2. Nothing passes through global memory and every sum has one fixed order.
 //
-// Measured, bfloat16. Warps alone, 64 x 512 x 1024: forward and gradient 118
-// us for 605 MB, 5.1 TB/s (a copy reaches 6.7): bound by memory, the rest is
-// the start and the end of the walks. Joined, 1 x 131072 x 512: 131 us for 403
-// MB, 3.1 TB/s: the gates are worked out in both passes, on the 96 SMs that
-// clusters of 12 can take, with 59% of the issue slots busy.
+// Measured, bfloat16. Warps alone, 64 x 512 x 1024: forward and gradient 124
+// us for 605 MB, 4.9 TB/s (a copy reaches 6.7): bound by memory, the rest is
+// the start and the end of the walks. Joined, 1 x 131072 x 512: 136 us for 403
+// MB, 3.0 TB/s: the gates are worked out in both passes, on the 96 SMs that
+// clusters of 12 can take, with 68% of the issue slots busy.
 //
 // A cut's map has m = -0, which no product of gates is, and composes by
 // selection: a state that is not finite does not pass a cut, and passes
@@ -128,7 +128,8 @@ __device__ __forceinline__ Gates<V> gates_of(Vf<V> g) {
   for (int v = 0; v < V; ++v) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(om.e[v]));
   Vf<V> a = one_less(om);
 #pragma unroll
-  for (int v = 0; v < V; ++v)  // (one instruction less than a product and a selection)
+  // (a predicated product: 1 x 131072 x 512 136 us, 145 with a product and a selection)
+  for (int v = 0; v < V; ++v)
     asm("{\n\t.reg .pred p;\n\tsetp.lt.f32 p, %1, 0f00000000;\n\t@p mul.f32 %0, %2, %3;\n\t}"
         : "+f"(a.e[v])
         : "f"(g.e[v]), "f"(e.e[v]), "f"(om.e[v]));
@@ -463,21 +464,21 @@ __global__ void __launch_bounds__(JOINED ? kWarpsMax * 32 : 32)
 
 // How a call's steps are shared out. Measured on GB300, us forward / gradient:
 //  - a warp walks alone from 5 channel groups per SM on, or where the walk is
-//    short: 64 x 512 x 1024 bf16 45 / 73 against 63 / 80 joined, 128 x 40 x
-//    2048 13 / 23 against 28 / 34; with 128 groups (8 x 4096 x 1024) alone
-//    171 / 276 against 53 / 74 joined;
+//    short: 64 x 512 x 1024 bf16 35 / 70 against 58 / 83 joined, 128 x 40 x
+//    2048 12 / 21 against 22 / 30; with 128 groups (8 x 4096 x 1024) alone
+//    127 / 259 against 54 / 78 joined;
 //  - joined, the blocks of a cluster are as many as let every group of channels
 //    have its cluster at once, which depends on how many SMs each of the
 //    device's processing clusters has: the runtime is asked. (8 clusters of 12
-//    fit, 7 of 13 to 16: 1 x 131072 x 512 (8 groups) 132 / 189 with 12, 183 /
-//    262 with 16, 166 / 222 with 8; 1 x 131072 x 832 (13) 178 / 251 with 10, 191
-//    / 286 with 8; 1 x 65536 x 1088 (17) 141 / 192 with 6, 189 / 279 with 8; 2 x
-//    16384 x 1024 (32) 54 / 77 with 4, 75 / 108 with 8 and 82 / 111 with 2.)
-//    Sizes are not tried where a smaller one did as well: 26 groups take 4 (96 /
-//    140) rather than 5 (113 / 133).
+//    fit, 7 of 13 to 16: 1 x 131072 x 512 (8 groups) 136 / 196 with 12, 208 /
+//    331 with 16, 171 / 239 with 8; 1 x 131072 x 832 (13) 185 / 266 with 10, 197
+//    / 308 with 8; 1 x 65536 x 1088 (17) 145 / 208 with 6, 195 / 302 with 8; 2 x
+//    16384 x 1024 (32) 55 / 81 with 4, 78 / 118 with 8 and 85 / 119 with 2.)
+//    Sizes are not tried where a smaller one did as well: 26 groups take 4 (99 /
+//    151) rather than 5 (117 / 140).
 //  - segments of 256 steps, or, where most SMs work, 128 forward and 64 in the
-//    gradient, which keep the second pass in L2: 8 x 4096 x 1024 53 / 74
-//    against 56 / 87.
+//    gradient, which keep the second pass in L2: 8 x 4096 x 1024 54 / 78
+//    against 54 / 87.
 struct Share {
   int blocks, warps, steps;  // blocks = 0: every warp alone
 };

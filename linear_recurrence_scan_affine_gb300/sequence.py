@@ -7,6 +7,10 @@ Argument marshalling only, as in ``binding``: PyTorch supplies device memory
 and the stream, every step runs in the CUDA library, and a status other than
 OK raises ``RlcsError``. Each function takes a `stream` (default: the current
 one); outputs and temporary copies are allocated on it.
+
+Nothing is recorded for automatic differentiation: results are detached, and
+the gradients come from the ``_backward`` calls (examples/sequence_policy.py
+wraps them in ``torch.autograd.Function``). Calls may come from any thread.
 """
 import ctypes
 import functools
