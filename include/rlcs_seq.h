@@ -3,7 +3,7 @@
  * mixing layers of a policy and critic over rollouts.
  *
  * The estimators of rlcs.h take `values` and `log_rhos`; a sequence model
- * over the same steps, cut at the same episode ends, produces them. Three
+ * over the same steps, cut at the same episode ends, produces them. Four
  * operators of such a model live here, each with its gradient and with its
  * form for single steps (acting):
  *
@@ -12,14 +12,17 @@
  *   head norm and rotation    RMS norm of each query and key head with
  *                             rotary positions, in one pass;
  *   causal attention          grouped heads over packed episodes, and one
- *                             new token over a long key/value cache.
+ *                             new token over a long key/value cache;
+ *   linear attention          the affine recurrence on matrices: a decaying
+ *                             sum of key/value products per head, over
+ *                             packed episodes and for one new token.
  *
  * Conventions beyond those of rlcs.h (device memory owned by the caller,
  * nothing allocated, asynchronous on `stream`, capturable, argument errors
  * returned before anything is launched):
  *
  * Types.     `dtype` is the element type of the activations (float32 or
- *            bfloat16; attention: bfloat16). Recurrent states, norm weights,
+ *            bfloat16; both kinds of attention: bfloat16). Recurrent states, norm weights,
  *            rotary tables, softmax statistics and every sum are float32; an
  *            activation result is rounded to `dtype` once, when written.
  * Strides.   Where a function takes strides they are counted in elements and
@@ -31,7 +34,8 @@
  *            at least one sequence, step and channel. Negative sizes are
  *            RLCS_ERR_INVALID_ARG.
  * Aliasing.  Outputs must not overlap any input or each other (inputs may
- *            overlap inputs), but rlcs_gated_step's new_state may be state.
+ *            overlap inputs), but the new_state of rlcs_gated_step and
+ *            rlcs_linear_attention_step may be state.
  * Order.     No result depends on the order of atomics: repeated calls on
  *            the same inputs give the same bits.
  */
@@ -218,6 +222,67 @@ rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_ba
                                 const int32_t *lengths, void *out, int64_t B, int64_t S,
                                 int64_t Hq, int64_t Hk, int64_t D, double scale, rlcs_dtype dtype,
                                 void *scratch, size_t scratch_bytes, rlcs_stream_t stream);
+
+/* Linear attention with a decay for each head, over packed episodes
+ * (bfloat16). State head h of Hk keeps a matrix per sequence, float32:
+ *   S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T          [D x D],  S_{-1} = state
+ *   o_t = scale q_t S_t        for each of the Hq/Hk query heads of the state
+ * q [tokens, Hq, D], k and v [tokens, Hk, D], strides and alignment, D,
+ * cu_seqlens and the tokens that no sequence holds as for rlcs_attention; out
+ * [tokens, Hq, D] contiguous. log_decay [Hk] float32 in device memory: 0 keeps
+ * everything, -infinity nothing but the token itself (positive values grow, as
+ * the formula has it). state [sequences, Hk, D, D] float32 (keys' dimension
+ * first) may be NULL (0); last_state, of the same shape, receives the state
+ * after each sequence's last token (of an empty sequence: `state`) and may be
+ * NULL. Both start on 16-byte boundaries. The bounds of the sequences must be
+ * nondecreasing. An element that is not finite makes the rest of its
+ * sequence so, and may make so the tokens before it in its own tile of 128;
+ * other sequences and heads stay as they are.
+ * `scratch`: rlcs_linear_attention_scratch_bytes(...) bytes, 16-byte aligned,
+ * used as that of rlcs_attention_backward. What waits that ran out leave
+ * behind is in rlcs_attention_status too. */
+size_t rlcs_linear_attention_scratch_bytes(int64_t sequences, int64_t tokens, int64_t Hq,
+                                           int64_t Hk, int64_t D);
+rlcs_status rlcs_linear_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                  const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                                  const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                                  const float *log_decay, const int32_t *cu_seqlens,
+                                  const float *state, void *out, float *last_state,
+                                  int64_t sequences, int64_t tokens, int64_t Hq, int64_t Hk,
+                                  int64_t D, double scale, rlcs_dtype dtype, void *scratch,
+                                  size_t scratch_bytes, rlcs_stream_t stream);
+
+/* Gradient of rlcs_linear_attention; the decays are constants of the layer.
+ * With G_t the gradient that reaches S_t and a = exp(log_decay[h]),
+ *   G_t = a G_{t+1} + scale sum_heads q_t dout_t^T    (dlast added at the last token)
+ *   dq_t = scale S_t dout_t,   dk_t = G_t v_t,   dv_t = G_t^T k_t,   dstate = a G_0
+ * (of an empty sequence: dstate = dlast). dout [tokens, Hq, D], dq, dk, dv
+ * contiguous; dlast and dstate [sequences, Hk, D, D] float32 may be NULL.
+ * dq is the operator itself on (dout, v, k); dv on (k, q, dout) and dk on (v,
+ * dout, q), walked from the end. */
+rlcs_status rlcs_linear_attention_backward(
+    const void *dout, const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
+    int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+    int64_t v_head_stride, const float *log_decay, const int32_t *cu_seqlens, const float *state,
+    const float *dlast, void *dq, void *dk, void *dv, float *dstate, int64_t sequences,
+    int64_t tokens, int64_t Hq, int64_t Hk, int64_t D, double scale, rlcs_dtype dtype,
+    void *scratch, size_t scratch_bytes, rlcs_stream_t stream);
+
+/* One step of linear attention for B states (bfloat16): q [B, Hq, D], k and v
+ * [B, Hk, D] with batch and head strides (in elements, the last dimension
+ * contiguous, no alignment beyond the element's), log_decay [Hk], state and
+ * new_state [B, Hk, D, D] float32 on 16-byte boundaries, out [B, Hq, D]
+ * contiguous. reset [B] may be NULL; where it is set the old state is dropped
+ * whatever it holds. new_state may be the same array as state. D a multiple
+ * of 8 up to 128. */
+rlcs_status rlcs_linear_attention_step(const void *q, int64_t q_batch_stride,
+                                       int64_t q_head_stride, const void *k,
+                                       int64_t k_batch_stride, int64_t k_head_stride,
+                                       const void *v, int64_t v_batch_stride,
+                                       int64_t v_head_stride, const float *log_decay,
+                                       const uint8_t *reset, const float *state, float *new_state,
+                                       void *out, int64_t B, int64_t Hq, int64_t Hk, int64_t D,
+                                       double scale, rlcs_dtype dtype, rlcs_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -8,8 +8,10 @@ package is a thin ctypes binding with the same names. Importing it loads
 ``librlcs.so`` and fails loudly if the library has not been built.
 
 The sequence operators of a policy and critic over the same rollouts (gated
-linear recurrence, head norm with rotary positions, causal attention over
-packed episodes) have their C ABI in include/rlcs_seq.h.
+linear recurrence, head norm with rotary positions, causal attention and linear
+attention over packed episodes) have their C ABI in include/rlcs_seq.h, the
+losses of a policy's logits (the clipped policy loss on the estimators'
+advantages, distillation from a teacher's top logits) in include/rlcs_loss.h.
 """
 from .binding import (  # noqa: F401
     RLCS_SHAPE_AUTO, RLCS_SHAPE_BLOCK_CHUNK, RLCS_SHAPE_BLOCK_TILE, RLCS_SHAPE_WARP_ROW, RlcsError,
@@ -23,5 +25,9 @@ from .binding import (  # noqa: F401
     workspace_for)
 from .sequence import (  # noqa: F401
     check_scratch, rlcs_attention, rlcs_attention_backward, rlcs_attention_step, rlcs_gated_scan,
-    rlcs_gated_scan_backward, rlcs_gated_step, rlcs_qk_norm_rope, rlcs_qk_norm_rope_backward,
-    rlcs_rope_table)
+    rlcs_gated_scan_backward, rlcs_gated_step, rlcs_linear_attention,
+    rlcs_linear_attention_backward, rlcs_linear_attention_step, rlcs_qk_norm_rope,
+    rlcs_qk_norm_rope_backward, rlcs_rope_table)
+from .losses import (  # noqa: F401
+    PolicyLoss, rlcs_distill_loss, rlcs_distill_loss_backward, rlcs_policy_loss,
+    rlcs_policy_loss_backward)

@@ -1,8 +1,9 @@
 """Sequence operators of ``librlcs.so`` (the C ABI in include/rlcs_seq.h).
 
 The mixing layers of a policy and critic over rollouts: a gated linear
-recurrence, the head norm with rotary positions, and causal attention over
-packed episodes, each with its gradient and its form for single steps.
+recurrence, the head norm with rotary positions, causal attention and linear
+attention over packed episodes, each with its gradient and its form for single
+steps.
 Argument marshalling only, as in ``binding``: PyTorch supplies device memory
 and the stream, every step runs in the CUDA library, and a status other than
 OK raises ``RlcsError``. Each function takes a `stream` (default: the current
@@ -25,7 +26,9 @@ ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
 EXPORTED = ("rlcs_gated_scan", "rlcs_gated_scan_backward", "rlcs_gated_step", "rlcs_rope_table",
             "rlcs_qk_norm_rope", "rlcs_qk_norm_rope_scratch_bytes", "rlcs_qk_norm_rope_backward",
             "rlcs_attention_status", "rlcs_attention_scratch_bytes", "rlcs_attention",
-            "rlcs_attention_backward", "rlcs_attention_step_scratch_bytes", "rlcs_attention_step")
+            "rlcs_attention_backward", "rlcs_attention_step_scratch_bytes", "rlcs_attention_step",
+            "rlcs_linear_attention_scratch_bytes", "rlcs_linear_attention",
+            "rlcs_linear_attention_backward", "rlcs_linear_attention_step")
 
 
 def _declare():
@@ -48,6 +51,11 @@ def _declare():
         "rlcs_attention_step_scratch_bytes": ([I64] * 5, SZ),
         "rlcs_attention_step": ([P] + [P, I64, I64, I64] * 2 + [P, P] + [I64] * 5
                                 + [F, I, P, SZ, P], I),
+        "rlcs_linear_attention_scratch_bytes": ([I64] * 5, SZ),
+        "rlcs_linear_attention": (view * 3 + [P] * 5 + [I64] * 5 + [F, I, P, SZ, P], I),
+        "rlcs_linear_attention_backward": ([P] + view * 3 + [P] * 8 + [I64] * 5
+                                           + [F, I, P, SZ, P], I),
+        "rlcs_linear_attention_step": (view * 3 + [P] * 5 + [I64] * 4 + [F, I, P], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(_lib, name)
@@ -449,3 +457,95 @@ def rlcs_attention_step(q, k_cache, v_cache, lengths, scale=None, out=None):
                        _raw_stream(dev), q.data_ptr(), *ks, *vs, lengths.data_ptr(), o.data_ptr(),
                        B, S, Hq, Hk, D, _scale(scale, D), _DTYPES[q.dtype])
     return o if out is None else o.view(q.shape)
+
+
+def _linear_args(q, k, v, log_decay, cu_seqlens, state):
+    dev, sizes, arrays, keep = _attention_args(q, k, v, cu_seqlens)
+    sequences, _, _, Hk, D = sizes
+    decay = _like(log_decay, "log_decay", (Hk,), torch.float32, dev)
+    state = _matrices(state, "state", sequences, Hk, D, dev)
+    return dev, sizes, arrays + (decay.data_ptr(), keep[3].data_ptr()), keep + (decay, state)
+
+
+def _matrices(t, name, B, H, D, dev):
+    """A [B, H, D, D] float32 array on a 16-byte boundary, or None."""
+    t = _maybe(t, name, (B, H, D, D), torch.float32, dev)
+    return t.clone() if t is not None and t.data_ptr() % 16 else t
+
+
+@_streamed
+def rlcs_linear_attention(q, k, v, log_decay, cu_seqlens, state=None, scale=None,
+                          return_state=False):
+    """Linear attention over packed sequences: S_t = exp(log_decay) S_{t-1} +
+    k_t v_t^T per key/value head, out_t = scale q_t S_t. q [tokens, Hq, D], k
+    and v [tokens, Hk, D], cu_seqlens and `scale` as for rlcs_attention;
+    log_decay [Hk] float32 (at most 0); `state` [sequences, Hk, D, D] float32,
+    the states before the first tokens, defaults to zeros. Returns out
+    [tokens, Hq, D], or (out, states after the last tokens) with
+    `return_state`. Tokens that no sequence holds get zeros."""
+    dev, sizes, arrays, keep = _linear_args(q, k, v, log_decay, cu_seqlens, state)
+    sequences, n, Hq, Hk, D = sizes
+    out = _rows_out(sequences, (n, Hq, D), q)
+    last = (torch.empty((sequences, Hk, D, D), dtype=torch.float32, device=q.device)
+            if return_state else None)
+    _attended.add(dev)
+    _call_with_scratch("rlcs_linear_attention",
+                       _scratch_bytes("rlcs_linear_attention_scratch_bytes", *sizes),
+                       _raw_stream(dev), *arrays, _at(keep[5]), out.data_ptr(), _at(last), *sizes,
+                       _scale(scale, D), _DTYPES[q.dtype])
+    return (out, last) if return_state else out
+
+
+@_streamed
+def rlcs_linear_attention_backward(dout, q, k, v, log_decay, cu_seqlens, state=None, dlast=None,
+                                   scale=None):
+    """Gradients (dq, dk, dv, dstate) of rlcs_linear_attention from those of
+    its output and (`dlast` [sequences, Hk, D, D] float32) of its last states.
+    The gradients of a shared key/value head sum over its query heads; dstate
+    is None where no `state` was given; the decays are constants."""
+    dev, sizes, arrays, keep = _linear_args(q, k, v, log_decay, cu_seqlens, state)
+    sequences, n, Hq, Hk, D = sizes
+    dout = _like(dout, "dout", (n, Hq, D), q.dtype, dev)
+    dout = dout.clone() if dout.data_ptr() % 16 else dout
+    dlast = _matrices(dlast, "dlast", sequences, Hk, D, dev)
+    dq = _rows_out(sequences, (n, Hq, D), q)
+    dk, dv = (_rows_out(sequences, (n, Hk, D), q) for _ in range(2))
+    dstate = None if state is None else torch.empty_like(keep[5])
+    _attended.add(dev)
+    _call_with_scratch("rlcs_linear_attention_backward",
+                       _scratch_bytes("rlcs_linear_attention_scratch_bytes", *sizes),
+                       _raw_stream(dev), dout.data_ptr(), *arrays, _at(keep[5]), _at(dlast),
+                       dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _at(dstate), *sizes,
+                       _scale(scale, D), _DTYPES[q.dtype])
+    return dq, dk, dv, dstate
+
+
+@_streamed
+def rlcs_linear_attention_step(q, k, v, log_decay, state, reset=None, scale=None, new_state=None):
+    """One step of linear attention for B states: q [B, Hq, D], k and v [B, Hk,
+    D] bfloat16 (strided views are read in place), state [B, Hk, D, D]
+    float32; `reset` [B] (bool or uint8) drops the old state where it is set.
+    Returns (out [B, Hq, D], new_state). Pass `new_state=state` to update the
+    states in place."""
+    q, dev = _main(q, "q", 3, (torch.bfloat16,))
+    q, qbs, qhs = _heads(q, "q", (torch.bfloat16,), dev, 1)
+    k, kbs, khs = _heads(k, "k", (torch.bfloat16,), dev, 1)
+    v, vbs, vhs = _heads(v, "v", (torch.bfloat16,), dev, 1)
+    B, Hq, D = q.shape
+    Hk = k.shape[1]
+    if k.shape != (B, Hk, D) or v.shape != (B, Hk, D):
+        raise ValueError("k and v must have shape (%d, heads, %d)" % (B, D))
+    if Hk == 0 or Hq % Hk:
+        raise ValueError("the query heads (%d) must be a multiple of the key/value heads (%d)"
+                         % (Hq, Hk))
+    decay = _like(log_decay, "log_decay", (Hk,), torch.float32, dev)
+    old = _matrices(state, "state", B, Hk, D, dev)
+    reset = _mask(reset, "reset", (B,), dev)
+    # written through its own memory, so a caller's buffer must be contiguous
+    new_state = torch.empty_like(old) if new_state is None else _b._out(new_state, "new_state", old)
+    out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+    _call("rlcs_linear_attention_step", q.data_ptr(), qbs, qhs, k.data_ptr(), kbs, khs,
+          v.data_ptr(), vbs, vhs, decay.data_ptr(), _at(reset), old.data_ptr(),
+          new_state.data_ptr(), out.data_ptr(), B, Hq, Hk, D, _scale(scale, D), _DTYPES[q.dtype],
+          _raw_stream(dev))
+    return out, new_state
