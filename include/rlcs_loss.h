@@ -44,6 +44,11 @@
 extern "C" {
 #endif
 
+/* What the losses on the current device have recorded since this was last
+ * asked: waits for the device, returns the highest code (RLCS_OK, or
+ * RLCS_ERR_TIMEOUT where a bounded wait ran out) and clears it. */
+rlcs_status rlcs_loss_status(void);
+
 /* Clipped policy loss. With p = softmax(logits[t]), a = actions[t],
  * l = log p_a, r = exp(l - old_logp[t]), A = advantages[t]:
  *   loss = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)

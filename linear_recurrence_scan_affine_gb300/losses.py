@@ -14,8 +14,8 @@ from . import binding as _b
 from . import sequence as _s
 
 _lib = _b.lib()
-EXPORTED = ("rlcs_policy_loss", "rlcs_policy_loss_backward", "rlcs_distill_loss",
-            "rlcs_distill_loss_backward")
+EXPORTED = ("rlcs_loss_status", "rlcs_policy_loss", "rlcs_policy_loss_backward",
+            "rlcs_distill_loss", "rlcs_distill_loss_backward")
 
 #: A token's loss, log probability of its action, entropy and (given a
 #: reference) KL term, each [tokens] float32; `kl` is None without ref_logp.
@@ -26,6 +26,7 @@ def _declare():
     P, I64, F, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_double, ctypes.c_int
     row = [P, I64]
     sig = {
+        "rlcs_loss_status": [],
         "rlcs_policy_loss": row + [P] * 9 + [I64] * 2 + [F] * 4 + [I, P],
         "rlcs_policy_loss_backward": [P] + row + [P] * 10 + [I64] * 2 + [F] * 4 + [I, P],
         "rlcs_distill_loss": row + [P] * 5 + [I64] * 3 + [F, I, P],
@@ -39,6 +40,7 @@ def _declare():
 
 _declare()
 _s._fn.update((name, getattr(_lib, name)) for name in EXPORTED)
+_s._statuses.append("rlcs_loss_status")
 
 
 def _rows(logits):
@@ -46,6 +48,7 @@ def _rows(logits):
     and device."""
     x, dev = _s._main(logits, "logits", 2)
     n, V = x.shape
+    _s._attended.add(dev)
     stride = V if n <= 1 else x.stride(0)
     if (V > 1 and x.stride(1) != 1) or stride < V:
         x, stride = x.contiguous(), V

@@ -83,7 +83,8 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 # it to next on this stream runs after them.
 _alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
 _free = torch._C._cuda_cudaCachingAllocator_raw_delete
-_attended = set()  # devices with attention calls
+_attended = set()  # devices with calls that may record a status
+_statuses = ["rlcs_attention_status"]  # and the functions that read it
 
 
 @functools.lru_cache(maxsize=256)
@@ -101,11 +102,12 @@ def _call_with_scratch(name, need, stream, *args):
 
 
 def check_scratch():
-    """Wait for every device with attention calls, and raise what they recorded
-    there since the last check."""
+    """Wait for every device with calls of attention, linear attention or the
+    losses, and raise what they recorded there since the last check."""
     for dev in sorted(_attended):
         with torch.cuda.device(dev):
-            _b._check(_fn["rlcs_attention_status"](), "rlcs_attention_status")
+            for name in _statuses:
+                _b._check(_fn[name](), name)
 
 
 def _streamed(f):
