@@ -8,6 +8,7 @@ namespace {
 // The highest code that a call has recorded on this device.
 __device__ uint32_t device_status;
 constexpr int kMaxTop = 1024;
+static_assert(2 * (kMaxTop * 16 + 2 * kMaxTop * 8) <= kLongEntries, "a block holds a token's entries");
 
 struct DistillArgs {
   const void *logits;
@@ -198,33 +199,54 @@ __global__ void __launch_bounds__(kTeamBlock, team_blocks(NV))
   }
 }
 
-// The leader's first kHeld entries of each lane come a row ahead.
+// The teacher's warp: a lane's first kHeld entries are asked for together. Two
+// sets of entries take turns: a row's are made ready while the row before is
+// stored.
+struct Taught {
+  float mass, w;  // of the teacher's q; dloss / T
+  int any;        // entries at all
+};
 template <class T, bool GRAD>
 struct DistillLeader {
-  static constexpr bool kAfter = GRAD;
+  static constexpr bool kTeacher = true;
   static constexpr int kHeld = 4;
   const DistillArgs &p;
-  Entries en;
-  int id[kHeld];
-  float t[kHeld];
-  float mass, a;
-  bool any;
-  __device__ __forceinline__ void ahead(int64_t row, bool on) {
-    const int lane = threadIdx.x & 31;
-    if (!on) return;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (lane + 32 * i < p.K) {
-        id[i] = p.ids[row * p.K + lane + 32 * i];
-        t[i] = p.top[row * p.K + lane + 32 * i];
-      }
+  float *raw;
+  Taught *taught;  // in shared memory, by turns
+  int turn;
+  __device__ __forceinline__ Entries set(int i) const {
+    return entries_at(raw + i * (4 * p.K + 2 * p.slots), p.K, p.slots);
   }
-  __device__ __forceinline__ void before(int64_t row, bool on) {
+  __device__ __forceinline__ void ahead(int64_t, bool) {}
+  __device__ __forceinline__ void before(int64_t, bool) {}
+  __device__ __forceinline__ float held() const { return 0.0f; }
+  __device__ __forceinline__ void plan(int64_t, const Stats &s, bool, int, LongSmem &sm) {
+    meet_wait<64>(kTaught);
+    if ((threadIdx.x & 31) == 0) {
+      const Taught t = taught[turn];
+      sm.k = {t.w * t.mass / s.z, 0.0f};
+      sm.word = -1;
+      sm.on = t.any;
+    }
+    turn ^= 1;
+  }
+
+  __device__ __forceinline__ void prepare(int64_t row, bool on, int turn) {
     const int lane = threadIdx.x & 31;
+    const Entries en = set(turn);
     const T *x = static_cast<const T *>(p.logits) + row * p.row_stride;
     Stats te = {-INFINITY, 0.0f, 0.0f};
+    float w = 0.0f;
     if (on) {
-      float held[kHeld];
+      if (GRAD) w = p.dloss[row] * p.inv_t;
+      int id[kHeld];
+      float t[kHeld], held[kHeld];
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (lane + 32 * i < p.K) {
+          id[i] = p.ids[row * p.K + lane + 32 * i];
+          t[i] = p.top[row * p.K + lane + 32 * i];
+        }
 #pragma unroll
       for (int i = 0; i < kHeld; ++i)
         held[i] = lane + 32 * i < p.K && !absent(p, id[i], t[i]) ? value(x + id[i]) : 0.0f;
@@ -238,49 +260,57 @@ struct DistillLeader {
       }
     }
     te = join<32, false>(te, kLog2e);
-    any = on && te.z != 0.0f;  // (a NaN is an entry)
-    mass = settle<32>(p, en, row, te, lane, any, GRAD);
+    const bool any = on && te.z != 0.0f;  // (a NaN is an entry)
+    const float mass = settle<32>(p, en, row, te, lane, any, GRAD);
+    // (the student's logits are in shared memory: they have been read before
+    // another block can store a gradient over them)
+    if (lane == 0) taught[turn] = {mass, any ? w : 0.0f, any};
+    meet_arrive<64>(kTaught);
     if (GRAD) count<32>(en, lane, any);
   }
-  // (the student's logits are in shared memory: they have been read)
-  __device__ __forceinline__ float held() const { return 0.0f; }
-  __device__ __forceinline__ void plan(int64_t row, const Stats &s, bool, int, LongSmem &sm) {
-    a = GRAD && any ? p.dloss[row] * p.inv_t : 0.0f;
-    if ((threadIdx.x & 31) != 0) return;
-    sm.k = {a * mass / s.z, 0.0f};
-    sm.word = -1;
-    sm.on = any;
-  }
-  __device__ __forceinline__ void after(int64_t row, const Stats &s, bool, int rank, int ranks,
-                                        LongSmem &sm) {
+  __device__ __forceinline__ void teach(int64_t row, bool on, int rank, int ranks, LongSmem &sm) {
     const int lane = threadIdx.x & 31;
-    const Base base = base_of(s.top, p.inv_t * kLog2e);
-    if (rank == 0) {
-      const float loss = lanes_sum<32>(any ? loss_part<32>(en, base, logf(s.z), lane) : 0.0f);
-      if (lane == 0 && p.loss) p.loss[row] = loss;
-    }
-    if (!GRAD) return;
-    const Row<T> r = row_of<T>(p, row, 0, rank, ranks);
-    T *dx = static_cast<T *>(p.dlogits) + row * p.V;
-    const float scale = a * mass / s.z;
-    meet_wait<kStored>();  // then the few elements with a target, again
-    if (any)
-      for (int j = lane; j < p.K; j += 32) {
-        const int id = en.id[j], word = (id + r.skip) / kWord<T> - r.w0;
-        if (id >= 0 && word >= 0 && word < r.left)
-          put(dx + id, fmaf(ex2(base.y(en.x[j])), scale, -a * target(en, j)));
+    prepare(row, on, 0);
+    for (int turn = 0; row < p.tokens; turn ^= 1) {
+      meet_wait<kLongBlock + 32>(kPlanned + turn);
+      const int64_t next = sm.next[turn];
+      const bool more = sm.more[turn];
+      const Stats s = sm.whole;
+      if (next < p.tokens) prepare(next, more, turn ^ 1);
+      const Entries en = set(turn);
+      const Taught t = taught[turn];
+      const Base base = base_of(s.top, p.inv_t * kLog2e);
+      if (rank == 0) {
+        const float loss = lanes_sum<32>(t.any ? loss_part<32>(en, base, logf(s.z), lane) : 0.0f);
+        if (lane == 0 && p.loss) p.loss[row] = loss;
       }
-    __syncwarp();
+      if (GRAD) {
+        const Row<T> r = row_of<T>(p, row, 0, rank, ranks);
+        T *dx = static_cast<T *>(p.dlogits) + row * p.V;
+        const float scale = t.w * t.mass / s.z;
+        meet_wait(kStored);  // then the few elements with a target, again
+        if (t.any)
+          for (int j = lane; j < p.K; j += 32) {
+            const int id = en.id[j], word = (id + r.skip) / kWord<T> - r.w0;
+            if (id >= 0 && word >= 0 && word < r.left)
+              put(dx + id, fmaf(ex2(base.y(en.x[j])), scale, -t.w * target(en, j)));
+          }
+        __syncwarp();
+      }
+      row = next;
+    }
   }
 };
 
 template <class T, bool GRAD, int NV>
-__global__ void __launch_bounds__(kLongBlock, long_blocks(NV))
+__global__ void __launch_bounds__(kLongBlock + 32, long_blocks(NV))
     distill_long_kernel(const DistillArgs p) {
-  extern __shared__ float raw[];
+  extern __shared__ __align__(128) unsigned char dynamic[];
+  __shared__ Taught taught[2];
   pdl_wait();
   pdl_launch_dependents();
-  DistillLeader<T, GRAD> leader = {p, entries_at(raw, p.K, p.slots)};
+  float *raw = reinterpret_cast<float *>(dynamic + NV * kTeam * 16);  // behind a row's words
+  DistillLeader<T, GRAD> leader = {p, raw, taught, 0};
   long_rows<T, GRAD, NV, false>(p, p.inv_t * kLog2e, &device_status, leader);
 }
 
@@ -362,7 +392,8 @@ struct Distill {
   }
   template <int NV>
   static rlcs_status block(const DistillArgs &p, int ranks, size_t entries, cudaStream_t st) {
-    return launch_long<distill_long_kernel<T, GRAD, NV>>(p, ranks, entries, st);
+    return launch_long<distill_long_kernel<T, GRAD, NV>, NV>(p, kLongBlock + 32, ranks, 2 * entries,
+                                                              st);
   }
   static rlcs_status any(const DistillArgs &p, cudaStream_t st) {
     return launch_any(distill_rows_kernel<T, GRAD>, p, st);

@@ -155,14 +155,16 @@ __global__ void __launch_bounds__(kTeamBlock, team_blocks(NV)) policy_team_kerne
 
 template <class T>
 struct PolicyLeader {
-  static constexpr bool kAfter = false;
+  static constexpr bool kTeacher = false;
   const PolicyArgs &p;
-  Token a;
+  Token a, soon;
   __device__ __forceinline__ void ahead(int64_t row, bool on) {
-    if (on) a = token_of(p, row);
+    if (on) soon = token_of(p, row);
   }
   __device__ __forceinline__ void before(int64_t row, bool on) {
-    if (on) a.xa = logit_of<T>(p, row, a);
+    if (!on) return;
+    a = soon;
+    a.xa = logit_of<T>(p, row, a);
   }
   // sent along with the statistics, so that it has been read before another
   // block can write its gradient over the logits
@@ -186,14 +188,14 @@ struct PolicyLeader {
     sm.element = place % kWord<T>;
     sm.on = 1;
   }
-  __device__ __forceinline__ void after(int64_t, const Stats &, bool, int, int, LongSmem &) {}
+  __device__ __forceinline__ void teach(int64_t, bool, int, int, LongSmem &) {}
 };
 
 template <class T, bool GRAD, int NV>
 __global__ void __launch_bounds__(kLongBlock, long_blocks(NV)) policy_long_kernel(const PolicyArgs p) {
   pdl_wait();
   pdl_launch_dependents();
-  PolicyLeader<T> leader = {p, {}};
+  PolicyLeader<T> leader = {p, {}, {}};
   long_rows<T, GRAD, NV, true>(p, kLog2e, &device_status, leader);
 }
 
@@ -235,7 +237,7 @@ struct Policy {
   }
   template <int NV>
   static rlcs_status block(const PolicyArgs &p, int ranks, size_t, cudaStream_t st) {
-    return launch_long<policy_long_kernel<T, GRAD, NV>>(p, ranks, 0, st);
+    return launch_long<policy_long_kernel<T, GRAD, NV>, NV>(p, kLongBlock, ranks, 0, st);
   }
   static rlcs_status any(const PolicyArgs &p, cudaStream_t st) {
     return launch_any(policy_rows_kernel<T, GRAD>, p, st);

@@ -323,12 +323,16 @@ __device__ __forceinline__ void gradient(const uint4 &q, float2 (&d)[kWord<T> / 
   }
 }
 
-// The next row's words are asked for as this row's are used up, so that copies
-// in run beside copies out. Words of the gradient are stored whole where its
-// row starts as far into a word as that of the logits does.
-template <class T, bool GRAD, int TEAM, int NV, bool ON, bool ENTROPY, class Fix>
-__device__ __forceinline__ void use_row(uint4 (&q)[NV], const Row<T> &r, Base base, Coefficients k,
-                                        const Row<T> &next, bool more, T *dx, int64_t V, Fix fix) {
+// A row's gradient. Words are stored whole where its row starts as far into a
+// word as that of the logits does. `then(n)` follows each word.
+struct Nothing {
+  __device__ __forceinline__ void operator()(int) const {}
+};
+template <class T, bool GRAD, int TEAM, int NV, bool ON, bool ENTROPY, class Fix,
+          class Then = Nothing>
+__device__ __forceinline__ void store_row(uint4 (&q)[NV], const Row<T> &r, Base base,
+                                          Coefficients k, T *dx, int64_t V, Fix fix,
+                                          Then then = Then()) {
   const bool alike = reinterpret_cast<uintptr_t>(dx) % 16 == (uintptr_t)(r.skip * sizeof(T));
   const int full = alike ? ((int)V + r.skip) / kWord<T> - r.w0 : 0;  // words stored whole
   const bool part = r.w0 == 0 && r.skip != 0;                        // but for the first
@@ -349,8 +353,17 @@ __device__ __forceinline__ void use_row(uint4 (&q)[NV], const Row<T> &r, Base ba
       else
         store_edge(dx, r.skip, V, r.w0 + n * TEAM, o);
     }
-    load_word(q[n], next.at + n * TEAM * 16, more && next.loads(n * TEAM), kNothing<T>);
+    then(n);
   }
+}
+// The same, and the next row's words are asked for as this row's are used up,
+// so that copies in run beside copies out.
+template <class T, bool GRAD, int TEAM, int NV, bool ON, bool ENTROPY, class Fix>
+__device__ __forceinline__ void use_row(uint4 (&q)[NV], const Row<T> &r, Base base, Coefficients k,
+                                        const Row<T> &next, bool more, T *dx, int64_t V, Fix fix) {
+  store_row<T, GRAD, TEAM, NV, ON, ENTROPY>(q, r, base, k, dx, V, fix, [&](int n) {
+    load_word(q[n], next.at + n * TEAM * 16, more && next.loads(n * TEAM), kNothing<T>);
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -364,7 +377,8 @@ constexpr int team_blocks(int nv) { return nv >= 8 ? 5 : (nv == 4 ? 6 : 8); }  /
 // blocks that share them, and one warp that leads. The leader takes what a
 // token has besides its logits, joins the statistics, works out the
 // coefficients of the gradient, and fetches the next row; the others wait for
-// nothing but their words and those coefficients.
+// nothing but their words and those coefficients. What a teacher adds to a
+// token takes as long as a row does: one more warp works on it, a row ahead.
 //
 // The grid has a block (or cluster) to each row, but one that is done takes a
 // row whose block has not started yet, by cancelling that block: rows that the
@@ -377,15 +391,17 @@ constexpr int long_blocks(int nv) { return nv >= 16 ? 2 : (nv == 8 ? 3 : 4); }  
 struct LongSmem {
   alignas(16) uint4 answer[2];      // of the requests for a row
   alignas(16) float4 ranks[2][kMaxRanks];  // top, z, t of each block of the cluster
-  Stats warps[kTeam / 32];
+  Stats warps[2][kTeam / 32];
   Coefficients k;
   float gain;      // added at element `element` of word `word`
   int word, element;
   Stats whole;
   int on;          // whether the row has a gradient
-  int more;        // whether a next row does
-  int64_t next;    // it, or past the last
-  uint64_t asked[2], told[2];       // barriers: an answer, the ranks' statistics
+  // The next row, or past the last, and whether it has one. By turns: the
+  // others read a row's when the leader may be at the row after.
+  int64_t next[2];
+  int more[2];
+  uint64_t asked[2], told[2], full;  // barriers: an answer, the ranks' statistics, a row's words
   int abort;
 };
 
@@ -399,18 +415,20 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-// Named barriers between the leader's warp and the others.
-template <int ID>
-__device__ __forceinline__ void meet_arrive() {
+// Named barriers between the leader's warp and the others, or some of them.
+template <int THREADS = kLongBlock>
+__device__ __forceinline__ void meet_arrive(int id) {
   __syncwarp();
-  asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(kLongBlock) : "memory");
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
 }
-template <int ID>
-__device__ __forceinline__ void meet_wait() {
+template <int THREADS = kLongBlock>
+__device__ __forceinline__ void meet_wait(int id) {
   __syncwarp();
-  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(kLongBlock) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
 }
-constexpr int kSummed = 1, kPlanned = 2, kStored = 3;
+// Rows take turns with the first three pairs: where no gradient is formed the
+// leader and the others are up to a row apart, either way.
+constexpr int kSummed = 1, kTaken = 3, kPlanned = 5, kStored = 7, kTaught = 8;
 
 // Ask for a block that has not started; the answer goes to every block of the
 // cluster. One thread of the cluster.
@@ -459,20 +477,26 @@ __device__ __forceinline__ void tell(const float4 *place, const uint64_t *bar, u
       : "memory");
 }
 
-// Leader, each call by its whole warp:
-//   ahead(row, on)    ask for the token's own numbers, a row ahead
-//   before(row, on)   what does not need the row's statistics
-//   held()            a number read from the row, sent with its statistics
-//   plan(...)         the gradient's coefficients, into shared memory
-//   after(...)        what nobody waits for
+// What a loss adds, each call by a whole warp. The leader:
+//   ahead(next, more)  ask for a token's own numbers, a row ahead
+//   before(next, more) what of them does not need the row's statistics
+//   held()             a number read from the row, sent with its statistics
+//   plan(...)          the gradient's coefficients, into shared memory
+// With kTeacher one more warp runs teach(), from a row's plan to the next's.
 template <class T, bool GRAD, int NV, bool ENTROPY, class Leader, class Args>
 __device__ __forceinline__ void long_rows(const Args &p, float c, uint32_t *status,
                                           Leader &leader) {
+  constexpr int kPlan = kLongBlock + (Leader::kTeacher ? 32 : 0);  // who meets at a plan
+  // Without a gradient the others need to know the next row alone.
+  constexpr bool kEarly = !GRAD && !Leader::kTeacher;
+  extern __shared__ __align__(128) unsigned char dynamic[];
+  uint4 *words = reinterpret_cast<uint4 *>(dynamic);  // of the next row
   __shared__ LongSmem sm;
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) mbar_init(&sm.asked[i], 1), mbar_init(&sm.told[i], 1);
+    for (uint64_t *b : {&sm.asked[0], &sm.asked[1], &sm.told[0], &sm.told[1], &sm.full})
+      mbar_init(b, 1);
     sm.abort = 0;
     fence_mbar_init();
   }
@@ -496,45 +520,57 @@ __device__ __forceinline__ void long_rows(const Args &p, float c, uint32_t *stat
       }
       __syncwarp();
     };
+    // a row's words into shared memory, those that lie inside the array
+    const auto fetch = [&](int64_t i) {
+      if (lane == 0) {
+        const Row<T> r = row_of<T>(p, i, 0, rank, ranks);
+        const int lo = r.out ? 1 : 0, n = r.inside - lo;
+        fence_proxy_async_shared();
+        mbar_arrive_expect_tx(&sm.full, n > 0 ? n * 16 : 0);
+        if (n > 0) bulk_g2s(words + lo, r.at + lo * 16, n * 16, &sm.full);
+      }
+      __syncwarp();
+    };
     request(0);
+    if (on) fetch(row);
     leader.ahead(row, on);
+    leader.before(row, on);
     for (int i = 0; row < p.tokens; ++i) {
-      leader.before(row, on);
+      const int turn = i & 1;
       // the next row: asked for a row ago
       int64_t next = p.tokens;
-      if (tc::warp_wait(&sm.asked[i & 1], (i >> 1) & 1, abort)) {
-        const int64_t block = granted(&sm.answer[i & 1]);
+      if (tc::warp_wait(&sm.asked[turn], (i >> 1) & 1, abort)) {
+        const int64_t block = granted(&sm.answer[turn]);
         if (block >= 0) next = block / ranks;
       }
       const bool more = live(next);
+      if (lane == 0) sm.next[turn] = next, sm.more[turn] = more;
+      if (kEarly) meet_arrive<kPlan>(kPlanned + turn);
+      leader.ahead(next, more);
+      if (on) meet_wait(kTaken + turn);  // the words of this row are in registers
+      if (more) fetch(next);
       Stats s = {-INFINITY, 0.0f, 0.0f};
-      meet_wait<kSummed>();
-      if (on) s = join<kTeam / 32, ENTROPY>(sm.warps[lane % (kTeam / 32)], c);
+      meet_wait(kSummed + turn);
+      if (on) s = join<kTeam / 32, ENTROPY>(sm.warps[turn][lane % (kTeam / 32)], c);
       if (ranks > 1) {
         // A set is told again two rows later, which no block comes to before
         // all have told the row between, and so have read this one.
-        const int set = i & 1;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.told[set], 16 * ranks);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.told[turn], 16 * ranks);
         __syncwarp();
         if (lane < ranks)
-          tell(&sm.ranks[set][rank], &sm.told[set], lane,
+          tell(&sm.ranks[turn][rank], &sm.told[turn], lane,
                make_float4(s.top, s.z, s.t, leader.held()));
-        tc::warp_wait(&sm.told[set], (i >> 1) & 1, abort);
-        const float4 v = lane % kMaxRanks < ranks ? sm.ranks[set][lane % kMaxRanks]
+        tc::warp_wait(&sm.told[turn], (i >> 1) & 1, abort);
+        const float4 v = lane % kMaxRanks < ranks ? sm.ranks[turn][lane % kMaxRanks]
                                                   : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
         s = join<kMaxRanks, ENTROPY>({v.x, v.y, v.z}, c);
       }
       // every block of the cluster has read the answer by now
       if (next < p.tokens) request(i + 1);
       leader.plan(row, s, on, rank, sm);
-      if (lane == 0) {
-        sm.whole = s;
-        sm.next = next;
-        sm.more = more;
-      }
-      meet_arrive<kPlanned>();
-      leader.ahead(next, more);
-      leader.after(row, s, on, rank, ranks, sm);
+      if (lane == 0) sm.whole = s;
+      if (!kEarly) meet_arrive<kPlan>(kPlanned + turn);
+      leader.before(next, more);
       row = next;
       on = more;
     }
@@ -542,24 +578,36 @@ __device__ __forceinline__ void long_rows(const Args &p, float c, uint32_t *stat
     return;
   }
 
+  if (Leader::kTeacher && warp == kTeam / 32 + 1) {
+    leader.teach(row, on, rank, ranks, sm);
+    return;
+  }
+
   uint4 q[NV];
   Row<T> r = row_of<T>(p, row, threadIdx.x, rank, ranks);
-  load_row<T, kTeam, NV>(q, r, on);
-  while (row < p.tokens) {
+  uint32_t phase = 0;
+  for (int i = 0; row < p.tokens; ++i) {
+    const int turn = i & 1;
     if (on) {
+      tc::warp_wait(&sm.full, phase, &sm.abort);
+      phase ^= 1;
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+        q[n] = r.loads(n * kTeam) ? words[threadIdx.x + n * kTeam] : nothing(kNothing<T>);
+      meet_arrive(kTaken + turn);
       trim_row<T, kTeam, NV>(q, p, row, r);
       const int mine = r.left + lane;  // words of the run from this warp's first on
       const int used = mine <= 0 ? 0 : (mine + kTeam - 1) / kTeam;
       const Stats s = lanes_stats<T, kTeam, NV, ENTROPY>(q, c, used);
-      if (lane == 0) sm.warps[warp] = s;
+      if (lane == 0) sm.warps[turn][warp] = s;
     }
-    meet_arrive<kSummed>();
-    meet_wait<kPlanned>();
-    const int64_t next = sm.next;
-    const bool more = sm.more;
-    const Row<T> rn = row_of<T>(p, next < p.tokens ? next : 0, threadIdx.x, rank, ranks);
+    meet_arrive(kSummed + turn);
+    meet_wait<kPlan>(kPlanned + turn);
+    const int64_t next = sm.next[turn];
+    const bool more = sm.more[turn];
     T *dx = GRAD ? static_cast<T *>(p.dlogits) + row * p.V : nullptr;
-    if (on && sm.on) {
+    if (!GRAD) {
+    } else if (on && sm.on) {
       const Coefficients k = sm.k;
       const Base base = base_of(sm.whole.top, c);
       const int offset = sm.word - r.w0;
@@ -571,16 +619,16 @@ __device__ __forceinline__ void long_rows(const Args &p, float c, uint32_t *stat
           if (i == element) (i % 2 ? d[i / 2].y : d[i / 2].x) += sm.gain;
       };
       if (ENTROPY && k.b != 0.0f)
-        use_row<T, GRAD, kTeam, NV, true, ENTROPY>(q, r, base, k, rn, more, dx, p.V, fix);
+        store_row<T, GRAD, kTeam, NV, true, ENTROPY>(q, r, base, k, dx, p.V, fix);
       else
-        use_row<T, GRAD, kTeam, NV, true, false>(q, r, base, k, rn, more, dx, p.V, fix);
+        store_row<T, GRAD, kTeam, NV, true, false>(q, r, base, k, dx, p.V, fix);
     } else {
-      use_row<T, GRAD, kTeam, NV, false, false>(q, r, {0.0f, 0.0f}, {0.0f, 0.0f}, rn, more, dx,
-                                                p.V, [](float2(&)[kWord<T> / 2], int) {});
+      store_row<T, GRAD, kTeam, NV, false, false>(q, r, {0.0f, 0.0f}, {0.0f, 0.0f}, dx, p.V,
+                                                  [](float2(&)[kWord<T> / 2], int) {});
     }
-    if (Leader::kAfter) meet_arrive<kStored>();
+    if (Leader::kTeacher && GRAD) meet_arrive(kStored);
     row = next;
-    r = rn;
+    r = row_of<T>(p, row < p.tokens ? row : 0, threadIdx.x, rank, ranks);
     on = more;
   }
 }
@@ -685,16 +733,16 @@ rlcs_status launch_team(const Args &p, int per_sm, size_t entries, cudaStream_t 
   return launched(launch_ex(Kernel, dim3((unsigned)(wanted < room ? wanted : room)),
                             dim3(kTeamBlock), smem, st, true, p));
 }
-template <auto Kernel, class Args>
-rlcs_status launch_long(const Args &p, int ranks, size_t entries, cudaStream_t st) {
-  if (entries > 0) {
-    const cudaError_t e = allow_dynamic_smem<Kernel>(40960);
-    if (e != cudaSuccess) return launched(e);
-  }
+constexpr size_t kLongEntries = 65536;  // a block's, at most
+template <auto Kernel, int NV, class Args>
+rlcs_status launch_long(const Args &p, int threads, int ranks, size_t entries, cudaStream_t st) {
+  constexpr size_t kWords = (size_t)NV * kTeam * 16;
+  const cudaError_t e = allow_dynamic_smem<Kernel>(kWords + kLongEntries);
+  if (e != cudaSuccess) return launched(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.tokens * ranks));
-  cfg.blockDim = dim3(kLongBlock);
-  cfg.dynamicSmemBytes = entries;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = kWords + entries;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
