@@ -8,6 +8,9 @@
 
 namespace rlcs {
 namespace seq {
+
+uint32_t *linear_status();  // where the linear attention kernels record on this device
+
 namespace {
 
 using bf = __nv_bfloat16;
@@ -1655,15 +1658,18 @@ using namespace rlcs::seq;
 extern "C" {
 
 rlcs_status rlcs_attention_status(void) {
-  uint32_t code = 0;
+  uint32_t code = 0, linear = 0;
   const uint32_t none = 0;
-  if (cudaDeviceSynchronize() != cudaSuccess ||
+  uint32_t *other = linear_status();
+  if (cudaDeviceSynchronize() != cudaSuccess || !other ||
       cudaMemcpyFromSymbol(&code, device_status, sizeof(code)) != cudaSuccess ||
-      (code && cudaMemcpyToSymbol(device_status, &none, sizeof(none)) != cudaSuccess)) {
+      cudaMemcpy(&linear, other, sizeof(linear), cudaMemcpyDeviceToHost) != cudaSuccess ||
+      (code && cudaMemcpyToSymbol(device_status, &none, sizeof(none)) != cudaSuccess) ||
+      (linear && cudaMemset(other, 0, sizeof(linear)) != cudaSuccess)) {
     cudaGetLastError();
     return RLCS_ERR_CUDA;
   }
-  return static_cast<rlcs_status>(code);
+  return static_cast<rlcs_status>(code > linear ? code : linear);
 }
 
 size_t rlcs_attention_scratch_bytes(int64_t tokens, int64_t Hq) {

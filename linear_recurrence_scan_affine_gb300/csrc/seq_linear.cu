@@ -11,6 +11,7 @@
 // A state is shared by the query heads of its group: they are several x
 // forwards, several y and z backwards.
 #include "seq_common.cuh"
+#include "tensor_core.cuh"
 
 namespace rlcs {
 namespace seq {
@@ -22,84 +23,696 @@ struct View {  // [tokens, heads, D]
   const bf *p;
   int64_t token, head;
 };
+
+// ---------------------------------------------------------------------------
+// Where a block works: segments of `length` tokens (a multiple of 128) of each
+// sequence. Segment j of sequence s has slot cu[s] / length + s + j: slots of
+// different sequences do not meet, and no sums over the sequences are needed.
+// ---------------------------------------------------------------------------
+constexpr int kChunk = 128;  // tokens whose weights are formed together
+
+struct Segment {
+  int seq, lo, len;      // the sequence's first token and length
+  int first, rows;       // the segment in it
+  bool any;
+};
+__device__ __forceinline__ int bound(const int32_t *cu, int64_t i, int tokens) {
+  const int b = __ldg(cu + i);
+  return b < 0 ? 0 : (b < tokens ? b : tokens);
+}
+__device__ __forceinline__ int slot_of(int lo, int seq, int length) { return lo / length + seq; }
+// One warp: the last sequence whose first slot is not past `slot`, by 32 probes
+// a round.
+__device__ __forceinline__ Segment find_segment(const int32_t *cu, int sequences, int tokens,
+                                                int slot, int length) {
+  const int lane = threadIdx.x & 31;
+  int from = 0, count = sequences;  // the sequence is in [from, from + count)
+  while (count > 1) {
+    const int step = (count + 31) / 32, at = from + lane * step;
+    const bool on = lane * step < count && slot_of(bound(cu, at, tokens), at, length) <= slot;
+    const unsigned b = __ballot_sync(kFull, on);
+    const int last = b ? 31 - __clz(b) : 0;
+    from += last * step;
+    count = count - last * step < step ? count - last * step : step;
+  }
+  Segment g;
+  g.seq = from;
+  g.lo = bound(cu, from, tokens);
+  const int hi = bound(cu, from + 1, tokens);
+  g.len = hi > g.lo ? hi - g.lo : 0;
+  const int64_t first = (int64_t)(slot - slot_of(g.lo, from, length)) * length;
+  g.any = first >= 0 && first < g.len;
+  g.first = g.any ? (int)first : 0;
+  g.rows = g.any ? (g.len - g.first < length ? g.len - g.first : length) : 0;
+  return g;
+}
+int64_t slots(int64_t sequences, int64_t tokens, int64_t length) {
+  return tokens / length + sequences;
+}
+
+// a^n for a = 2^l2; 1 for n = 0 whatever a is.
+__device__ __forceinline__ float power(float l2, int n) {
+  return n == 0 ? 1.0f : exp2f(l2 * (float)n);
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The highest code that a call has recorded on this device.
+__device__ uint32_t device_status;
+
+// ---------------------------------------------------------------------------
+// The walk in chunks of 128 tokens, a block to a segment and head of x.
+//
+// Per chunk, with rows r of x and c of y and z, d = r - c (c - r backwards),
+//   P = X Y^T,  P' = P a^d for d >= 0 and 0 elsewhere,
+//   O1 = P' Z,  O2 = X S,  out = O1 + a^into O2,  U = (a^left Y)^T Z,  S = a^n S + U,
+// into the steps from the state to a row, left those from a row to the state.
+// Warps 0..7 turn P into P' and sums into results, two threads to a row; the
+// decays of a thread's columns stay in registers, the same for every chunk.
+// Warps 8..15 scale Y in place, keep S (float32, in registers) and hand its
+// rounding to bfloat16 to the next chunk. Warp 16 copies, warp 17 issues
+// products. In tensor memory: P (P' over it), O1, O2, U.
+// ---------------------------------------------------------------------------
 struct WalkArgs {
-  View x, y, z;
   const float *log_decay;
   const int32_t *cu;
-  const float *init;  // [sequences, Hk, D, D] or null
-  float *last;        // the same
-  bf *out;            // [tokens, Hk * nx, D]
+  const float *init;   // [slots or sequences, Hk, D, D] or null
+  bf *out;             // [tokens, heads of x, D]
   int64_t sequences, tokens;
-  int Hk, nx, ny, D;
-  bool backward, transposed;  // walk from the end; init is [z's dimension, y's]
+  int heads, nx, ny;   // heads of x; of x and of y and z to a state
+  int D, length;       // of a segment
+  bool by_slot;        // init is by slot, else by sequence
+  bool transposed;     // init is [z's dimension, y's]
   float in_scale, out_scale;  // of y z^T, and of x S
 };
 
-// One column of the state to a thread.
 template <int DP>
-__global__ void __launch_bounds__(DP) linear_walk_kernel(const WalkArgs p) {
-  __shared__ float x[DP], y[DP];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int e = threadIdx.x, h = blockIdx.x % p.Hk, D = p.D;
-  const int64_t s = blockIdx.x / p.Hk, tokens = p.tokens;
-  const auto bound = [&](int64_t i) {
-    const int64_t b = p.cu[i];
-    return b < 0 ? 0 : (b < tokens ? b : tokens);
-  };
-  if (s == p.sequences) {  // tokens that no sequence holds
-    const int64_t lo = bound(0), hi = bound(p.sequences);
-    for (int64_t t = 0; t < tokens; ++t)
-      if ((t < lo || t >= hi) && e < D)
-        for (int i = 0; i < p.nx; ++i)
-          p.out[((t * p.Hk + h) * p.nx + i) * D + e] = __float2bfloat16_rn(0.0f);
-    return;
-  }
-  const int64_t lo = bound(s), hi = bound(s + 1), n = hi > lo ? hi - lo : 0;
-  const float a = expf(p.log_decay[h]);
-  const int64_t base = (s * p.Hk + h) * D * D;
-  float S[DP];
-#pragma unroll
-  for (int d = 0; d < DP; ++d)
-    S[d] = p.init && d < D && e < D ? p.init[base + (p.transposed ? e * D + d : d * D + e)] : 0.0f;
-  for (int64_t i = 0; i < n; ++i) {
-    const int64_t t = p.backward ? hi - 1 - i : lo + i;
-    if (!p.backward)
-#pragma unroll
-      for (int d = 0; d < DP; ++d) S[d] = a == 0.0f ? 0.0f : S[d] * a;
-    for (int j = 0; j < p.ny; ++j) {
-      __syncthreads();
-      y[e] = e < D ? __bfloat162float(p.y.p[t * p.y.token + (h * p.ny + j) * p.y.head + e]) : 0.0f;
-      __syncthreads();
-      const float z = e < D ? p.in_scale * __bfloat162float(
-                                  p.z.p[t * p.z.token + (h * p.ny + j) * p.z.head + e]) : 0.0f;
-#pragma unroll
-      for (int d = 0; d < DP; ++d) S[d] = fmaf(y[d], z, S[d]);
-    }
-    for (int j = 0; j < p.nx; ++j) {
-      __syncthreads();
-      x[e] = e < D ? __bfloat162float(p.x.p[t * p.x.token + (h * p.nx + j) * p.x.head + e]) : 0.0f;
-      __syncthreads();
-      float o = 0.0f;
-#pragma unroll
-      for (int d = 0; d < DP; ++d) o = fmaf(x[d], S[d], o);
-      if (e < D)
-        p.out[((t * p.Hk + h) * p.nx + j) * D + e] = __float2bfloat16_rn(o * p.out_scale);
-    }
-    if (p.backward)
-#pragma unroll
-      for (int d = 0; d < DP; ++d) S[d] = a == 0.0f ? 0.0f : S[d] * a;
-  }
-  if (p.last && e < D)
-#pragma unroll
-    for (int d = 0; d < DP; ++d)
-      if (d < D) p.last[base + (p.transposed ? e * D + d : d * D + e)] = S[d];
+struct WalkSmem {
+  // (z after y: with 64 columns a product reads past y, into rows of its result
+  // that are not used)
+  alignas(1024) unsigned char x[2][DP * 256], y[2][DP * 256], z[2][DP * 256], s[DP * DP * 2];
+  float power[kChunk + 1];
+  uint64_t x_empty[2], full[2], empty[2];
+  uint64_t p_full, p_ready, o_full, o_free, y_ready, u_full, s_ready;
+  Segment segment;
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kWalkThreads = 18 * 32;
+
+__device__ __forceinline__ void settle(int abort) {
+  if (!abort) return;
+  for (int i = 0; i < 1000; ++i) __nanosleep(2000);
+  if (threadIdx.x == 0) atomicMax(&device_status, (uint32_t)RLCS_ERR_TIMEOUT);
 }
 
-cudaError_t launch_walk(const WalkArgs &p, cudaStream_t st) {
-  const dim3 grid((unsigned)((p.sequences + 1) * p.Hk));
-  return p.D <= 64 ? launch_ex(linear_walk_kernel<64>, grid, dim3(64), 0, st, true, p)
-                   : launch_ex(linear_walk_kernel<128>, grid, dim3(128), 0, st, true, p);
+// A = Y in shared memory, its columns the rows of the product.
+template <int DP>
+__device__ __forceinline__ void product_tn(uint32_t lead, uint32_t d, uint32_t y, uint32_t z,
+                                           bool add) {
+  const uint32_t a = tc::operand_n<kChunk>(y), b = tc::operand_n<kChunk>(z);
+#pragma unroll
+  for (int k = 0; k < kChunk / 16; ++k)
+    tc::mma_ss(lead, d, a + k * (2048 >> 4), b + k * (2048 >> 4),
+               tc::instr(DP, true) | (1u << 15), add || k > 0);
+}
+// X [128 x DP] S [DP x DP]
+template <int DP>
+__device__ __forceinline__ void product_state(uint32_t lead, uint32_t d, uint32_t x, uint32_t s) {
+  const uint32_t a = tc::operand_k(x), b = tc::operand_n<DP>(s);
+#pragma unroll
+  for (int k = 0; k < DP / 16; ++k)
+    tc::mma_ss(lead, d, a + (((k / 4) * 16384 + (k % 4) * 32) >> 4), b + k * (2048 >> 4),
+               tc::instr(DP, true), k > 0);
+}
+
+// Eight bf16 values times f.
+__device__ __forceinline__ uint4 scaled(const uint4 &v, float f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = pack_bf16(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Rows of out that no sequence holds, each block taking a share.
+__device__ __noinline__ void zero_unheld(bf *out, int width, int lo, int hi, int tokens, int thread,
+                                         int threads) {
+  const int eights = width / 8;
+  const int64_t n = (int64_t)(lo + tokens - hi) * eights;
+  for (int64_t i = (int64_t)blockIdx.x * threads + thread; i < n;
+       i += (int64_t)gridDim.x * threads) {
+    const int64_t row = i / eights;
+    reinterpret_cast<uint4 *>(out + (row < lo ? row : row - lo + hi) * width)[i % eights] =
+        make_uint4(0, 0, 0, 0);
+  }
+}
+
+template <int DP, bool BACK>
+__global__ void __launch_bounds__(kWalkThreads, 1)
+    linear_walk_kernel(const __grid_constant__ CUtensorMap mx,
+                       const __grid_constant__ CUtensorMap my,
+                       const __grid_constant__ CUtensorMap mz, const WalkArgs p) {
+  extern __shared__ __align__(1024) unsigned char raw[];
+  WalkSmem<DP> &sm = *reinterpret_cast<WalkSmem<DP> *>(raw);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
+  const int h = blockIdx.x % p.heads, state_head = h / p.nx;
+  const int tokens = (int)p.tokens, sequences = (int)p.sequences;
+  if (warp == 17) tc::tmem_alloc(&sm.tmem, 512);
+  if (warp == 16) {
+    const Segment g = find_segment(p.cu, sequences, tokens, blockIdx.x / p.heads, p.length);
+    if (lane == 0) {
+      sm.segment = g;
+      sm.abort = (tc::smem_addr(raw) & 1023) != 0;  // the swizzle counts from there
+      for (uint64_t *b : {&sm.x_empty[0], &sm.x_empty[1], &sm.full[0], &sm.full[1], &sm.empty[0],
+                          &sm.empty[1], &sm.p_full, &sm.o_full, &sm.u_full})
+        mbar_init(b, 1);
+      for (uint64_t *b : {&sm.p_ready, &sm.o_free, &sm.y_ready, &sm.s_ready}) mbar_init(b, 8);
+      fence_mbar_init();
+    }
+  }
+  const float l2 = __ldg(p.log_decay + state_head) * kLog2e;
+  if (threadIdx.x <= kChunk) sm.power[threadIdx.x] = power(l2, threadIdx.x);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const Segment g = sm.segment;
+  const int lo = bound(p.cu, 0, tokens), hi = bound(p.cu, sequences, tokens);
+  if (warp < 8 && (lo > 0 || hi < tokens))
+    zero_unheld(p.out, p.heads * p.D, lo, hi > lo ? hi : lo, tokens, threadIdx.x, 256);
+  if (!g.any || sm.abort) {
+    if (warp == 17) tc::tmem_dealloc(sm.tmem, 512);
+    if (sm.abort && threadIdx.x == 0) atomicMax(&device_status, (uint32_t)RLCS_ERR_CUDA);
+    return;
+  }
+  const int chunks = (g.rows + kChunk - 1) / kChunk;
+  // chunk number `c` in the order walked: its first row in the sequence
+  const auto first_row = [&](int c) {
+    return g.first + (BACK ? chunks - 1 - c : c) * kChunk;
+  };
+  const auto rows_of = [&](int c) {
+    const int left = g.first + g.rows - first_row(c);
+    return left < kChunk ? left : kChunk;
+  };
+  const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
+  const uint32_t tP = tmem, tO = tmem + 128, tX = tmem + 256, tU = tmem + 384;
+  volatile int *abort = &sm.abort;
+  const uint32_t lead = lane == 0;
+
+  if (warp == 16) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int c = 0, it = 0; c < chunks && ok; ++c)
+        for (int j = 0; j < p.ny && ok; ++j, ++it) {
+          const int st = it & 1, token = g.lo + first_row(c);
+          if (it >= 2) ok = tc::mbar_wait(&sm.empty[st], ((it >> 1) - 1) & 1, abort);
+          if (ok && j == 0 && c >= 2) ok = tc::mbar_wait(&sm.x_empty[c & 1], ((c >> 1) - 1) & 1, abort);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&sm.full[st], DP * 256 * (j == 0 ? 3 : 2));
+          const int head = state_head * p.ny + j;
+#pragma unroll
+          for (int b = 0; b < DP / 64; ++b) {
+            if (j == 0)
+              tc::load_box(sm.x[c & 1] + b * 16384, &mx, &sm.full[st], b * 64, h, token);
+            tc::load_box(sm.y[st] + b * 16384, &my, &sm.full[st], b * 64, head, token);
+            tc::load_box(sm.z[st] + b * 16384, &mz, &sm.full[st], b * 64, head, token);
+          }
+        }
+    }
+  } else if (warp == 17) {
+    bool ok = true;
+    for (int c = 0, it = 0; c < chunks && ok; ++c) {
+      const int n = rows_of(c);
+      const uint32_t x = tc::smem_addr(sm.x[c & 1]);
+      for (int j = 0; j < p.ny && ok; ++j, ++it) {
+        const int st = it & 1;
+        const uint32_t y = tc::smem_addr(sm.y[st]), z = tc::smem_addr(sm.z[st]);
+        if (!(ok = tc::warp_wait(&sm.full[st], (it >> 1) & 1, abort))) break;
+        if (n < kChunk) {  // what follows the sequence is another's: it must be finite
+          if (j == 0) tc::clear_rows<DP, kChunk>(sm.x[c & 1], n, lane);
+          tc::clear_rows<DP, kChunk>(sm.y[st], n, lane);
+          tc::clear_rows<DP, kChunk>(sm.z[st], n, lane);
+          __syncwarp();
+        }
+        tc::product_nt<DP, kChunk>(lead, tP, x, y);
+        tc::commit(lead, &sm.p_full);
+        if (j == 0) {
+          ok = tc::warp_wait(&sm.s_ready, c & 1, abort) &&
+               (c == 0 || tc::warp_wait(&sm.o_free, (c - 1) & 1, abort));
+          if (!ok) break;
+          tc::fence_after_sync();
+          product_state<DP>(lead, tX, x, tc::smem_addr(sm.s));
+        }
+        if (!(ok = tc::warp_wait(&sm.p_ready, it & 1, abort))) break;
+        tc::fence_after_sync();
+        tc::product_parts<DP, kChunk, 4>(lead, tO, tP, z, j > 0);
+        if (j + 1 == p.ny) tc::commit(lead, &sm.o_full);
+        if (!(ok = tc::warp_wait(&sm.y_ready, it & 1, abort))) break;
+        tc::fence_after_sync();
+        product_tn<DP>(lead, tU, y, z, j > 0);
+        tc::commit(lead, &sm.empty[st]);
+        if (j + 1 == p.ny) {
+          tc::commit(lead, &sm.u_full);
+          tc::commit(lead, &sm.x_empty[c & 1]);
+        }
+      }
+    }
+  } else if (warp < 8) {
+    const int r = threadIdx.x & 127, half = warp >> 2;  // the row, and half of its columns
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    float decay[64];
+#pragma unroll
+    for (int c = 0; c < 64; ++c) {
+      const int d = BACK ? half * 64 + c - r : r - (half * 64 + c);
+      decay[c] = d >= 0 ? sm.power[d >= 0 ? d : 0] * p.in_scale : 0.0f;
+    }
+    for (int c = 0, it = 0; c < chunks; ++c) {
+      for (int j = 0; j < p.ny; ++j, ++it) {
+        tc::warp_wait(&sm.p_full, it & 1, abort);
+        tc::fence_after_sync();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t at = tP + lanes + half * 64 + i * 32;
+          uint32_t v[32], w[16];
+          tc::ld32(at, v);
+          tc::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 t = __fmul2_rn(make_float2(__uint_as_float(v[2 * e]),
+                                                    __uint_as_float(v[2 * e + 1])),
+                                        make_float2(decay[i * 32 + 2 * e], decay[i * 32 + 2 * e + 1]));
+            w[e] = pack_bf16(t.x, t.y);  // the type that the product takes
+          }
+          tc::st16(at, w);
+        }
+        tc::wait_st();
+        tc::fence_before_sync();
+        tc::warp_arrive(&sm.p_ready, lead);
+      }
+      const int n = rows_of(c), to_row = BACK ? n - 1 - r : r + 1;
+      const float into = sm.power[to_row < 0 ? 0 : to_row] * p.out_scale;
+      const int64_t row = (int64_t)g.lo + first_row(c) + r;
+      bf *out = p.out + (row * p.heads + h) * p.D + half * (DP / 2);
+      tc::warp_wait(&sm.o_full, c & 1, abort);
+      tc::fence_after_sync();
+#pragma unroll
+      for (int i = 0; i < DP / 64; ++i) {
+        uint32_t a[32], b[32];
+        tc::ld32(tO + lanes + half * (DP / 2) + i * 32, a);
+        tc::ld32(tX + lanes + half * (DP / 2) + i * 32, b);
+        tc::wait_ld();
+        if (i + 1 == DP / 64) {
+          tc::fence_before_sync();
+          tc::warp_arrive(&sm.o_free, lead);
+        }
+        if (r < n && !*abort)
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            if (half * (DP / 2) + i * 32 + e < p.D) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = make_float2(into, into), o = make_float2(p.out_scale, p.out_scale);
+                const int q = e + 2 * k;
+                float2 t = __fmul2_rn(make_float2(__uint_as_float(a[q]), __uint_as_float(a[q + 1])), o);
+                // (a row that the state does not reach takes nothing of it, whatever it holds)
+                if (into != 0.0f)
+                  t = __ffma2_rn(make_float2(__uint_as_float(b[q]), __uint_as_float(b[q + 1])), f, t);
+                w[k] = pack_bf16(t.x, t.y);
+              }
+              *reinterpret_cast<uint4 *>(out + i * 32 + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+      }
+    }
+  } else {
+    const int t = threadIdx.x - 256, r = t & 127, half = (warp - 8) >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    constexpr int HC = DP / 2;  // columns of the state to a thread, in row r of it
+    const bool holds = r < DP;
+    float s[HC];
+    {
+      const int64_t at =
+          ((p.by_slot ? (int64_t)(blockIdx.x / p.heads) : (int64_t)g.seq) * (p.heads / p.nx) +
+           state_head) * p.D * p.D;
+#pragma unroll
+      for (int c = 0; c < HC; ++c) {
+        const int col = half * HC + c;
+        s[c] = p.init && r < p.D && col < p.D
+                   ? __ldg(p.init + at + (p.transposed ? (int64_t)col * p.D + r
+                                                       : (int64_t)r * p.D + col))
+                   : 0.0f;
+      }
+    }
+    // rows of the state as the product's second operand: boxes of 64 columns
+    const auto hand_over = [&] {
+      if (holds)
+#pragma unroll
+        for (int c = 0; c < HC; c += 8) {
+          const int col = half * HC + c, chunk = (col % 64) / 8;
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = pack_bf16(s[c + 2 * k], s[c + 2 * k + 1]);
+          *reinterpret_cast<uint4 *>(sm.s + (col / 64) * DP * 128 + r * 128 +
+                                     ((chunk ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      fence_proxy_async_shared();
+      tc::warp_arrive(&sm.s_ready, lead);
+    };
+    hand_over();
+    for (int c = 0, it = 0; c < chunks; ++c) {
+      const int n = rows_of(c);
+      for (int j = 0; j < p.ny; ++j, ++it) {
+        uint4 *y = reinterpret_cast<uint4 *>(sm.y[it & 1]);
+        tc::warp_wait(&sm.p_full, it & 1, abort);  // P has been formed from the unscaled keys
+#pragma unroll 4
+        for (int i = t; i < DP * 16; i += 256) {
+          const int row = i / 8 % kChunk, left = BACK ? row + 1 : n - 1 - row;
+          y[i] = row < n ? scaled(y[i], sm.power[left < 0 ? 0 : left] * p.in_scale)
+                         : make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_shared();
+        tc::warp_arrive(&sm.y_ready, lead);
+      }
+      tc::warp_wait(&sm.u_full, c & 1, abort);
+      if (c + 1 == chunks) break;
+      tc::fence_after_sync();
+      const float keep = sm.power[n];
+#pragma unroll
+      for (int i = 0; i < HC / 32; ++i) {
+        uint32_t u[32];
+        tc::ld32(tU + lanes + half * HC + i * 32, u);
+        tc::wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          // (a decay of zero keeps nothing, whatever the state holds)
+          const float old = keep == 0.0f ? 0.0f : keep * s[i * 32 + e];
+          s[i * 32 + e] = old + __uint_as_float(u[e]);
+        }
+      }
+      tc::fence_before_sync();
+      hand_over();
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  settle(sm.abort);
+  if (warp == 17) tc::tmem_dealloc(sm.tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// What a segment adds to the state: sum a^left y z^T over its tokens, left the
+// steps to its end. Float32 results come from here, so a decayed key is held in
+// two bfloat16 parts, off by at most 2^-16 together: two products.
+// ---------------------------------------------------------------------------
+struct SumArgs {
+  const float *log_decay;
+  const int32_t *cu;
+  const float *init;  // [sequences, Hk, D, D] or null, where the sums are final
+  float *sums;        // [slots, Hk, D, D], or [sequences, Hk, D, D] where final
+  int64_t sequences, tokens;
+  int Hk, ny, D, length;
+  bool final;         // one segment to a sequence: add what is left of init
+  bool all;           // sums of every segment, not only of those that others follow
+  float in_scale;
+};
+template <int DP>
+struct SumSmem {
+  // (in this order: with 64 columns a product reads past y and rest, into rows
+  // of its result that are not used)
+  alignas(1024) unsigned char y[2][DP * 256], rest[2][DP * 256], z[2][DP * 256];
+  uint64_t full[2], empty[2], ready[2], done;
+  Segment segment;
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kSumThreads = 10 * 32;
+
+template <int DP, bool BACK>
+__global__ void __launch_bounds__(kSumThreads, 1)
+    linear_sum_kernel(const __grid_constant__ CUtensorMap my,
+                      const __grid_constant__ CUtensorMap mz, const SumArgs p) {
+  extern __shared__ __align__(1024) unsigned char raw[];
+  SumSmem<DP> &sm = *reinterpret_cast<SumSmem<DP> *>(raw);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
+  const int h = blockIdx.x % p.Hk, slot = blockIdx.x / p.Hk;
+  const int tokens = (int)p.tokens, sequences = (int)p.sequences;
+  if (warp == 9) tc::tmem_alloc(&sm.tmem, 128);
+  if (warp == 8) {
+    const Segment g = find_segment(p.cu, sequences, tokens, slot, p.length);
+    if (lane == 0) {
+      sm.segment = g;
+      sm.abort = (tc::smem_addr(raw) & 1023) != 0;
+      for (uint64_t *b : {&sm.full[0], &sm.full[1], &sm.empty[0], &sm.empty[1], &sm.done})
+        mbar_init(b, 1);
+      for (uint64_t *b : {&sm.ready[0], &sm.ready[1]}) mbar_init(b, 8);
+      fence_mbar_init();
+    }
+  }
+  const float l2 = __ldg(p.log_decay + h) * kLog2e;
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const Segment g = sm.segment;
+  // a segment that no other follows in the walk is summed for the last state alone
+  const bool followed = BACK ? g.first > 0 : g.first + g.rows < g.len;
+  const bool work = g.any && !sm.abort && (p.all || followed);
+  if (!work) {
+    if (warp == 9) tc::tmem_dealloc(sm.tmem, 128);
+    if (sm.abort && threadIdx.x == 0) atomicMax(&device_status, (uint32_t)RLCS_ERR_CUDA);
+    // an empty sequence's last state is its first
+    if (p.final && !g.any && slot == slot_of(g.lo, g.seq, p.length) && g.len == 0) {
+      const int64_t at = ((int64_t)g.seq * p.Hk + h) * p.D * p.D;
+      for (int i = threadIdx.x; i < p.D * p.D; i += kSumThreads)
+        p.sums[at + i] = p.init ? p.init[at + i] : 0.0f;
+    }
+    return;
+  }
+  const int chunks = (g.rows + kChunk - 1) / kChunk, items = chunks * p.ny;
+  const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
+  volatile int *abort = &sm.abort;
+  const uint32_t lead = lane == 0;
+  if (warp == 8) {
+    if (lane == 0)
+      for (int it = 0; it < items; ++it) {
+        const int st = it & 1, token = g.lo + g.first + it / p.ny * kChunk;
+        if (it >= 2 && !tc::mbar_wait(&sm.empty[st], ((it >> 1) - 1) & 1, abort)) break;
+        mbar_arrive_expect_tx(&sm.full[st], DP * 256 * 2);
+#pragma unroll
+        for (int b = 0; b < DP / 64; ++b) {
+          tc::load_box(sm.y[st] + b * 16384, &my, &sm.full[st], b * 64, h * p.ny + it % p.ny, token);
+          tc::load_box(sm.z[st] + b * 16384, &mz, &sm.full[st], b * 64, h * p.ny + it % p.ny, token);
+        }
+      }
+  } else if (warp == 9) {
+    for (int it = 0; it < items; ++it) {
+      const int st = it & 1, n = g.rows - it / p.ny * kChunk;
+      if (!tc::warp_wait(&sm.full[st], (it >> 1) & 1, abort)) break;
+      if (n < kChunk) {
+        tc::clear_rows<DP, kChunk>(sm.z[st], n, lane);
+        __syncwarp();
+      }
+      if (!tc::warp_wait(&sm.ready[st], (it >> 1) & 1, abort)) break;
+      tc::fence_after_sync();
+      const uint32_t z = tc::smem_addr(sm.z[st]);
+      product_tn<DP>(lead, tmem, tc::smem_addr(sm.rest[st]), z, it > 0);
+      product_tn<DP>(lead, tmem, tc::smem_addr(sm.y[st]), z, true);
+      tc::commit(lead, &sm.empty[st]);
+    }
+    tc::commit(lead, &sm.done);
+  } else {
+    for (int it = 0; it < items; ++it) {
+      const int st = it & 1, first = it / p.ny * kChunk;
+      tc::warp_wait(&sm.full[st], (it >> 1) & 1, abort);
+      uint4 *y = reinterpret_cast<uint4 *>(sm.y[st]), *rest = reinterpret_cast<uint4 *>(sm.rest[st]);
+#pragma unroll 4
+      for (int i = threadIdx.x; i < DP * 16; i += 256) {
+        const int row = first + i / 8 % kChunk, left = BACK ? row + 1 : g.rows - 1 - row;
+        const float f = row < g.rows ? power(l2, left) * p.in_scale : 0.0f;
+        const uint4 v = row < g.rows ? y[i] : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float t0 = __uint_as_float(w[k] << 16) * f, t1 = __uint_as_float(w[k] & 0xffff0000u) * f;
+          a[k] = pack_bf16(t0, t1);
+          b[k] = pack_bf16(t0 - __uint_as_float(a[k] << 16), t1 - __uint_as_float(a[k] & 0xffff0000u));
+        }
+        y[i] = make_uint4(a[0], a[1], a[2], a[3]);
+        rest[i] = make_uint4(b[0], b[1], b[2], b[3]);
+      }
+      fence_proxy_async_shared();
+      tc::warp_arrive(&sm.ready[st], lead);
+    }
+    const int r = threadIdx.x & 127, half = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const bool fine = tc::warp_wait(&sm.done, 0, abort);
+    tc::fence_after_sync();
+    const int64_t at = ((p.final ? (int64_t)g.seq : (int64_t)slot) * p.Hk + h) * p.D * p.D;
+    const float keep = p.final ? power(l2, g.rows) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < DP / 64; ++i) {
+      const int col = half * (DP / 2) + i * 32;
+      uint32_t u[32];
+      tc::ld32(tmem + lanes + col, u);
+      tc::wait_ld();
+      if (fine && r < p.D)
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          if (col + e < p.D) {
+            const int64_t to = at + (int64_t)r * p.D + col + e;
+            float4 v = make_float4(__uint_as_float(u[e]), __uint_as_float(u[e + 1]),
+                                   __uint_as_float(u[e + 2]), __uint_as_float(u[e + 3]));
+            if (p.init && keep != 0.0f) {
+              const float4 o = __ldg(reinterpret_cast<const float4 *>(p.init + to));
+              v.x = fmaf(keep, o.x, v.x);
+              v.y = fmaf(keep, o.y, v.y);
+              v.z = fmaf(keep, o.z, v.z);
+              v.w = fmaf(keep, o.w, v.w);
+            }
+            *reinterpret_cast<float4 *>(p.sums + to) = v;
+          }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  settle(sm.abort);
+  if (warp == 9) tc::tmem_dealloc(sm.tmem, 128);
+}
+
+// The states before each segment from what the segments add, in place, and
+// the state after the last: an element to a thread.
+struct JoinArgs {
+  const float *log_decay;
+  const int32_t *cu;
+  const float *init;
+  float *sums, *last;
+  int64_t sequences, tokens;
+  int Hk, D, length;
+  bool back, transposed;
+};
+__global__ void __launch_bounds__(256) linear_join_kernel(const JoinArgs p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int size = p.D * p.D, i = blockIdx.x * 256 + threadIdx.x;
+  const int64_t unit = blockIdx.y + (int64_t)blockIdx.z * 65535;
+  if (i >= size || unit >= p.sequences * p.Hk) return;
+  const int seq = (int)(unit / p.Hk), h = (int)(unit % p.Hk);
+  const int lo = bound(p.cu, seq, (int)p.tokens), hi = bound(p.cu, seq + 1, (int)p.tokens);
+  const int len = hi > lo ? hi - lo : 0, n = (len + p.length - 1) / p.length;
+  const float l2 = __ldg(p.log_decay + h) * kLog2e;
+  const int64_t own = unit * size + (p.transposed ? i % p.D * p.D + i / p.D : i);
+  float run = p.init ? __ldg(p.init + own) : 0.0f;
+  float *at = p.sums + ((int64_t)slot_of(lo, seq, p.length) * p.Hk + h) * size + i;
+  const int64_t step = (int64_t)p.Hk * size;
+  for (int j = 0; j < n; j += 8) {
+    float add[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int seg = p.back ? n - 1 - j - k : j + k;
+      // the last one walked is summed only if the last state is asked for
+      add[k] = j + k < n - 1 || (j + k == n - 1 && p.last) ? at[seg * step] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (j + k >= n) break;
+      const int seg = p.back ? n - 1 - j - k : j + k;
+      const int rows = len - seg * p.length < p.length ? len - seg * p.length : p.length;
+      const float keep = power(l2, rows);
+      at[seg * step] = run;
+      run = (keep == 0.0f ? 0.0f : keep * run) + add[k];
+    }
+  }
+  if (p.last) p.last[own] = run;
+}
+
+// ---------------------------------------------------------------------------
+// Host: one walk
+// ---------------------------------------------------------------------------
+struct Walk {
+  View x, y, z;
+  const float *log_decay;
+  const int32_t *cu;
+  const float *init;
+  float *last;
+  bf *out;
+  int64_t sequences, tokens;
+  int Hk, nx, ny, D;
+  bool back, transposed;
+  float in_scale, out_scale;
+};
+
+// Tokens to a segment. Segments cost a second reading of y and z and a pass
+// over the states, so they are taken where sequences and heads alone leave
+// SMs without work: as many as make two blocks to an SM, none under 1024 tokens.
+int64_t segment_length(int64_t sequences, int64_t tokens, int64_t heads) {
+  const int64_t whole = (tokens + kChunk - 1) / kChunk * kChunk;
+  if (sequences * heads * 4 >= kSms * 3 || tokens <= 2048) return whole > 0 ? whole : kChunk;
+  const int64_t each = (tokens * heads + 2 * kSms - 1) / (2 * kSms);
+  const int64_t length = (each + kChunk - 1) / kChunk * kChunk;
+  return length < 1024 ? 1024 : length;
+}
+size_t sums_bytes(int64_t sequences, int64_t tokens, int64_t heads, int64_t Hk, int64_t D) {
+  const int64_t length = segment_length(sequences, tokens, heads);
+  if (length >= tokens) return 0;
+  return (size_t)(slots(sequences, tokens, length) * Hk * D * D) * 4;
+}
+
+bool map_of(CUtensorMap *m, const View &v, const Walk &w, int heads) {
+  return tc::make_map(m, v.p, w.tokens, heads, w.D, v.token, v.head, kChunk);
+}
+
+template <int DP, bool BACK>
+rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
+  const int64_t length = segment_length(w.sequences, w.tokens, (int64_t)w.Hk * w.nx);
+  const int64_t n = slots(w.sequences, w.tokens, length);
+  const bool split = length < w.tokens;
+  CUtensorMap mx, my, mz;
+  if (w.tokens > 0 && (!map_of(&mx, w.x, w, w.Hk * w.nx) || !map_of(&my, w.y, w, w.Hk * w.ny) ||
+                       !map_of(&mz, w.z, w, w.Hk * w.ny)))
+    return RLCS_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  if (split || w.last) {
+    const SumArgs a = {w.log_decay, w.cu, split ? nullptr : w.init, split ? sums : w.last,
+                       w.sequences, w.tokens, w.Hk, w.ny, w.D, (int)length, !split,
+                       w.last != nullptr, w.in_scale};
+    constexpr size_t smem = sizeof(SumSmem<DP>);
+    e = allow_dynamic_smem<linear_sum_kernel<DP, BACK>>(smem);
+    if (e != cudaSuccess) return launched(e);
+    if (w.tokens == 0) my = mz = CUtensorMap{};  // (no block comes to use them)
+    e = launch_ex(linear_sum_kernel<DP, BACK>, dim3((unsigned)(n * w.Hk)), dim3(kSumThreads), smem,
+                  st, true, my, mz, a);
+    if (e != cudaSuccess) return launched(e);
+  }
+  if (split) {
+    const JoinArgs a = {w.log_decay, w.cu, w.init, sums, w.last, w.sequences, w.tokens, w.Hk, w.D,
+                        (int)length, BACK, w.transposed};
+    const int64_t units = w.sequences * w.Hk;
+    const dim3 grid((unsigned)ceil_div(w.D * w.D, 256), (unsigned)(units < 65535 ? units : 65535),
+                    (unsigned)ceil_div(units, 65535));
+    e = launch_ex(linear_join_kernel, grid, dim3(256), 0, st, true, a);
+    if (e != cudaSuccess) return launched(e);
+  }
+  if (w.tokens == 0) return RLCS_OK;
+  const WalkArgs a = {w.log_decay, w.cu, split ? sums : w.init, w.out, w.sequences, w.tokens,
+                      w.Hk * w.nx, w.nx, w.ny, w.D, (int)length, split, !split && w.transposed,
+                      w.in_scale, w.out_scale};
+  constexpr size_t smem = sizeof(WalkSmem<DP>);
+  static_assert(smem <= 232448 && sizeof(SumSmem<DP>) <= 232448, "a block has 227 KB");
+  e = allow_dynamic_smem<linear_walk_kernel<DP, BACK>>(smem);
+  if (e != cudaSuccess) return launched(e);
+  return launched(launch_ex(linear_walk_kernel<DP, BACK>, dim3((unsigned)(n * w.Hk * w.nx)),
+                            dim3(kWalkThreads), smem, st, true, mx, my, mz, a));
+}
+rlcs_status launch(const Walk &w, float *sums, cudaStream_t st) {
+  if (w.D <= 64)
+    return w.back ? launch_walk<64, true>(w, sums, st) : launch_walk<64, false>(w, sums, st);
+  return w.back ? launch_walk<128, true>(w, sums, st) : launch_walk<128, false>(w, sums, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -167,6 +780,13 @@ bool linear_sizes(int64_t sequences, int64_t tokens, int64_t Hq, int64_t Hk, int
 }
 
 }  // namespace
+
+uint32_t *linear_status() {
+  void *at = nullptr;
+  return cudaGetSymbolAddress(&at, device_status) == cudaSuccess ? static_cast<uint32_t *>(at)
+                                                                 : nullptr;
+}
+
 }  // namespace seq
 }  // namespace rlcs
 
@@ -178,7 +798,9 @@ extern "C" {
 size_t rlcs_linear_attention_scratch_bytes(int64_t sequences, int64_t tokens, int64_t Hq,
                                            int64_t Hk, int64_t D) {
   if (!linear_sizes(sequences, tokens, Hq, Hk, D, 1.0, RLCS_BF16)) return 0;
-  return 64;
+  const size_t a = sums_bytes(sequences, tokens, Hq, Hk, D),
+               b = sums_bytes(sequences, tokens, Hk, Hk, D);
+  return 64 + (a > b ? a : b);
 }
 
 rlcs_status rlcs_linear_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
@@ -215,24 +837,26 @@ rlcs_status rlcs_linear_attention(const void *q, int64_t q_token_stride, int64_t
   if (!scratch || !aligned(scratch, 16) ||
       scratch_bytes < rlcs_linear_attention_scratch_bytes(sequences, tokens, Hq, Hk, D))
     return RLCS_ERR_WORKSPACE;
-  WalkArgs a = {};
-  a.x = {static_cast<const bf *>(q), q_token_stride, q_head_stride};
-  a.y = {static_cast<const bf *>(k), k_token_stride, k_head_stride};
-  a.z = {static_cast<const bf *>(v), v_token_stride, v_head_stride};
-  a.log_decay = log_decay;
-  a.cu = cu_seqlens;
-  a.init = state;
-  a.last = last_state;
-  a.out = static_cast<bf *>(out);
-  a.sequences = sequences;
-  a.tokens = tokens;
-  a.Hk = (int)Hk;
-  a.nx = (int)(Hq / Hk);
-  a.ny = 1;
-  a.D = (int)D;
-  a.in_scale = 1.0f;
-  a.out_scale = (float)scale;
-  return launched(launch_walk(a, reinterpret_cast<cudaStream_t>(stream)));
+  const Walk w = {{static_cast<const bf *>(q), q_token_stride, q_head_stride},
+                  {static_cast<const bf *>(k), k_token_stride, k_head_stride},
+                  {static_cast<const bf *>(v), v_token_stride, v_head_stride},
+                  log_decay,
+                  cu_seqlens,
+                  state,
+                  last_state,
+                  static_cast<bf *>(out),
+                  sequences,
+                  tokens,
+                  (int)Hk,
+                  (int)(Hq / Hk),
+                  1,
+                  (int)D,
+                  false,
+                  false,
+                  1.0f,
+                  (float)scale};
+  return launch(w, reinterpret_cast<float *>(static_cast<char *>(scratch) + 64),
+                reinterpret_cast<cudaStream_t>(stream));
 }
 
 rlcs_status rlcs_linear_attention_backward(
@@ -275,35 +899,24 @@ rlcs_status rlcs_linear_attention_backward(
              vk = {static_cast<const bf *>(k), k_token_stride, k_head_stride},
              vv = {static_cast<const bf *>(v), v_token_stride, v_head_stride},
              vd = {static_cast<const bf *>(dout), Hq * D, D};
-  WalkArgs a = {};
-  a.log_decay = log_decay;
-  a.cu = cu_seqlens;
-  a.sequences = sequences;
-  a.tokens = tokens;
-  a.Hk = (int)Hk;
-  a.D = (int)D;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // dq
-  a.x = vd, a.y = vv, a.z = vk;
-  a.nx = (int)(Hq / Hk), a.ny = 1;
-  a.in_scale = 1.0f, a.out_scale = (float)scale;
-  a.init = state, a.last = nullptr, a.transposed = true, a.backward = false;
-  a.out = static_cast<bf *>(dq);
-  cudaError_t e = launch_walk(a, st);
-  if (e != cudaSuccess) return launched(e);
-  // dv
-  a.x = vk, a.y = vq, a.z = vd;
-  a.nx = 1, a.ny = (int)(Hq / Hk);
-  a.in_scale = (float)scale, a.out_scale = 1.0f;
-  a.init = dlast, a.last = dstate, a.transposed = false, a.backward = true;
-  a.out = static_cast<bf *>(dv);
-  e = launch_walk(a, st);
-  if (e != cudaSuccess) return launched(e);
-  // dk
-  a.x = vv, a.y = vd, a.z = vq;
-  a.last = nullptr, a.transposed = true;
-  a.out = static_cast<bf *>(dk);
-  return launched(launch_walk(a, st));
+  float *sums = reinterpret_cast<float *>(static_cast<char *>(scratch) + 64);
+  const int group = (int)(Hq / Hk);
+  Walk w = {vd, vv, vk, log_decay, cu_seqlens, state, nullptr, static_cast<bf *>(dq), sequences,
+            tokens, (int)Hk, group, 1, (int)D, false, true, 1.0f, (float)scale};
+  rlcs_status e = launch(w, sums, st);
+  if (e != RLCS_OK) return e;
+  w.x = vk, w.y = vq, w.z = vd;
+  w.nx = 1, w.ny = group;
+  w.in_scale = (float)scale, w.out_scale = 1.0f;
+  w.init = dlast, w.last = dstate, w.transposed = false, w.back = true;
+  w.out = static_cast<bf *>(dv);
+  e = launch(w, sums, st);
+  if (e != RLCS_OK) return e;
+  w.x = vv, w.y = vd, w.z = vq;
+  w.last = nullptr, w.transposed = true;
+  w.out = static_cast<bf *>(dk);
+  return launch(w, sums, st);
 }
 
 rlcs_status rlcs_linear_attention_step(const void *q, int64_t q_batch_stride,
