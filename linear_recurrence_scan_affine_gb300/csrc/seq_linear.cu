@@ -80,17 +80,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ uint32_t device_status;
 
 // ---------------------------------------------------------------------------
-// The walk in chunks of 128 tokens, a block to a segment and head of x.
+// The walk in chunks of 128 tokens, a block to a segment and to one or more
+// heads of x that read the same state.
 //
 // Per chunk, with rows r of x and c of y and z, d = r - c (c - r backwards),
 //   P = X Y^T,  P' = P a^d for d >= 0 and 0 elsewhere,
 //   O1 = P' Z,  O2 = X S,  out = O1 + a^into O2,  U = (a^left Y)^T Z,  S = a^n S + U,
 // into the steps from the state to a row, left those from a row to the state.
-// Warps 0..7 turn P into P' and sums into results, two threads to a row; the
-// decays of a thread's columns stay in registers, the same for every chunk.
-// Warps 8..15 scale Y in place, keep S (float32, in registers) and hand its
-// rounding to bfloat16 to the next chunk. Warp 16 copies, warp 17 issues
-// products. In tensor memory: P (P' over it), O1, O2, U.
+// Forwards a chunk has one Y and Z and `nx` X (an item each, with a result of
+// its own); backwards one X and `ny` Y and Z (items that add up).
+// Warps 0..7 turn P into P' and sums into results, two threads to a row; warps
+// 8..15 scale Y in place, keep S (float32, in registers) and hand its rounding
+// to bfloat16 to the next chunk. Warp 16 copies, warp 17 issues products. In
+// tensor memory: P (P' over it), O1, O2, U.
 // ---------------------------------------------------------------------------
 struct WalkArgs {
   const float *log_decay;
@@ -98,7 +100,8 @@ struct WalkArgs {
   const float *init;   // [slots or sequences, Hk, D, D] or null
   bf *out;             // [tokens, heads of x, D]
   int64_t sequences, tokens;
-  int heads, nx, ny;   // heads of x; of x and of y and z to a state
+  int heads, group;    // heads of x; of x to a state
+  int nx, ny;          // a block's heads of x; heads of y and z to a state
   int D, length;       // of a segment
   bool by_slot;        // init is by slot, else by sequence
   bool transposed;     // init is [z's dimension, y's]
@@ -111,8 +114,8 @@ struct WalkSmem {
   // that are not used)
   alignas(1024) unsigned char x[2][DP * 256], y[2][DP * 256], z[2][DP * 256], s[DP * DP * 2];
   float power[kChunk + 1];
-  uint64_t x_empty[2], full[2], empty[2];
-  uint64_t p_full, p_ready, o_full, o_free, y_ready, u_full, s_ready;
+  uint64_t x_full[2], x_empty[2], y_full[2], y_empty[2];
+  uint64_t p_full, p_ready, o_full, o_free, y_used, y_ready, u_full, s_ready;
   Segment segment;
   uint32_t tmem;
   int abort;
@@ -178,16 +181,18 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
-  const int h = blockIdx.x % p.heads, state_head = h / p.nx;
+  const int blocks = p.heads / p.nx;  // to a segment
+  const int h0 = blockIdx.x % blocks * p.nx, state_head = h0 / p.group;
   const int tokens = (int)p.tokens, sequences = (int)p.sequences;
   if (warp == 17) tc::tmem_alloc(&sm.tmem, 512);
   if (warp == 16) {
-    const Segment g = find_segment(p.cu, sequences, tokens, blockIdx.x / p.heads, p.length);
+    const Segment g = find_segment(p.cu, sequences, tokens, blockIdx.x / blocks, p.length);
     if (lane == 0) {
       sm.segment = g;
       sm.abort = (tc::smem_addr(raw) & 1023) != 0;  // the swizzle counts from there
-      for (uint64_t *b : {&sm.x_empty[0], &sm.x_empty[1], &sm.full[0], &sm.full[1], &sm.empty[0],
-                          &sm.empty[1], &sm.p_full, &sm.o_full, &sm.u_full})
+      for (uint64_t *b : {&sm.x_full[0], &sm.x_full[1], &sm.x_empty[0], &sm.x_empty[1],
+                          &sm.y_full[0], &sm.y_full[1], &sm.y_empty[0], &sm.y_empty[1],
+                          &sm.p_full, &sm.o_full, &sm.y_used, &sm.u_full})
         mbar_init(b, 1);
       for (uint64_t *b : {&sm.p_ready, &sm.o_free, &sm.y_ready, &sm.s_ready}) mbar_init(b, 8);
       fence_mbar_init();
@@ -208,6 +213,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     return;
   }
   const int chunks = (g.rows + kChunk - 1) / kChunk;
+  const int nx = BACK ? 1 : p.nx, ny = BACK ? p.ny : 1, items = BACK ? ny : nx;  // to a chunk
   // chunk number `c` in the order walked: its first row in the sequence
   const auto first_row = [&](int c) {
     return g.first + (BACK ? chunks - 1 - c : c) * kChunk;
@@ -223,151 +229,194 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 
   if (warp == 16) {
     if (lane == 0) {
-      bool ok = true;
-      for (int c = 0, it = 0; c < chunks && ok; ++c)
-        for (int j = 0; j < p.ny && ok; ++j, ++it) {
-          const int st = it & 1, token = g.lo + first_row(c);
-          if (it >= 2) ok = tc::mbar_wait(&sm.empty[st], ((it >> 1) - 1) & 1, abort);
-          if (ok && j == 0 && c >= 2) ok = tc::mbar_wait(&sm.x_empty[c & 1], ((c >> 1) - 1) & 1, abort);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&sm.full[st], DP * 256 * (j == 0 ? 3 : 2));
-          const int head = state_head * p.ny + j;
+      // tile number i of one ring: into its stage when that is free
+      const auto load = [&](unsigned char *to, const CUtensorMap *m, uint64_t *full, int head,
+                            int token) {
 #pragma unroll
-          for (int b = 0; b < DP / 64; ++b) {
-            if (j == 0)
-              tc::load_box(sm.x[c & 1] + b * 16384, &mx, &sm.full[st], b * 64, h, token);
-            tc::load_box(sm.y[st] + b * 16384, &my, &sm.full[st], b * 64, head, token);
-            tc::load_box(sm.z[st] + b * 16384, &mz, &sm.full[st], b * 64, head, token);
+        for (int b = 0; b < DP / 64; ++b)
+          tc::load_box(to + b * 16384, m, full, b * 64, head, token);
+      };
+      bool ok = true;
+      for (int c = 0, xi = 0, yi = 0; c < chunks && ok; ++c) {
+        const int token = g.lo + first_row(c);
+        for (int j = 0; j < items; ++j) {
+          if (!BACK || j == 0) {
+            const int st = xi & 1;
+            if (xi >= 2 && !(ok = tc::mbar_wait(&sm.x_empty[st], ((xi >> 1) - 1) & 1, abort))) break;
+            mbar_arrive_expect_tx(&sm.x_full[st], DP * 256);
+            load(sm.x[st], &mx, &sm.x_full[st], h0 + (BACK ? 0 : j), token);
+            ++xi;
+          }
+          if (BACK || j == 0) {
+            const int st = yi & 1, head = state_head * ny + (BACK ? j : 0);
+            if (yi >= 2 && !(ok = tc::mbar_wait(&sm.y_empty[st], ((yi >> 1) - 1) & 1, abort))) break;
+            mbar_arrive_expect_tx(&sm.y_full[st], DP * 512);
+            load(sm.y[st], &my, &sm.y_full[st], head, token);
+            load(sm.z[st], &mz, &sm.y_full[st], head, token);
+            ++yi;
           }
         }
+      }
     }
   } else if (warp == 17) {
     bool ok = true;
-    for (int c = 0, it = 0; c < chunks && ok; ++c) {
+    // x, y: tiles of each ring; it: items; o: results
+    for (int c = 0, xi = 0, yi = 0, it = 0, o = 0, u = 0; c < chunks && ok; ++c) {
       const int n = rows_of(c);
-      const uint32_t x = tc::smem_addr(sm.x[c & 1]);
-      for (int j = 0; j < p.ny && ok; ++j, ++it) {
-        const int st = it & 1;
-        const uint32_t y = tc::smem_addr(sm.y[st]), z = tc::smem_addr(sm.z[st]);
-        if (!(ok = tc::warp_wait(&sm.full[st], (it >> 1) & 1, abort))) break;
+      for (int j = 0; j < items; ++j, ++it) {
+        const bool new_x = !BACK || j == 0, new_y = BACK || j == 0, last = j + 1 == items;
+        unsigned char *x = sm.x[xi & 1], *y = sm.y[yi & 1], *z = sm.z[yi & 1];
+        if (new_x && !(ok = tc::warp_wait(&sm.x_full[xi & 1], (xi >> 1) & 1, abort))) break;
+        if (new_y && !(ok = tc::warp_wait(&sm.y_full[yi & 1], (yi >> 1) & 1, abort))) break;
         if (n < kChunk) {  // what follows the sequence is another's: it must be finite
-          if (j == 0) tc::clear_rows<DP, kChunk>(sm.x[c & 1], n, lane);
-          tc::clear_rows<DP, kChunk>(sm.y[st], n, lane);
-          tc::clear_rows<DP, kChunk>(sm.z[st], n, lane);
+          if (new_x) tc::clear_rows<DP, kChunk>(x, n, lane);
+          if (new_y) tc::clear_rows<DP, kChunk>(y, n, lane);
+          if (new_y) tc::clear_rows<DP, kChunk>(z, n, lane);
           __syncwarp();
         }
-        tc::product_nt<DP, kChunk>(lead, tP, x, y);
+        tc::product_nt<DP, kChunk>(lead, tP, tc::smem_addr(x), tc::smem_addr(y));
         tc::commit(lead, &sm.p_full);
-        if (j == 0) {
-          ok = tc::warp_wait(&sm.s_ready, c & 1, abort) &&
-               (c == 0 || tc::warp_wait(&sm.o_free, (c - 1) & 1, abort));
-          if (!ok) break;
+        if (BACK || last) tc::commit(lead, &sm.y_used);  // every product of the unscaled keys
+        if (new_x) {
+          if (j == 0 && !(ok = tc::warp_wait(&sm.s_ready, c & 1, abort))) break;
+          if (o > 0 && !(ok = tc::warp_wait(&sm.o_free, (o - 1) & 1, abort))) break;
           tc::fence_after_sync();
-          product_state<DP>(lead, tX, x, tc::smem_addr(sm.s));
+          product_state<DP>(lead, tX, tc::smem_addr(x), tc::smem_addr(sm.s));
         }
         if (!(ok = tc::warp_wait(&sm.p_ready, it & 1, abort))) break;
         tc::fence_after_sync();
-        tc::product_parts<DP, kChunk, 4>(lead, tO, tP, z, j > 0);
-        if (j + 1 == p.ny) tc::commit(lead, &sm.o_full);
-        if (!(ok = tc::warp_wait(&sm.y_ready, it & 1, abort))) break;
-        tc::fence_after_sync();
-        product_tn<DP>(lead, tU, y, z, j > 0);
-        tc::commit(lead, &sm.empty[st]);
-        if (j + 1 == p.ny) {
-          tc::commit(lead, &sm.u_full);
-          tc::commit(lead, &sm.x_empty[c & 1]);
+        tc::product_parts<DP, kChunk, 8>(lead, tO, tP, tc::smem_addr(z), BACK && j > 0);
+        if (!BACK || last) {
+          tc::commit(lead, &sm.o_full);
+          tc::commit(lead, &sm.x_empty[xi & 1]);
+          ++o;
+          ++xi;
+        }
+        if (BACK || last) {
+          if (!(ok = tc::warp_wait(&sm.y_ready, u++ & 1, abort))) break;
+          tc::fence_after_sync();
+          product_tn<DP>(lead, tU, tc::smem_addr(y), tc::smem_addr(z), BACK && j > 0);
+          if (last) tc::commit(lead, &sm.u_full);
+          tc::commit(lead, &sm.y_empty[yi & 1]);
+          ++yi;
         }
       }
     }
   } else if (warp < 8) {
-    const int r = threadIdx.x & 127, half = warp >> 2;  // the row, and half of its columns
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    float decay[64];
+    // Blocks of 16 columns, every other one of a row to a thread. Where a block
+    // lies wholly on the seen side its decays are products of two powers, one
+    // of the thread and one of the column.
+    const int r = threadIdx.x & 127, half = warp >> 2, row0 = (warp & 3) * 32;
+    const uint32_t lanes = (uint32_t)row0 << 16;
+    float2 within[8];
 #pragma unroll
-    for (int c = 0; c < 64; ++c) {
-      const int d = BACK ? half * 64 + c - r : r - (half * 64 + c);
-      decay[c] = d >= 0 ? sm.power[d >= 0 ? d : 0] * p.in_scale : 0.0f;
-    }
-    for (int c = 0, it = 0; c < chunks; ++c) {
-      for (int j = 0; j < p.ny; ++j, ++it) {
+    for (int e = 0; e < 8; ++e)
+      within[e] = make_float2(sm.power[BACK ? 2 * e : 15 - 2 * e] * p.in_scale,
+                              sm.power[BACK ? 2 * e + 1 : 14 - 2 * e] * p.in_scale);
+    for (int c = 0, it = 0, o = 0; c < chunks; ++c) {
+      for (int j = 0; j < items; ++j, ++it) {
         tc::warp_wait(&sm.p_full, it & 1, abort);
         tc::fence_after_sync();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t at = tP + lanes + half * 64 + i * 32;
-          uint32_t v[32], w[16];
-          tc::ld32(at, v);
-          tc::wait_ld();
+        for (int i = 0; i < 4; ++i) {
+          const int c0 = (2 * i + half) * 16;
+          const uint32_t at = tP + lanes + c0;
+          uint32_t w[8];
+          // (the same for the whole warp)
+          if (BACK ? c0 + 15 < row0 : c0 > row0 + 31) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 t = __fmul2_rn(make_float2(__uint_as_float(v[2 * e]),
-                                                    __uint_as_float(v[2 * e + 1])),
-                                        make_float2(decay[i * 32 + 2 * e], decay[i * 32 + 2 * e + 1]));
-            w[e] = pack_bf16(t.x, t.y);  // the type that the product takes
+            for (int e = 0; e < 8; ++e) w[e] = 0;
+          } else {
+            uint32_t v[16];
+            tc::ld16(at, v);
+            tc::wait_ld();
+            if (BACK ? c0 >= row0 + 31 : c0 + 15 <= row0) {
+              const float f = sm.power[BACK ? c0 - r : r - c0 - 15];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 d = __fmul2_rn(within[e], make_float2(f, f));
+                const float2 t = __fmul2_rn(make_float2(__uint_as_float(v[2 * e]),
+                                                        __uint_as_float(v[2 * e + 1])), d);
+                w[e] = pack_bf16(t.x, t.y);  // the type that the product takes
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int d0 = BACK ? c0 + 2 * e - r : r - c0 - 2 * e, d1 = BACK ? d0 + 1 : d0 - 1;
+                const float a = d0 < 0 ? 0.0f : __uint_as_float(v[2 * e]) * (sm.power[d0 < 0 ? 0 : d0] * p.in_scale);
+                const float b = d1 < 0 ? 0.0f : __uint_as_float(v[2 * e + 1]) * (sm.power[d1 < 0 ? 0 : d1] * p.in_scale);
+                w[e] = pack_bf16(a, b);
+              }
+            }
           }
-          tc::st16(at, w);
+          tc::st8(at, w);
         }
         tc::wait_st();
         tc::fence_before_sync();
         tc::warp_arrive(&sm.p_ready, lead);
-      }
-      const int n = rows_of(c), to_row = BACK ? n - 1 - r : r + 1;
-      const float into = sm.power[to_row < 0 ? 0 : to_row] * p.out_scale;
-      const int64_t row = (int64_t)g.lo + first_row(c) + r;
-      bf *out = p.out + (row * p.heads + h) * p.D + half * (DP / 2);
-      tc::warp_wait(&sm.o_full, c & 1, abort);
-      tc::fence_after_sync();
+        if (BACK && j + 1 < items) continue;
+        const int n = rows_of(c), to_row = BACK ? n - 1 - r : r + 1;
+        const float into = sm.power[to_row < 0 ? 0 : to_row] * p.out_scale;
+        const int64_t row = (int64_t)g.lo + first_row(c) + r;
+        bf *out = p.out + (row * p.heads + h0 + (BACK ? 0 : j)) * p.D + half * (DP / 2);
+        tc::warp_wait(&sm.o_full, o++ & 1, abort);
+        tc::fence_after_sync();
+        const bool on = r < n && !*abort;
+        const float2 f = make_float2(into, into), os = make_float2(p.out_scale, p.out_scale);
 #pragma unroll
-      for (int i = 0; i < DP / 64; ++i) {
-        uint32_t a[32], b[32];
-        tc::ld32(tO + lanes + half * (DP / 2) + i * 32, a);
-        tc::ld32(tX + lanes + half * (DP / 2) + i * 32, b);
-        tc::wait_ld();
-        if (i + 1 == DP / 64) {
-          tc::fence_before_sync();
-          tc::warp_arrive(&sm.o_free, lead);
-        }
-        if (r < n && !*abort)
+        for (int i = 0; i < DP / 32; ++i) {
+          uint32_t a[16], b[16];
+          tc::ld16(tO + lanes + half * (DP / 2) + i * 16, a);
+          tc::ld16(tX + lanes + half * (DP / 2) + i * 16, b);
+          tc::wait_ld();
+          if (i + 1 == DP / 32) {
+            tc::fence_before_sync();
+            tc::warp_arrive(&sm.o_free, lead);
+          }
+          if (!on) continue;
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            if (half * (DP / 2) + i * 32 + e < p.D) {
+          for (int e = 0; e < 16; e += 8)
+            if (half * (DP / 2) + i * 16 + e < p.D) {
               uint32_t w[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const float2 f = make_float2(into, into), o = make_float2(p.out_scale, p.out_scale);
                 const int q = e + 2 * k;
-                float2 t = __fmul2_rn(make_float2(__uint_as_float(a[q]), __uint_as_float(a[q + 1])), o);
+                float2 t = __fmul2_rn(make_float2(__uint_as_float(a[q]), __uint_as_float(a[q + 1])), os);
                 // (a row that the state does not reach takes nothing of it, whatever it holds)
                 if (into != 0.0f)
                   t = __ffma2_rn(make_float2(__uint_as_float(b[q]), __uint_as_float(b[q + 1])), f, t);
                 w[k] = pack_bf16(t.x, t.y);
               }
-              *reinterpret_cast<uint4 *>(out + i * 32 + e) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4 *>(out + i * 16 + e) = make_uint4(w[0], w[1], w[2], w[3]);
             }
+        }
       }
     }
   } else {
     const int t = threadIdx.x - 256, r = t & 127, half = (warp - 8) >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     constexpr int HC = DP / 2;  // columns of the state to a thread, in row r of it
-    const bool holds = r < DP;
     float s[HC];
-    {
-      const int64_t at =
-          ((p.by_slot ? (int64_t)(blockIdx.x / p.heads) : (int64_t)g.seq) * (p.heads / p.nx) +
-           state_head) * p.D * p.D;
 #pragma unroll
-      for (int c = 0; c < HC; ++c) {
-        const int col = half * HC + c;
-        s[c] = p.init && r < p.D && col < p.D
-                   ? __ldg(p.init + at + (p.transposed ? (int64_t)col * p.D + r
-                                                       : (int64_t)r * p.D + col))
-                   : 0.0f;
+    for (int c = 0; c < HC; ++c) s[c] = 0.0f;
+    if (p.init && r < p.D) {
+      const float *from = p.init + ((p.by_slot ? (int64_t)(blockIdx.x / blocks) : (int64_t)g.seq) *
+                                        (p.heads / p.group) + state_head) * p.D * p.D;
+      if (p.transposed) {
+#pragma unroll
+        for (int c = 0; c < HC; ++c)
+          if (half * HC + c < p.D) s[c] = __ldg(from + (int64_t)(half * HC + c) * p.D + r);
+      } else {
+#pragma unroll
+        for (int c = 0; c < HC; c += 4)
+          if (half * HC + c < p.D)
+            *reinterpret_cast<float4 *>(s + c) =
+                __ldg(reinterpret_cast<const float4 *>(from + (int64_t)r * p.D + half * HC + c));
       }
     }
     // rows of the state as the product's second operand: boxes of 64 columns
     const auto hand_over = [&] {
-      if (holds)
+      if (r < DP)
 #pragma unroll
         for (int c = 0; c < HC; c += 8) {
           const int col = half * HC + c, chunk = (col % 64) / 8;
@@ -381,16 +430,26 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       tc::warp_arrive(&sm.s_ready, lead);
     };
     hand_over();
-    for (int c = 0, it = 0; c < chunks; ++c) {
+    constexpr int kTimes = DP * 16 / 256;  // words of a tile to a thread: rows t / 8, t / 8 + 32, ...
+    for (int c = 0, yi = 0; c < chunks; ++c) {
       const int n = rows_of(c);
-      for (int j = 0; j < p.ny; ++j, ++it) {
-        uint4 *y = reinterpret_cast<uint4 *>(sm.y[it & 1]);
-        tc::warp_wait(&sm.p_full, it & 1, abort);  // P has been formed from the unscaled keys
-#pragma unroll 4
-        for (int i = t; i < DP * 16; i += 256) {
-          const int row = i / 8 % kChunk, left = BACK ? row + 1 : n - 1 - row;
-          y[i] = row < n ? scaled(y[i], sm.power[left < 0 ? 0 : left] * p.in_scale)
-                         : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < ny; ++j, ++yi) {
+        tc::warp_wait(&sm.y_used, yi & 1, abort);
+        uint4 *y = reinterpret_cast<uint4 *>(sm.y[yi & 1]) + t;
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = t / 8 + i * 32, left = BACK ? row + 1 : n - 1 - row;
+          f[i] = row < n ? sm.power[left < 0 ? 0 : left] * p.in_scale : 0.0f;
+        }
+#pragma unroll
+        for (int i0 = 0; i0 < kTimes; i0 += 4) {
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = y[(i0 + i) * 256];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // (rows that are not the sequence's are zeros already)
+            y[(i0 + i) * 256] = t / 8 + i * 32 < n ? scaled(v[i], f[i]) : make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_shared();
         tc::warp_arrive(&sm.y_ready, lead);
@@ -399,17 +458,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       if (c + 1 == chunks) break;
       tc::fence_after_sync();
       const float keep = sm.power[n];
+      if (keep == 0.0f)  // (nothing is kept, whatever the state holds)
 #pragma unroll
-      for (int i = 0; i < HC / 32; ++i) {
-        uint32_t u[32];
-        tc::ld32(tU + lanes + half * HC + i * 32, u);
+        for (int e = 0; e < HC; ++e) s[e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < HC / 16; ++i) {
+        uint32_t u[16];
+        tc::ld16(tU + lanes + half * HC + i * 16, u);
         tc::wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          // (a decay of zero keeps nothing, whatever the state holds)
-          const float old = keep == 0.0f ? 0.0f : keep * s[i * 32 + e];
-          s[i * 32 + e] = old + __uint_as_float(u[e]);
-        }
+        for (int e = 0; e < 16; ++e) s[i * 16 + e] = fmaf(keep, s[i * 16 + e], __uint_as_float(u[e]));
       }
       tc::fence_before_sync();
       hand_over();
@@ -647,18 +705,32 @@ struct Walk {
   float in_scale, out_scale;
 };
 
-// Tokens to a segment. Segments cost a second reading of y and z and a pass
-// over the states, so they are taken where sequences and heads alone leave
-// SMs without work: as many as make two blocks to an SM, none under 1024 tokens.
-int64_t segment_length(int64_t sequences, int64_t tokens, int64_t heads) {
-  const int64_t whole = (tokens + kChunk - 1) / kChunk * kChunk;
-  if (sequences * heads * 4 >= kSms * 3 || tokens <= 2048) return whole > 0 ? whole : kChunk;
-  const int64_t each = (tokens * heads + 2 * kSms - 1) / (2 * kSms);
-  const int64_t length = (each + kChunk - 1) / kChunk * kChunk;
-  return length < 1024 ? 1024 : length;
+// How a walk is laid out. Heads of x that share a state go to one block, which
+// then reads y and z and forms the state once, as far as two blocks to an SM
+// are left. Where sequences and heads alone leave SMs without work, sequences
+// are cut into segments: that costs a second reading of y and z and a pass over
+// the states, and none is under 1024 tokens.
+struct Layout {
+  int64_t length;  // of a segment
+  int nx;          // heads of x to a block
+};
+Layout layout_of(int64_t sequences, int64_t tokens, int64_t Hk, int64_t group) {
+  Layout l = {(tokens + kChunk - 1) / kChunk * kChunk, 1};
+  if (l.length == 0) l.length = kChunk;
+  for (int64_t nx = group; nx > 1; --nx)
+    if (group % nx == 0 && sequences * Hk * (group / nx) >= 2 * kSms) {
+      l.nx = (int)nx;
+      break;
+    }
+  const int64_t blocks = sequences * Hk * (group / l.nx);
+  if (blocks * 4 >= kSms * 3 || tokens <= 2048) return l;
+  const int64_t each = (tokens * Hk * group + 2 * kSms - 1) / (2 * kSms);
+  l.length = (each + kChunk - 1) / kChunk * kChunk;
+  if (l.length < 1024) l.length = 1024;
+  return l;
 }
-size_t sums_bytes(int64_t sequences, int64_t tokens, int64_t heads, int64_t Hk, int64_t D) {
-  const int64_t length = segment_length(sequences, tokens, heads);
+size_t sums_bytes(int64_t sequences, int64_t tokens, int64_t group, int64_t Hk, int64_t D) {
+  const int64_t length = layout_of(sequences, tokens, Hk, group).length;
   if (length >= tokens) return 0;
   return (size_t)(slots(sequences, tokens, length) * Hk * D * D) * 4;
 }
@@ -669,7 +741,8 @@ bool map_of(CUtensorMap *m, const View &v, const Walk &w, int heads) {
 
 template <int DP, bool BACK>
 rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
-  const int64_t length = segment_length(w.sequences, w.tokens, (int64_t)w.Hk * w.nx);
+  const Layout l = layout_of(w.sequences, w.tokens, w.Hk, w.nx);
+  const int64_t length = l.length;
   const int64_t n = slots(w.sequences, w.tokens, length);
   const bool split = length < w.tokens;
   CUtensorMap mx, my, mz;
@@ -700,13 +773,13 @@ rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
   }
   if (w.tokens == 0) return RLCS_OK;
   const WalkArgs a = {w.log_decay, w.cu, split ? sums : w.init, w.out, w.sequences, w.tokens,
-                      w.Hk * w.nx, w.nx, w.ny, w.D, (int)length, split, !split && w.transposed,
-                      w.in_scale, w.out_scale};
+                      w.Hk * w.nx, w.nx, l.nx, w.ny, w.D, (int)length, split,
+                      !split && w.transposed, w.in_scale, w.out_scale};
   constexpr size_t smem = sizeof(WalkSmem<DP>);
   static_assert(smem <= 232448 && sizeof(SumSmem<DP>) <= 232448, "a block has 227 KB");
   e = allow_dynamic_smem<linear_walk_kernel<DP, BACK>>(smem);
   if (e != cudaSuccess) return launched(e);
-  return launched(launch_ex(linear_walk_kernel<DP, BACK>, dim3((unsigned)(n * w.Hk * w.nx)),
+  return launched(launch_ex(linear_walk_kernel<DP, BACK>, dim3((unsigned)(n * w.Hk * (w.nx / l.nx))),
                             dim3(kWalkThreads), smem, st, true, mx, my, mz, a));
 }
 rlcs_status launch(const Walk &w, float *sums, cudaStream_t st) {
@@ -716,7 +789,9 @@ rlcs_status launch(const Walk &w, float *sums, cudaStream_t st) {
 }
 
 // ---------------------------------------------------------------------------
-// One step: the state's rows are spread over a warp each
+// One step: a block to a state, four columns to a lane, DP / 4 lanes to a row.
+// The state is read and written once, all of a thread's rows asked for before
+// the first is used; it stays in registers for the query heads that share it.
 // ---------------------------------------------------------------------------
 struct StepArgs {
   View q, k, v;
@@ -725,38 +800,83 @@ struct StepArgs {
   const float *state;
   float *next;
   bf *out;
-  int64_t B;
   int Hk, group, D;
   float scale;
 };
+constexpr int kStepWarps = 8, kStepHeads = 4;  // query heads summed up together
 
-__global__ void __launch_bounds__(128) linear_step_kernel(const StepArgs p) {
-  __shared__ float q[128], k[128];
+template <int DP>
+__global__ void __launch_bounds__(kStepWarps * 32, 2) linear_step_kernel(const StepArgs p) {
+  constexpr int kLanes = DP / 4, kAtOnce = kStepWarps * 32 / kLanes, kRows = DP / kAtOnce;
+  __shared__ float k[DP], q[kStepHeads][DP], part[kStepHeads][kStepWarps][DP];
   pdl_wait();
   pdl_launch_dependents();
-  const int e = threadIdx.x, D = p.D;
-  for (int64_t unit = blockIdx.x; unit < p.B * p.Hk; unit += gridDim.x) {
-    const int64_t b = unit / p.Hk;
-    const int h = (int)(unit % p.Hk);
-    const float a = p.reset && p.reset[b] ? 0.0f : expf(p.log_decay[h]);
-    const bool on = e < D;
-    __syncthreads();
-    k[e] = on ? __bfloat162float(p.k.p[b * p.k.token + h * p.k.head + e]) : 0.0f;
-    __syncthreads();
-    const float v = on ? __bfloat162float(p.v.p[b * p.v.token + h * p.v.head + e]) : 0.0f;
-    for (int d = 0; on && d < D; ++d) {
-      const int64_t at = (unit * D + d) * D + e;
-      const float kept = a == 0.0f ? 0.0f : a * p.state[at];
-      p.next[at] = fmaf(k[d], v, kept);
+  const int64_t unit = blockIdx.x, b = unit / p.Hk;
+  const int h = (int)(unit % p.Hk), D = p.D, warp = threadIdx.x >> 5;
+  const int col = threadIdx.x % kLanes * 4, first = threadIdx.x / kLanes;
+  const float a = p.reset && p.reset[b] ? 0.0f : expf(p.log_decay[h]);
+  const int64_t at = unit * D * D;
+  float4 s[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int row = first + i * kAtOnce;
+    s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (a != 0.0f && row < D && col < D)  // (dropped whatever it holds)
+      s[i] = *reinterpret_cast<const float4 *>(p.state + at + (int64_t)row * D + col);
+  }
+  if (threadIdx.x < DP)
+    k[threadIdx.x] = threadIdx.x < D ? __bfloat162float(p.k.p[b * p.k.token + h * p.k.head + threadIdx.x])
+                                     : 0.0f;
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    v[e] = col + e < D ? __bfloat162float(p.v.p[b * p.v.token + h * p.v.head + col + e]) : 0.0f;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int row = first + i * kAtOnce;
+    const float x = k[row];
+    s[i] = make_float4(fmaf(x, v[0], a * s[i].x), fmaf(x, v[1], a * s[i].y),
+                       fmaf(x, v[2], a * s[i].z), fmaf(x, v[3], a * s[i].w));
+    if (row < D && col < D)
+      *reinterpret_cast<float4 *>(p.next + at + (int64_t)row * D + col) = s[i];
+  }
+  for (int g = 0; g < p.group; g += kStepHeads) {
+    const int heads = p.group - g < kStepHeads ? p.group - g : kStepHeads;
+    for (int i = threadIdx.x; i < heads * DP; i += kStepWarps * 32) {
+      const int d = i % DP;
+      q[i / DP][d] = d < D ? __bfloat162float(p.q.p[b * p.q.token +
+                                                    (h * p.group + g + i / DP) * p.q.head + d])
+                           : 0.0f;
     }
-    for (int g = 0; g < p.group; ++g) {
-      __syncthreads();
-      const int head = h * p.group + g;
-      q[e] = on ? __bfloat162float(p.q.p[b * p.q.token + head * p.q.head + e]) : 0.0f;
-      __syncthreads();
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kStepHeads; ++j) {
+      if (j >= heads) break;
+      float o[4] = {};
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const float x = q[j][first + i * kAtOnce];
+        o[0] = fmaf(x, s[i].x, o[0]);
+        o[1] = fmaf(x, s[i].y, o[1]);
+        o[2] = fmaf(x, s[i].z, o[2]);
+        o[3] = fmaf(x, s[i].w, o[3]);
+      }
+#pragma unroll
+      for (int w = kLanes; w < 32; w <<= 1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += __shfl_xor_sync(kFull, o[e], w);
+      if ((threadIdx.x & 31) < kLanes)
+        *reinterpret_cast<float4 *>(&part[j][warp][col]) = make_float4(o[0], o[1], o[2], o[3]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < heads * DP; i += kStepWarps * 32) {
+      const int d = i % DP;
       float o = 0.0f;
-      for (int d = 0; on && d < D; ++d) o = fmaf(q[d], p.next[(unit * D + d) * D + e], o);
-      if (on) p.out[(unit * p.group + g) * D + e] = __float2bfloat16_rn(o * p.scale);
+#pragma unroll
+      for (int w = 0; w < kStepWarps; ++w) o += part[i / DP][w][d];
+      if (d < D)
+        p.out[(unit * p.group + g + i / DP) * D + d] = __float2bfloat16_rn(o * p.scale);
     }
   }
 }
@@ -798,8 +918,8 @@ extern "C" {
 size_t rlcs_linear_attention_scratch_bytes(int64_t sequences, int64_t tokens, int64_t Hq,
                                            int64_t Hk, int64_t D) {
   if (!linear_sizes(sequences, tokens, Hq, Hk, D, 1.0, RLCS_BF16)) return 0;
-  const size_t a = sums_bytes(sequences, tokens, Hq, Hk, D),
-               b = sums_bytes(sequences, tokens, Hk, Hk, D);
+  const size_t a = sums_bytes(sequences, tokens, Hq / Hk, Hk, D),
+               b = sums_bytes(sequences, tokens, 1, Hk, D);
   return 64 + (a > b ? a : b);
 }
 
@@ -957,15 +1077,14 @@ rlcs_status rlcs_linear_attention_step(const void *q, int64_t q_batch_stride,
                       state,
                       new_state,
                       static_cast<bf *>(out),
-                      B,
                       (int)Hk,
                       (int)(Hq / Hk),
                       (int)D,
                       (float)scale};
-  const int64_t units = B * Hk;
-  return launched(launch_ex(linear_step_kernel,
-                            dim3((unsigned)(units < kSms * 8 ? units : kSms * 8)), dim3(128), 0,
-                            reinterpret_cast<cudaStream_t>(stream), true, a));
+  const dim3 grid((unsigned)(B * Hk)), block(kStepWarps * 32);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return launched(D <= 64 ? launch_ex(linear_step_kernel<64>, grid, block, 0, st, true, a)
+                          : launch_ex(linear_step_kernel<128>, grid, block, 0, st, true, a));
 }
 
 }  // extern "C"

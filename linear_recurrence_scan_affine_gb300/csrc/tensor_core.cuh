@@ -108,6 +108,13 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&r)[16]) {
       : "memory");
 }
 
+__device__ __forceinline__ void st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
+      : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Matrix products: D[128 x N] (+)= A[128 x 16] B[16 x N], bf16 in, fp32 out
 // ---------------------------------------------------------------------------
