@@ -199,6 +199,67 @@ __global__ void __launch_bounds__(kTeamBlock, team_blocks(NV))
   }
 }
 
+// A token's entries are gone through by its thread, in their order.
+template <class T, bool GRAD>
+__global__ void __launch_bounds__(kFewBlock) distill_few_kernel(const DistillArgs p) {
+  extern __shared__ float x[];
+  __shared__ uint8_t live[kFewBlock];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t row0 = (int64_t)blockIdx.x * kFewBlock, row = row0 + threadIdx.x;
+  const int rows = p.tokens - row0 < kFewBlock ? (int)(p.tokens - row0) : kFewBlock;
+  const int V = (int)p.V, pitch = V | 1;
+  const bool held = row < p.tokens;
+  bool on = held && (!p.mask || p.mask[row]);
+  live[threadIdx.x] = on;
+  const int32_t *ids = p.ids + row * p.K;
+  const float *top = p.top + row * p.K;
+  Stats te = {-INFINITY, 0.0f, 0.0f};
+  if (on)
+    for (int j = 0; j < p.K; ++j) {
+      const float t = top[j] * p.inv_t;
+      if (absent(p, ids[j], top[j])) continue;
+      if (t > te.top) te.z *= expf(te.top - t), te.top = t;
+      te.z += expf(t - te.top);
+    }
+  if (p.mask) __syncthreads();
+  few_copy<T, true>(p, static_cast<T *>(nullptr), x, rows, row0, pitch,
+                    [&](int i) { return !p.mask || live[i]; });
+  __syncthreads();
+  on = on && te.z != 0.0f;  // (a NaN is an entry)
+  float *mine = x + threadIdx.x * pitch;
+  float loss = 0.0f;
+  if (on) {
+    const float c = p.inv_t * kLog2e;
+    const Stats s = few_stats<false>(mine, V, c);
+    const Base base = base_of(s.top, c);
+    const float logz = logf(s.z);
+    float lse = te.top + logf(te.z), mass = 1.0f;
+    if (p.teacher_lse) {
+      lse = p.teacher_lse[row];
+      mass = te.z * expf(te.top - lse);
+    }
+    for (int j = 0; j < p.K; ++j) {
+      if (absent(p, ids[j], top[j])) continue;
+      const float lq = top[j] * p.inv_t - lse, e = expf(lq);
+      if (e > 0.0f || e != e) loss += e * (lq - (base.y(mine[ids[j]]) * kLn2 - logz));
+    }
+    if (GRAD) {
+      const float w = p.dloss[row] * p.inv_t, a = w * mass / s.z;
+      for (int i = 0; i < V; ++i) mine[i] = ex2(base.y(mine[i])) * a;
+      for (int j = 0; j < p.K; ++j)
+        if (!absent(p, ids[j], top[j])) mine[ids[j]] -= w * expf(top[j] * p.inv_t - lse);
+    }
+  } else if (GRAD && held) {
+    for (int i = 0; i < V; ++i) mine[i] = 0.0f;
+  }
+  if (held && p.loss) p.loss[row] = loss;
+  if (!GRAD) return;
+  __syncthreads();
+  few_copy<T, false>(p, static_cast<T *>(p.dlogits), x, rows, row0, pitch,
+                     [](int) { return true; });
+}
+
 // The teacher's warp: a lane's first kHeld entries are asked for together. Two
 // sets of entries take turns: a row's are made ready while the row before is
 // stored.
@@ -386,6 +447,9 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillArg
 
 template <class T, bool GRAD>
 struct Distill {
+  static rlcs_status few(const DistillArgs &p, cudaStream_t st) {
+    return launch_few<distill_few_kernel<T, GRAD>>(p, st);
+  }
   template <int TEAM, int NV>
   static rlcs_status team(const DistillArgs &p, size_t entries, cudaStream_t st) {
     return launch_team<distill_team_kernel<T, GRAD, TEAM, NV>, TEAM>(p, team_blocks(NV), entries, st);

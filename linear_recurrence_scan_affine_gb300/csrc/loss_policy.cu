@@ -153,6 +153,48 @@ __global__ void __launch_bounds__(kTeamBlock, team_blocks(NV)) policy_team_kerne
   }
 }
 
+template <class T, bool GRAD>
+__global__ void __launch_bounds__(kFewBlock) policy_few_kernel(const PolicyArgs p) {
+  extern __shared__ float x[];
+  __shared__ uint8_t live[kFewBlock];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t row0 = (int64_t)blockIdx.x * kFewBlock, row = row0 + threadIdx.x;
+  const int rows = p.tokens - row0 < kFewBlock ? (int)(p.tokens - row0) : kFewBlock;
+  const int V = (int)p.V, pitch = V | 1;
+  const bool held = row < p.tokens, on = held && (!p.mask || p.mask[row]);
+  live[threadIdx.x] = on;
+  Token a = {};
+  if (on) a = token_of(p, row);
+  if (p.mask) __syncthreads();
+  few_copy<T, true>(p, static_cast<T *>(nullptr), x, rows, row0, pitch,
+                    [&](int i) { return !p.mask || live[i]; });
+  __syncthreads();
+  float *mine = x + threadIdx.x * pitch;
+  if (on) {
+    if (a.there) a.xa = mine[a.action];
+    const Stats s = few_stats<true>(mine, V, kLog2e);
+    float gain;
+    const Coefficients k = finish(p, row, a, s, true, gain);
+    if (GRAD) {
+      const Base base = base_of(s.top, kLog2e);
+      for (int i = 0; i < V; ++i) {
+        const float y = base.y(mine[i]);
+        mine[i] = ex2(y) * fmaf(k.b, bounded(y), k.a);
+      }
+      if (a.there) mine[a.action] += gain;
+    }
+  } else if (held) {
+    zero_scalars(p, row);
+    if (GRAD)
+      for (int i = 0; i < V; ++i) mine[i] = 0.0f;
+  }
+  if (!GRAD) return;
+  __syncthreads();
+  few_copy<T, false>(p, static_cast<T *>(p.dlogits), x, rows, row0, pitch,
+                     [](int) { return true; });
+}
+
 template <class T>
 struct PolicyLeader {
   static constexpr bool kTeacher = false;
@@ -231,6 +273,9 @@ __global__ void __launch_bounds__(kThreads) policy_rows_kernel(const PolicyArgs 
 
 template <class T, bool GRAD>
 struct Policy {
+  static rlcs_status few(const PolicyArgs &p, cudaStream_t st) {
+    return launch_few<policy_few_kernel<T, GRAD>>(p, st);
+  }
   template <int TEAM, int NV>
   static rlcs_status team(const PolicyArgs &p, size_t, cudaStream_t st) {
     return launch_team<policy_team_kernel<T, GRAD, TEAM, NV>, TEAM>(p, team_blocks(NV), 0, st);

@@ -373,6 +373,48 @@ constexpr int kTeamBlock = 128;
 constexpr int team_blocks(int nv) { return nv >= 8 ? 5 : (nv == 4 ? 6 : 8); }  // to an SM
 
 // ---------------------------------------------------------------------------
+// The shortest rows: a thread to each, 256 rows of a block together in shared
+// memory, so that what is copied in and out is whole. A row is `pitch` words
+// apart, odd, so that a warp's threads meet no bank twice.
+// ---------------------------------------------------------------------------
+constexpr int kFew = 32, kFewBlock = 256;  // elements of a row at most; rows to a block
+
+// Copies between the block's rows and shared memory, an element to a thread in
+// the arrays' order; rows that are left out (of the copy in) are not read.
+template <class T, bool IN, class Args, class On>
+__device__ __forceinline__ void few_copy(const Args &p, T *dx, float *x, int rows, int64_t row0,
+                                         int pitch, On on) {
+  const int V = (int)p.V, n = rows * V;
+  int row = threadIdx.x / V, col = threadIdx.x % V;
+  const int drow = kFewBlock / V, dcol = kFewBlock % V;
+  for (int i = threadIdx.x; i < n; i += kFewBlock) {
+    if (IN) {
+      if (on(row))
+        x[row * pitch + col] =
+            value(static_cast<const T *>(p.logits) + (row0 + row) * p.row_stride + col);
+    } else {
+      put(dx + row0 * V + i, x[row * pitch + col]);
+    }
+    row += drow;
+    col += dcol;
+    if (col >= V) col -= V, ++row;
+  }
+}
+template <bool ENTROPY>
+__device__ __forceinline__ Stats few_stats(const float *x, int V, float c) {
+  float top = x[0];
+  for (int i = 1; i < V; ++i) top = fmaxf(top, x[i]);
+  const Base base = base_of(top, c);
+  Stats s = {top, 0.0f, 0.0f};
+  for (int i = 0; i < V; ++i) {
+    const float y = base.y(x[i]), e = ex2(y);
+    s.z += e;
+    if (ENTROPY) s.t = fmaf(e, bounded(y), s.t);
+  }
+  return s;
+}
+
+// ---------------------------------------------------------------------------
 // Long rows: blocks of 8 warps that hold a row's words, or of a cluster of
 // blocks that share them, and one warp that leads. The leader takes what a
 // token has besides its logits, joins the statistics, works out the
@@ -733,6 +775,12 @@ rlcs_status launch_team(const Args &p, int per_sm, size_t entries, cudaStream_t 
   return launched(launch_ex(Kernel, dim3((unsigned)(wanted < room ? wanted : room)),
                             dim3(kTeamBlock), smem, st, true, p));
 }
+template <auto Kernel, class Args>
+rlcs_status launch_few(const Args &p, cudaStream_t st) {
+  const size_t smem = (size_t)kFewBlock * ((int)p.V | 1) * 4;
+  return launched(launch_ex(Kernel, dim3((unsigned)seq::ceil_div(p.tokens, kFewBlock)),
+                            dim3(kFewBlock), smem, st, true, p));
+}
 constexpr size_t kLongEntries = 65536;  // a block's, at most
 template <auto Kernel, int NV, class Args>
 rlcs_status launch_long(const Args &p, int threads, int ranks, size_t entries, cudaStream_t st) {
@@ -757,11 +805,13 @@ rlcs_status launch_long(const Args &p, int threads, int ranks, size_t entries, c
 
 // How a call's rows are spread: the smallest team that holds a row. A row that
 // starts inside a word may straddle one more than it fills. `On` has the
-// kernels: team<TEAM, NV>, block<NV> and any.
+// kernels: few, team<TEAM, NV>, block<NV> and any. (524288 rows of 6 float32:
+// 78 us by teams of eight lanes, 25 by threads.)
 template <class T, class On, class Args>
 rlcs_status spread(const Args &p, size_t entries, cudaStream_t st) {
   const bool whole = aligned(p.logits, 16) && (p.tokens == 1 || p.row_stride % kWord<T> == 0);
   const int64_t words = (p.V + kWord<T> - 1) / kWord<T> + (whole ? 0 : 1);
+  if (p.V <= kFew && p.tokens > 2 * seq::kSms) return On::few(p, st);
   const bool narrow = entries * 4 <= kTeamEntries;  // four teams of 8 to a warp
   if (words <= 8 && narrow) return On::template team<8, 1>(p, entries, st);
   if (words <= 16 && narrow) return On::template team<8, 2>(p, entries, st);

@@ -75,9 +75,10 @@ def _policy_args(logits, actions, old_logp, advantages, ref_logp, mask):
 
 
 def _policy_results(x, ref):
-    make = [torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
-            for _ in range(3 if ref is None else 4)]
-    return PolicyLoss(*(make if ref is not None else make + [None]))
+    """A PolicyLoss of new arrays: rows of one allocation."""
+    rows = torch.empty((3 if ref is None else 4, x.shape[0]), dtype=torch.float32,
+                       device=x.device).unbind(0)
+    return PolicyLoss(*rows) if ref is not None else PolicyLoss(*rows, None)
 
 
 @_s._streamed
