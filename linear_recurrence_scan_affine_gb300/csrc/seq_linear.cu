@@ -85,14 +85,14 @@ __device__ uint32_t device_status;
 //
 // Per chunk, with rows r of x and c of y and z, d = r - c (c - r backwards),
 //   P = X Y^T,  P' = P a^d for d >= 0 and 0 elsewhere,
-//   O1 = P' Z,  O2 = X S,  out = O1 + a^into O2,  U = (a^left Y)^T Z,  S = a^n S + U,
+//   O1 = P' Z,  O2 = X S,  out = O1 + a^into O2,  S = a^n S + (a^left Y)^T Z,
 // into the steps from the state to a row, left those from a row to the state.
 // Forwards a chunk has one Y and Z and `nx` X (an item each, with a result of
 // its own); backwards one X and `ny` Y and Z (items that add up).
 // Warps 0..7 turn P into P' and sums into results, two threads to a row; warps
-// 8..15 scale Y in place, keep S (float32, in registers) and hand its rounding
-// to bfloat16 to the next chunk. Warp 16 copies, warp 17 issues products. In
-// tensor memory: P (P' over it), O1, O2, U.
+// 8..15 scale Y in place, decay S and hand its rounding to bfloat16 to the next
+// chunk. Warp 16 copies in, warp 18 out, warp 17 issues products. In tensor memory, float32: P
+// (P' over it), O1, O2, S.
 // ---------------------------------------------------------------------------
 struct WalkArgs {
   const float *log_decay;
@@ -113,14 +113,18 @@ struct WalkSmem {
   // (z after y: with 64 columns a product reads past y, into rows of its result
   // that are not used)
   alignas(1024) unsigned char x[2][DP * 256], y[2][DP * 256], z[2][DP * 256], s[DP * DP * 2];
-  float power[kChunk + 1];
+  float power[kChunk + 1];  // of the decay
+  // what weights are multiplied by: decays d steps long at 31 + d, zeros before
+  // them; and the columns' part of them in a block of 16
+  float decay[31 + kChunk];
+  alignas(16) float near[16];
   uint64_t x_full[2], x_empty[2], y_full[2], y_empty[2];
   uint64_t p_full, p_ready, o_full, o_free, y_used, y_ready, u_full, s_ready;
   Segment segment;
   uint32_t tmem;
   int abort;
 };
-constexpr int kWalkThreads = 18 * 32;
+constexpr int kWalkThreads = 19 * 32;
 
 __device__ __forceinline__ void settle(int abort) {
   if (!abort) return;
@@ -148,14 +152,30 @@ __device__ __forceinline__ void product_state(uint32_t lead, uint32_t d, uint32_
                tc::instr(DP, true), k > 0);
 }
 
-// Eight bf16 values times f.
-__device__ __forceinline__ uint4 scaled(const uint4 &v, float f) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t o[4];
+// A factor as two bf16 parts, each twice: v f = v high + v low, rounded to
+// bf16 once but for the rounding of v low, 2^-9 of the other.
+struct Factor {
+  __nv_bfloat162 high, low;
+};
+__device__ __forceinline__ Factor factor(float f) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(f), l = __float2bfloat16_rn(f - __bfloat162float(h));
+  return {__bfloat162bfloat162(h), __bfloat162bfloat162(l)};
+}
+__device__ __forceinline__ uint4 scaled(uint4 v, const Factor &f) {
+  __nv_bfloat162 *x = reinterpret_cast<__nv_bfloat162 *>(&v);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = pack_bf16(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  for (int i = 0; i < 4; ++i) x[i] = __hfma2(x[i], f.high, __hmul2(x[i], f.low));
+  return v;
+}
+
+// A box of a tile of results to its place.
+__device__ __forceinline__ void store_box(const void *from, const CUtensorMap *map, int col, int head,
+                                          int token) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          map),
+      "r"(tc::smem_addr(from)), "r"(col), "r"(head), "r"(token)
+      : "memory");
 }
 
 // Rows of out that no sequence holds, each block taking a share.
@@ -175,7 +195,8 @@ template <int DP, bool BACK>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     linear_walk_kernel(const __grid_constant__ CUtensorMap mx,
                        const __grid_constant__ CUtensorMap my,
-                       const __grid_constant__ CUtensorMap mz, const WalkArgs p) {
+                       const __grid_constant__ CUtensorMap mz,
+                       const __grid_constant__ CUtensorMap mo, const WalkArgs p) {
   extern __shared__ __align__(1024) unsigned char raw[];
   WalkSmem<DP> &sm = *reinterpret_cast<WalkSmem<DP> *>(raw);
   pdl_wait();
@@ -200,6 +221,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   }
   const float l2 = __ldg(p.log_decay + state_head) * kLog2e;
   if (threadIdx.x <= kChunk) sm.power[threadIdx.x] = power(l2, threadIdx.x);
+  const float weight_scale = p.in_scale * p.out_scale;
+  if (threadIdx.x < 31 + kChunk)
+    sm.decay[threadIdx.x] = threadIdx.x < 31 ? 0.0f : weight_scale * power(l2, threadIdx.x - 31);
+  if (threadIdx.x < 16) sm.near[threadIdx.x] = weight_scale * power(l2, BACK ? threadIdx.x : 15 - threadIdx.x);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -223,7 +248,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     return left < kChunk ? left : kChunk;
   };
   const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
-  const uint32_t tP = tmem, tO = tmem + 128, tX = tmem + 256, tU = tmem + 384;
+  const uint32_t tP = tmem, tO = tmem + 128, tX = tmem + 256, tU = tmem + 384;  // P, O1, O2, S
   volatile int *abort = &sm.abort;
   const uint32_t lead = lane == 0;
 
@@ -288,14 +313,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         tc::product_parts<DP, kChunk, 8>(lead, tO, tP, tc::smem_addr(z), BACK && j > 0);
         if (!BACK || last) {
           tc::commit(lead, &sm.o_full);
-          tc::commit(lead, &sm.x_empty[xi & 1]);
           ++o;
           ++xi;
         }
         if (BACK || last) {
           if (!(ok = tc::warp_wait(&sm.y_ready, u++ & 1, abort))) break;
           tc::fence_after_sync();
-          product_tn<DP>(lead, tU, tc::smem_addr(y), tc::smem_addr(z), BACK && j > 0);
+          product_tn<DP>(lead, tU, tc::smem_addr(y), tc::smem_addr(z), true);
           if (last) tc::commit(lead, &sm.u_full);
           tc::commit(lead, &sm.y_empty[yi & 1]);
           ++yi;
@@ -308,48 +332,46 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     // of the thread and one of the column.
     const int r = threadIdx.x & 127, half = warp >> 2, row0 = (warp & 3) * 32;
     const uint32_t lanes = (uint32_t)row0 << 16;
-    float2 within[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      within[e] = make_float2(sm.power[BACK ? 2 * e : 15 - 2 * e] * p.in_scale,
-                              sm.power[BACK ? 2 * e + 1 : 14 - 2 * e] * p.in_scale);
     for (int c = 0, it = 0, o = 0; c < chunks; ++c) {
       for (int j = 0; j < items; ++j, ++it) {
         tc::warp_wait(&sm.p_full, it & 1, abort);
         tc::fence_after_sync();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c0 = (2 * i + half) * 16;
-          const uint32_t at = tP + lanes + c0;
-          uint32_t w[8];
-          // (the same for the whole warp)
-          if (BACK ? c0 + 15 < row0 : c0 > row0 + 31) {
+        for (int i0 = 0; i0 < 4; i0 += 2) {
+          // (two blocks are asked for together: a load takes some 300 clocks)
+          uint32_t v[2][16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 0;
-          } else {
-            uint32_t v[16];
-            tc::ld16(at, v);
-            tc::wait_ld();
-            if (BACK ? c0 >= row0 + 31 : c0 + 15 <= row0) {
+          for (int i = 0; i < 2; ++i) tc::ld16(tP + lanes + (2 * (i0 + i) + half) * 16, v[i]);
+          tc::wait_ld();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c0 = (2 * (i0 + i) + half) * 16;
+            uint32_t w[8];
+            // (the same for the whole warp)
+            if (i0 + i == (warp & 3)) {  // the row's own 32 columns are among these
+              const float *d = sm.decay + 31 + (BACK ? c0 - r : r - c0);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)  // the type that the product takes
+                w[e] = pack_bf16(__uint_as_float(v[i][2 * e]) * d[BACK ? 2 * e : -2 * e],
+                                 __uint_as_float(v[i][2 * e + 1]) * d[BACK ? 2 * e + 1 : -2 * e - 1]);
+            } else if (BACK ? i0 + i < (warp & 3) : i0 + i > (warp & 3)) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = 0;
+            } else {
               const float f = sm.power[BACK ? c0 - r : r - c0 - 15];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 d = __fmul2_rn(within[e], make_float2(f, f));
-                const float2 t = __fmul2_rn(make_float2(__uint_as_float(v[2 * e]),
-                                                        __uint_as_float(v[2 * e + 1])), d);
-                w[e] = pack_bf16(t.x, t.y);  // the type that the product takes
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int d0 = BACK ? c0 + 2 * e - r : r - c0 - 2 * e, d1 = BACK ? d0 + 1 : d0 - 1;
-                const float a = d0 < 0 ? 0.0f : __uint_as_float(v[2 * e]) * (sm.power[d0 < 0 ? 0 : d0] * p.in_scale);
-                const float b = d1 < 0 ? 0.0f : __uint_as_float(v[2 * e + 1]) * (sm.power[d1 < 0 ? 0 : d1] * p.in_scale);
-                w[e] = pack_bf16(a, b);
+              for (int e = 0; e < 16; e += 4) {
+                const float4 k = *reinterpret_cast<const float4 *>(sm.near + e);
+                const float2 a = __fmul2_rn(make_float2(k.x, k.y), make_float2(f, f)),
+                             b = __fmul2_rn(make_float2(k.z, k.w), make_float2(f, f));
+                const float2 x = __fmul2_rn(make_float2(__uint_as_float(v[i][e]), __uint_as_float(v[i][e + 1])), a),
+                             y = __fmul2_rn(make_float2(__uint_as_float(v[i][e + 2]), __uint_as_float(v[i][e + 3])), b);
+                w[e / 2] = pack_bf16(x.x, x.y);
+                w[e / 2 + 1] = pack_bf16(y.x, y.y);
               }
             }
+            tc::st8(tP + lanes + c0, w);
           }
-          tc::st8(at, w);
         }
         tc::wait_st();
         tc::fence_before_sync();
@@ -358,40 +380,73 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         const int n = rows_of(c), to_row = BACK ? n - 1 - r : r + 1;
         const float into = sm.power[to_row < 0 ? 0 : to_row] * p.out_scale;
         const int64_t row = (int64_t)g.lo + first_row(c) + r;
-        bf *out = p.out + (row * p.heads + h0 + (BACK ? 0 : j)) * p.D + half * (DP / 2);
-        tc::warp_wait(&sm.o_full, o++ & 1, abort);
+        const int head = h0 + (BACK ? 0 : j);
+        bf *out = p.out + (row * p.heads + head) * p.D + half * (DP / 2);
+        // A whole chunk's results take the place of its X and are copied out
+        // from there; rows of the last one are stored as they are.
+        const bool whole = n == kChunk;
+        unsigned char *tile = sm.x[o & 1];
+        tc::warp_wait(&sm.o_full, o & 1, abort);
         tc::fence_after_sync();
-        const bool on = r < n && !*abort;
-        const float2 f = make_float2(into, into), os = make_float2(p.out_scale, p.out_scale);
+        const bool on = (whole || r < n) && !*abort;
+        const float2 f = make_float2(into, into);
 #pragma unroll
-        for (int i = 0; i < DP / 32; ++i) {
-          uint32_t a[16], b[16];
-          tc::ld16(tO + lanes + half * (DP / 2) + i * 16, a);
-          tc::ld16(tX + lanes + half * (DP / 2) + i * 16, b);
+        for (int i = 0; i < DP / 64; ++i) {
+          uint32_t a[32], b[32];
+          tc::ld32(tO + lanes + half * (DP / 2) + i * 32, a);
+          tc::ld32(tX + lanes + half * (DP / 2) + i * 32, b);
           tc::wait_ld();
-          if (i + 1 == DP / 32) {
+          if (i + 1 == DP / 64) {
             tc::fence_before_sync();
             tc::warp_arrive(&sm.o_free, lead);
           }
-          if (!on) continue;
+          // (a row that the state does not reach takes nothing of it, whatever it holds)
+          if (into == 0.0f)
 #pragma unroll
-          for (int e = 0; e < 16; e += 8)
-            if (half * (DP / 2) + i * 16 + e < p.D) {
-              uint32_t w[4];
+            for (int e = 0; e < 32; ++e) b[e] = 0;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int q = e + 2 * k;
-                float2 t = __fmul2_rn(make_float2(__uint_as_float(a[q]), __uint_as_float(a[q + 1])), os);
-                // (a row that the state does not reach takes nothing of it, whatever it holds)
-                if (into != 0.0f)
-                  t = __ffma2_rn(make_float2(__uint_as_float(b[q]), __uint_as_float(b[q + 1])), f, t);
-                w[k] = pack_bf16(t.x, t.y);
-              }
-              *reinterpret_cast<uint4 *>(out + i * 16 + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int e = 0; e < 32; e += 8) {
+            const int col = half * (DP / 2) + i * 32 + e;
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int q = e + 2 * k;
+              const float2 t =
+                  __ffma2_rn(make_float2(__uint_as_float(b[q]), __uint_as_float(b[q + 1])), f,
+                             make_float2(__uint_as_float(a[q]), __uint_as_float(a[q + 1])));
+              w[k] = pack_bf16(t.x, t.y);
             }
+            const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+            if (whole)
+              *reinterpret_cast<uint4 *>(tile + col / 64 * 16384 + r * 128 +
+                                         ((col % 64 / 8 ^ (r & 7)) * 16)) = v;
+            else if (on && col < p.D)
+              *reinterpret_cast<uint4 *>(out + i * 32 + e) = v;
+          }
         }
+        if (whole) fence_proxy_async_shared();
+        __syncwarp();
+        asm volatile("bar.arrive %0, 288;" ::"r"(1 + (o & 1)) : "memory");
+        ++o;
       }
     }
+  } else if (warp == 18) {
+    // results of a whole chunk, from where X was; X is free when they have been read
+    for (int c = 0, o = 0; c < chunks; ++c)
+      for (int j = 0; j < nx; ++j, ++o) {
+        asm volatile("bar.sync %0, 288;" ::"r"(1 + (o & 1)) : "memory");
+        if (lane == 0) {
+          if (rows_of(c) == kChunk && !*abort) {
+#pragma unroll
+            for (int b = 0; b < DP / 64; ++b)
+              if (b * 64 < p.D)
+                store_box(sm.x[o & 1] + b * 16384, &mo, b * 64, h0 + j, g.lo + first_row(c));
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          }
+        }
+        tc::warp_arrive(&sm.x_empty[o & 1], lead);
+      }
   } else {
     const int t = threadIdx.x - 256, r = t & 127, half = (warp - 8) >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -414,8 +469,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 __ldg(reinterpret_cast<const float4 *>(from + (int64_t)r * p.D + half * HC + c));
       }
     }
-    // rows of the state as the product's second operand: boxes of 64 columns
-    const auto hand_over = [&] {
+    // The state before a chunk: rounded, as the product's second operand (rows
+    // in boxes of 64 columns), and times the chunk's decay back to where the
+    // chunk's own part is added.
+    const auto hand_over = [&](int n) {
+      const float keep = sm.power[n];
       if (r < DP)
 #pragma unroll
         for (int c = 0; c < HC; c += 8) {
@@ -426,21 +484,37 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
           *reinterpret_cast<uint4 *>(sm.s + (col / 64) * DP * 128 + r * 128 +
                                      ((chunk ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+      if (keep == 0.0f)  // (nothing is kept, whatever the state holds)
+#pragma unroll
+        for (int c = 0; c < HC; ++c) s[c] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < HC; c += 16) {
+        uint32_t u[16];
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const float2 k = __fmul2_rn(make_float2(s[c + e], s[c + e + 1]), make_float2(keep, keep));
+          u[e] = __float_as_uint(k.x);
+          u[e + 1] = __float_as_uint(k.y);
+        }
+        tc::st16(tU + lanes + half * HC + c, u);
+      }
       fence_proxy_async_shared();
+      tc::wait_st();
+      tc::fence_before_sync();
       tc::warp_arrive(&sm.s_ready, lead);
     };
-    hand_over();
+    hand_over(rows_of(0));
     constexpr int kTimes = DP * 16 / 256;  // words of a tile to a thread: rows t / 8, t / 8 + 32, ...
     for (int c = 0, yi = 0; c < chunks; ++c) {
       const int n = rows_of(c);
       for (int j = 0; j < ny; ++j, ++yi) {
         tc::warp_wait(&sm.y_used, yi & 1, abort);
         uint4 *y = reinterpret_cast<uint4 *>(sm.y[yi & 1]) + t;
-        float f[4];
+        Factor f[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = t / 8 + i * 32, left = BACK ? row + 1 : n - 1 - row;
-          f[i] = row < n ? sm.power[left < 0 ? 0 : left] * p.in_scale : 0.0f;
+          f[i] = factor(sm.power[left < 0 ? 0 : left] * p.in_scale);
         }
 #pragma unroll
         for (int i0 = 0; i0 < kTimes; i0 += 4) {
@@ -457,20 +531,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       tc::warp_wait(&sm.u_full, c & 1, abort);
       if (c + 1 == chunks) break;
       tc::fence_after_sync();
-      const float keep = sm.power[n];
-      if (keep == 0.0f)  // (nothing is kept, whatever the state holds)
 #pragma unroll
-        for (int e = 0; e < HC; ++e) s[e] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < HC / 16; ++i) {
-        uint32_t u[16];
-        tc::ld16(tU + lanes + half * HC + i * 16, u);
-        tc::wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[i * 16 + e] = fmaf(keep, s[i * 16 + e], __uint_as_float(u[e]));
-      }
-      tc::fence_before_sync();
-      hand_over();
+      for (int i = 0; i < HC / 32; ++i)
+        tc::ld32(tU + lanes + half * HC + i * 32, *reinterpret_cast<uint32_t(*)[32]>(s + i * 32));
+      tc::wait_ld();
+      hand_over(rows_of(c + 1));
     }
   }
   tc::fence_before_sync();
@@ -745,9 +810,10 @@ rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
   const int64_t length = l.length;
   const int64_t n = slots(w.sequences, w.tokens, length);
   const bool split = length < w.tokens;
-  CUtensorMap mx, my, mz;
+  CUtensorMap mx, my, mz, mo;
   if (w.tokens > 0 && (!map_of(&mx, w.x, w, w.Hk * w.nx) || !map_of(&my, w.y, w, w.Hk * w.ny) ||
-                       !map_of(&mz, w.z, w, w.Hk * w.ny)))
+                       !map_of(&mz, w.z, w, w.Hk * w.ny) ||
+                       !map_of(&mo, {w.out, (int64_t)w.Hk * w.nx * w.D, w.D}, w, w.Hk * w.nx)))
     return RLCS_ERR_CUDA;
   cudaError_t e = cudaSuccess;
   if (split || w.last) {
@@ -780,7 +846,7 @@ rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
   e = allow_dynamic_smem<linear_walk_kernel<DP, BACK>>(smem);
   if (e != cudaSuccess) return launched(e);
   return launched(launch_ex(linear_walk_kernel<DP, BACK>, dim3((unsigned)(n * w.Hk * (w.nx / l.nx))),
-                            dim3(kWalkThreads), smem, st, true, mx, my, mz, a));
+                            dim3(kWalkThreads), smem, st, true, mx, my, mz, mo, a));
 }
 rlcs_status launch(const Walk &w, float *sums, cudaStream_t st) {
   if (w.D <= 64)
