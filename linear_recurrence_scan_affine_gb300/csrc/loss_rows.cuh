@@ -472,36 +472,6 @@ __device__ __forceinline__ void meet_wait(int id) {
 // leader and the others are up to a row apart, either way.
 constexpr int kSummed = 1, kTaken = 3, kPlanned = 5, kStored = 7, kTaught = 8;
 
-// Ask for a block that has not started; the answer goes to every block of the
-// cluster. One thread of the cluster.
-__device__ __forceinline__ void ask(uint4 *answer, uint64_t *bar, bool cluster) {
-  if (cluster)
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
-        ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(tc::smem_addr(answer)),
-        "r"(tc::smem_addr(bar))
-        : "memory");
-  else
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
-        ".b128 [%0], [%1];" ::"r"(tc::smem_addr(answer)),
-        "r"(tc::smem_addr(bar))
-        : "memory");
-}
-// The block whose place was given, or -1.
-__device__ __forceinline__ int64_t granted(const uint4 *answer) {
-  uint32_t ok, x;
-  asm volatile(
-      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
-      "ld.shared.b128 h, [%2];\n\t"
-      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
-      : "=r"(ok), "=r"(x)
-      : "r"(tc::smem_addr(answer))
-      : "memory");
-  return ok ? (int64_t)x : -1;
-}
 // Four numbers into another block's shared memory, counted on its barrier.
 __device__ __forceinline__ void tell(const float4 *place, const uint64_t *bar, uint32_t rank,
                                      const float4 &v) {
@@ -558,7 +528,7 @@ __device__ __forceinline__ void long_rows(const Args &p, float c, uint32_t *stat
       if (lane == 0) {
         fence_proxy_async_shared();
         mbar_arrive_expect_tx(&sm.asked[i & 1], 16);
-        if (rank == 0) ask(&sm.answer[i & 1], &sm.asked[i & 1], ranks > 1);
+        if (rank == 0) tc::ask(&sm.answer[i & 1], &sm.asked[i & 1], ranks > 1);
       }
       __syncwarp();
     };
@@ -582,7 +552,7 @@ __device__ __forceinline__ void long_rows(const Args &p, float c, uint32_t *stat
       // the next row: asked for a row ago
       int64_t next = p.tokens;
       if (tc::warp_wait(&sm.asked[turn], (i >> 1) & 1, abort)) {
-        const int64_t block = granted(&sm.answer[turn]);
+        const int64_t block = tc::granted(&sm.answer[turn]);
         if (block >= 0) next = block / ranks;
       }
       const bool more = live(next);

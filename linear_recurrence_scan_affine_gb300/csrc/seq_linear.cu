@@ -80,8 +80,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ uint32_t device_status;
 
 // ---------------------------------------------------------------------------
-// The walk in chunks of 128 tokens, a block to a segment and to one or more
-// heads of x that read the same state.
+// The walk in chunks of 128 tokens. A unit of work is a segment and one or more
+// heads of x that read the same state. The grid has a block to each; one that
+// runs takes over units of blocks that have not started, and what it copies in
+// runs ahead into the next unit. (48 packed episodes: TAKEN us; with units
+// dealt out beforehand 303, without running ahead 238.)
 //
 // Per chunk, with rows r of x and c of y and z, d = r - c (c - r backwards),
 //   P = X Y^T,  P' = P a^d for d >= 0 and 0 elsewhere,
@@ -108,19 +111,26 @@ struct WalkArgs {
   float in_scale, out_scale;  // of y z^T, and of x S
 };
 
-template <int DP>
-struct WalkSmem {
-  // (z after y: with 64 columns a product reads past y, into rows of its result
-  // that are not used)
-  alignas(1024) unsigned char x[2][DP * 256], y[2][DP * 256], z[2][DP * 256], s[DP * DP * 2];
+struct Unit {
+  Segment g;
+  int slot, h0;             // the first head of x
+  bool end;                 // no unit: the block is done
   float power[kChunk + 1];  // of the decay
   // what weights are multiplied by: decays d steps long at 31 + d, zeros before
   // them; and the columns' part of them in a block of 16
   float decay[31 + kChunk];
   alignas(16) float near[16];
+};
+template <int DP>
+struct WalkSmem {
+  // (z after y: with 64 columns a product reads past y, into rows of its result
+  // that are not used)
+  alignas(1024) unsigned char x[2][DP * 256], y[2][DP * 256], z[2][DP * 256], s[DP * DP * 2];
+  Unit unit[2];
+  alignas(16) uint4 answer[2];  // of the requests for a unit
+  uint64_t asked[2], unit_full[2], unit_empty[2];
   uint64_t x_full[2], x_empty[2], y_full[2], y_empty[2];
   uint64_t p_full, p_ready, o_full, o_free, y_used, y_ready, u_full, s_ready;
-  Segment segment;
   uint32_t tmem;
   int abort;
 };
@@ -202,92 +212,144 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
-  const int blocks = p.heads / p.nx;  // to a segment
-  const int h0 = blockIdx.x % blocks * p.nx, state_head = h0 / p.group;
+  const int blocks = p.heads / p.nx;  // units to a segment
   const int tokens = (int)p.tokens, sequences = (int)p.sequences;
   if (warp == 17) tc::tmem_alloc(&sm.tmem, 512);
-  if (warp == 16) {
-    const Segment g = find_segment(p.cu, sequences, tokens, blockIdx.x / blocks, p.length);
-    if (lane == 0) {
-      sm.segment = g;
-      sm.abort = (tc::smem_addr(raw) & 1023) != 0;  // the swizzle counts from there
-      for (uint64_t *b : {&sm.x_full[0], &sm.x_full[1], &sm.x_empty[0], &sm.x_empty[1],
-                          &sm.y_full[0], &sm.y_full[1], &sm.y_empty[0], &sm.y_empty[1],
-                          &sm.p_full, &sm.o_full, &sm.y_used, &sm.u_full})
-        mbar_init(b, 1);
-      for (uint64_t *b : {&sm.p_ready, &sm.o_free, &sm.y_ready, &sm.s_ready}) mbar_init(b, 8);
-      fence_mbar_init();
-    }
+  if (threadIdx.x == 0) {
+    sm.abort = (tc::smem_addr(raw) & 1023) != 0;  // the swizzle counts from there
+    for (uint64_t *b : {&sm.x_full[0], &sm.x_full[1], &sm.x_empty[0], &sm.x_empty[1],
+                        &sm.y_full[0], &sm.y_full[1], &sm.y_empty[0], &sm.y_empty[1], &sm.p_full,
+                        &sm.o_full, &sm.y_used, &sm.u_full, &sm.unit_full[0], &sm.unit_full[1],
+                        &sm.asked[0], &sm.asked[1]})
+      mbar_init(b, 1);
+    for (uint64_t *b : {&sm.p_ready, &sm.o_free, &sm.y_ready, &sm.s_ready}) mbar_init(b, 8);
+    for (uint64_t *b : {&sm.unit_empty[0], &sm.unit_empty[1]}) mbar_init(b, 18);
+    fence_mbar_init();
   }
-  const float l2 = __ldg(p.log_decay + state_head) * kLog2e;
-  if (threadIdx.x <= kChunk) sm.power[threadIdx.x] = power(l2, threadIdx.x);
-  const float weight_scale = p.in_scale * p.out_scale;
-  if (threadIdx.x < 31 + kChunk)
-    sm.decay[threadIdx.x] = threadIdx.x < 31 ? 0.0f : weight_scale * power(l2, threadIdx.x - 31);
-  if (threadIdx.x < 16) sm.near[threadIdx.x] = weight_scale * power(l2, BACK ? threadIdx.x : 15 - threadIdx.x);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const Segment g = sm.segment;
   const int lo = bound(p.cu, 0, tokens), hi = bound(p.cu, sequences, tokens);
   if (warp < 8 && (lo > 0 || hi < tokens))
     zero_unheld(p.out, p.heads * p.D, lo, hi > lo ? hi : lo, tokens, threadIdx.x, 256);
-  if (!g.any || sm.abort) {
+  if (sm.abort) {
     if (warp == 17) tc::tmem_dealloc(sm.tmem, 512);
-    if (sm.abort && threadIdx.x == 0) atomicMax(&device_status, (uint32_t)RLCS_ERR_CUDA);
+    if (threadIdx.x == 0) atomicMax(&device_status, (uint32_t)RLCS_ERR_CUDA);
     return;
   }
-  const int chunks = (g.rows + kChunk - 1) / kChunk;
   const int nx = BACK ? 1 : p.nx, ny = BACK ? p.ny : 1, items = BACK ? ny : nx;  // to a chunk
-  // chunk number `c` in the order walked: its first row in the sequence
-  const auto first_row = [&](int c) {
-    return g.first + (BACK ? chunks - 1 - c : c) * kChunk;
-  };
-  const auto rows_of = [&](int c) {
-    const int left = g.first + g.rows - first_row(c);
-    return left < kChunk ? left : kChunk;
-  };
   const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
   const uint32_t tP = tmem, tO = tmem + 128, tX = tmem + 256, tU = tmem + 384;  // P, O1, O2, S
   volatile int *abort = &sm.abort;
   const uint32_t lead = lane == 0;
+  // chunk number `c` of a segment in the order walked: its first row in the
+  // sequence, and its rows
+  const auto chunks_of = [](const Segment &g) { return (g.rows + kChunk - 1) / kChunk; };
+  const auto first_row = [&](const Segment &g, int c) {
+    return g.first + (BACK ? chunks_of(g) - 1 - c : c) * kChunk;
+  };
+  const auto rows_of = [&](const Segment &g, int c) {
+    const int left = g.first + g.rows - first_row(g, c);
+    return left < kChunk ? left : kChunk;
+  };
+  // Units come to the other warps by turns; every count of tiles and barriers
+  // goes on from one to the next.
+  const auto next_unit = [&](int k) -> const Unit * {
+    if (!tc::warp_wait(&sm.unit_full[k & 1], (k >> 1) & 1, abort)) return nullptr;
+    const Unit *u = &sm.unit[k & 1];
+    return u->end ? nullptr : u;
+  };
+  const auto unit_done = [&](int k) { tc::warp_arrive(&sm.unit_empty[k & 1], lead); };
 
   if (warp == 16) {
-    if (lane == 0) {
-      // tile number i of one ring: into its stage when that is free
-      const auto load = [&](unsigned char *to, const CUtensorMap *m, uint64_t *full, int head,
-                            int token) {
+    int xi = 0, yi = 0;
+    bool ok = true;
+    const auto request = [&](int i) {
+      if (lane == 0) {
+        fence_proxy_async_shared();
+        mbar_arrive_expect_tx(&sm.asked[i & 1], 16);
+        tc::ask(&sm.answer[i & 1], &sm.asked[i & 1], false);
+      }
+      __syncwarp();
+    };
+    request(0);
+    int64_t block = blockIdx.x;
+    for (int i = 0, k = 0; ok; ++i) {
+      const bool end = block < 0;
+      const int slot = end ? 0 : (int)(block / blocks), h0 = end ? 0 : (int)(block % blocks) * p.nx;
+      // the unit after this one, asked for a unit ago
+      if (!end) {
+        if (!(ok = tc::warp_wait(&sm.asked[i & 1], (i >> 1) & 1, abort))) break;
+        block = tc::granted(&sm.answer[i & 1]);
+        __syncwarp();
+        if (block >= 0) request(i + 1);
+      }
+      Segment g = {};
+      if (!end) {
+        g = find_segment(p.cu, sequences, tokens, slot, p.length);
+        if (!g.any) continue;
+      }
+      if (k >= 2) ok = tc::warp_wait(&sm.unit_empty[k & 1], ((k >> 1) - 1) & 1, abort);
+      if (!ok) break;
+      Unit &u = sm.unit[k & 1];
+      const int state_head = h0 / p.group;
+      if (!end) {
+        const float l2 = __ldg(p.log_decay + state_head) * kLog2e;
+        const float scale = p.in_scale * p.out_scale;
+        for (int i = lane; i < 31 + kChunk; i += 32) {
+          const float f = i < 31 ? 0.0f : power(l2, i - 31);
+          u.decay[i] = scale * f;
+          if (i >= 31) u.power[i - 31] = f;
+        }
+        if (lane == 0) u.power[kChunk] = power(l2, kChunk);
+        if (lane < 16) u.near[lane] = scale * power(l2, BACK ? lane : 15 - lane);
+      }
+      if (lane == 0) u.g = g, u.slot = slot, u.h0 = h0, u.end = end;
+      tc::warp_arrive(&sm.unit_full[k & 1], lead);
+      ++k;
+      if (end) break;
+      if (lane == 0) {
+        const auto load = [&](unsigned char *to, const CUtensorMap *m, uint64_t *full, int head,
+                              int token) {
 #pragma unroll
-        for (int b = 0; b < DP / 64; ++b)
-          tc::load_box(to + b * 16384, m, full, b * 64, head, token);
-      };
-      bool ok = true;
-      for (int c = 0, xi = 0, yi = 0; c < chunks && ok; ++c) {
-        const int token = g.lo + first_row(c);
-        for (int j = 0; j < items; ++j) {
-          if (!BACK || j == 0) {
-            const int st = xi & 1;
-            if (xi >= 2 && !(ok = tc::mbar_wait(&sm.x_empty[st], ((xi >> 1) - 1) & 1, abort))) break;
-            mbar_arrive_expect_tx(&sm.x_full[st], DP * 256);
-            load(sm.x[st], &mx, &sm.x_full[st], h0 + (BACK ? 0 : j), token);
-            ++xi;
-          }
-          if (BACK || j == 0) {
-            const int st = yi & 1, head = state_head * ny + (BACK ? j : 0);
-            if (yi >= 2 && !(ok = tc::mbar_wait(&sm.y_empty[st], ((yi >> 1) - 1) & 1, abort))) break;
-            mbar_arrive_expect_tx(&sm.y_full[st], DP * 512);
-            load(sm.y[st], &my, &sm.y_full[st], head, token);
-            load(sm.z[st], &mz, &sm.y_full[st], head, token);
-            ++yi;
+          for (int i = 0; i < DP / 64; ++i)
+            tc::load_box(to + i * 16384, m, full, i * 64, head, token);
+        };
+        const int chunks = chunks_of(g);
+        for (int c = 0; c < chunks && ok; ++c) {
+          const int token = g.lo + first_row(g, c);
+          for (int j = 0; j < items; ++j) {
+            if (!BACK || j == 0) {
+              const int st = xi & 1;
+              if (xi >= 2 && !(ok = tc::mbar_wait(&sm.x_empty[st], ((xi >> 1) - 1) & 1, abort))) break;
+              mbar_arrive_expect_tx(&sm.x_full[st], DP * 256);
+              load(sm.x[st], &mx, &sm.x_full[st], h0 + (BACK ? 0 : j), token);
+              ++xi;
+            }
+            if (BACK || j == 0) {
+              const int st = yi & 1, head = state_head * ny + (BACK ? j : 0);
+              if (yi >= 2 && !(ok = tc::mbar_wait(&sm.y_empty[st], ((yi >> 1) - 1) & 1, abort))) break;
+              mbar_arrive_expect_tx(&sm.y_full[st], DP * 512);
+              load(sm.y[st], &my, &sm.y_full[st], head, token);
+              load(sm.z[st], &mz, &sm.y_full[st], head, token);
+              ++yi;
+            }
           }
         }
       }
+      ok = __shfl_sync(kFull, (int)ok, 0) != 0;
     }
   } else if (warp == 17) {
     bool ok = true;
-    // x, y: tiles of each ring; it: items; o: results
-    for (int c = 0, xi = 0, yi = 0, it = 0, o = 0, u = 0; c < chunks && ok; ++c) {
-      const int n = rows_of(c);
+    // x, y: tiles of each ring; it: items; o: results; s: chunks
+    int xi = 0, yi = 0, it = 0, o = 0, u = 0, sc = 0;
+    for (int k = 0; ok; ++k) {
+      const Unit *unit = next_unit(k);
+      if (!unit) break;
+      const Segment g = unit->g;
+      const int chunks = chunks_of(g);
+      for (int c = 0; c < chunks && ok; ++c, ++sc) {
+      const int n = rows_of(g, c);
       for (int j = 0; j < items; ++j, ++it) {
         const bool new_x = !BACK || j == 0, new_y = BACK || j == 0, last = j + 1 == items;
         unsigned char *x = sm.x[xi & 1], *y = sm.y[yi & 1], *z = sm.z[yi & 1];
@@ -303,7 +365,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         tc::commit(lead, &sm.p_full);
         if (BACK || last) tc::commit(lead, &sm.y_used);  // every product of the unscaled keys
         if (new_x) {
-          if (j == 0 && !(ok = tc::warp_wait(&sm.s_ready, c & 1, abort))) break;
+          if (j == 0 && !(ok = tc::warp_wait(&sm.s_ready, sc & 1, abort))) break;
           if (o > 0 && !(ok = tc::warp_wait(&sm.o_free, (o - 1) & 1, abort))) break;
           tc::fence_after_sync();
           product_state<DP>(lead, tX, tc::smem_addr(x), tc::smem_addr(sm.s));
@@ -325,6 +387,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
           ++yi;
         }
       }
+      }
+      unit_done(k);
     }
   } else if (warp < 8) {
     // Blocks of 16 columns, every other one of a row to a thread. Where a block
@@ -332,7 +396,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     // of the thread and one of the column.
     const int r = threadIdx.x & 127, half = warp >> 2, row0 = (warp & 3) * 32;
     const uint32_t lanes = (uint32_t)row0 << 16;
-    for (int c = 0, it = 0, o = 0; c < chunks; ++c) {
+    int it = 0, o = 0;
+    for (int k = 0;; ++k) {
+      const Unit *unit = next_unit(k);
+      if (!unit) break;
+      const Segment g = unit->g;
+      const int chunks = chunks_of(g), h0 = unit->h0;
+      for (int c = 0; c < chunks; ++c) {
       for (int j = 0; j < items; ++j, ++it) {
         tc::warp_wait(&sm.p_full, it & 1, abort);
         tc::fence_after_sync();
@@ -349,7 +419,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             uint32_t w[8];
             // (the same for the whole warp)
             if (i0 + i == (warp & 3)) {  // the row's own 32 columns are among these
-              const float *d = sm.decay + 31 + (BACK ? c0 - r : r - c0);
+              const float *d = unit->decay + 31 + (BACK ? c0 - r : r - c0);
 #pragma unroll
               for (int e = 0; e < 8; ++e)  // the type that the product takes
                 w[e] = pack_bf16(__uint_as_float(v[i][2 * e]) * d[BACK ? 2 * e : -2 * e],
@@ -358,10 +428,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
               for (int e = 0; e < 8; ++e) w[e] = 0;
             } else {
-              const float f = sm.power[BACK ? c0 - r : r - c0 - 15];
+              const float f = unit->power[BACK ? c0 - r : r - c0 - 15];
 #pragma unroll
               for (int e = 0; e < 16; e += 4) {
-                const float4 k = *reinterpret_cast<const float4 *>(sm.near + e);
+                const float4 k = *reinterpret_cast<const float4 *>(unit->near + e);
                 const float2 a = __fmul2_rn(make_float2(k.x, k.y), make_float2(f, f)),
                              b = __fmul2_rn(make_float2(k.z, k.w), make_float2(f, f));
                 const float2 x = __fmul2_rn(make_float2(__uint_as_float(v[i][e]), __uint_as_float(v[i][e + 1])), a),
@@ -377,9 +447,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         tc::fence_before_sync();
         tc::warp_arrive(&sm.p_ready, lead);
         if (BACK && j + 1 < items) continue;
-        const int n = rows_of(c), to_row = BACK ? n - 1 - r : r + 1;
-        const float into = sm.power[to_row < 0 ? 0 : to_row] * p.out_scale;
-        const int64_t row = (int64_t)g.lo + first_row(c) + r;
+        const int n = rows_of(g, c), to_row = BACK ? n - 1 - r : r + 1;
+        const float into = unit->power[to_row < 0 ? 0 : to_row] * p.out_scale;
+        const int64_t row = (int64_t)g.lo + first_row(g, c) + r;
         const int head = h0 + (BACK ? 0 : j);
         bf *out = p.out + (row * p.heads + head) * p.D + half * (DP / 2);
         // A whole chunk's results take the place of its X and are copied out
@@ -429,51 +499,41 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         asm volatile("bar.arrive %0, 288;" ::"r"(1 + (o & 1)) : "memory");
         ++o;
       }
+      }
+      unit_done(k);
     }
   } else if (warp == 18) {
     // results of a whole chunk, from where X was; X is free when they have been read
-    for (int c = 0, o = 0; c < chunks; ++c)
-      for (int j = 0; j < nx; ++j, ++o) {
-        asm volatile("bar.sync %0, 288;" ::"r"(1 + (o & 1)) : "memory");
-        if (lane == 0) {
-          if (rows_of(c) == kChunk && !*abort) {
+    int o = 0;
+    for (int k = 0;; ++k) {
+      const Unit *unit = next_unit(k);
+      if (!unit) break;
+      const Segment g = unit->g;
+      const int chunks = chunks_of(g), h0 = unit->h0;
+      for (int c = 0; c < chunks; ++c)
+        for (int j = 0; j < nx; ++j, ++o) {
+          asm volatile("bar.sync %0, 288;" ::"r"(1 + (o & 1)) : "memory");
+          if (lane == 0 && rows_of(g, c) == kChunk && !*abort) {
 #pragma unroll
             for (int b = 0; b < DP / 64; ++b)
               if (b * 64 < p.D)
-                store_box(sm.x[o & 1] + b * 16384, &mo, b * 64, h0 + j, g.lo + first_row(c));
+                store_box(sm.x[o & 1] + b * 16384, &mo, b * 64, h0 + j, g.lo + first_row(g, c));
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           }
+          tc::warp_arrive(&sm.x_empty[o & 1], lead);
         }
-        tc::warp_arrive(&sm.x_empty[o & 1], lead);
-      }
+      unit_done(k);
+    }
   } else {
     const int t = threadIdx.x - 256, r = t & 127, half = (warp - 8) >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     constexpr int HC = DP / 2;  // columns of the state to a thread, in row r of it
     float s[HC];
-#pragma unroll
-    for (int c = 0; c < HC; ++c) s[c] = 0.0f;
-    if (p.init && r < p.D) {
-      const float *from = p.init + ((p.by_slot ? (int64_t)(blockIdx.x / blocks) : (int64_t)g.seq) *
-                                        (p.heads / p.group) + state_head) * p.D * p.D;
-      if (p.transposed) {
-#pragma unroll
-        for (int c = 0; c < HC; ++c)
-          if (half * HC + c < p.D) s[c] = __ldg(from + (int64_t)(half * HC + c) * p.D + r);
-      } else {
-#pragma unroll
-        for (int c = 0; c < HC; c += 4)
-          if (half * HC + c < p.D)
-            *reinterpret_cast<float4 *>(s + c) =
-                __ldg(reinterpret_cast<const float4 *>(from + (int64_t)r * p.D + half * HC + c));
-      }
-    }
     // The state before a chunk: rounded, as the product's second operand (rows
     // in boxes of 64 columns), and times the chunk's decay back to where the
     // chunk's own part is added.
-    const auto hand_over = [&](int n) {
-      const float keep = sm.power[n];
+    const auto hand_over = [&](float keep) {
       if (r < DP)
 #pragma unroll
         for (int c = 0; c < HC; c += 8) {
@@ -503,10 +563,33 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       tc::fence_before_sync();
       tc::warp_arrive(&sm.s_ready, lead);
     };
-    hand_over(rows_of(0));
     constexpr int kTimes = DP * 16 / 256;  // words of a tile to a thread: rows t / 8, t / 8 + 32, ...
-    for (int c = 0, yi = 0; c < chunks; ++c) {
-      const int n = rows_of(c);
+    int yi = 0, sc = 0;
+    for (int k = 0;; ++k) {
+      const Unit *unit = next_unit(k);
+      if (!unit) break;
+      const Segment g = unit->g;
+      const int chunks = chunks_of(g);
+#pragma unroll
+      for (int c = 0; c < HC; ++c) s[c] = 0.0f;
+      if (p.init && r < p.D) {
+        const float *from = p.init + ((p.by_slot ? (int64_t)unit->slot : (int64_t)g.seq) *
+                                          (p.heads / p.group) + unit->h0 / p.group) * p.D * p.D;
+        if (p.transposed) {
+#pragma unroll
+          for (int c = 0; c < HC; ++c)
+            if (half * HC + c < p.D) s[c] = __ldg(from + (int64_t)(half * HC + c) * p.D + r);
+        } else {
+#pragma unroll
+          for (int c = 0; c < HC; c += 4)
+            if (half * HC + c < p.D)
+              *reinterpret_cast<float4 *>(s + c) =
+                  __ldg(reinterpret_cast<const float4 *>(from + (int64_t)r * p.D + half * HC + c));
+        }
+      }
+      hand_over(unit->power[rows_of(g, 0)]);
+      for (int c = 0; c < chunks; ++c, ++sc) {
+      const int n = rows_of(g, c);
       for (int j = 0; j < ny; ++j, ++yi) {
         tc::warp_wait(&sm.y_used, yi & 1, abort);
         uint4 *y = reinterpret_cast<uint4 *>(sm.y[yi & 1]) + t;
@@ -514,7 +597,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = t / 8 + i * 32, left = BACK ? row + 1 : n - 1 - row;
-          f[i] = factor(sm.power[left < 0 ? 0 : left] * p.in_scale);
+          f[i] = factor(unit->power[left < 0 ? 0 : left] * p.in_scale);
         }
 #pragma unroll
         for (int i0 = 0; i0 < kTimes; i0 += 4) {
@@ -528,14 +611,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         fence_proxy_async_shared();
         tc::warp_arrive(&sm.y_ready, lead);
       }
-      tc::warp_wait(&sm.u_full, c & 1, abort);
-      if (c + 1 == chunks) break;
+      tc::warp_wait(&sm.u_full, sc & 1, abort);
+      if (c + 1 == chunks) continue;
       tc::fence_after_sync();
 #pragma unroll
       for (int i = 0; i < HC / 32; ++i)
         tc::ld32(tU + lanes + half * HC + i * 32, *reinterpret_cast<uint32_t(*)[32]>(s + i * 32));
       tc::wait_ld();
-      hand_over(rows_of(c + 1));
+      hand_over(unit->power[rows_of(g, c + 1)]);
+      }
+      unit_done(k);
     }
   }
   tc::fence_before_sync();
@@ -838,6 +923,7 @@ rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
     if (e != cudaSuccess) return launched(e);
   }
   if (w.tokens == 0) return RLCS_OK;
+  const int64_t units = n * w.Hk * (w.nx / l.nx);
   const WalkArgs a = {w.log_decay, w.cu, split ? sums : w.init, w.out, w.sequences, w.tokens,
                       w.Hk * w.nx, w.nx, l.nx, w.ny, w.D, (int)length, split,
                       !split && w.transposed, w.in_scale, w.out_scale};
@@ -845,7 +931,7 @@ rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
   static_assert(smem <= 232448 && sizeof(SumSmem<DP>) <= 232448, "a block has 227 KB");
   e = allow_dynamic_smem<linear_walk_kernel<DP, BACK>>(smem);
   if (e != cudaSuccess) return launched(e);
-  return launched(launch_ex(linear_walk_kernel<DP, BACK>, dim3((unsigned)(n * w.Hk * (w.nx / l.nx))),
+  return launched(launch_ex(linear_walk_kernel<DP, BACK>, dim3((unsigned)units),
                             dim3(kWalkThreads), smem, st, true, mx, my, mz, mo, a));
 }
 rlcs_status launch(const Walk &w, float *sums, cudaStream_t st) {

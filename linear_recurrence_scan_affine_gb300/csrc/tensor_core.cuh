@@ -1,5 +1,6 @@
-// tcgen05, tensor memory and tensor-map copies for sm_103a: the PTX wrappers
-// the attention kernels use, with the operand layouts they assume.
+// tcgen05, tensor memory, tensor-map copies and the taking over of blocks for
+// sm_103a: the PTX wrappers that the attention kernels and the losses use, with
+// the operand layouts they assume.
 //
 // Operand tiles in shared memory are boxes of 64 bf16 columns (128 bytes) by
 // R rows, 128-byte swizzled as the tensor-map copy writes them; a tile of 128
@@ -247,6 +248,39 @@ __device__ __noinline__ void clear_special(unsigned char *tile, int lane) {
   fence_proxy_async_shared();
 }
 
+// ---------------------------------------------------------------------------
+// Work of blocks that have not started
+// ---------------------------------------------------------------------------
+// Ask for a block that has not started; the answer goes to every block of the
+// cluster. One thread of the cluster.
+__device__ __forceinline__ void ask(uint4 *answer, uint64_t *bar, bool cluster) {
+  if (cluster)
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+  else
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".b128 [%0], [%1];" ::"r"(smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+// The block whose place was given, or -1.
+__device__ __forceinline__ int64_t granted(const uint4 *answer) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_addr(answer))
+      : "memory");
+  return ok ? (int64_t)x : -1;
+}
 // Host: the map of a [tokens, heads, D] bf16 view, in 64-column boxes of
 // `rows` tokens of one head.
 inline bool make_map(CUtensorMap *map, const void *base, int64_t tokens, int64_t heads, int64_t D,
