@@ -66,6 +66,38 @@ __device__ __forceinline__ Segment find_segment(const int32_t *cu, int sequences
   g.rows = g.any ? (g.len - g.first < length ? g.len - g.first : length) : 0;
   return g;
 }
+// The whole of sequence `seq`.
+__device__ __forceinline__ Segment whole_sequence(const int32_t *cu, int tokens, int seq) {
+  Segment g;
+  g.seq = seq;
+  g.lo = bound(cu, seq, tokens);
+  const int hi = bound(cu, seq + 1, tokens);
+  g.len = hi > g.lo ? hi - g.lo : 0;
+  g.first = 0;
+  g.rows = g.len;
+  g.any = g.len > 0;
+  return g;
+}
+// Sequences that are not cut, the longest first, in shared memory: a block's
+// threads count for each how many come before it. (48 packed episodes of up to
+// 1024 in their own order: UNSORTED us, in this one SORTED.)
+constexpr int kOrdered = 128;
+__device__ __forceinline__ void order_sequences(const int32_t *cu, int sequences, int tokens,
+                                                int *len, uint8_t *order) {
+  const int t = threadIdx.x;
+  int own = 0;
+  if (t < sequences) {
+    const int lo = bound(cu, t, tokens), hi = bound(cu, t + 1, tokens);
+    len[t] = own = hi > lo ? hi - lo : 0;
+  }
+  __syncthreads();
+  if (t < sequences) {
+    int before = 0;
+    for (int i = 0; i < sequences; ++i) before += len[i] > own || (len[i] == own && i < t);
+    order[before] = (uint8_t)t;
+  }
+  __syncthreads();
+}
 int64_t slots(int64_t sequences, int64_t tokens, int64_t length) {
   return tokens / length + sequences;
 }
@@ -122,15 +154,22 @@ struct Unit {
   alignas(16) float near[16];
 };
 template <int DP>
+constexpr int stages() {  // of the rings of tiles
+  return DP == 64 ? 4 : 2;
+}
+template <int DP>
 struct WalkSmem {
+  static constexpr int kStages = stages<DP>();
   // (z after y: with 64 columns a product reads past y, into rows of its result
   // that are not used)
-  alignas(1024) unsigned char x[2][DP * 256], y[2][DP * 256], z[2][DP * 256], s[DP * DP * 2];
+  alignas(1024) unsigned char x[kStages][DP * 256], y[kStages][DP * 256], z[kStages][DP * 256],
+      s[DP * DP * 2];
   Unit unit[2];
   alignas(16) uint4 answer[2];  // of the requests for a unit
   uint64_t asked[2], unit_full[2], unit_empty[2];
-  uint64_t x_full[2], x_empty[2], y_full[2], y_empty[2];
-  uint64_t p_full, p_ready, o_full, o_free, y_used, y_ready, u_full, s_ready;
+  uint64_t x_full[kStages], x_empty[kStages], y_full[kStages], y_empty[kStages];
+  uint64_t p_full[2], p_ready[2], y_used[2], y_ready[2], o_full, o_free, u_full, s_ready, s_used;
+  uint8_t order[kOrdered];
   uint32_t tmem;
   int abort;
 };
@@ -213,19 +252,26 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   const int blocks = p.heads / p.nx;  // units to a segment
+  constexpr int kStages = stages<DP>();
   const int tokens = (int)p.tokens, sequences = (int)p.sequences;
   if (warp == 17) tc::tmem_alloc(&sm.tmem, 512);
   if (threadIdx.x == 0) {
     sm.abort = (tc::smem_addr(raw) & 1023) != 0;  // the swizzle counts from there
-    for (uint64_t *b : {&sm.x_full[0], &sm.x_full[1], &sm.x_empty[0], &sm.x_empty[1],
-                        &sm.y_full[0], &sm.y_full[1], &sm.y_empty[0], &sm.y_empty[1], &sm.p_full,
-                        &sm.o_full, &sm.y_used, &sm.u_full, &sm.unit_full[0], &sm.unit_full[1],
-                        &sm.asked[0], &sm.asked[1]})
+    for (int i = 0; i < kStages; ++i)
+      for (uint64_t *b : {&sm.x_full[i], &sm.x_empty[i], &sm.y_full[i], &sm.y_empty[i]})
+        mbar_init(b, 1);
+    for (uint64_t *b : {&sm.p_full[0], &sm.p_full[1], &sm.y_used[0], &sm.y_used[1], &sm.o_full,
+                        &sm.u_full, &sm.s_used, &sm.unit_full[0], &sm.unit_full[1], &sm.asked[0], &sm.asked[1]})
       mbar_init(b, 1);
-    for (uint64_t *b : {&sm.p_ready, &sm.o_free, &sm.y_ready, &sm.s_ready}) mbar_init(b, 8);
+    for (uint64_t *b : {&sm.p_ready[0], &sm.p_ready[1], &sm.y_ready[0], &sm.y_ready[1], &sm.o_free,
+                        &sm.s_ready})
+      mbar_init(b, 8);
     for (uint64_t *b : {&sm.unit_empty[0], &sm.unit_empty[1]}) mbar_init(b, 18);
     fence_mbar_init();
   }
+  const bool ordered = p.length >= tokens && sequences <= kOrdered;
+  if (ordered)  // (the lengths lie where tiles come later)
+    order_sequences(p.cu, sequences, tokens, reinterpret_cast<int *>(sm.x[0]), sm.order);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -239,7 +285,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   }
   const int nx = BACK ? 1 : p.nx, ny = BACK ? p.ny : 1, items = BACK ? ny : nx;  // to a chunk
   const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
-  const uint32_t tP = tmem, tO = tmem + 128, tX = tmem + 256, tU = tmem + 384;  // P, O1, O2, S
+  // P (two, where heads are up to 64 wide), O1, O2, S
+  constexpr int kP = DP == 64 ? 2 : 1;
+  const uint32_t tP = tmem, tO = tmem + kP * 128, tX = tO + DP, tU = tX + DP;
   volatile int *abort = &sm.abort;
   const uint32_t lead = lane == 0;
   // chunk number `c` of a segment in the order walked: its first row in the
@@ -286,7 +334,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       }
       Segment g = {};
       if (!end) {
-        g = find_segment(p.cu, sequences, tokens, slot, p.length);
+        if (!ordered)
+          g = find_segment(p.cu, sequences, tokens, slot, p.length);
+        else if (slot < sequences)
+          g = whole_sequence(p.cu, tokens, sm.order[slot]);
         if (!g.any) continue;
       }
       if (k >= 2) ok = tc::warp_wait(&sm.unit_empty[k & 1], ((k >> 1) - 1) & 1, abort);
@@ -320,15 +371,15 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
           const int token = g.lo + first_row(g, c);
           for (int j = 0; j < items; ++j) {
             if (!BACK || j == 0) {
-              const int st = xi & 1;
-              if (xi >= 2 && !(ok = tc::mbar_wait(&sm.x_empty[st], ((xi >> 1) - 1) & 1, abort))) break;
+              const int st = xi % kStages, use = xi / kStages;
+              if (use > 0 && !(ok = tc::mbar_wait(&sm.x_empty[st], (use - 1) & 1, abort))) break;
               mbar_arrive_expect_tx(&sm.x_full[st], DP * 256);
               load(sm.x[st], &mx, &sm.x_full[st], h0 + (BACK ? 0 : j), token);
               ++xi;
             }
             if (BACK || j == 0) {
-              const int st = yi & 1, head = state_head * ny + (BACK ? j : 0);
-              if (yi >= 2 && !(ok = tc::mbar_wait(&sm.y_empty[st], ((yi >> 1) - 1) & 1, abort))) break;
+              const int st = yi % kStages, use = yi / kStages, head = state_head * ny + (BACK ? j : 0);
+              if (use > 0 && !(ok = tc::mbar_wait(&sm.y_empty[st], (use - 1) & 1, abort))) break;
               mbar_arrive_expect_tx(&sm.y_full[st], DP * 512);
               load(sm.y[st], &my, &sm.y_full[st], head, token);
               load(sm.z[st], &mz, &sm.y_full[st], head, token);
@@ -340,55 +391,117 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       ok = __shfl_sync(kFull, (int)ok, 0) != 0;
     }
   } else if (warp == 17) {
+    // Items of all units in their order. P of an item is formed as soon as its
+    // tiles are there and P's place is free; with two places an item ahead.
+    struct Item {
+      int k, c, j, chunks, n;  // unit, chunk, item of it; rows of the chunk
+      Segment g;
+      bool any;
+    };
+    const auto enter = [&](Item &x) {  // the first item of unit k
+      const Unit *unit = next_unit(x.k);
+      x.any = unit != nullptr;
+      if (!x.any) return;
+      x.g = unit->g;
+      x.c = x.j = 0;
+      x.chunks = chunks_of(x.g);
+      x.n = rows_of(x.g, 0);
+    };
+    const auto advance = [&](Item &x) {
+      if (++x.j < items) return;
+      x.j = 0;
+      if (++x.c < x.chunks) {
+        x.n = rows_of(x.g, x.c);
+        return;
+      }
+      ++x.k;
+      enter(x);
+    };
     bool ok = true;
-    // x, y: tiles of each ring; it: items; o: results; s: chunks
-    int xi = 0, yi = 0, it = 0, o = 0, u = 0, sc = 0;
-    for (int k = 0; ok; ++k) {
-      const Unit *unit = next_unit(k);
-      if (!unit) break;
-      const Segment g = unit->g;
-      const int chunks = chunks_of(g);
-      for (int c = 0; c < chunks && ok; ++c, ++sc) {
-      const int n = rows_of(g, c);
-      for (int j = 0; j < items; ++j, ++it) {
-        const bool new_x = !BACK || j == 0, new_y = BACK || j == 0, last = j + 1 == items;
-        unsigned char *x = sm.x[xi & 1], *y = sm.y[yi & 1], *z = sm.z[yi & 1];
-        if (new_x && !(ok = tc::warp_wait(&sm.x_full[xi & 1], (xi >> 1) & 1, abort))) break;
-        if (new_y && !(ok = tc::warp_wait(&sm.y_full[yi & 1], (yi >> 1) & 1, abort))) break;
-        if (n < kChunk) {  // what follows the sequence is another's: it must be finite
-          if (new_x) tc::clear_rows<DP, kChunk>(x, n, lane);
-          if (new_y) tc::clear_rows<DP, kChunk>(y, n, lane);
-          if (new_y) tc::clear_rows<DP, kChunk>(z, n, lane);
-          __syncwarp();
-        }
-        tc::product_nt<DP, kChunk>(lead, tP, tc::smem_addr(x), tc::smem_addr(y));
-        tc::commit(lead, &sm.p_full);
-        if (BACK || last) tc::commit(lead, &sm.y_used);  // every product of the unscaled keys
-        if (new_x) {
-          if (j == 0 && !(ok = tc::warp_wait(&sm.s_ready, sc & 1, abort))) break;
-          if (o > 0 && !(ok = tc::warp_wait(&sm.o_free, (o - 1) & 1, abort))) break;
-          tc::fence_after_sync();
-          product_state<DP>(lead, tX, tc::smem_addr(x), tc::smem_addr(sm.s));
-        }
-        if (!(ok = tc::warp_wait(&sm.p_ready, it & 1, abort))) break;
+    int pi = 0, px = 0, py = 0;  // items, x tiles and y tiles that P has been formed from
+    const auto weights = [&](const Item &x) {
+      const bool new_x = !BACK || x.j == 0, new_y = BACK || x.j == 0, last = x.j + 1 == items;
+      const int xi = new_x ? px++ : px - 1, yi = new_y ? py++ : py - 1;
+      const int xs = xi % kStages, ys = yi % kStages;
+      unsigned char *tx = sm.x[xs], *ty = sm.y[ys], *tz = sm.z[ys];
+      if (new_x) ok = ok && tc::warp_wait(&sm.x_full[xs], (xi / kStages) & 1, abort);
+      if (new_y) ok = ok && tc::warp_wait(&sm.y_full[ys], (yi / kStages) & 1, abort);
+      if (!ok) return;
+      if (x.n < kChunk) {  // what follows the sequence is another's: it must be finite
+        if (new_x) tc::clear_rows<DP, kChunk>(tx, x.n, lane);
+        if (new_y) tc::clear_rows<DP, kChunk>(ty, x.n, lane);
+        if (new_y) tc::clear_rows<DP, kChunk>(tz, x.n, lane);
+        __syncwarp();
+      }
+      tc::product_nt<DP, kChunk>(lead, tP + (kP > 1 ? (pi & 1) * 128 : 0), tc::smem_addr(tx),
+                                 tc::smem_addr(ty));
+      tc::commit(lead, &sm.p_full[pi & 1]);
+      if (BACK || last) tc::commit(lead, &sm.y_used[yi & 1]);  // every product of the unscaled keys
+      ++pi;
+    };
+    Item ahead = {}, now;
+    enter(ahead);
+    // x, y: tiles of each ring; it: items; o: results; sc: chunks
+    int xi = 0, yi = 0, o = 0, sc = 0;
+    if (ahead.any) weights(ahead);
+    for (int it = 0; ahead.any && ok; ++it) {
+      now = ahead;
+      if (kP > 1) {
+        advance(ahead);
+        if (ahead.any) weights(ahead);
+        if (!ok) break;
+      }
+      const int j = now.j;
+      const bool new_x = !BACK || j == 0, last = j + 1 == items;
+      const uint32_t x = tc::smem_addr(sm.x[xi % kStages]), y = tc::smem_addr(sm.y[yi % kStages]),
+                     z = tc::smem_addr(sm.z[yi % kStages]);
+      const auto state_product = [&] {
+        if (!new_x) return true;
+        if (o > 0 && !tc::warp_wait(&sm.o_free, (o - 1) & 1, abort)) return false;
         tc::fence_after_sync();
-        tc::product_parts<DP, kChunk, 8>(lead, tO, tP, tc::smem_addr(z), BACK && j > 0);
-        if (!BACK || last) {
-          tc::commit(lead, &sm.o_full);
-          ++o;
-          ++xi;
-        }
-        if (BACK || last) {
-          if (!(ok = tc::warp_wait(&sm.y_ready, u++ & 1, abort))) break;
-          tc::fence_after_sync();
-          product_tn<DP>(lead, tU, tc::smem_addr(y), tc::smem_addr(z), true);
-          if (last) tc::commit(lead, &sm.u_full);
-          tc::commit(lead, &sm.y_empty[yi & 1]);
-          ++yi;
-        }
+        product_state<DP>(lead, tX, x, tc::smem_addr(sm.s));
+        if (!BACK && !last) return true;
+        tc::commit(lead, &sm.s_used);  // every product of the rounded state
+        return true;
+      };
+      const auto own_product = [&] {
+        if (!tc::warp_wait(&sm.p_ready[it & 1], (it >> 1) & 1, abort)) return false;
+        tc::fence_after_sync();
+        tc::product_parts<DP, kChunk, 8>(lead, tO, tP + (kP > 1 ? (it & 1) * 128 : 0), z,
+                                         BACK && j > 0);
+        if (!BACK || last) tc::commit(lead, &sm.o_full);
+        return true;
+      };
+      const auto sum_product = [&] {
+        if (!BACK && !last) return true;
+        if (!tc::warp_wait(&sm.y_ready[yi & 1], (yi >> 1) & 1, abort)) return false;
+        tc::fence_after_sync();
+        product_tn<DP>(lead, tU, y, z, true);
+        if (last) tc::commit(lead, &sm.u_full);
+        return true;
+      };
+      if (j == 0 && !(ok = tc::warp_wait(&sm.s_ready, sc++ & 1, abort))) break;
+      // What the next state waits for comes first where its keys have long been
+      // scaled, and last where they are scaled while the others run.
+      if (kP > 1)
+        ok = sum_product() && state_product() && own_product();
+      else
+        ok = state_product() && own_product() && sum_product();
+      if (!ok) break;
+      if (!BACK || last) ++o, ++xi;
+      if (BACK || last) {
+        tc::commit(lead, &sm.y_empty[yi % kStages]);
+        ++yi;
       }
+      const int k = now.k;
+      const bool done = last && now.c + 1 == now.chunks;
+      if (kP == 1) {
+        if (done) unit_done(k);
+        advance(ahead);
+        if (ahead.any) weights(ahead);
+      } else if (done) {
+        unit_done(k);
       }
-      unit_done(k);
     }
   } else if (warp < 8) {
     // Blocks of 16 columns, every other one of a row to a thread. Where a block
@@ -404,14 +517,15 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       const int chunks = chunks_of(g), h0 = unit->h0;
       for (int c = 0; c < chunks; ++c) {
       for (int j = 0; j < items; ++j, ++it) {
-        tc::warp_wait(&sm.p_full, it & 1, abort);
+        tc::warp_wait(&sm.p_full[it & 1], (it >> 1) & 1, abort);
+        const uint32_t scores = tP + (kP > 1 ? (it & 1) * 128 : 0) + lanes;
         tc::fence_after_sync();
 #pragma unroll
         for (int i0 = 0; i0 < 4; i0 += 2) {
           // (two blocks are asked for together: a load takes some 300 clocks)
           uint32_t v[2][16];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) tc::ld16(tP + lanes + (2 * (i0 + i) + half) * 16, v[i]);
+          for (int i = 0; i < 2; ++i) tc::ld16(scores + (2 * (i0 + i) + half) * 16, v[i]);
           tc::wait_ld();
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -440,12 +554,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 w[e / 2 + 1] = pack_bf16(y.x, y.y);
               }
             }
-            tc::st8(tP + lanes + c0, w);
+            tc::st8(scores + c0, w);
           }
         }
         tc::wait_st();
         tc::fence_before_sync();
-        tc::warp_arrive(&sm.p_ready, lead);
+        tc::warp_arrive(&sm.p_ready[it & 1], lead);
         if (BACK && j + 1 < items) continue;
         const int n = rows_of(g, c), to_row = BACK ? n - 1 - r : r + 1;
         const float into = unit->power[to_row < 0 ? 0 : to_row] * p.out_scale;
@@ -455,7 +569,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         // A whole chunk's results take the place of its X and are copied out
         // from there; rows of the last one are stored as they are.
         const bool whole = n == kChunk;
-        unsigned char *tile = sm.x[o & 1];
+        unsigned char *tile = sm.x[o % kStages];
         tc::warp_wait(&sm.o_full, o & 1, abort);
         tc::fence_after_sync();
         const bool on = (whole || r < n) && !*abort;
@@ -496,7 +610,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         }
         if (whole) fence_proxy_async_shared();
         __syncwarp();
-        asm volatile("bar.arrive %0, 288;" ::"r"(1 + (o & 1)) : "memory");
+        asm volatile("bar.arrive %0, 288;" ::"r"(1 + o % kStages) : "memory");
         ++o;
       }
       }
@@ -512,16 +626,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       const int chunks = chunks_of(g), h0 = unit->h0;
       for (int c = 0; c < chunks; ++c)
         for (int j = 0; j < nx; ++j, ++o) {
-          asm volatile("bar.sync %0, 288;" ::"r"(1 + (o & 1)) : "memory");
+          asm volatile("bar.sync %0, 288;" ::"r"(1 + o % kStages) : "memory");
           if (lane == 0 && rows_of(g, c) == kChunk && !*abort) {
 #pragma unroll
             for (int b = 0; b < DP / 64; ++b)
               if (b * 64 < p.D)
-                store_box(sm.x[o & 1] + b * 16384, &mo, b * 64, h0 + j, g.lo + first_row(g, c));
+                store_box(sm.x[o % kStages] + b * 16384, &mo, b * 64, h0 + j, g.lo + first_row(g, c));
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           }
-          tc::warp_arrive(&sm.x_empty[o & 1], lead);
+          tc::warp_arrive(&sm.x_empty[o % kStages], lead);
         }
       unit_done(k);
     }
@@ -533,7 +647,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     // The state before a chunk: rounded, as the product's second operand (rows
     // in boxes of 64 columns), and times the chunk's decay back to where the
     // chunk's own part is added.
+    int handed = 0;
     const auto hand_over = [&](float keep) {
+      if (handed++ > 0) tc::warp_wait(&sm.s_used, handed & 1, abort);
       if (r < DP)
 #pragma unroll
         for (int c = 0; c < HC; c += 8) {
@@ -587,12 +703,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                   __ldg(reinterpret_cast<const float4 *>(from + (int64_t)r * p.D + half * HC + c));
         }
       }
+      // (asked for before the last unit's last product is waited for)
+      if (k > 0) tc::warp_wait(&sm.u_full, (sc - 1) & 1, abort);
       hand_over(unit->power[rows_of(g, 0)]);
       for (int c = 0; c < chunks; ++c, ++sc) {
       const int n = rows_of(g, c);
       for (int j = 0; j < ny; ++j, ++yi) {
-        tc::warp_wait(&sm.y_used, yi & 1, abort);
-        uint4 *y = reinterpret_cast<uint4 *>(sm.y[yi & 1]) + t;
+        tc::warp_wait(&sm.y_used[yi & 1], (yi >> 1) & 1, abort);
+        uint4 *y = reinterpret_cast<uint4 *>(sm.y[yi % kStages]) + t;
         Factor f[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -609,10 +727,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             y[(i0 + i) * 256] = t / 8 + i * 32 < n ? scaled(v[i], f[i]) : make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_shared();
-        tc::warp_arrive(&sm.y_ready, lead);
+        tc::warp_arrive(&sm.y_ready[yi & 1], lead);
       }
-      tc::warp_wait(&sm.u_full, sc & 1, abort);
       if (c + 1 == chunks) continue;
+      tc::warp_wait(&sm.u_full, sc & 1, abort);
       tc::fence_after_sync();
 #pragma unroll
       for (int i = 0; i < HC / 32; ++i)
@@ -737,21 +855,35 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       const int st = it & 1, first = it / p.ny * kChunk;
       tc::warp_wait(&sm.full[st], (it >> 1) & 1, abort);
       uint4 *y = reinterpret_cast<uint4 *>(sm.y[st]), *rest = reinterpret_cast<uint4 *>(sm.rest[st]);
-#pragma unroll 4
-      for (int i = threadIdx.x; i < DP * 16; i += 256) {
-        const int row = first + i / 8 % kChunk, left = BACK ? row + 1 : g.rows - 1 - row;
-        const float f = row < g.rows ? power(l2, left) * p.in_scale : 0.0f;
-        const uint4 v = row < g.rows ? y[i] : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t a[4], b[4];
+      float f[4];  // of rows threadIdx.x / 8, + 32, + 64, + 96
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float t0 = __uint_as_float(w[k] << 16) * f, t1 = __uint_as_float(w[k] & 0xffff0000u) * f;
-          a[k] = pack_bf16(t0, t1);
-          b[k] = pack_bf16(t0 - __uint_as_float(a[k] << 16), t1 - __uint_as_float(a[k] & 0xffff0000u));
+      for (int i = 0; i < 4; ++i) {
+        const int row = first + threadIdx.x / 8 + i * 32, left = BACK ? row + 1 : g.rows - 1 - row;
+        f[i] = row < g.rows ? power(l2, left) * p.in_scale : 0.0f;
+      }
+      y += threadIdx.x, rest += threadIdx.x;
+#pragma unroll
+      for (int i0 = 0; i0 < DP / 16; i0 += 4) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = y[(i0 + i) * 256];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // (rows that are not the sequence's may hold anything)
+          if (first + (int)threadIdx.x / 8 + i * 32 >= g.rows) v[i] = make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          const float2 f2 = make_float2(f[i], f[i]);
+          uint32_t a[4], b[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 t = __fmul2_rn(make_float2(__uint_as_float(w[k] << 16),
+                                                    __uint_as_float(w[k] & 0xffff0000u)), f2);
+            a[k] = pack_bf16(t.x, t.y);
+            b[k] = pack_bf16(t.x - __uint_as_float(a[k] << 16), t.y - __uint_as_float(a[k] & 0xffff0000u));
+          }
+          y[(i0 + i) * 256] = make_uint4(a[0], a[1], a[2], a[3]);
+          rest[(i0 + i) * 256] = make_uint4(b[0], b[1], b[2], b[3]);
         }
-        y[i] = make_uint4(a[0], a[1], a[2], a[3]);
-        rest[i] = make_uint4(b[0], b[1], b[2], b[3]);
       }
       fence_proxy_async_shared();
       tc::warp_arrive(&sm.ready[st], lead);
@@ -818,16 +950,17 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const JoinArgs p) {
   float run = p.init ? __ldg(p.init + own) : 0.0f;
   float *at = p.sums + ((int64_t)slot_of(lo, seq, p.length) * p.Hk + h) * size + i;
   const int64_t step = (int64_t)p.Hk * size;
-  for (int j = 0; j < n; j += 8) {
-    float add[8];
+  constexpr int kAtOnce = 20;
+  for (int j = 0; j < n; j += kAtOnce) {
+    float add[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kAtOnce; ++k) {
       const int seg = p.back ? n - 1 - j - k : j + k;
       // the last one walked is summed only if the last state is asked for
       add[k] = j + k < n - 1 || (j + k == n - 1 && p.last) ? at[seg * step] : 0.0f;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kAtOnce; ++k) {
       if (j + k >= n) break;
       const int seg = p.back ? n - 1 - j - k : j + k;
       const int rows = len - seg * p.length < p.length ? len - seg * p.length : p.length;
@@ -868,7 +1001,7 @@ Layout layout_of(int64_t sequences, int64_t tokens, int64_t Hk, int64_t group) {
   Layout l = {(tokens + kChunk - 1) / kChunk * kChunk, 1};
   if (l.length == 0) l.length = kChunk;
   for (int64_t nx = group; nx > 1; --nx)
-    if (group % nx == 0 && sequences * Hk * (group / nx) >= 2 * kSms) {
+    if (group % nx == 0 && sequences * Hk * (group / nx) >= kSms) {
       l.nx = (int)nx;
       break;
     }
