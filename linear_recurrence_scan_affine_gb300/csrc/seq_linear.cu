@@ -764,13 +764,16 @@ struct SumArgs {
   bool all;           // sums of every segment, not only of those that others follow
   float in_scale;
 };
+constexpr int kSumStages = 3;
 template <int DP>
 struct SumSmem {
   // (in this order: with 64 columns a product reads past y and rest, into rows
   // of its result that are not used)
-  alignas(1024) unsigned char y[2][DP * 256], rest[2][DP * 256], z[2][DP * 256];
-  uint64_t full[2], empty[2], ready[2], done;
+  alignas(1024) unsigned char y[kSumStages][DP * 256], rest[DP * 256], z[kSumStages][DP * 256];
+  uint64_t full[kSumStages], empty[kSumStages], ready, rest_free, done;
   Segment segment;
+  int len[kOrdered];
+  uint8_t order[kOrdered];
   uint32_t tmem;
   int abort;
 };
@@ -788,14 +791,21 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   const int h = blockIdx.x % p.Hk, slot = blockIdx.x / p.Hk;
   const int tokens = (int)p.tokens, sequences = (int)p.sequences;
   if (warp == 9) tc::tmem_alloc(&sm.tmem, 128);
+  const bool ordered = p.length >= tokens && sequences <= kOrdered;
+  if (ordered) order_sequences(p.cu, sequences, tokens, sm.len, sm.order);
   if (warp == 8) {
-    const Segment g = find_segment(p.cu, sequences, tokens, slot, p.length);
+    Segment g = {};
+    if (!ordered)
+      g = find_segment(p.cu, sequences, tokens, slot, p.length);
+    else if (slot < sequences)
+      g = whole_sequence(p.cu, tokens, sm.order[slot]);
     if (lane == 0) {
       sm.segment = g;
       sm.abort = (tc::smem_addr(raw) & 1023) != 0;
-      for (uint64_t *b : {&sm.full[0], &sm.full[1], &sm.empty[0], &sm.empty[1], &sm.done})
-        mbar_init(b, 1);
-      for (uint64_t *b : {&sm.ready[0], &sm.ready[1]}) mbar_init(b, 8);
+      for (int i = 0; i < kSumStages; ++i) mbar_init(&sm.full[i], 1), mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.rest_free, 1);
+      mbar_init(&sm.done, 1);
+      mbar_init(&sm.ready, 8);
       fence_mbar_init();
     }
   }
@@ -811,7 +821,8 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     if (warp == 9) tc::tmem_dealloc(sm.tmem, 128);
     if (sm.abort && threadIdx.x == 0) atomicMax(&device_status, (uint32_t)RLCS_ERR_CUDA);
     // an empty sequence's last state is its first
-    if (p.final && !g.any && slot == slot_of(g.lo, g.seq, p.length) && g.len == 0) {
+    if (p.final && !g.any && g.len == 0 &&
+        (ordered ? slot < sequences : slot == slot_of(g.lo, g.seq, p.length))) {
       const int64_t at = ((int64_t)g.seq * p.Hk + h) * p.D * p.D;
       for (int i = threadIdx.x; i < p.D * p.D; i += kSumThreads)
         p.sums[at + i] = p.init ? p.init[at + i] : 0.0f;
@@ -825,8 +836,8 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   if (warp == 8) {
     if (lane == 0)
       for (int it = 0; it < items; ++it) {
-        const int st = it & 1, token = g.lo + g.first + it / p.ny * kChunk;
-        if (it >= 2 && !tc::mbar_wait(&sm.empty[st], ((it >> 1) - 1) & 1, abort)) break;
+        const int st = it % kSumStages, use = it / kSumStages, token = g.lo + g.first + it / p.ny * kChunk;
+        if (use > 0 && !tc::mbar_wait(&sm.empty[st], (use - 1) & 1, abort)) break;
         mbar_arrive_expect_tx(&sm.full[st], DP * 256 * 2);
 #pragma unroll
         for (int b = 0; b < DP / 64; ++b) {
@@ -836,25 +847,27 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       }
   } else if (warp == 9) {
     for (int it = 0; it < items; ++it) {
-      const int st = it & 1, n = g.rows - it / p.ny * kChunk;
-      if (!tc::warp_wait(&sm.full[st], (it >> 1) & 1, abort)) break;
+      const int st = it % kSumStages, n = g.rows - it / p.ny * kChunk;
+      if (!tc::warp_wait(&sm.full[st], (it / kSumStages) & 1, abort)) break;
       if (n < kChunk) {
         tc::clear_rows<DP, kChunk>(sm.z[st], n, lane);
         __syncwarp();
       }
-      if (!tc::warp_wait(&sm.ready[st], (it >> 1) & 1, abort)) break;
+      if (!tc::warp_wait(&sm.ready, it & 1, abort)) break;
       tc::fence_after_sync();
       const uint32_t z = tc::smem_addr(sm.z[st]);
-      product_tn<DP>(lead, tmem, tc::smem_addr(sm.rest[st]), z, it > 0);
+      product_tn<DP>(lead, tmem, tc::smem_addr(sm.rest), z, it > 0);
+      tc::commit(lead, &sm.rest_free);
       product_tn<DP>(lead, tmem, tc::smem_addr(sm.y[st]), z, true);
       tc::commit(lead, &sm.empty[st]);
     }
     tc::commit(lead, &sm.done);
   } else {
     for (int it = 0; it < items; ++it) {
-      const int st = it & 1, first = it / p.ny * kChunk;
-      tc::warp_wait(&sm.full[st], (it >> 1) & 1, abort);
-      uint4 *y = reinterpret_cast<uint4 *>(sm.y[st]), *rest = reinterpret_cast<uint4 *>(sm.rest[st]);
+      const int st = it % kSumStages, first = it / p.ny * kChunk;
+      tc::warp_wait(&sm.full[st], (it / kSumStages) & 1, abort);
+      if (it > 0) tc::warp_wait(&sm.rest_free, (it - 1) & 1, abort);
+      uint4 *y = reinterpret_cast<uint4 *>(sm.y[st]), *rest = reinterpret_cast<uint4 *>(sm.rest);
       float f[4];  // of rows threadIdx.x / 8, + 32, + 64, + 96
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -886,7 +899,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         }
       }
       fence_proxy_async_shared();
-      tc::warp_arrive(&sm.ready[st], lead);
+      tc::warp_arrive(&sm.ready, lead);
     }
     const int r = threadIdx.x & 127, half = warp >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
