@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     for (int k = 0;; ++k) {
       const Unit *unit = next_unit(k);
       if (!unit) break;
-      const Segment g = unit->g;
+      const Segment &g = unit->g;
       const int chunks = chunks_of(g), h0 = unit->h0;
       for (int c = 0; c < chunks; ++c) {
       for (int j = 0; j < items; ++j, ++it) {
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     for (int k = 0;; ++k) {
       const Unit *unit = next_unit(k);
       if (!unit) break;
-      const Segment g = unit->g;
+      const Segment &g = unit->g;
       const int chunks = chunks_of(g), h0 = unit->h0;
       for (int c = 0; c < chunks; ++c)
         for (int j = 0; j < nx; ++j, ++o) {
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     for (int k = 0;; ++k) {
       const Unit *unit = next_unit(k);
       if (!unit) break;
-      const Segment g = unit->g;
+      const Segment &g = unit->g;
       const int chunks = chunks_of(g);
 #pragma unroll
       for (int c = 0; c < HC; ++c) s[c] = 0.0f;
