@@ -133,19 +133,28 @@ struct WalkArgs {
   const float *log_decay;
   const int32_t *cu;
   const float *init;   // [slots or sequences, Hk, D, D] or null
-  bf *out;             // [tokens, heads of x, D]
+  // Backwards dv and dk are two walks over the same queries, gradients and
+  // states: the units of one segment stand side by side in the grid, so that
+  // the second finds in L2 what the first has read (8 x 4096, 16 heads of 128:
+  // PAIRED us for both, 195 in two launches).
+  int walks;           // 1, or 2
+  bf *out[2];          // [tokens, heads of x, D]
+  bool transposed[2];  // init is [z's dimension, y's]
   int64_t sequences, tokens;
   int heads, group;    // heads of x; of x to a state
   int nx, ny;          // a block's heads of x; heads of y and z to a state
   int D, length;       // of a segment
   bool by_slot;        // init is by slot, else by sequence
-  bool transposed;     // init is [z's dimension, y's]
   float in_scale, out_scale;  // of y z^T, and of x S
+};
+struct WalkMaps {
+  CUtensorMap x, y, z, out;
 };
 
 struct Unit {
   Segment g;
   int slot, h0;             // the first head of x
+  int walk;
   bool end;                 // no unit: the block is done
   float power[kChunk + 1];  // of the decay
   // what weights are multiplied by: decays d steps long at 31 + d, zeros before
@@ -242,10 +251,8 @@ __device__ __noinline__ void zero_unheld(bf *out, int width, int lo, int hi, int
 
 template <int DP, bool BACK>
 __global__ void __launch_bounds__(kWalkThreads, 1)
-    linear_walk_kernel(const __grid_constant__ CUtensorMap mx,
-                       const __grid_constant__ CUtensorMap my,
-                       const __grid_constant__ CUtensorMap mz,
-                       const __grid_constant__ CUtensorMap mo, const WalkArgs p) {
+    linear_walk_kernel(const __grid_constant__ WalkMaps first,
+                       const __grid_constant__ WalkMaps second, const WalkArgs p) {
   extern __shared__ __align__(1024) unsigned char raw[];
   WalkSmem<DP> &sm = *reinterpret_cast<WalkSmem<DP> *>(raw);
   pdl_wait();
@@ -277,7 +284,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   tc::fence_after_sync();
   const int lo = bound(p.cu, 0, tokens), hi = bound(p.cu, sequences, tokens);
   if (warp < 8 && (lo > 0 || hi < tokens))
-    zero_unheld(p.out, p.heads * p.D, lo, hi > lo ? hi : lo, tokens, threadIdx.x, 256);
+    for (int i = 0; i < p.walks; ++i)
+      zero_unheld(p.out[i], p.heads * p.D, lo, hi > lo ? hi : lo, tokens, threadIdx.x, 256);
   if (sm.abort) {
     if (warp == 17) tc::tmem_dealloc(sm.tmem, 512);
     if (threadIdx.x == 0) atomicMax(&device_status, (uint32_t)RLCS_ERR_CUDA);
@@ -324,7 +332,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     int64_t block = blockIdx.x;
     for (int i = 0, k = 0; ok; ++i) {
       const bool end = block < 0;
-      const int slot = end ? 0 : (int)(block / blocks), h0 = end ? 0 : (int)(block % blocks) * p.nx;
+      const int walk = end ? 0 : (int)(block % p.walks);
+      const int64_t at = end ? 0 : block / p.walks;
+      const int slot = (int)(at / blocks), h0 = (int)(at % blocks) * p.nx;
       // the unit after this one, asked for a unit ago
       if (!end) {
         if (!(ok = tc::warp_wait(&sm.asked[i & 1], (i >> 1) & 1, abort))) break;
@@ -355,7 +365,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         if (lane == 0) u.power[kChunk] = power(l2, kChunk);
         if (lane < 16) u.near[lane] = scale * power(l2, BACK ? lane : 15 - lane);
       }
-      if (lane == 0) u.g = g, u.slot = slot, u.h0 = h0, u.end = end;
+      if (lane == 0) u.g = g, u.slot = slot, u.h0 = h0, u.walk = walk, u.end = end;
       tc::warp_arrive(&sm.unit_full[k & 1], lead);
       ++k;
       if (end) break;
@@ -366,6 +376,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
           for (int i = 0; i < DP / 64; ++i)
             tc::load_box(to + i * 16384, m, full, i * 64, head, token);
         };
+        const WalkMaps &m = walk ? second : first;
         const int chunks = chunks_of(g);
         for (int c = 0; c < chunks && ok; ++c) {
           const int token = g.lo + first_row(g, c);
@@ -374,15 +385,15 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
               const int st = xi % kStages, use = xi / kStages;
               if (use > 0 && !(ok = tc::mbar_wait(&sm.x_empty[st], (use - 1) & 1, abort))) break;
               mbar_arrive_expect_tx(&sm.x_full[st], DP * 256);
-              load(sm.x[st], &mx, &sm.x_full[st], h0 + (BACK ? 0 : j), token);
+              load(sm.x[st], &m.x, &sm.x_full[st], h0 + (BACK ? 0 : j), token);
               ++xi;
             }
             if (BACK || j == 0) {
               const int st = yi % kStages, use = yi / kStages, head = state_head * ny + (BACK ? j : 0);
               if (use > 0 && !(ok = tc::mbar_wait(&sm.y_empty[st], (use - 1) & 1, abort))) break;
               mbar_arrive_expect_tx(&sm.y_full[st], DP * 512);
-              load(sm.y[st], &my, &sm.y_full[st], head, token);
-              load(sm.z[st], &mz, &sm.y_full[st], head, token);
+              load(sm.y[st], &m.y, &sm.y_full[st], head, token);
+              load(sm.z[st], &m.z, &sm.y_full[st], head, token);
               ++yi;
             }
           }
@@ -565,7 +576,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         const float into = unit->power[to_row < 0 ? 0 : to_row] * p.out_scale;
         const int64_t row = (int64_t)g.lo + first_row(g, c) + r;
         const int head = h0 + (BACK ? 0 : j);
-        bf *out = p.out + (row * p.heads + head) * p.D + half * (DP / 2);
+        bf *out = p.out[unit->walk] + (row * p.heads + head) * p.D + half * (DP / 2);
         // A whole chunk's results take the place of its X and are copied out
         // from there; rows of the last one are stored as they are.
         const bool whole = n == kChunk;
@@ -631,7 +642,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
             for (int b = 0; b < DP / 64; ++b)
               if (b * 64 < p.D)
-                store_box(sm.x[o % kStages] + b * 16384, &mo, b * 64, h0 + j, g.lo + first_row(g, c));
+                store_box(sm.x[o % kStages] + b * 16384, unit->walk ? &second.out : &first.out, b * 64,
+                          h0 + j, g.lo + first_row(g, c));
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           }
@@ -691,7 +703,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       if (p.init && r < p.D) {
         const float *from = p.init + ((p.by_slot ? (int64_t)unit->slot : (int64_t)g.seq) *
                                           (p.heads / p.group) + unit->h0 / p.group) * p.D * p.D;
-        if (p.transposed) {
+        if (p.transposed[unit->walk]) {
 #pragma unroll
           for (int c = 0; c < HC; ++c)
             if (half * HC + c < p.D) s[c] = __ldg(from + (int64_t)(half * HC + c) * p.D + r);
@@ -989,15 +1001,16 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const JoinArgs p) {
 // Host: one walk
 // ---------------------------------------------------------------------------
 struct Walk {
-  View x, y, z;
+  View x[2], y[2], z[2];  // of one walk or two (see WalkArgs)
+  bf *out[2];
+  bool transposed[2];
+  int walks;
   const float *log_decay;
   const int32_t *cu;
   const float *init;
-  float *last;
-  bf *out;
+  float *last;  // of the first walk
   int64_t sequences, tokens;
   int Hk, nx, ny, D;
-  bool back, transposed;
   float in_scale, out_scale;
 };
 
@@ -1041,11 +1054,12 @@ rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
   const int64_t length = l.length;
   const int64_t n = slots(w.sequences, w.tokens, length);
   const bool split = length < w.tokens;
-  CUtensorMap mx, my, mz, mo;
-  if (w.tokens > 0 && (!map_of(&mx, w.x, w, w.Hk * w.nx) || !map_of(&my, w.y, w, w.Hk * w.ny) ||
-                       !map_of(&mz, w.z, w, w.Hk * w.ny) ||
-                       !map_of(&mo, {w.out, (int64_t)w.Hk * w.nx * w.D, w.D}, w, w.Hk * w.nx)))
-    return RLCS_ERR_CUDA;
+  WalkMaps m[2] = {};
+  for (int i = 0; w.tokens > 0 && i < w.walks; ++i)
+    if (!map_of(&m[i].x, w.x[i], w, w.Hk * w.nx) || !map_of(&m[i].y, w.y[i], w, w.Hk * w.ny) ||
+        !map_of(&m[i].z, w.z[i], w, w.Hk * w.ny) ||
+        !map_of(&m[i].out, {w.out[i], (int64_t)w.Hk * w.nx * w.D, w.D}, w, w.Hk * w.nx))
+      return RLCS_ERR_CUDA;
   cudaError_t e = cudaSuccess;
   if (split || w.last) {
     const SumArgs a = {w.log_decay, w.cu, split ? nullptr : w.init, split ? sums : w.last,
@@ -1054,14 +1068,13 @@ rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
     constexpr size_t smem = sizeof(SumSmem<DP>);
     e = allow_dynamic_smem<linear_sum_kernel<DP, BACK>>(smem);
     if (e != cudaSuccess) return launched(e);
-    if (w.tokens == 0) my = mz = CUtensorMap{};  // (no block comes to use them)
     e = launch_ex(linear_sum_kernel<DP, BACK>, dim3((unsigned)(n * w.Hk)), dim3(kSumThreads), smem,
-                  st, true, my, mz, a);
+                  st, true, m[0].y, m[0].z, a);
     if (e != cudaSuccess) return launched(e);
   }
   if (split) {
     const JoinArgs a = {w.log_decay, w.cu, w.init, sums, w.last, w.sequences, w.tokens, w.Hk, w.D,
-                        (int)length, BACK, w.transposed};
+                        (int)length, BACK, w.transposed[0]};
     const int64_t units = w.sequences * w.Hk;
     const dim3 grid((unsigned)ceil_div(w.D * w.D, 256), (unsigned)(units < 65535 ? units : 65535),
                     (unsigned)ceil_div(units, 65535));
@@ -1069,21 +1082,38 @@ rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
     if (e != cudaSuccess) return launched(e);
   }
   if (w.tokens == 0) return RLCS_OK;
-  const int64_t units = n * w.Hk * (w.nx / l.nx);
-  const WalkArgs a = {w.log_decay, w.cu, split ? sums : w.init, w.out, w.sequences, w.tokens,
-                      w.Hk * w.nx, w.nx, l.nx, w.ny, w.D, (int)length, split,
-                      !split && w.transposed, w.in_scale, w.out_scale};
+  // the sums of segments lie as the first walk has its state
+  WalkArgs a = {};
+  a.log_decay = w.log_decay;
+  a.cu = w.cu;
+  a.init = split ? sums : w.init;
+  a.walks = w.walks;
+  for (int i = 0; i < w.walks; ++i) {
+    a.out[i] = w.out[i];
+    a.transposed[i] = split ? w.transposed[i] != w.transposed[0] : w.transposed[i];
+  }
+  a.sequences = w.sequences;
+  a.tokens = w.tokens;
+  a.heads = w.Hk * w.nx;
+  a.group = w.nx;
+  a.nx = l.nx;
+  a.ny = w.ny;
+  a.D = w.D;
+  a.length = (int)length;
+  a.by_slot = split;
+  a.in_scale = w.in_scale;
+  a.out_scale = w.out_scale;
   constexpr size_t smem = sizeof(WalkSmem<DP>);
   static_assert(smem <= 232448 && sizeof(SumSmem<DP>) <= 232448, "a block has 227 KB");
   e = allow_dynamic_smem<linear_walk_kernel<DP, BACK>>(smem);
   if (e != cudaSuccess) return launched(e);
-  return launched(launch_ex(linear_walk_kernel<DP, BACK>, dim3((unsigned)units),
-                            dim3(kWalkThreads), smem, st, true, mx, my, mz, mo, a));
+  return launched(launch_ex(linear_walk_kernel<DP, BACK>,
+                            dim3((unsigned)(n * w.Hk * (w.nx / l.nx) * w.walks)),
+                            dim3(kWalkThreads), smem, st, true, m[0], m[1], a));
 }
+template <bool BACK>
 rlcs_status launch(const Walk &w, float *sums, cudaStream_t st) {
-  if (w.D <= 64)
-    return w.back ? launch_walk<64, true>(w, sums, st) : launch_walk<64, false>(w, sums, st);
-  return w.back ? launch_walk<128, true>(w, sums, st) : launch_walk<128, false>(w, sums, st);
+  return w.D <= 64 ? launch_walk<64, BACK>(w, sums, st) : launch_walk<128, BACK>(w, sums, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -1194,7 +1224,7 @@ bool linear_sizes(int64_t sequences, int64_t tokens, int64_t Hq, int64_t Hk, int
   return sequences >= 0 && tokens >= 0 && tokens <= INT32_MAX && Hq > 0 && Hk > 0 &&
          Hq % Hk == 0 && D > 0 && D <= 128 && D % 8 == 0 && t == RLCS_BF16 && scale >= 1e-30 &&
          scale <= 1e30 && product_fits(tokens, Hq, D) && sequences < INT32_MAX - 1024 &&
-         Hq < INT32_MAX && (sequences + tokens / 64 + 1) * Hq < (int64_t)INT32_MAX;
+         Hq < INT32_MAX && (sequences + tokens / 64 + 1) * Hq < (int64_t)INT32_MAX / 2;
 }
 
 }  // namespace
@@ -1255,26 +1285,26 @@ rlcs_status rlcs_linear_attention(const void *q, int64_t q_token_stride, int64_t
   if (!scratch || !aligned(scratch, 16) ||
       scratch_bytes < rlcs_linear_attention_scratch_bytes(sequences, tokens, Hq, Hk, D))
     return RLCS_ERR_WORKSPACE;
-  const Walk w = {{static_cast<const bf *>(q), q_token_stride, q_head_stride},
-                  {static_cast<const bf *>(k), k_token_stride, k_head_stride},
-                  {static_cast<const bf *>(v), v_token_stride, v_head_stride},
-                  log_decay,
-                  cu_seqlens,
-                  state,
-                  last_state,
-                  static_cast<bf *>(out),
-                  sequences,
-                  tokens,
-                  (int)Hk,
-                  (int)(Hq / Hk),
-                  1,
-                  (int)D,
-                  false,
-                  false,
-                  1.0f,
-                  (float)scale};
-  return launch(w, reinterpret_cast<float *>(static_cast<char *>(scratch) + 64),
-                reinterpret_cast<cudaStream_t>(stream));
+  Walk w = {};
+  w.x[0] = {static_cast<const bf *>(q), q_token_stride, q_head_stride};
+  w.y[0] = {static_cast<const bf *>(k), k_token_stride, k_head_stride};
+  w.z[0] = {static_cast<const bf *>(v), v_token_stride, v_head_stride};
+  w.out[0] = static_cast<bf *>(out);
+  w.walks = 1;
+  w.log_decay = log_decay;
+  w.cu = cu_seqlens;
+  w.init = state;
+  w.last = last_state;
+  w.sequences = sequences;
+  w.tokens = tokens;
+  w.Hk = (int)Hk;
+  w.nx = (int)(Hq / Hk);
+  w.ny = 1;
+  w.D = (int)D;
+  w.in_scale = 1.0f;
+  w.out_scale = (float)scale;
+  return launch<false>(w, reinterpret_cast<float *>(static_cast<char *>(scratch) + 64),
+                       reinterpret_cast<cudaStream_t>(stream));
 }
 
 rlcs_status rlcs_linear_attention_backward(
@@ -1320,21 +1350,34 @@ rlcs_status rlcs_linear_attention_backward(
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   float *sums = reinterpret_cast<float *>(static_cast<char *>(scratch) + 64);
   const int group = (int)(Hq / Hk);
-  Walk w = {vd, vv, vk, log_decay, cu_seqlens, state, nullptr, static_cast<bf *>(dq), sequences,
-            tokens, (int)Hk, group, 1, (int)D, false, true, 1.0f, (float)scale};
-  rlcs_status e = launch(w, sums, st);
+  Walk w = {};
+  w.log_decay = log_decay;
+  w.cu = cu_seqlens;
+  w.sequences = sequences;
+  w.tokens = tokens;
+  w.Hk = (int)Hk;
+  w.D = (int)D;
+  // dq
+  w.x[0] = vd, w.y[0] = vv, w.z[0] = vk;
+  w.out[0] = static_cast<bf *>(dq);
+  w.transposed[0] = true;
+  w.walks = 1;
+  w.init = state;
+  w.nx = group, w.ny = 1;
+  w.in_scale = 1.0f, w.out_scale = (float)scale;
+  const rlcs_status e = launch<false>(w, sums, st);
   if (e != RLCS_OK) return e;
-  w.x = vk, w.y = vq, w.z = vd;
+  // dv and dk
+  w.x[0] = vk, w.y[0] = vq, w.z[0] = vd;
+  w.x[1] = vv, w.y[1] = vd, w.z[1] = vq;
+  w.out[0] = static_cast<bf *>(dv);
+  w.out[1] = static_cast<bf *>(dk);
+  w.transposed[0] = false, w.transposed[1] = true;
+  w.walks = 2;
+  w.init = dlast, w.last = dstate;
   w.nx = 1, w.ny = group;
   w.in_scale = (float)scale, w.out_scale = 1.0f;
-  w.init = dlast, w.last = dstate, w.transposed = false, w.back = true;
-  w.out = static_cast<bf *>(dv);
-  e = launch(w, sums, st);
-  if (e != RLCS_OK) return e;
-  w.x = vv, w.y = vd, w.z = vq;
-  w.last = nullptr, w.transposed = true;
-  w.out = static_cast<bf *>(dk);
-  return launch(w, sums, st);
+  return launch<true>(w, sums, st);
 }
 
 rlcs_status rlcs_linear_attention_step(const void *q, int64_t q_batch_stride,
