@@ -300,7 +300,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
   const uint32_t lead = lane == 0;
   // chunk number `c` of a segment in the order walked: its first row in the
   // sequence, and its rows
-  const auto chunks_of = [](const Segment &g) { return (g.rows + kChunk - 1) / kChunk; };
+  const auto chunks_of = [](const Segment &g) {
+    return (int)((unsigned)(g.rows + kChunk - 1) / (unsigned)kChunk);
+  };
   const auto first_row = [&](const Segment &g, int c) {
     return g.first + (BACK ? chunks_of(g) - 1 - c : c) * kChunk;
   };
@@ -405,26 +407,23 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     // Items of all units in their order. P of an item is formed as soon as its
     // tiles are there and P's place is free; with two places an item ahead.
     struct Item {
-      int k, c, j, chunks, n;  // unit, chunk, item of it; rows of the chunk
-      Segment g;
+      int k, c, j, chunks;  // unit, chunk and item of it; chunks of the unit
+      int part, rows;       // the one chunk that may be short, and its rows
       bool any;
     };
     const auto enter = [&](Item &x) {  // the first item of unit k
       const Unit *unit = next_unit(x.k);
       x.any = unit != nullptr;
       if (!x.any) return;
-      x.g = unit->g;
       x.c = x.j = 0;
-      x.chunks = chunks_of(x.g);
-      x.n = rows_of(x.g, 0);
+      x.chunks = chunks_of(unit->g);
+      x.part = BACK ? 0 : x.chunks - 1;
+      x.rows = rows_of(unit->g, x.part);
     };
     const auto advance = [&](Item &x) {
       if (++x.j < items) return;
       x.j = 0;
-      if (++x.c < x.chunks) {
-        x.n = rows_of(x.g, x.c);
-        return;
-      }
+      if (++x.c < x.chunks) return;
       ++x.k;
       enter(x);
     };
@@ -438,10 +437,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       if (new_x) ok = ok && tc::warp_wait(&sm.x_full[xs], (xi / kStages) & 1, abort);
       if (new_y) ok = ok && tc::warp_wait(&sm.y_full[ys], (yi / kStages) & 1, abort);
       if (!ok) return;
-      if (x.n < kChunk) {  // what follows the sequence is another's: it must be finite
-        if (new_x) tc::clear_rows<DP, kChunk>(tx, x.n, lane);
-        if (new_y) tc::clear_rows<DP, kChunk>(ty, x.n, lane);
-        if (new_y) tc::clear_rows<DP, kChunk>(tz, x.n, lane);
+      if (x.c == x.part && x.rows < kChunk) {  // what follows is another's: it must be finite
+        if (new_x) tc::clear_rows<DP, kChunk>(tx, x.rows, lane);
+        if (new_y) tc::clear_rows<DP, kChunk>(ty, x.rows, lane);
+        if (new_y) tc::clear_rows<DP, kChunk>(tz, x.rows, lane);
         __syncwarp();
       }
       tc::product_nt<DP, kChunk>(lead, tP + (kP > 1 ? (pi & 1) * 128 : 0), tc::smem_addr(tx),
@@ -471,8 +470,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         if (o > 0 && !tc::warp_wait(&sm.o_free, (o - 1) & 1, abort)) return false;
         tc::fence_after_sync();
         product_state<DP>(lead, tX, x, tc::smem_addr(sm.s));
-        if (!BACK && !last) return true;
-        tc::commit(lead, &sm.s_used);  // every product of the rounded state
+        // every product of the rounded state (with one place for P the sum comes
+        // after them, and stands for them)
+        if (kP > 1 && (BACK || last)) tc::commit(lead, &sm.s_used);
         return true;
       };
       const auto own_product = [&] {
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     // chunk's own part is added.
     int handed = 0;
     const auto hand_over = [&](float keep) {
-      if (handed++ > 0) tc::warp_wait(&sm.s_used, handed & 1, abort);
+      if (kP > 1 && handed++ > 0) tc::warp_wait(&sm.s_used, handed & 1, abort);
       if (r < DP)
 #pragma unroll
         for (int c = 0; c < HC; c += 8) {
