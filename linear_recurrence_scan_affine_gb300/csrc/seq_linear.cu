@@ -113,7 +113,9 @@ __device__ uint32_t device_status;
 
 // ---------------------------------------------------------------------------
 // The walk in chunks of 128 tokens. A unit of work is a segment and one or more
-// heads of x that read the same state. The grid has a block to each; one that
+// heads of x that read the same state, of one chunk at least: the warp that
+// issues products looks a unit ahead, and no further, or it would wait for a
+// place that it has to give up itself. The grid has a block to each; one that
 // runs takes over units of blocks that have not started, and what it copies in
 // runs ahead into the next unit. (48 packed episodes: TAKEN us; with units
 // dealt out beforehand 303, without running ahead 238.)
@@ -126,8 +128,8 @@ __device__ uint32_t device_status;
 // its own); backwards one X and `ny` Y and Z (items that add up).
 // Warps 0..7 turn P into P' and sums into results, two threads to a row; warps
 // 8..15 scale Y in place, decay S and hand its rounding to bfloat16 to the next
-// chunk. Warp 16 copies in, warp 18 out, warp 17 issues products. In tensor memory, float32: P
-// (P' over it), O1, O2, S.
+// chunk. Warp 16 copies in, warp 18 out, warp 17 issues products. In tensor
+// memory, float32: P (P' over it), O1, O2, S.
 // ---------------------------------------------------------------------------
 struct WalkArgs {
   const float *log_decay;
@@ -236,13 +238,13 @@ __device__ __forceinline__ void store_box(const void *from, const CUtensorMap *m
       : "memory");
 }
 
-// Rows of out that no sequence holds, each block taking a share.
-__device__ __noinline__ void zero_unheld(bf *out, int width, int lo, int hi, int tokens, int thread,
-                                         int threads) {
+// Rows of out that no sequence holds, [0, lo) and [hi, tokens): share number
+// `share` of `shares`, by a warp.
+__device__ __noinline__ void zero_unheld(bf *out, int width, int lo, int hi, int tokens,
+                                         int64_t share, int64_t shares) {
   const int eights = width / 8;
   const int64_t n = (int64_t)(lo + tokens - hi) * eights;
-  for (int64_t i = (int64_t)blockIdx.x * threads + thread; i < n;
-       i += (int64_t)gridDim.x * threads) {
+  for (int64_t i = share * 32 + (threadIdx.x & 31); i < n; i += shares * 32) {
     const int64_t row = i / eights;
     reinterpret_cast<uint4 *>(out + (row < lo ? row : row - lo + hi) * width)[i % eights] =
         make_uint4(0, 0, 0, 0);
@@ -277,15 +279,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     fence_mbar_init();
   }
   const bool ordered = p.length >= tokens && sequences <= kOrdered;
-  if (ordered)  // (the lengths lie where tiles come later)
-    order_sequences(p.cu, sequences, tokens, reinterpret_cast<int *>(sm.x[0]), sm.order);
+  static_assert(sizeof(sm.unit[0].decay) >= kOrdered * sizeof(int), "room for the lengths");
+  if (ordered)  // (the lengths lie where a unit's decays come later)
+    order_sequences(p.cu, sequences, tokens, reinterpret_cast<int *>(sm.unit[0].decay), sm.order);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const int lo = bound(p.cu, 0, tokens), hi = bound(p.cu, sequences, tokens);
-  if (warp < 8 && (lo > 0 || hi < tokens))
-    for (int i = 0; i < p.walks; ++i)
-      zero_unheld(p.out[i], p.heads * p.D, lo, hi > lo ? hi : lo, tokens, threadIdx.x, 256);
+  // Rows of results that no sequence holds are zeros: each unit has a share of
+  // them, units without a segment too, and the warp that copies in writes it.
+  const int lo = bound(p.cu, 0, tokens), hi = max(lo, bound(p.cu, sequences, tokens));
+  const bool unheld = lo > 0 || hi < tokens;
   if (sm.abort) {
     if (warp == 17) tc::tmem_dealloc(sm.tmem, 512);
     if (threadIdx.x == 0) atomicMax(&device_status, (uint32_t)RLCS_ERR_CUDA);
@@ -350,6 +353,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
           g = find_segment(p.cu, sequences, tokens, slot, p.length);
         else if (slot < sequences)
           g = whole_sequence(p.cu, tokens, sm.order[slot]);
+        if (unheld)
+          zero_unheld(p.out[walk], p.heads * p.D, lo, hi, tokens, at, gridDim.x / p.walks);
         if (!g.any) continue;
       }
       if (k >= 2) ok = tc::warp_wait(&sm.unit_empty[k & 1], ((k >> 1) - 1) & 1, abort);
@@ -415,8 +420,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       const Unit *unit = next_unit(x.k);
       x.any = unit != nullptr;
       if (!x.any) return;
-      x.c = x.j = 0;
       x.chunks = chunks_of(unit->g);
+      x.c = x.j = 0;
       x.part = BACK ? 0 : x.chunks - 1;
       x.rows = rows_of(unit->g, x.part);
     };
@@ -527,103 +532,103 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       const Segment &g = unit->g;
       const int chunks = chunks_of(g), h0 = unit->h0;
       for (int c = 0; c < chunks; ++c) {
-      for (int j = 0; j < items; ++j, ++it) {
-        tc::warp_wait(&sm.p_full[it & 1], (it >> 1) & 1, abort);
-        const uint32_t scores = tP + (kP > 1 ? (it & 1) * 128 : 0) + lanes;
-        tc::fence_after_sync();
+        for (int j = 0; j < items; ++j, ++it) {
+          tc::warp_wait(&sm.p_full[it & 1], (it >> 1) & 1, abort);
+          const uint32_t scores = tP + (kP > 1 ? (it & 1) * 128 : 0) + lanes;
+          tc::fence_after_sync();
 #pragma unroll
-        for (int i0 = 0; i0 < 4; i0 += 2) {
-          // (two blocks are asked for together: a load takes some 300 clocks)
-          uint32_t v[2][16];
+          for (int i0 = 0; i0 < 4; i0 += 2) {
+            // (two blocks are asked for together: a load takes some 300 clocks)
+            uint32_t v[2][16];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) tc::ld16(scores + (2 * (i0 + i) + half) * 16, v[i]);
-          tc::wait_ld();
+            for (int i = 0; i < 2; ++i) tc::ld16(scores + (2 * (i0 + i) + half) * 16, v[i]);
+            tc::wait_ld();
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int c0 = (2 * (i0 + i) + half) * 16;
-            uint32_t w[8];
-            // (the same for the whole warp)
-            if (i0 + i == (warp & 3)) {  // the row's own 32 columns are among these
-              const float *d = unit->decay + 31 + (BACK ? c0 - r : r - c0);
+            for (int i = 0; i < 2; ++i) {
+              const int c0 = (2 * (i0 + i) + half) * 16;
+              uint32_t w[8];
+              // (the same for the whole warp)
+              if (i0 + i == (warp & 3)) {  // the row's own 32 columns are among these
+                const float *d = unit->decay + 31 + (BACK ? c0 - r : r - c0);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)  // the type that the product takes
-                w[e] = pack_bf16(__uint_as_float(v[i][2 * e]) * d[BACK ? 2 * e : -2 * e],
-                                 __uint_as_float(v[i][2 * e + 1]) * d[BACK ? 2 * e + 1 : -2 * e - 1]);
-            } else if (BACK ? i0 + i < (warp & 3) : i0 + i > (warp & 3)) {
+                for (int e = 0; e < 8; ++e)  // the type that the product takes
+                  w[e] = pack_bf16(__uint_as_float(v[i][2 * e]) * d[BACK ? 2 * e : -2 * e],
+                                   __uint_as_float(v[i][2 * e + 1]) * d[BACK ? 2 * e + 1 : -2 * e - 1]);
+              } else if (BACK ? i0 + i < (warp & 3) : i0 + i > (warp & 3)) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) w[e] = 0;
-            } else {
-              const float f = unit->power[BACK ? c0 - r : r - c0 - 15];
+                for (int e = 0; e < 8; ++e) w[e] = 0;
+              } else {
+                const float f = unit->power[BACK ? c0 - r : r - c0 - 15];
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                const float4 k = *reinterpret_cast<const float4 *>(unit->near + e);
-                const float2 a = __fmul2_rn(make_float2(k.x, k.y), make_float2(f, f)),
-                             b = __fmul2_rn(make_float2(k.z, k.w), make_float2(f, f));
-                const float2 x = __fmul2_rn(make_float2(__uint_as_float(v[i][e]), __uint_as_float(v[i][e + 1])), a),
-                             y = __fmul2_rn(make_float2(__uint_as_float(v[i][e + 2]), __uint_as_float(v[i][e + 3])), b);
-                w[e / 2] = pack_bf16(x.x, x.y);
-                w[e / 2 + 1] = pack_bf16(y.x, y.y);
+                for (int e = 0; e < 16; e += 4) {
+                  const float4 k = *reinterpret_cast<const float4 *>(unit->near + e);
+                  const float2 a = __fmul2_rn(make_float2(k.x, k.y), make_float2(f, f)),
+                               b = __fmul2_rn(make_float2(k.z, k.w), make_float2(f, f));
+                  const float2 x = __fmul2_rn(make_float2(__uint_as_float(v[i][e]), __uint_as_float(v[i][e + 1])), a),
+                               y = __fmul2_rn(make_float2(__uint_as_float(v[i][e + 2]), __uint_as_float(v[i][e + 3])), b);
+                  w[e / 2] = pack_bf16(x.x, x.y);
+                  w[e / 2 + 1] = pack_bf16(y.x, y.y);
+                }
               }
+              tc::st8(scores + c0, w);
             }
-            tc::st8(scores + c0, w);
           }
-        }
-        tc::wait_st();
-        tc::fence_before_sync();
-        tc::warp_arrive(&sm.p_ready[it & 1], lead);
-        if (BACK && j + 1 < items) continue;
-        const int n = rows_of(g, c), to_row = BACK ? n - 1 - r : r + 1;
-        const float into = unit->power[to_row < 0 ? 0 : to_row] * p.out_scale;
-        const int64_t row = (int64_t)g.lo + first_row(g, c) + r;
-        const int head = h0 + (BACK ? 0 : j);
-        bf *out = p.out[unit->walk] + (row * p.heads + head) * p.D + half * (DP / 2);
-        // A whole chunk's results take the place of its X and are copied out
-        // from there; rows of the last one are stored as they are.
-        const bool whole = n == kChunk;
-        unsigned char *tile = sm.x[o % kStages];
-        tc::warp_wait(&sm.o_full, o & 1, abort);
-        tc::fence_after_sync();
-        const bool on = (whole || r < n) && !*abort;
-        const float2 f = make_float2(into, into);
+          tc::wait_st();
+          tc::fence_before_sync();
+          tc::warp_arrive(&sm.p_ready[it & 1], lead);
+          if (BACK && j + 1 < items) continue;
+          const int n = rows_of(g, c), to_row = BACK ? n - 1 - r : r + 1;
+          const float into = unit->power[to_row < 0 ? 0 : to_row] * p.out_scale;
+          const int64_t row = (int64_t)g.lo + first_row(g, c) + r;
+          const int head = h0 + (BACK ? 0 : j);
+          bf *out = p.out[unit->walk] + (row * p.heads + head) * p.D + half * (DP / 2);
+          // A whole chunk's results take the place of its X and are copied out
+          // from there; rows of the last one are stored as they are.
+          const bool whole = n == kChunk;
+          unsigned char *tile = sm.x[o % kStages];
+          tc::warp_wait(&sm.o_full, o & 1, abort);
+          tc::fence_after_sync();
+          const bool on = (whole || r < n) && !*abort;
+          const float2 f = make_float2(into, into);
 #pragma unroll
-        for (int i = 0; i < DP / 64; ++i) {
-          uint32_t a[32], b[32];
-          tc::ld32(tO + lanes + half * (DP / 2) + i * 32, a);
-          tc::ld32(tX + lanes + half * (DP / 2) + i * 32, b);
-          tc::wait_ld();
-          if (i + 1 == DP / 64) {
-            tc::fence_before_sync();
-            tc::warp_arrive(&sm.o_free, lead);
-          }
-          // (a row that the state does not reach takes nothing of it, whatever it holds)
-          if (into == 0.0f)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) b[e] = 0;
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            const int col = half * (DP / 2) + i * 32 + e;
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int q = e + 2 * k;
-              const float2 t =
-                  __ffma2_rn(make_float2(__uint_as_float(b[q]), __uint_as_float(b[q + 1])), f,
-                             make_float2(__uint_as_float(a[q]), __uint_as_float(a[q + 1])));
-              w[k] = pack_bf16(t.x, t.y);
+          for (int i = 0; i < DP / 64; ++i) {
+            uint32_t a[32], b[32];
+            tc::ld32(tO + lanes + half * (DP / 2) + i * 32, a);
+            tc::ld32(tX + lanes + half * (DP / 2) + i * 32, b);
+            tc::wait_ld();
+            if (i + 1 == DP / 64) {
+              tc::fence_before_sync();
+              tc::warp_arrive(&sm.o_free, lead);
             }
-            const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
-            if (whole)
-              *reinterpret_cast<uint4 *>(tile + col / 64 * 16384 + r * 128 +
-                                         ((col % 64 / 8 ^ (r & 7)) * 16)) = v;
-            else if (on && col < p.D)
-              *reinterpret_cast<uint4 *>(out + i * 32 + e) = v;
+            // (a row that the state does not reach takes nothing of it, whatever it holds)
+            if (into == 0.0f)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) b[e] = 0;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              const int col = half * (DP / 2) + i * 32 + e;
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int q = e + 2 * k;
+                const float2 t =
+                    __ffma2_rn(make_float2(__uint_as_float(b[q]), __uint_as_float(b[q + 1])), f,
+                               make_float2(__uint_as_float(a[q]), __uint_as_float(a[q + 1])));
+                w[k] = pack_bf16(t.x, t.y);
+              }
+              const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+              if (whole)
+                *reinterpret_cast<uint4 *>(tile + col / 64 * 16384 + r * 128 +
+                                           ((col % 64 / 8 ^ (r & 7)) * 16)) = v;
+              else if (on && col < p.D)
+                *reinterpret_cast<uint4 *>(out + i * 32 + e) = v;
+            }
           }
+          if (whole) fence_proxy_async_shared();
+          __syncwarp();
+          asm volatile("bar.arrive %0, 288;" ::"r"(1 + o % kStages) : "memory");
+          ++o;
         }
-        if (whole) fence_proxy_async_shared();
-        __syncwarp();
-        asm volatile("bar.arrive %0, 288;" ::"r"(1 + o % kStages) : "memory");
-        ++o;
-      }
       }
       unit_done(k);
     }
@@ -716,42 +721,44 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         }
       }
       // (asked for before the last unit's last product is waited for)
-      if (k > 0) tc::warp_wait(&sm.u_full, (sc - 1) & 1, abort);
+      if (sc > 0) tc::warp_wait(&sm.u_full, (sc - 1) & 1, abort);
       hand_over(unit->power[rows_of(g, 0)]);
       for (int c = 0; c < chunks; ++c, ++sc) {
-      const int n = rows_of(g, c);
-      for (int j = 0; j < ny; ++j, ++yi) {
-        tc::warp_wait(&sm.y_used[yi & 1], (yi >> 1) & 1, abort);
-        uint4 *y = reinterpret_cast<uint4 *>(sm.y[yi % kStages]) + t;
-        Factor f[4];
+        const int n = rows_of(g, c);
+        for (int j = 0; j < ny; ++j, ++yi) {
+          tc::warp_wait(&sm.y_used[yi & 1], (yi >> 1) & 1, abort);
+          uint4 *y = reinterpret_cast<uint4 *>(sm.y[yi % kStages]) + t;
+          Factor f[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = t / 8 + i * 32, left = BACK ? row + 1 : n - 1 - row;
-          f[i] = factor(unit->power[left < 0 ? 0 : left] * p.in_scale);
+          for (int i = 0; i < 4; ++i) {
+            const int row = t / 8 + i * 32, left = BACK ? row + 1 : n - 1 - row;
+            f[i] = factor(unit->power[left < 0 ? 0 : left] * p.in_scale);
+          }
+#pragma unroll
+          for (int i0 = 0; i0 < kTimes; i0 += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = y[(i0 + i) * 256];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // (rows that are not the sequence's are zeros already)
+              y[(i0 + i) * 256] = t / 8 + i * 32 < n ? scaled(v[i], f[i]) : make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_shared();
+          tc::warp_arrive(&sm.y_ready[yi & 1], lead);
         }
+        if (c + 1 == chunks) continue;
+        tc::warp_wait(&sm.u_full, sc & 1, abort);
+        tc::fence_after_sync();
 #pragma unroll
-        for (int i0 = 0; i0 < kTimes; i0 += 4) {
-          uint4 v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = y[(i0 + i) * 256];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)  // (rows that are not the sequence's are zeros already)
-            y[(i0 + i) * 256] = t / 8 + i * 32 < n ? scaled(v[i], f[i]) : make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_shared();
-        tc::warp_arrive(&sm.y_ready[yi & 1], lead);
-      }
-      if (c + 1 == chunks) continue;
-      tc::warp_wait(&sm.u_full, sc & 1, abort);
-      tc::fence_after_sync();
-#pragma unroll
-      for (int i = 0; i < HC / 32; ++i)
-        tc::ld32(tU + lanes + half * HC + i * 32, *reinterpret_cast<uint32_t(*)[32]>(s + i * 32));
-      tc::wait_ld();
-      hand_over(unit->power[rows_of(g, c + 1)]);
+        for (int i = 0; i < HC / 32; ++i)
+          tc::ld32(tU + lanes + half * HC + i * 32, *reinterpret_cast<uint32_t(*)[32]>(s + i * 32));
+        tc::wait_ld();
+        hand_over(unit->power[rows_of(g, c + 1)]);
       }
       unit_done(k);
     }
+    // no product is under way when tensor memory is given up
+    if (sc > 0) tc::warp_wait(&sm.u_full, (sc - 1) & 1, abort);
   }
   tc::fence_before_sync();
   __syncthreads();

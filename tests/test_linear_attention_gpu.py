@@ -160,6 +160,30 @@ def test_tokens_of_no_sequence(rl):
                                                lens))
 
 
+def test_many_units_and_tokens_of_no_sequence(rl):
+    # more units of work than run at once, and most tokens in none of them
+    H, D, n, first = 16, 64, 9000, 700
+    g = gen(31)
+    lens = torch.randint(0, 60, (40,), generator=g).tolist()
+    q, k, v, do = (rand(g, n, H, D).cuda() for _ in range(4))
+    ld = -torch.rand(H, generator=g).cuda()
+    cu = bounds(lens, first).cuda()
+    inside = slice(first, first + sum(lens))
+    for t in (q, k, v, do):
+        t[:first], t[inside.stop:] = math.nan, math.nan
+    junk = torch.full((1 << 26,), math.nan, device="cuda")  # memory the results may come from
+    del junk
+    out = rl.rlcs_linear_attention(q, k, v, ld, cu)
+    grads = rl.rlcs_linear_attention_backward(do, q, k, v, ld, cu)[:3]
+    part = [t[inside].contiguous() for t in (do, q, k, v)]
+    small = [rl.rlcs_linear_attention(*part[1:], ld, bounds(lens).cuda()),
+             *rl.rlcs_linear_attention_backward(*part, ld, bounds(lens).cuda())[:3]]
+    for t, w in zip((out, *grads), small):
+        assert not t[:first].any() and not t[inside.stop:].any()
+        assert torch.equal(t[inside], w)
+    rl.check_scratch()
+
+
 def test_no_tokens_and_no_sequences(rl):
     S = torch.randn(3, 2, 64, 64, device="cuda")
     e = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
@@ -238,6 +262,31 @@ def test_a_nan_state_passes_no_closed_head(rl):
     got = rl.rlcs_linear_attention(*cuda(q, k, v, ld), bounds([40, 200]).cuda(), state=S.cuda(),
                                    return_state=True)
     assert all(torch.equal(a, b) for a, b in zip(clean, got))
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(6, 2, 64), (4, 4, 128), (12, 3, 32)])
+def test_empty_sequences_between_many(rl, Hq, Hk, D):
+    # blocks take up unit after unit, some without a token, of one chunk and of several
+    g = gen(41)
+    lens = [0 if torch.rand(1, generator=g) < 0.4 else
+            int(torch.randint(1, 400, (1,), generator=g)) for _ in range(300)]
+    for some in (lens, lens[:120]):  # more sequences than are put in order, and fewer
+        q, k, v, ld, S, do, dl = cuda(*case(43, some, Hq, Hk, D, True))
+        cu = bounds(some).cuda()
+        out, last = rl.rlcs_linear_attention(q, k, v, ld, cu, state=S, return_state=True)
+        grads = rl.rlcs_linear_attention_backward(do, q, k, v, ld, cu, state=S, dlast=dl)
+        rl.check_scratch()
+        at = cu.tolist()
+        for s in range(0, len(some), 17):  # each sequence as if alone
+            r = slice(at[s], at[s + 1])
+            one = bounds([some[s]]).cuda()
+            args = (q[r], k[r], v[r], ld, one)
+            o, l = rl.rlcs_linear_attention(*args, state=S[s:s + 1], return_state=True)
+            b = rl.rlcs_linear_attention_backward(do[r], *args, state=S[s:s + 1],
+                                                  dlast=dl[s:s + 1])
+            assert torch.equal(out[r], o) and torch.equal(last[s:s + 1], l), s
+            assert all(torch.equal(x[r], y) for x, y in zip(grads[:3], b)), s
+            assert torch.equal(grads[3][s:s + 1], b[3]), s
 
 
 def test_gradient_against_differences(rl):
