@@ -90,7 +90,8 @@ rlcs_status rlcs_policy_loss_backward(
  * adds nothing to the loss. Entries whose id lies outside [0, V) or whose
  * logit is -infinity are absent; a token all of whose entries are absent has
  * loss 0 and gradient 0, whatever its logits. An id may occur more
- * than once: its entries are separate terms. loss [tokens]. temperature > 0; 1 <= K <= 1024; 1 <= V < 2^31. */
+ * than once: its entries are separate terms. loss [tokens]. 1e-6 <=
+ * temperature <= 1e6; 1 <= K <= 1024; 1 <= V < 2^31. */
 rlcs_status rlcs_distill_loss(const void *logits, int64_t row_stride, const int32_t *top_ids,
                               const float *top_logits, const float *teacher_lse,
                               const uint8_t *mask, float *loss, int64_t tokens, int64_t V,

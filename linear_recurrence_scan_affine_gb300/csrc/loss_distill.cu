@@ -280,9 +280,13 @@ struct DistillLeader {
   }
   __device__ __forceinline__ void ahead(int64_t, bool) {}
   __device__ __forceinline__ void before(int64_t, bool) {}
-  __device__ __forceinline__ float held() const { return 0.0f; }
-  __device__ __forceinline__ void plan(int64_t, const Stats &s, bool, int, LongSmem &sm) {
+  // The teacher's warp has put the student's logits of its entries into shared
+  // memory: they have been read.
+  __device__ __forceinline__ float held() const {
     meet_wait<64>(kTaught);
+    return 0.0f;
+  }
+  __device__ __forceinline__ void plan(int64_t, const Stats &s, bool, int, LongSmem &sm) {
     if ((threadIdx.x & 31) == 0) {
       const Taught t = taught[turn];
       sm.k = {t.w * t.mass / s.z, 0.0f};
@@ -323,8 +327,6 @@ struct DistillLeader {
     te = join<32, false>(te, kLog2e);
     const bool any = on && te.z != 0.0f;  // (a NaN is an entry)
     const float mass = settle<32>(p, en, row, te, lane, any, GRAD);
-    // (the student's logits are in shared memory: they have been read before
-    // another block can store a gradient over them)
     if (lane == 0) taught[turn] = {mass, any ? w : 0.0f, any};
     meet_arrive<64>(kTaught);
     if (GRAD) count<32>(en, lane, any);

@@ -208,8 +208,7 @@ struct PolicyLeader {
     a = soon;
     a.xa = logit_of<T>(p, row, a);
   }
-  // sent along with the statistics, so that it has been read before another
-  // block can write its gradient over the logits
+  // (a number that is sent has been read)
   __device__ __forceinline__ float held() const { return a.xa; }
   __device__ __forceinline__ void plan(int64_t row, const Stats &s, bool on, int rank,
                                        LongSmem &sm) {

@@ -295,6 +295,21 @@ def test_in_place(rl, V, dtype):
     assert got.data_ptr() == x.data_ptr() and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("V,dtype", [(120000, "f32"), (250000, "bf16")])
+def test_in_place_with_many_entries(rl, V, dtype):
+    # rows that blocks of a cluster share: none may write over a logit that
+    # another has still to read for its entries
+    n, K = 400, 1000
+    x = (torch.randn(n, V, device="cuda") * 2).to(DT[dtype])
+    ids = torch.randint(0, V, (n, K), device="cuda", dtype=torch.int32)
+    top, w = torch.randn(n, K, device="cuda"), torch.rand(n, device="cuda") + 0.5
+    want, loss = rl.rlcs_distill_loss_backward(w, x, ids, top, return_loss=True)
+    for _ in range(3):
+        y = x.clone()
+        got, same = rl.rlcs_distill_loss_backward(w, y, ids, top, out=y, return_loss=True)
+        assert torch.equal(same, loss) and torch.equal(got, want)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [6, 33, 1000, 5000, 40001, 140000])
 def test_rows_that_are_not_finite(rl, V, dtype):
