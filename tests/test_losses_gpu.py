@@ -119,6 +119,32 @@ def check_policy(rl, data, kl_coef=0.0, ent=0.0, low=0.2, high=0.2, use_ref=True
     close("dlogits", dx, wdx, slope * p)
     assert torch.equal(dx, alone)
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,V,below", [(1, 26, 60.0), (3, 130, 20.0), (2, 1000, 60.0),
+                                       (4, 20000, 30.0), (300, 5, 60.0), (1, 131075, 80.0)])
+def test_policy_close_to_its_reference(rl, dtype, n, V, below):
+    """kl where ref_logp is within a hundredth of a log probability far below 0:
+    off by (e^d - 1) times the error of l, which is that of log z alone, not a
+    rounding of l's own size (2^-24 below). z: 2^-22 from each power of two, a few
+    2^-24 from the rounded exponents near the top and some from adding: 2^-20.
+    kl itself comes from d by a few roundings, 2^-21 of it."""
+    g = gen(V + n)
+    x = (2.0 * torch.randn(n, V, generator=g)).to(DT[dtype])
+    a = torch.randint(0, V, (n,), generator=g, dtype=torch.int32)
+    x[torch.arange(n), a.long()] = -below - 3.0 * torch.rand(n, generator=g).to(DT[dtype])
+    l = ref.logs(x).gather(1, a.long()[:, None])[:, 0]
+    against = (l + 0.01 * torch.randn(n, generator=g, dtype=torch.float64)).float()
+    old, adv = l.float(), torch.randn(n, generator=g)
+    want = ref.policy(x, a, old, adv, against)
+    got = rl.rlcs_policy_loss(*cuda(x, a, old, adv), ref_logp=against.cuda())
+    d = against.double() - l
+    tol = torch.expm1(d).abs() * 2.0 ** -20 + want[3] * 2.0 ** -21 + 2.0 ** -40
+    off = (got.kl.double().cpu() - want[3]).abs()
+    assert bool((off <= tol).all()), float((off / tol).max())
+    off = (got.logp.double().cpu() - l).abs()  # one rounding, to the type it has
+    assert bool((off <= 2.0 ** -20 + l.abs() * 2.0 ** -24).all())
+
+
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", SIZES)
