@@ -61,48 +61,54 @@ __device__ __forceinline__ void zero_scalars(const PolicyArgs &p, int64_t row) {
   if (p.entropy) p.entropy[row] = 0.0f;
   if (p.kl) p.kl[row] = 0.0f;
 }
+// log z = k ln 2 + log f with f near 1.
+struct LogZ {
+  float k, f;
+  __device__ __forceinline__ float whole() const { return fmaf(k, kLn2, f); }
+};
+__device__ __forceinline__ LogZ log_of(float z) {
+  if (!(z >= 0.5f && z < 1e30f)) return {0.0f, logf(z)};  // (a NaN, or no finite logit)
+  const int bits = __float_as_int(z), k = (bits - 0x3f400000) >> 23;
+  return {(float)k, logf(__int_as_float(bits - (k << 23)))};  // of 0.75 to 1.5
+}
 // log p of an element in two parts, so that its difference from another log
 // probability keeps its digits: off by what z is, about 1e-7, not by roundings
-// of l's own size. y is formed with its rounding's remainder and z = 2^k f with f
-// near 1; c stands for log2 e, off by kOff of it, which moves log z by the mean
-// of y.
+// of l's own size. y is formed with its rounding's remainder; c stands for
+// log2 e, off by kOff of it, which moves log z by the mean of y. A block's other
+// warps wait for this: with a division and a logarithm more of its own it took 8
+// us of 300 at 16384 x 32768 bf16.
 struct LogProb {
   float high, low;
   __device__ __forceinline__ float above(float v) const { return (v - high) - low; }  // v - l
 };
-__device__ __forceinline__ LogProb log_prob(float x, const Stats &s, const Base &base) {
-  constexpr double kLn2 = 0.693147180559945309417232, kLog2 = 1.442695040888963407359925;
-  constexpr float kHigh = (float)kLn2, kLow = (float)(kLn2 - (double)kHigh);
+__device__ __forceinline__ LogProb log_prob(float x, const LogZ &z, float mean, const Base &base) {
+  constexpr double kExact = 0.693147180559945309417232, kLog2 = 1.442695040888963407359925;
+  constexpr float kLow = (float)(kExact - (double)kLn2);
   constexpr float kOff = (float)(kLog2 / (double)kLog2e - 1.0);
-  const float plain = base.y(x);
-  if (!(fabsf(plain) < 1e30f) || !(s.z > 0.0f && s.z < 1e30f))
-    return {plain * kHigh - logf(s.z), 0.0f};
   // (each operation rounded by itself: none may be fused with the next)
   const float xc = __fmul_rn(x, base.c), xc_rest = fmaf(x, base.c, -xc);
   const float y = __fsub_rn(xc, base.m), back = __fsub_rn(y, xc);
   const float y_rest = __fadd_rn(
       __fadd_rn(__fsub_rn(xc, __fsub_rn(y, back)), __fsub_rn(-base.m, back)), xc_rest);
-  const int bits = __float_as_int(s.z), k = (bits - 0x3f400000) >> 23;
-  const float f = __int_as_float(bits - (k << 23)), kf = (float)k;  // 0.75 <= f < 1.5
-  const float a = __fsub_rn(y, kf), a_back = __fsub_rn(a, y);
+  const float a = __fsub_rn(y, z.k), a_back = __fsub_rn(a, y);
   const float a_rest =
-      __fadd_rn(__fsub_rn(y, __fsub_rn(a, a_back)), __fsub_rn(-kf, a_back));
-  const float high = __fmul_rn(a, kHigh);
-  float low = fmaf(a, kHigh, -high);
-  low = fmaf(a, kLow, low);
-  low = fmaf(a_rest + y_rest, kHigh, low);
-  low = fmaf(kOff * kHigh, y - s.t / s.z, low);
-  return {high, low - logf(f)};
+      __fadd_rn(__fsub_rn(y, __fsub_rn(a, a_back)), __fsub_rn(-z.k, a_back));
+  const float high = __fmul_rn(a, kLn2);
+  float low = fmaf(a, kLow, fmaf(a, kLn2, -high));
+  low = fmaf(a_rest + y_rest, kLn2, low);
+  low = fmaf(kOff * kLn2, y - mean, low);
+  return {high, (fabsf(y) < 1e30f ? low : 0.0f) - z.f};
 }
 // The row's scalars, written by the thread that `writes`, and its gradient:
 // e (a + b y) and `gain` more at the action.
 __device__ __forceinline__ Coefficients finish(const PolicyArgs &p, int64_t row, const Token &a,
                                                const Stats &s, bool writes, float &gain) {
-  const float logz = logf(s.z);
-  float H = logz - s.t / s.z * kLn2;
+  const LogZ z = log_of(s.z);
+  const float logz = z.whole(), inv = 1.0f / s.z, mean = s.t * inv;
+  float H = fmaf(-mean, kLn2, logz);
   if (H < 0.0f) H = 0.0f;  // (a certain action, by a rounding)
   LogProb l = {NAN, 0.0f};
-  if (a.there) l = log_prob(a.xa, s, base_of(s.top, kLog2e));
+  if (a.there) l = log_prob(a.xa, z, mean, base_of(s.top, kLog2e));
   if (l.high + l.low > 0.0f) l = {0.0f, 0.0f};
   const float ratio = expf(-l.above(a.old));
   const float free = ratio * a.adv, held = fminf(fmaxf(ratio, p.low), p.high) * a.adv;
@@ -123,7 +129,7 @@ __device__ __forceinline__ Coefficients finish(const PolicyArgs &p, int64_t row,
     if (p.logp) p.logp[row] = l.high + l.low;
     if (p.entropy) p.entropy[row] = H;
   }
-  const float u = a.w / s.z;
+  const float u = a.w * inv;
   gain = a.w * g;
   return {u * (p.entropy_coef * (H - logz) - g), u * p.entropy_coef * kLn2};
 }
