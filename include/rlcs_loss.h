@@ -20,9 +20,8 @@
  * argument errors returned before anything is launched):
  *
  * Types.     logits and dlogits are float32 or bfloat16 (`dtype`); every other
- *            number is float32, sums over a row are float32 and the few
- *            numbers of a token whose differences cancel (log probabilities)
- *            are formed in double.
+ *            number is float32, and so are sums over a row. A log probability
+ *            whose difference from another counts is formed in two parts.
  * Layout.    logits rows start `row_stride` elements apart (at least V), on any
  *            boundary of the element type; dlogits is contiguous. dlogits may be
  *            the logits themselves (same address, row_stride = V), no other

@@ -8,7 +8,8 @@ namespace {
 // The highest code that a call has recorded on this device.
 __device__ uint32_t device_status;
 constexpr int kMaxTop = 1024;
-static_assert(2 * (kMaxTop * 16 + 2 * kMaxTop * 8) <= kLongEntries, "a block holds a token's entries");
+static_assert(2 * (kMaxTop * 16 + 2 * kMaxTop * 8) <= kLongEntries,
+              "a block holds a token's entries");
 
 struct DistillArgs {
   const void *logits;
@@ -102,7 +103,8 @@ __device__ __forceinline__ void count(const Entries &en, int lane, bool on) {
     for (int j = lane; j < en.K; j += LANES) {
       const int id = en.id[j];
       if (id < 0) continue;
-      for (int s = slot_of(en, id);; s = (s + 1) & (en.slots - 1)) {  // (half of the slots stay free)
+      // (half of the slots stay free)
+      for (int s = slot_of(en, id);; s = (s + 1) & (en.slots - 1)) {
         const int was = atomicCAS(&en.table[s], -1, id);
         if (was == -1 || was == id) {
           atomicAdd(&en.times[s], 1);
@@ -454,7 +456,8 @@ struct Distill {
   }
   template <int TEAM, int NV>
   static rlcs_status team(const DistillArgs &p, size_t entries, cudaStream_t st) {
-    return launch_team<distill_team_kernel<T, GRAD, TEAM, NV>, TEAM>(p, team_blocks(NV), entries, st);
+    return launch_team<distill_team_kernel<T, GRAD, TEAM, NV>, TEAM>(p, team_blocks(NV), entries,
+                                                                     st);
   }
   template <int NV>
   static rlcs_status block(const DistillArgs &p, int ranks, size_t entries, cudaStream_t st) {

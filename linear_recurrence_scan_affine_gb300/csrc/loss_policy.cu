@@ -135,7 +135,8 @@ __device__ __forceinline__ Coefficients finish(const PolicyArgs &p, int64_t row,
 }
 
 template <class T, bool GRAD, int TEAM, int NV>
-__global__ void __launch_bounds__(kTeamBlock, team_blocks(NV)) policy_team_kernel(const PolicyArgs p) {
+__global__ void __launch_bounds__(kTeamBlock, team_blocks(NV))
+    policy_team_kernel(const PolicyArgs p) {
   pdl_wait();
   pdl_launch_dependents();
   constexpr int kTeams = kTeamBlock / TEAM;
@@ -272,7 +273,8 @@ struct PolicyLeader {
 };
 
 template <class T, bool GRAD, int NV>
-__global__ void __launch_bounds__(kLongBlock, long_blocks(NV)) policy_long_kernel(const PolicyArgs p) {
+__global__ void __launch_bounds__(kLongBlock, long_blocks(NV))
+    policy_long_kernel(const PolicyArgs p) {
   pdl_wait();
   pdl_launch_dependents();
   PolicyLeader<T> leader = {p, {}, {}};

@@ -429,7 +429,7 @@ __device__ __forceinline__ Stats few_stats(const float *x, int V, float c) {
 //
 // The next row's words come into shared memory, by one bulk copy, while this
 // row's are worked on in registers. Policy loss and gradient of 16384 x 32768
-// bfloat16, a quarter masked: 298 us, 6.3 TB/s, 0.94 of the copy rate (326 with
+// bfloat16, a quarter masked: 304 us, 6.2 TB/s, 0.92 of the copy rate (326 with
 // loads to registers as these were used up; 391 with fixed rows, 16 warps of half
 // as many words and no leader, where every warp worked out every row's scalars).
 // Distillation over 4096 x 131072 bfloat16, 64 entries, four blocks to a row: 383

@@ -571,7 +571,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)  // the type that the product takes
                   w[e] = pack_bf16(__uint_as_float(v[i][2 * e]) * d[BACK ? 2 * e : -2 * e],
-                                   __uint_as_float(v[i][2 * e + 1]) * d[BACK ? 2 * e + 1 : -2 * e - 1]);
+                                   __uint_as_float(v[i][2 * e + 1]) *
+                                       d[BACK ? 2 * e + 1 : -2 * e - 1]);
               } else if (BACK ? i0 + i < (warp & 3) : i0 + i > (warp & 3)) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = 0;
@@ -663,7 +664,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
             for (int b = 0; b < DP / 64; ++b)
               if (b * 64 < p.D)
-                store_box(sm.x[o % kStages] + b * 16384, unit->walk ? &second.out : &first.out, b * 64,
+                store_box(sm.x[o % kStages] + b * 16384,
+                          unit->walk ? &second.out : &first.out, b * 64,
                           h0 + j, g.lo + first_row(g, c));
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
