@@ -801,6 +801,11 @@ struct SumArgs {
   int Hk, ny, D, length;
   bool final;         // one segment to a sequence: add what is left of init
   bool all;           // sums of every segment, not only of those that others follow
+  // Launched behind the walk, whose results are not read here: blocks take the
+  // SMs that the walk's end leaves idle. All blocks of the walk have waited for
+  // what came before when the first of these starts, so the wait, which is for
+  // the walk, stands at the end: what comes next may count on both.
+  bool beside;
   float in_scale;
 };
 constexpr int kSumStages = 3;
@@ -824,7 +829,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
                       const __grid_constant__ CUtensorMap mz, const SumArgs p) {
   extern __shared__ __align__(1024) unsigned char raw[];
   SumSmem<DP> &sm = *reinterpret_cast<SumSmem<DP> *>(raw);
-  pdl_wait();
+  if (!p.beside) pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
   const int h = blockIdx.x % p.Hk, slot = blockIdx.x / p.Hk;
@@ -866,6 +871,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       for (int i = threadIdx.x; i < p.D * p.D; i += kSumThreads)
         p.sums[at + i] = p.init ? p.init[at + i] : 0.0f;
     }
+    if (p.beside) pdl_wait();
     return;
   }
   const int chunks = (g.rows + kChunk - 1) / kChunk, items = chunks * p.ny;
@@ -977,6 +983,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   tc::fence_after_sync();
   settle(sm.abort);
   if (warp == 9) tc::tmem_dealloc(sm.tmem, 128);
+  if (p.beside) pdl_wait();
 }
 
 // The states before each segment from what the segments add, in place, and
@@ -1090,15 +1097,18 @@ rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
         !map_of(&m[i].out, {w.out[i], (int64_t)w.Hk * w.nx * w.D, w.D}, w, w.Hk * w.nx))
       return RLCS_ERR_CUDA;
   cudaError_t e = cudaSuccess;
-  if (split || w.last) {
+  const auto sum = [&](bool beside) {
     const SumArgs a = {w.log_decay, w.cu, split ? nullptr : w.init, split ? sums : w.last,
                        w.sequences, w.tokens, w.Hk, w.ny, w.D, (int)length, !split,
-                       w.last != nullptr, w.in_scale};
+                       w.last != nullptr, beside, w.in_scale};
     constexpr size_t smem = sizeof(SumSmem<DP>);
-    e = allow_dynamic_smem<linear_sum_kernel<DP, BACK>>(smem);
-    if (e != cudaSuccess) return launched(e);
-    e = launch_ex(linear_sum_kernel<DP, BACK>, dim3((unsigned)(n * w.Hk)), dim3(kSumThreads), smem,
-                  st, true, m[0].y, m[0].z, a);
+    const cudaError_t e = allow_dynamic_smem<linear_sum_kernel<DP, BACK>>(smem);
+    if (e != cudaSuccess) return e;
+    return launch_ex(linear_sum_kernel<DP, BACK>, dim3((unsigned)(n * w.Hk)), dim3(kSumThreads),
+                     smem, st, true, m[0].y, m[0].z, a);
+  };
+  if (split || (w.last && w.tokens == 0)) {
+    e = sum(false);
     if (e != cudaSuccess) return launched(e);
   }
   if (split) {
@@ -1136,9 +1146,11 @@ rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
   static_assert(smem <= 232448 && sizeof(SumSmem<DP>) <= 232448, "a block has 227 KB");
   e = allow_dynamic_smem<linear_walk_kernel<DP, BACK>>(smem);
   if (e != cudaSuccess) return launched(e);
-  return launched(launch_ex(linear_walk_kernel<DP, BACK>,
-                            dim3((unsigned)(n * w.Hk * (w.nx / l.nx) * w.walks)),
-                            dim3(kWalkThreads), smem, st, true, m[0], m[1], a));
+  e = launch_ex(linear_walk_kernel<DP, BACK>,
+                dim3((unsigned)(n * w.Hk * (w.nx / l.nx) * w.walks)), dim3(kWalkThreads), smem, st,
+                true, m[0], m[1], a);
+  if (e == cudaSuccess && w.last && !split) e = sum(true);
+  return launched(e);
 }
 template <bool BACK>
 rlcs_status launch(const Walk &w, float *sums, cudaStream_t st) {
