@@ -416,6 +416,41 @@ def test_repeats_streams_and_graphs(rl):
     rl.check_scratch()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_calls_one_behind_another(rl, D):
+    """Last states come from a launch that runs beside the one before it: calls
+    that follow each other without a pause, each on what the last has just written
+    and with its inputs written over at once, give the bits of calls that wait."""
+    lens = [1000, 3, 0, 517] + [40] * 30
+    H = 6
+    args = case(33, lens, H, H, D, True)
+    cu = bounds(lens).cuda()
+
+    def chain(pause):
+        q, k, v, ld, S, do, dl = cuda(*args)
+        stop = torch.cuda.synchronize if pause else (lambda: None)
+        got = []
+        # (keys grow by the product of states and values: 1, 10, 30, 5000, 10^8, 10^19
+        # and then, at the sixth call, gradients past float32's range)
+        for _ in range(4):
+            stop()
+            out, last = rl.rlcs_linear_attention(q, k, v, ld, cu, state=S, return_state=True)
+            stop()
+            grads = rl.rlcs_linear_attention_backward(out, q, k, v, ld, cu, state=S, dlast=last)
+            stop()
+            got += [t.clone() for t in (out, last, *grads)]
+            stop()
+            for t in (k, v, S):
+                t.fill_(float("nan"))
+            k, v, S = grads[1].mul_(0.01), out.mul_(0.1), last
+        return got
+
+    want = chain(True)
+    for _ in range(3):
+        for a, b in zip(want, chain(False)):
+            assert bool(torch.isfinite(a).all()) and torch.equal(a, b)
+
+
 def test_offsets_past_32_bits(rl):
     # 2^31 elements and more to an array: its last sequence equals a small call's
     H, D = 128, 128
