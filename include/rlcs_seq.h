@@ -230,8 +230,9 @@ rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_ba
  * q [tokens, Hq, D], k and v [tokens, Hk, D], strides and alignment, D,
  * cu_seqlens and the tokens that no sequence holds as for rlcs_attention; out
  * [tokens, Hq, D] contiguous. log_decay [Hk] float32 in device memory: 0 keeps
- * everything, -infinity nothing but the token itself (positive values grow, as
- * the formula has it). state [sequences, Hk, D, D] float32 (keys' dimension
+ * everything, -infinity nothing but the token itself; positive values grow, as
+ * the formula has it, and results stand as long as the powers that they need
+ * are in float32's range. state [sequences, Hk, D, D] float32 (keys' dimension
  * first) may be NULL (0); last_state, of the same shape, receives the state
  * after each sequence's last token (of an empty sequence: `state`) and may be
  * NULL. Both start on 16-byte boundaries. The bounds of the sequences must be

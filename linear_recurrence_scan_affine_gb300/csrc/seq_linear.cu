@@ -174,9 +174,14 @@ struct Unit {
   int slot, h0;             // the first head of x
   int walk;
   bool end;                 // no unit: the block is done
-  float power[kChunk + 1];  // of the decay
-  // what weights are multiplied by: decays d steps long at 31 + d, zeros before
-  // them; and the columns' part of them in a block of 16
+  // Powers of the decay, and what weights are multiplied by: decays d steps long
+  // at 31 + d, zeros before them; and the columns' part of them in a block of 16.
+  // A growing decay may be infinite at more steps than a segment of one chunk
+  // has weights for, and there are zeros: backwards a row meets columns past the
+  // segment's end, where P is 0, and without a state to begin with the last row
+  // takes in nothing by one step more than its longest weight. (Where another
+  // chunk follows, its weights are as long.)
+  float power[kChunk + 1];
   float decay[31 + kChunk];
   alignas(16) float near[16];
 };
@@ -383,10 +388,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         const float scale = p.in_scale * p.out_scale;
         for (int i = lane; i < 31 + kChunk; i += 32) {
           const float f = i < 31 ? 0.0f : power(l2, i - 31);
-          u.decay[i] = scale * f;
-          if (i >= 31) u.power[i - 31] = f;
+          u.decay[i] = i - 31 < g.rows ? scale * f : 0.0f;
+          if (i >= 31) u.power[i - 31] = i - 31 < g.rows || p.init ? f : 0.0f;
         }
-        if (lane == 0) u.power[kChunk] = power(l2, kChunk);
+        if (lane == 0) u.power[kChunk] = g.rows > kChunk || p.init ? power(l2, kChunk) : 0.0f;
         if (lane < 16) u.near[lane] = scale * power(l2, BACK ? lane : 15 - lane);
       }
       if (lane == 0) u.g = g, u.slot = slot, u.h0 = h0, u.walk = walk, u.end = end;
@@ -549,6 +554,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       if (!unit) break;
       const Segment &g = unit->g;
       const int chunks = chunks_of(g), h0 = unit->h0;
+      const bool one = BACK && g.rows < kChunk;
       for (int c = 0; c < chunks; ++c) {
         for (int j = 0; j < items; ++j, ++it) {
           tc::warp_wait(&sm.p_full[it & 1], (it >> 1) & 1, abort);
@@ -565,8 +571,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             for (int i = 0; i < 2; ++i) {
               const int c0 = (2 * (i0 + i) + half) * 16;
               uint32_t w[8];
-              // (the same for the whole warp)
-              if (i0 + i == (warp & 3)) {  // the row's own 32 columns are among these
+              // (the same for the whole warp; the row's own 32 columns are among these,
+              // or it is a short segment backwards, see Unit::decay)
+              if (i0 + i == (warp & 3) || (one && i0 + i > (warp & 3))) {
                 const float *d = unit->decay + 31 + (BACK ? c0 - r : r - c0);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)  // the type that the product takes

@@ -481,7 +481,8 @@ def rlcs_linear_attention(q, k, v, log_decay, cu_seqlens, state=None, scale=None
     """Linear attention over packed sequences: S_t = exp(log_decay) S_{t-1} +
     k_t v_t^T per key/value head, out_t = scale q_t S_t. q [tokens, Hq, D], k
     and v [tokens, Hk, D], cu_seqlens and `scale` as for rlcs_attention;
-    log_decay [Hk] float32 (at most 0); `state` [sequences, Hk, D, D] float32,
+    log_decay [Hk] float32 (0 keeps everything, -inf nothing but the token,
+    positive values grow); `state` [sequences, Hk, D, D] float32,
     the states before the first tokens, defaults to zeros. Returns out
     [tokens, Hq, D], or (out, states after the last tokens) with
     `return_state`. Tokens that no sequence holds get zeros."""
