@@ -126,13 +126,14 @@ __device__ __forceinline__ float target(const Entries &en, int j) {
 }
 // The lane's part of the loss.
 template <int LANES>
-__device__ __forceinline__ float loss_part(const Entries &en, const Base &base, float logz,
-                                           int lane) {
+__device__ __forceinline__ float loss_part(const Entries &en, const Base &base, float c,
+                                           float logz, int lane) {
+  const float ln2 = log_of_2(base, c);
   float loss = 0.0f;
   for (int j = lane; j < en.K; j += LANES) {
     const float e = en.q[j];
     if (en.id[j] >= 0 && (e > 0.0f || e != e))
-      loss += e * (en.lq[j] - (base.y(en.x[j]) * kLn2 - logz));
+      loss += e * (en.lq[j] - (base.y(en.x[j]) * ln2 - logz));
   }
   return loss;
 }
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kTeamBlock, team_blocks(NV))
     if (GRAD) count<TEAM>(en, lane, on);
     const Stats s = lanes_stats<T, TEAM, NV, false>(q, c, NV);
     const Base base = base_of(s.top, c);
-    const float loss = lanes_sum<TEAM>(on ? loss_part<TEAM>(en, base, logf(s.z), lane) : 0.0f);
+    const float loss = lanes_sum<TEAM>(on ? loss_part<TEAM>(en, base, c, logf(s.z), lane) : 0.0f);
     if (row < p.tokens && lane == 0 && p.loss) p.loss[row] = loss;
     const float w = GRAD && on ? p.dloss[row] * p.inv_t : 0.0f;
     const Coefficients k = {w * mass / s.z, 0.0f};
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kFewBlock) distill_few_kernel(const DistillArg
     const float c = p.inv_t * kLog2e;
     const Stats s = few_stats<false>(mine, V, c);
     const Base base = base_of(s.top, c);
-    const float logz = logf(s.z);
+    const float logz = logf(s.z), ln2 = log_of_2(base, c);
     float lse = te.top + logf(te.z), mass = 1.0f;
     if (p.teacher_lse) {
       lse = p.teacher_lse[row];
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kFewBlock) distill_few_kernel(const DistillArg
     for (int j = 0; j < p.K; ++j) {
       if (absent(p, ids[j], top[j])) continue;
       const float lq = top[j] * p.inv_t - lse, e = expf(lq);
-      if (e > 0.0f || e != e) loss += e * (lq - (base.y(mine[ids[j]]) * kLn2 - logz));
+      if (e > 0.0f || e != e) loss += e * (lq - (base.y(mine[ids[j]]) * ln2 - logz));
     }
     if (GRAD) {
       const float w = p.dloss[row] * p.inv_t, a = w * mass / s.z;
@@ -344,9 +345,10 @@ struct DistillLeader {
       if (next < p.tokens) prepare(next, more, turn ^ 1);
       const Entries en = set(turn);
       const Taught t = taught[turn];
-      const Base base = base_of(s.top, p.inv_t * kLog2e);
+      const float c = p.inv_t * kLog2e;
+      const Base base = base_of(s.top, c);
       if (rank == 0) {
-        const float loss = lanes_sum<32>(t.any ? loss_part<32>(en, base, logf(s.z), lane) : 0.0f);
+        const float loss = lanes_sum<32>(t.any ? loss_part<32>(en, base, c, logf(s.z), lane) : 0.0f);
         if (lane == 0 && p.loss) p.loss[row] = loss;
       }
       if (GRAD) {
@@ -420,8 +422,8 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillArg
       lse = top + logf(block_sum(sum, part));
     }
     const Stats s = row_stats<T, false>(x, p.V, c, part);
-    const float logz = logf(s.z);
     const Base base = base_of(s.top, c);
+    const float logz = logf(s.z), ln2 = log_of_2(base, c);
     float mass = 0.0f, loss = 0.0f;
     for (int j = threadIdx.x; j < p.K; j += kThreads) {
       q[j] = 0.0f;
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillArg
       const float lq = logq[j] - lse, e = expf(lq);
       q[j] = e;
       mass += e;
-      if (e > 0.0f || e != e) loss += e * (lq - (base.y(at[j]) * kLn2 - logz));
+      if (e > 0.0f || e != e) loss += e * (lq - (base.y(at[j]) * ln2 - logz));
     }
     mass = block_sum(mass, part);
     loss = block_sum(loss, part);

@@ -67,7 +67,7 @@ struct LogZ {
   __device__ __forceinline__ float whole() const { return fmaf(k, kLn2, f); }
 };
 __device__ __forceinline__ LogZ log_of(float z) {
-  if (!(z >= 0.5f && z < 1e30f)) return {0.0f, logf(z)};  // (a NaN, or no finite logit)
+  if (!(z >= 1e-30f && z < 1e30f)) return {0.0f, logf(z)};  // (a NaN, or no finite logit)
   const int bits = __float_as_int(z), k = (bits - 0x3f400000) >> 23;
   return {(float)k, logf(__int_as_float(bits - (k << 23)))};  // of 0.75 to 1.5
 }
@@ -81,15 +81,19 @@ struct LogProb {
   float high, low;
   __device__ __forceinline__ float above(float v) const { return (v - high) - low; }  // v - l
 };
-__device__ __forceinline__ LogProb log_prob(float x, const LogZ &z, float mean, const Base &base) {
+__device__ __forceinline__ LogProb log_prob(float x, const LogZ &z, float mean, float top) {
   constexpr double kExact = 0.693147180559945309417232, kLog2 = 1.442695040888963407359925;
   constexpr float kLow = (float)(kExact - (double)kLn2);
   constexpr float kOff = (float)(kLog2 / (double)kLog2e - 1.0);
+  const Base base = base_of(top, kLog2e);
+  if (__builtin_expect(base.c != kLog2e, false)) return {x - top, -z.whole()};
   // (each operation rounded by itself: none may be fused with the next)
-  const float xc = __fmul_rn(x, base.c), xc_rest = fmaf(x, base.c, -xc);
-  const float y = __fsub_rn(xc, base.m), back = __fsub_rn(y, xc);
+  const float xc = __fmul_rn(x, base.c);
+  const float xc_rest = fabsf(xc) < 1e30f ? fmaf(x, base.c, -xc) : 0.0f;
+  const float d = __fsub_rn(xc, base.m), back = __fsub_rn(d, xc), y = __fadd_rn(d, xc_rest);
   const float y_rest = __fadd_rn(
-      __fadd_rn(__fsub_rn(xc, __fsub_rn(y, back)), __fsub_rn(-base.m, back)), xc_rest);
+      __fadd_rn(__fsub_rn(xc, __fsub_rn(d, back)), __fsub_rn(-base.m, back)),
+      __fsub_rn(xc_rest, __fsub_rn(y, d)));
   const float a = __fsub_rn(y, z.k), a_back = __fsub_rn(a, y);
   const float a_rest =
       __fadd_rn(__fsub_rn(y, __fsub_rn(a, a_back)), __fsub_rn(-z.k, a_back));
@@ -108,7 +112,7 @@ __device__ __forceinline__ Coefficients finish(const PolicyArgs &p, int64_t row,
   float H = fmaf(-mean, kLn2, logz);
   if (H < 0.0f) H = 0.0f;  // (a certain action, by a rounding)
   LogProb l = {NAN, 0.0f};
-  if (a.there) l = log_prob(a.xa, z, mean, base_of(s.top, kLog2e));
+  if (a.there) l = log_prob(a.xa, z, mean, s.top);
   if (l.high + l.low > 0.0f) l = {0.0f, 0.0f};
   const float ratio = expf(-l.above(a.old));
   const float free = ratio * a.adv, held = fminf(fmaxf(ratio, p.low), p.high) * a.adv;

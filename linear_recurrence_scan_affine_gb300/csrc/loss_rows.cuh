@@ -7,7 +7,10 @@
 // a row's distribution is p_i = e_i / z with log p_i = y_i ln 2 - log z, and
 // both gradients are e_i (A + B y_i) plus terms at a few named elements. y is
 // one fused multiply and add, rounded once at its own size: a common offset of
-// the logits, however large, costs no digits.
+// the logits costs no digits. (What m is rounded by is in every y alike: 1/2 at
+// most up to c top = 2^24, 32 at 2^30, where logits differ by half a power of
+// two and more and an entropy is off by up to 2^-17. For rows yet further from 0
+// see Base.)
 #pragma once
 
 #include <type_traits>
@@ -43,18 +46,28 @@ __device__ __forceinline__ float value(const bf *p) { return __bfloat162float(*p
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(bf *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// What y is formed with. Where c times the largest logit would pass float32's
-// range, logits differ by nothing or by far more than any exponent holds: c is
-// 1 there. A row (or part of one) with nothing above -infinity has e = 0.
+// What y is formed with. In a row with c top above 2^30 logits differ by nothing
+// or by 64 powers of two and more, so that only its largest count, and c may be
+// any larger number: a power of two, which rounds no product with top, or 1 where
+// that would pass float32's range. A row (or part of one) with nothing above
+// -infinity has e = 0.
 struct Base {
   float c, m;
   __device__ __forceinline__ float y(float x) const { return fmaf(x, c, -m); }
 };
-constexpr float kFar = 1e38f;
+constexpr float kFar = 1073741824.0f;
 __device__ __forceinline__ Base base_of(float top, float c) {
-  if (top == -INFINITY) return {c, 0.0f};
   const float m = top * c;
-  return fabsf(m) <= kFar ? Base{c, m} : Base{1.0f, top};
+  if (__builtin_expect(fabsf(m) <= kFar, true)) return {c, m};
+  if (top == -INFINITY) return {c, 0.0f};
+  const float power = __int_as_float((__float_as_int(c) + 0x7fffff) & 0x7f800000);
+  const float other = fabsf(m) <= 1e38f ? power : 1.0f;
+  return {other, top * other};
+}
+// A y of 1 in natural logarithms (base.c is c, or a power of two).
+__device__ __forceinline__ float log_of_2(const Base &base, float c) {
+  if (__builtin_expect(base.c == c, true)) return kLn2;
+  return kLn2 * c * __int_as_float(0x7f000000 - __float_as_int(base.c));
 }
 // A row's statistics: its largest logit, z and sum e y.
 struct Stats {
@@ -66,8 +79,11 @@ __device__ __forceinline__ float bounded(float y) { return fmaxf(y, -200.0f); }
 // How far (in base 2) a part's base lies below the whole's.
 __device__ __forceinline__ float below(float part, float whole, float c) {
   const float a = part * c, b = whole * c;
-  if (fabsf(a) <= kFar && fabsf(b) <= kFar) return a - b;
-  return part == whole ? 0.0f : -INFINITY;
+  if (__builtin_expect(fabsf(a) <= kFar && fabsf(b) <= kFar, true)) return a - b;
+  if (part == whole) return 0.0f;
+  // (a part whose e are all 0 is as far as can be)
+  return fabsf(a) <= kFar ? fmaf(-whole, c, a)
+                          : (fabsf(b) <= kFar ? fmaf(part, c, -b) : (part - whole) * c);
 }
 
 __device__ __forceinline__ float warp_max(float x) {
