@@ -33,7 +33,7 @@ struct DistillArgs {
 // more than once.
 struct Entries {
   int *id;    // -1 where absent
-  float *q;   // the teacher's logit / T, then q, then the sum of q over the id
+  float *q;   // the teacher's logit, then q
   float *lq;  // log q
   float *x;   // the student's logit
   int *table, *times;
@@ -60,33 +60,52 @@ __device__ __forceinline__ Entries entries_at(float *raw, int K, int slots) {
 __device__ __forceinline__ bool absent(const DistillArgs &p, int id, float t) {
   return id < 0 || id >= p.V || t == -INFINITY;
 }
-// One entry, and the lane's sum of exp over its entries.
+// Teachers' logits are taken from their largest before anything else: an offset
+// that they have in common costs no digits, and one at the type's lowest value
+// has no weight, whatever the temperature makes of it. z is the sum of
+// exp((t - top) / T).
+__device__ __forceinline__ void add_entry(const DistillArgs &p, float t, Stats &sum) {
+  if (t > sum.top) sum.z *= expf((sum.top - t) * p.inv_t), sum.top = t;  // (0 at first)
+  sum.z += expf((t - sum.top) * p.inv_t);
+}
+__device__ __forceinline__ float log_q(const DistillArgs &p, int64_t row, const Stats &sum,
+                                       float log_sum, float t) {
+  return p.teacher_lse ? fmaf(t, p.inv_t, -p.teacher_lse[row])
+                       : (t - sum.top) * p.inv_t - log_sum;
+}
+// The sum of q, of entries that have any.
+__device__ __forceinline__ float mass_of(const DistillArgs &p, int64_t row, const Stats &sum) {
+  return p.teacher_lse ? sum.z * expf(fmaf(sum.top, p.inv_t, -p.teacher_lse[row])) : 1.0f;
+}
+template <int LANES>
+__device__ __forceinline__ Stats join_entries(const DistillArgs &p, const Stats &sum) {
+  const float top = lanes_max<LANES>(sum.top);
+  const float f = sum.top == top ? 1.0f : expf((sum.top - top) * p.inv_t);
+  return {top, lanes_sum<LANES>(f * sum.z), 0.0f};
+}
+// One entry, and the lane's sum over its entries.
 __device__ __forceinline__ void enter(const DistillArgs &p, const Entries &en, int j, int id,
                                       float t, float x, Stats &sum) {
   if (absent(p, id, t)) id = -1;
   en.id[j] = id;
-  en.q[j] = t *= p.inv_t;
+  en.q[j] = t;
   en.x[j] = x;
-  if (id < 0) return;
-  if (t > sum.top) sum.z *= expf(sum.top - t), sum.top = t;  // (0 at first)
-  sum.z += expf(t - sum.top);
+  if (id >= 0) add_entry(p, t, sum);
 }
-// After all have been entered: q, log q, their mass, and at last the sum of q
-// over every entry of the same id. Only an id that occurs twice is looked for
-// in all entries, in their order.
+// After all have been entered: q, log q and their mass, and the table of ids to
+// begin with. Only an id that occurs twice is looked for in all entries, in their
+// order.
 template <int LANES>
 __device__ __forceinline__ float settle(const DistillArgs &p, const Entries &en, int64_t row,
                                         const Stats &sum, int lane, bool on, bool grad) {
   float mass = 1.0f;
   if (on) {
-    float lse = sum.top + logf(sum.z);
-    if (p.teacher_lse) {
-      lse = p.teacher_lse[row];
-      mass = sum.z * expf(sum.top - lse);
-    }
+    const float log_sum = logf(sum.z);
+    mass = mass_of(p, row, sum);
     for (int j = lane; j < en.K; j += LANES) {
-      en.lq[j] = en.q[j] - lse;
-      en.q[j] = expf(en.lq[j]);
+      const float lq = log_q(p, row, sum, log_sum, en.q[j]);
+      en.lq[j] = lq;
+      en.q[j] = expf(lq);
     }
     if (grad)
       for (int i = lane; i < en.slots; i += LANES) en.table[i] = -1, en.times[i] = 0;
@@ -171,7 +190,7 @@ __global__ void __launch_bounds__(kTeamBlock, team_blocks(NV))
         enter(p, en, j, id, t, absent(p, id, t) ? 0.0f : value(x + id), te);
       }
     }
-    te = join<TEAM, false>(te, kLog2e);
+    te = join_entries<TEAM>(p, te);
     on = on && te.z != 0.0f;  // (a NaN is an entry)
     const float mass = settle<TEAM>(p, en, row, te, lane, on, GRAD);
     if (GRAD) count<TEAM>(en, lane, on);
@@ -219,12 +238,8 @@ __global__ void __launch_bounds__(kFewBlock) distill_few_kernel(const DistillArg
   const float *top = p.top + row * p.K;
   Stats te = {-INFINITY, 0.0f, 0.0f};
   if (on)
-    for (int j = 0; j < p.K; ++j) {
-      const float t = top[j] * p.inv_t;
-      if (absent(p, ids[j], top[j])) continue;
-      if (t > te.top) te.z *= expf(te.top - t), te.top = t;
-      te.z += expf(t - te.top);
-    }
+    for (int j = 0; j < p.K; ++j)
+      if (!absent(p, ids[j], top[j])) add_entry(p, top[j], te);
   if (p.mask) __syncthreads();
   few_copy<T, true>(p, static_cast<T *>(nullptr), x, rows, row0, pitch,
                     [&](int i) { return !p.mask || live[i]; });
@@ -237,21 +252,18 @@ __global__ void __launch_bounds__(kFewBlock) distill_few_kernel(const DistillArg
     const Stats s = few_stats<false>(mine, V, c);
     const Base base = base_of(s.top, c);
     const float logz = logf(s.z), ln2 = log_of_2(base, c);
-    float lse = te.top + logf(te.z), mass = 1.0f;
-    if (p.teacher_lse) {
-      lse = p.teacher_lse[row];
-      mass = te.z * expf(te.top - lse);
-    }
+    const float log_sum = logf(te.z);
     for (int j = 0; j < p.K; ++j) {
       if (absent(p, ids[j], top[j])) continue;
-      const float lq = top[j] * p.inv_t - lse, e = expf(lq);
+      const float lq = log_q(p, row, te, log_sum, top[j]), e = expf(lq);
       if (e > 0.0f || e != e) loss += e * (lq - (base.y(mine[ids[j]]) * ln2 - logz));
     }
     if (GRAD) {
-      const float w = p.dloss[row] * p.inv_t, a = w * mass / s.z;
+      const float w = p.dloss[row] * p.inv_t, a = w * mass_of(p, row, te) / s.z;
       for (int i = 0; i < V; ++i) mine[i] = ex2(base.y(mine[i])) * a;
       for (int j = 0; j < p.K; ++j)
-        if (!absent(p, ids[j], top[j])) mine[ids[j]] -= w * expf(top[j] * p.inv_t - lse);
+        if (!absent(p, ids[j], top[j]))
+          mine[ids[j]] -= w * expf(log_q(p, row, te, log_sum, top[j]));
     }
   } else if (GRAD && held) {
     for (int i = 0; i < V; ++i) mine[i] = 0.0f;
@@ -327,7 +339,7 @@ struct DistillLeader {
         enter(p, en, j, i, v, absent(p, i, v) ? 0.0f : value(x + i), te);
       }
     }
-    te = join<32, false>(te, kLog2e);
+    te = join_entries<32>(p, te);
     const bool any = on && te.z != 0.0f;  // (a NaN is an entry)
     const float mass = settle<32>(p, en, row, te, lane, any, GRAD);
     if (lane == 0) taught[turn] = {mass, any ? w : 0.0f, any};
@@ -400,9 +412,9 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillArg
         const float v = p.top[row * p.K + j];
         const bool there = i >= 0 && i < p.V && !(v == -INFINITY);
         id[j] = there ? i : -1;
-        logq[j] = v * p.inv_t;
+        logq[j] = v;
         at[j] = there ? value(x + i) : 0.0f;
-        if (there) top = fmaxf(top, v != v ? INFINITY : logq[j]);
+        if (there) top = fmaxf(top, v != v ? INFINITY : v);
       }
     top = block_max(top, part);
     on = on && top > -INFINITY;
@@ -412,15 +424,13 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillArg
         for (int64_t i = threadIdx.x; i < p.V; i += kThreads) put(dx + i, 0.0f);
       continue;
     }
-    float lse;
-    if (p.teacher_lse) {
-      lse = p.teacher_lse[row];
-    } else {
-      float sum = 0.0f;
+    Stats te = {top, 0.0f, 0.0f};
+    if (!p.teacher_lse) {
       for (int j = threadIdx.x; j < p.K; j += kThreads)
-        if (id[j] >= 0) sum += expf(logq[j] - top);
-      lse = top + logf(block_sum(sum, part));
+        if (id[j] >= 0) te.z += expf((logq[j] - top) * p.inv_t);
+      te.z = block_sum(te.z, part);
     }
+    const float log_sum = logf(te.z);
     const Stats s = row_stats<T, false>(x, p.V, c, part);
     const Base base = base_of(s.top, c);
     const float logz = logf(s.z), ln2 = log_of_2(base, c);
@@ -428,7 +438,7 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillArg
     for (int j = threadIdx.x; j < p.K; j += kThreads) {
       q[j] = 0.0f;
       if (id[j] < 0) continue;
-      const float lq = logq[j] - lse, e = expf(lq);
+      const float lq = log_q(p, row, te, log_sum, logq[j]), e = expf(lq);
       q[j] = e;
       mass += e;
       if (e > 0.0f || e != e) loss += e * (lq - (base.y(at[j]) * ln2 - logz));
