@@ -200,6 +200,7 @@ struct WalkSmem {
   alignas(16) uint4 answer[2];  // of the requests for a unit
   uint64_t asked[2], unit_full[2], unit_empty[2];
   uint64_t x_full[kStages], x_empty[kStages], y_full[kStages], y_empty[kStages];
+  uint64_t result[kStages];  // a chunk's results are in the place of its x
   uint64_t p_full[2], p_ready[2], y_used[2], y_ready[2], o_full, o_free, u_full, s_ready, s_used;
   uint8_t order[kOrdered];
   uint32_t tmem;
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     for (uint64_t *b : {&sm.p_ready[0], &sm.p_ready[1], &sm.y_ready[0], &sm.y_ready[1], &sm.o_free,
                         &sm.s_ready})
       mbar_init(b, 8);
+    for (int i = 0; i < kStages; ++i) mbar_init(&sm.result[i], 8);
     for (uint64_t *b : {&sm.unit_empty[0], &sm.unit_empty[1]}) mbar_init(b, 18);
     fence_mbar_init();
   }
@@ -649,8 +651,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             }
           }
           if (whole) fence_proxy_async_shared();
-          __syncwarp();
-          asm volatile("bar.arrive %0, 288;" ::"r"(1 + o % kStages) : "memory");
+          tc::warp_arrive(&sm.result[o % kStages], lead);
           ++o;
         }
       }
@@ -666,18 +667,19 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       const int chunks = chunks_of(g), h0 = unit->h0;
       for (int c = 0; c < chunks; ++c)
         for (int j = 0; j < nx; ++j, ++o) {
-          asm volatile("bar.sync %0, 288;" ::"r"(1 + o % kStages) : "memory");
-          if (lane == 0 && rows_of(g, c) == kChunk && !*abort) {
+          const int st = o % kStages;
+          const bool there = tc::warp_wait(&sm.result[st], (o / kStages) & 1, abort);
+          if (lane == 0 && there && rows_of(g, c) == kChunk && !*abort) {
 #pragma unroll
             for (int b = 0; b < DP / 64; ++b)
               if (b * 64 < p.D)
-                store_box(sm.x[o % kStages] + b * 16384,
+                store_box(sm.x[st] + b * 16384,
                           unit->walk ? &second.out : &first.out, b * 64,
                           h0 + j, g.lo + first_row(g, c));
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           }
-          tc::warp_arrive(&sm.x_empty[o % kStages], lead);
+          tc::warp_arrive(&sm.x_empty[st], lead);
         }
       unit_done(k);
     }
