@@ -236,7 +236,7 @@ rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_ba
  * first) may be NULL (0); last_state, of the same shape, receives the state
  * after each sequence's last token (of an empty sequence: `state`) and may be
  * NULL. Both start on 16-byte boundaries. The bounds of the sequences must be
- * nondecreasing. An element that is not finite makes the rest of its
+ * nondecreasing; at most 2^31 - 128 tokens. An element that is not finite makes the rest of its
  * sequence so, and may make so the tokens before it in its own tile of 128;
  * other sequences and heads stay as they are.
  * `scratch`: rlcs_linear_attention_scratch_bytes(...) bytes, 16-byte aligned,

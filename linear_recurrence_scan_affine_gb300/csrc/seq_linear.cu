@@ -265,7 +265,7 @@ __device__ __forceinline__ void store_box(const void *from, const CUtensorMap *m
 __device__ __noinline__ void zero_unheld(bf *out, int width, int lo, int hi, int tokens,
                                          int64_t share, int64_t shares) {
   const int eights = width / 8;
-  const int64_t n = (int64_t)(lo + tokens - hi) * eights;
+  const int64_t n = ((int64_t)lo + tokens - hi) * eights;
   for (int64_t i = share * 32 + (threadIdx.x & 31); i < n; i += shares * 32) {
     const int64_t row = i / eights;
     reinterpret_cast<uint4 *>(out + (row < lo ? row : row - lo + hi) * width)[i % eights] =
@@ -1272,9 +1272,11 @@ rlcs_status strides_usable(const void *p, int64_t ts, int64_t hs, int64_t tokens
   return ts % 8 == 0 && hs % 8 == 0 && aligned(p, 16) ? RLCS_OK : RLCS_ERR_MISALIGNED;
 }
 
+// (rounded up to whole chunks, a segment's length is an int)
+constexpr int64_t kMaxTokens = INT32_MAX / kChunk * kChunk;
 bool linear_sizes(int64_t sequences, int64_t tokens, int64_t Hq, int64_t Hk, int64_t D,
                   double scale, rlcs_dtype t) {
-  return sequences >= 0 && tokens >= 0 && tokens <= INT32_MAX && Hq > 0 && Hk > 0 &&
+  return sequences >= 0 && tokens >= 0 && tokens <= kMaxTokens && Hq > 0 && Hk > 0 &&
          Hq % Hk == 0 && D > 0 && D <= 128 && D % 8 == 0 && t == RLCS_BF16 && scale >= 1e-30 &&
          scale <= 1e30 && product_fits(tokens, Hq, D) && sequences < INT32_MAX - 1024 &&
          Hq < INT32_MAX && (sequences + tokens / 64 + 1) * Hq < (int64_t)INT32_MAX / 2;
