@@ -1014,7 +1014,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const JoinArgs p) {
   if (i >= size || unit >= p.sequences * p.Hk) return;
   const int seq = (int)(unit / p.Hk), h = (int)(unit % p.Hk);
   const int lo = bound(p.cu, seq, (int)p.tokens), hi = bound(p.cu, seq + 1, (int)p.tokens);
-  const int len = hi > lo ? hi - lo : 0, n = (len + p.length - 1) / p.length;
+  const int len = hi > lo ? hi - lo : 0, n = len / p.length + (len % p.length != 0);
   const float l2 = __ldg(p.log_decay + h) * kLog2e;
   const int64_t own = unit * size + (p.transposed ? i % p.D * p.D + i / p.D : i);
   float run = p.init ? __ldg(p.init + own) : 0.0f;
