@@ -513,6 +513,22 @@ __device__ __forceinline__ void tell(const float4 *place, const uint64_t *bar, u
       : "memory");
 }
 
+// The end of a block one of whose waits ran out, by its leader's warp: copies under
+// way arrive, and while other blocks of the cluster still write to its shared
+// memory it stays. (A cluster's barrier opens when all threads that have not ended
+// are there; what the others wait for before they end has limits.) Every other
+// block has had all that is sent to it when it ends. (With __nanosleep in the loop,
+// never run, 4096 x 131072 with a teacher took 405 us for 392.)
+__device__ __forceinline__ void settle(int ranks) {
+  const uint64_t until = globaltimer_ns() + 2000000;
+  while (globaltimer_ns() < until) {
+  }
+  __syncwarp();
+  if (ranks == 1) return;
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // What a loss adds, each call by a whole warp. The leader:
 //   ahead(next, more)  ask for a token's own numbers, a row ahead
 //   before(next, more) what of them does not need the row's statistics
@@ -600,8 +616,8 @@ __device__ __forceinline__ void long_rows(const Args &p, float c, uint32_t *stat
           tell(&sm.ranks[turn][rank], &sm.told[turn], lane,
                make_float4(s.top, s.z, s.t, held));
         tc::warp_wait(&sm.told[turn], (i >> 1) & 1, abort);
-        const float4 v = lane % kMaxRanks < ranks ? sm.ranks[turn][lane % kMaxRanks]
-                                                  : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+        float4 v = sm.ranks[turn][lane & (ranks - 1)];
+        if (lane % kMaxRanks >= ranks) v.y = v.z = 0.0f;  // (a part of nothing)
         s = join<kMaxRanks, ENTROPY>({v.x, v.y, v.z}, c);
       }
       // every block of the cluster has read the answer by now
@@ -613,7 +629,10 @@ __device__ __forceinline__ void long_rows(const Args &p, float c, uint32_t *stat
       row = next;
       on = more;
     }
-    if (lane == 0 && *abort) atomicMax(status, (uint32_t)RLCS_ERR_TIMEOUT);
+    if (*abort) {
+      if (lane == 0) atomicMax(status, (uint32_t)RLCS_ERR_TIMEOUT);
+      settle(ranks);
+    }
     return;
   }
 
