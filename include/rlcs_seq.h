@@ -236,9 +236,12 @@ rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_ba
  * first) may be NULL (0); last_state, of the same shape, receives the state
  * after each sequence's last token (of an empty sequence: `state`) and may be
  * NULL. Both start on 16-byte boundaries. The bounds of the sequences must be
- * nondecreasing; at most 2^31 - 128 tokens. An element that is not finite makes the rest of its
- * sequence so, and may make so the tokens before it in its own tile of 128;
- * other sequences and heads stay as they are.
+ * nondecreasing; at most 2^31 - 128 tokens. An element that is not finite
+ * makes not finite what depends on it by the definition, to the end of its
+ * sequence, and nothing else: no earlier token, sequence or head.
+ * Keys' products with queries, decayed keys and the state, where a product
+ * takes them, are rounded to bfloat16 for it; sums and the state itself are
+ * float32.
  * `scratch`: rlcs_linear_attention_scratch_bytes(...) bytes, 16-byte aligned,
  * used as that of rlcs_attention_backward. What waits that ran out leave
  * behind is in rlcs_attention_status too. */

@@ -109,6 +109,17 @@ __device__ __forceinline__ float power(float l2, int n) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Eight products of bf16, summed in fp32.
+__device__ __forceinline__ float dot8(const uint4 &u, const uint4 &v) {
+  const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
+  float t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), t);
+    t = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), t);
+  }
+  return t;
+}
 __device__ __forceinline__ float2 pair(const uint32_t *r) {
   return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
@@ -157,6 +168,7 @@ struct WalkArgs {
   // of 8 x 4096, 16 heads of 128, 292 and 303).
   int walks;           // 1, or 2
   bf *out[2];          // [tokens, heads of x, D]
+  View x[2], y[2], z[2];
   bool transposed[2];  // init is [z's dimension, y's]
   int64_t sequences, tokens;
   int heads, group;    // heads of x; of x to a state
@@ -201,6 +213,7 @@ struct WalkSmem {
   uint64_t asked[2], unit_full[2], unit_empty[2];
   uint64_t x_full[kStages], x_empty[kStages], y_full[kStages], y_empty[kStages];
   uint64_t result[kStages];  // a chunk's results are in the place of its x
+  uint64_t odd[kStages][8];  // to a warp: columns of them without P' Z, see add_seen
   uint64_t p_full[2], p_ready[2], y_used[2], y_ready[2], o_full, o_free, u_full, s_ready, s_used;
   uint8_t order[kOrdered];
   uint32_t tmem;
@@ -273,6 +286,109 @@ __device__ __noinline__ void zero_unheld(bf *out, int width, int lo, int hi, int
   }
 }
 
+// Of row r of a tile, where column col's word of 16 bytes lies.
+__device__ __forceinline__ int place(int r, int col) {
+  return col / 64 * 16384 + r * 128 + ((col % 64 / 8 ^ (r & 7)) * 16);
+}
+// A tile's product P' Z adds 0 times each token that a row does not see, and so a NaN
+// for one that is not finite. A warp that finds such columns leaves P' Z out of them in
+// its rows (bits of `odd`), and the warp that copies out adds it, from memory and to
+// each row from the tokens that it sees alone. What the state gives is rounded to
+// bfloat16 before: once more than elsewhere, in such columns alone.
+template <int DP, bool BACK>
+__device__ __forceinline__ void add_seen(const WalkArgs &p, const Unit *u, int j, int first, int n,
+                                         uint64_t *odd, unsigned char *tile) {
+  constexpr int kPairs = DP / 64;  // columns 2 lane + 64 m and the next to a lane
+  const int lane = threadIdx.x & 31, ny = BACK ? p.ny : 1, head = u->h0 + (BACK ? 0 : j);
+  const View x = p.x[u->walk], y = p.y[u->walk], z = p.z[u->walk];
+  const int64_t token = (int64_t)u->g.lo + first, head0 = (int64_t)(u->h0 / p.group) * ny;
+  const auto word = [&](const View &v, int c, int s, int col) {
+    return *reinterpret_cast<const uint32_t *>(v.p + (token + c) * v.token +
+                                               (head0 + s) * v.head + col);
+  };
+  // Tokens in the order seen (backwards from the last): how many a row may see before
+  // one makes a column, or by its key all of them, not finite for good.
+  int until[kPairs][2], all = kChunk;
+#pragma unroll
+  for (int m = 0; m < kPairs; ++m) until[m][0] = until[m][1] = kChunk;
+  for (int s = 0; s < ny; ++s)
+#pragma unroll 4
+    for (int k = n - 1; k >= 0; --k)
+#pragma unroll
+      for (int m = 0; m < kPairs; ++m) {
+        const int col = 2 * lane + 64 * m, c = BACK ? n - 1 - k : k;
+        if (col >= p.D) continue;
+        const uint32_t a = word(y, c, s, col), b = word(z, c, s, col);
+        if (tc::special(a)) all = min(all, k);
+        if (tc::special(b) & 0x8000u) until[m][0] = min(until[m][0], k);
+        if (tc::special(b) & 0x80000000u) until[m][1] = min(until[m][1], k);
+      }
+  all = __reduce_min_sync(kFull, all);
+#pragma unroll 1
+  for (int r = 0; r < n; ++r) {
+    const int sees = BACK ? n - r : r + 1;  // tokens
+    const bf *xr = x.p + (token + r) * x.token + head * x.head;
+    uint32_t own = 0;
+#pragma unroll
+    for (int m = 0; m < kPairs; ++m)
+      if (2 * lane + 64 * m < p.D)
+        own |= tc::special(*reinterpret_cast<const uint32_t *>(xr + 2 * lane + 64 * m));
+    const int lasts = __any_sync(kFull, own != 0) ? 0 : all;
+    bool fix[kPairs][2], wanted = false;    // columns to form, and those with a sum to form
+    float sum[kPairs][2];
+#pragma unroll
+    for (int m = 0; m < kPairs; ++m)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = 2 * lane + 64 * m + e;
+        fix[m][e] = odd[col / (DP / 2) * 4 + r / 32] >> col % (DP / 2) & 1;
+        const bool lost = min(lasts, until[m][e]) < sees;
+        sum[m][e] = lost ? NAN : 0.0f;
+        wanted |= fix[m][e] && !lost;
+      }
+    if (__any_sync(kFull, wanted)) {
+#pragma unroll 1
+      for (int i0 = 0; i0 < ny * sees; i0 += 32) {
+        float w = 0.0f;  // a term to a lane
+        if (i0 + lane < ny * sees) {
+          const int apart = (i0 + lane) % sees;
+          const bf *yr = y.p + (token + (BACK ? r + apart : r - apart)) * y.token +
+                         (head0 + (i0 + lane) / sees) * y.head;
+#pragma unroll 1
+          for (int d = 0; d < p.D; d += 8)
+            w += dot8(*reinterpret_cast<const uint4 *>(xr + d),
+                      *reinterpret_cast<const uint4 *>(yr + d));
+          w *= u->decay[31 + apart];
+        }
+#pragma unroll 4
+        for (int i = i0; i < min(i0 + 32, ny * sees); ++i) {
+          const float f = __shfl_sync(kFull, w, i - i0);
+#pragma unroll
+          for (int m = 0; m < kPairs; ++m)
+            if (2 * lane + 64 * m < p.D) {
+              const uint32_t v = word(z, BACK ? r + i % sees : r - i % sees, i / sees,
+                                      2 * lane + 64 * m);
+              sum[m][0] = fmaf(f, __uint_as_float(v << 16), sum[m][0]);
+              sum[m][1] = fmaf(f, __uint_as_float(v & 0xffff0000u), sum[m][1]);
+            }
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < kPairs; ++m) {
+      const int col = 2 * lane + 64 * m;
+      if (col >= p.D || !(fix[m][0] || fix[m][1])) continue;
+      uint32_t *at = reinterpret_cast<uint32_t *>(tile + place(r, col) + col % 8 * 2);
+      *at = pack_bf16(__uint_as_float(*at << 16) + (fix[m][0] ? sum[m][0] : 0.0f),
+                      __uint_as_float(*at & 0xffff0000u) + (fix[m][1] ? sum[m][1] : 0.0f));
+    }
+  }
+  __syncwarp();
+  if (lane < 8) odd[lane] = 0;
+  fence_proxy_async_shared();
+  __syncwarp();
+}
+
 template <int DP, bool BACK>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     linear_walk_kernel(const __grid_constant__ WalkMaps first,
@@ -299,6 +415,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                         &sm.s_ready})
       mbar_init(b, 8);
     for (int i = 0; i < kStages; ++i) mbar_init(&sm.result[i], 8);
+    for (int i = 0; i < kStages * 8; ++i) sm.odd[0][i] = 0;
     for (uint64_t *b : {&sm.unit_empty[0], &sm.unit_empty[1]}) mbar_init(b, 18);
     fence_mbar_init();
   }
@@ -607,16 +724,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
           if (BACK && j + 1 < items) continue;
           const int n = rows_of(g, c), to_row = BACK ? n - 1 - r : r + 1;
           const float into = unit->power[to_row < 0 ? 0 : to_row] * p.out_scale;
-          const int64_t row = (int64_t)g.lo + first_row(g, c) + r;
-          const int head = h0 + (BACK ? 0 : j);
-          bf *out = p.out[unit->walk] + (row * p.heads + head) * p.D + half * (DP / 2);
-          // A whole chunk's results take the place of its X and are copied out
-          // from there; rows of the last one are stored as they are.
-          const bool whole = n == kChunk;
+          // Results take the place of their X and are copied out from there.
           unsigned char *tile = sm.x[o % kStages];
           tc::warp_wait(&sm.o_full, o & 1, abort);
           tc::fence_after_sync();
-          const bool on = (whole || r < n) && !*abort;
           const float2 f = make_float2(into, into);
 #pragma unroll
           for (int i = 0; i < DP / 64; ++i) {
@@ -624,10 +735,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tc::ld32(tO + lanes + half * (DP / 2) + i * 32, a);
             tc::ld32(tX + lanes + half * (DP / 2) + i * 32, b);
             tc::wait_ld();
-            if (i + 1 == DP / 64) {
-              tc::fence_before_sync();
-              tc::warp_arrive(&sm.o_free, lead);
-            }
             // (a row that the state does not reach takes nothing of it, whatever it holds)
             if (into == 0.0f)
 #pragma unroll
@@ -643,14 +750,52 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 w[k] = pack_bf16(t.x, t.y);
               }
               const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
-              if (whole)
-                *reinterpret_cast<uint4 *>(tile + col / 64 * 16384 + r * 128 +
-                                           ((col % 64 / 8 ^ (r & 7)) * 16)) = v;
-              else if (on && col < p.D)
-                *reinterpret_cast<uint4 *>(out + i * 32 + e) = v;
+              *reinterpret_cast<uint4 *>(tile + place(r, col)) = v;
             }
           }
-          if (whole) fence_proxy_async_shared();
+          // The row of these 32 that sees the fewest of them has all columns finite, or
+          // something is looked at: see add_seen.
+          __syncwarp();
+          const int least = row0 + (BACK ? 31 : 0), pick = half * (DP / 2) + lane * (DP / 64);
+          const unsigned char *at = tile + place(least, pick) + pick % 8 * 2;
+          const uint32_t odd = DP == 128 ? tc::special(*reinterpret_cast<const uint32_t *>(at))
+                                         : tc::special(*reinterpret_cast<const uint16_t *>(at));
+          if (__any_sync(kFull, odd != 0) && row0 < n && !*abort) {
+            uint64_t own = 0;  // columns of P' Z that have it (it may be the state's alone)
+#pragma unroll 1
+            for (int i = 0; i < DP / 2; i += 8) {
+              uint32_t a[8];
+              tc::ld8(tO + lanes + half * (DP / 2) + i, a);
+              tc::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const bool fine = fabsf(__uint_as_float(a[e])) < INFINITY;
+                own |= (uint64_t)(__any_sync(kFull, r < n && !fine) != 0) << (i + e);
+              }
+            }
+#pragma unroll 1
+            for (int i = 0; i < DP / 2; i += 8) {
+              if (!(own >> i & 255)) continue;
+              uint32_t a[8], b[8], w[4];
+              tc::ld8(tO + lanes + half * (DP / 2) + i, a);
+              tc::ld8(tX + lanes + half * (DP / 2) + i, b);
+              tc::wait_ld();
+              float t[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                t[e] = into == 0.0f ? 0.0f : __uint_as_float(b[e]) * into;
+                if (!(own >> (i + e) & 1)) t[e] += __uint_as_float(a[e]);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[k] = pack_bf16(t[2 * k], t[2 * k + 1]);
+              *reinterpret_cast<uint4 *>(tile + place(r, half * (DP / 2) + i)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (lane == 0) sm.odd[o % kStages][warp] = own;
+          }
+          tc::fence_before_sync();
+          tc::warp_arrive(&sm.o_free, lead);
+          fence_proxy_async_shared();
           tc::warp_arrive(&sm.result[o % kStages], lead);
           ++o;
         }
@@ -658,7 +803,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
       unit_done(k);
     }
   } else if (warp == 18) {
-    // results of a whole chunk, from where X was; X is free when they have been read
+    // results, from where X was; X is free when they have been read
     int o = 0;
     for (int k = 0;; ++k) {
       const Unit *unit = next_unit(k);
@@ -669,7 +814,20 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         for (int j = 0; j < nx; ++j, ++o) {
           const int st = o % kStages;
           const bool there = tc::warp_wait(&sm.result[st], (o / kStages) & 1, abort);
-          if (lane == 0 && there && rows_of(g, c) == kChunk && !*abort) {
+          const int n = rows_of(g, c);
+          if (there && __any_sync(kFull, sm.odd[st][lane & 7] != 0) && !*abort)
+            add_seen<DP, BACK>(p, unit, j, first_row(g, c), n, sm.odd[st], sm.x[st]);
+          if (!there || *abort) {
+          } else if (n < kChunk) {  // (what follows in memory is another's)
+            bf *out = p.out[unit->walk] +
+                      (((int64_t)g.lo + first_row(g, c)) * p.heads + h0 + j) * p.D;
+            const int row = lane / (DP / 8), col = lane % (DP / 8) * 8;
+            if (col < p.D)
+#pragma unroll 4
+              for (int r = row; r < n; r += 256 / DP)
+                *reinterpret_cast<uint4 *>(out + (int64_t)r * p.heads * p.D + col) =
+                    *reinterpret_cast<const uint4 *>(sm.x[st] + place(r, col));
+          } else if (lane == 0) {
 #pragma unroll
             for (int b = 0; b < DP / 64; ++b)
               if (b * 64 < p.D)
@@ -1138,6 +1296,9 @@ rlcs_status launch_walk(const Walk &w, float *sums, cudaStream_t st) {
   a.walks = w.walks;
   for (int i = 0; i < w.walks; ++i) {
     a.out[i] = w.out[i];
+    a.x[i] = w.x[i];
+    a.y[i] = w.y[i];
+    a.z[i] = w.z[i];
     a.transposed[i] = split ? w.transposed[i] != w.transposed[0] : w.transposed[i];
   }
   a.sequences = w.sequences;

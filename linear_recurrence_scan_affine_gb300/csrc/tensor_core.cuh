@@ -100,6 +100,14 @@ __device__ __forceinline__ void ld16(uint32_t addr, uint32_t (&r)[16]) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void ld8(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -230,8 +238,12 @@ __device__ __forceinline__ void clear_rows(unsigned char *tile, int from, int la
       reinterpret_cast<uint4 *>(tile + c * ROWS * 128)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_shared();
 }
-// Nonzero where one of eight bf16 values is infinite or NaN: its exponent's
-// eight ones carry into the sign's place.
+// The signs' places of two bf16 values, set where one is infinite or NaN: its
+// exponent's eight ones carry there.
+__device__ __forceinline__ uint32_t special(uint32_t w) {
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+// The same of eight values together.
 __device__ __forceinline__ uint32_t special(const uint4 &x) {
   auto carry = [](uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; };
   return (carry(x.x) | carry(x.y) | carry(x.z) | carry(x.w)) & 0x80008000u;
