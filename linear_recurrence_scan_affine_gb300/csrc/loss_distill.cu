@@ -360,7 +360,8 @@ struct DistillLeader {
       const float c = p.inv_t * kLog2e;
       const Base base = base_of(s.top, c);
       if (rank == 0) {
-        const float loss = lanes_sum<32>(t.any ? loss_part<32>(en, base, c, logf(s.z), lane) : 0.0f);
+        const float loss =
+            lanes_sum<32>(t.any ? loss_part<32>(en, base, c, logf(s.z), lane) : 0.0f);
         if (lane == 0 && p.loss) p.loss[row] = loss;
       }
       if (GRAD) {

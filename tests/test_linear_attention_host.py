@@ -38,9 +38,9 @@ def test_token_counts_past_whole_chunks_are_refused():
         assert need(1, n, 1, 1, 8) == 0
         q, k, v, ld, cu, out, scratch = (ctypes.c_void_p(0x7f0000000000 + (i << 36))
                                          for i in range(7))
-        assert lib.rlcs_linear_attention(q, 8, 8, k, 8, 8, v, 8, 8, ld, cu, None, out, None, 1, n, 1,
-                                         1, 8, 1.0, BF16, scratch, 1 << 30, None) == INVALID
+        views = (q, 8, 8, k, 8, 8, v, 8, 8, ld, cu, None)
+        assert lib.rlcs_linear_attention(*views, out, None, 1, n, 1, 1, 8, 1.0, BF16, scratch,
+                                         1 << 30, None) == INVALID
         dq, dk, dv = (ctypes.c_void_p(0x7f0000000000 + (i << 36)) for i in range(7, 10))
-        assert lib.rlcs_linear_attention_backward(out, q, 8, 8, k, 8, 8, v, 8, 8, ld, cu, None, None,
-                                                  dq, dk, dv, None, 1, n, 1, 1, 8, 1.0, BF16,
-                                                  scratch, 1 << 30, None) == INVALID
+        assert lib.rlcs_linear_attention_backward(out, *views, None, dq, dk, dv, None, 1, n, 1, 1,
+                                                  8, 1.0, BF16, scratch, 1 << 30, None) == INVALID

@@ -1,7 +1,6 @@
 """The losses where logits are large, against their definitions in 64 bits
-(tests/loss_reference.py), on every way that rows are
-laid out: a thread, lanes or a warp to a row, a block, a cluster, a row read
-twice.
+(tests/loss_reference.py), on every way that rows are laid out: a thread, lanes or
+a warp to a row, a block, a cluster, a row read twice.
 
 Bounds. As in tests/test_losses_gpu.py: F of the larger of a result's size and
 the array's root mean square. A log probability is a difference of logits, each
@@ -51,7 +50,8 @@ def some(g, near, k=1):
                         for r in near]).int()
 
 
-SIZES = [1e7, 2e7, -2e7, 1e8, -3e8, 7e8, 3e9, -3e9, 5e9, -1e10, 1e20, -1e20, 1e30, -1e30, 1e38, -2e38]
+SIZES = [1e7, 2e7, -2e7, 1e8, -3e8, 7e8, 3e9, -3e9, 5e9, -1e10, 1e20, -1e20, 1e30, -1e30, 1e38,
+         -2e38]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

@@ -19,4 +19,5 @@ def test_a_block_whose_wait_ran_out_stays_for_its_cluster():
     body = src[src.index("__device__ __forceinline__ void long_rows("):]
     leader = body[body.index("if (warp == kTeam / 32)"):]
     leader = leader[:leader.index("return;")]
-    assert re.search(r"if \(\*abort\) \{[^}]*RLCS_ERR_TIMEOUT[^}]*settle\(ranks\);\s*\}\s*$", leader)
+    assert re.search(r"if \(\*abort\) \{[^}]*RLCS_ERR_TIMEOUT[^}]*settle\(ranks\);\s*\}\s*$",
+                     leader)
