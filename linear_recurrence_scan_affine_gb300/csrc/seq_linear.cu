@@ -146,6 +146,11 @@ __device__ uint32_t device_status;
 // chunk. Warp 16 copies in, warp 18 out, warp 17 issues products. In tensor
 // memory, float32: P (P' over it), O1, O2, S. Rounded to bfloat16, the type of
 // the products' operands: P', the scaled Y and S as an operand; S itself is not.
+// Results are within 2.7e-3 of 64 bits (2-norm) where rounding them alone makes
+// 1.7e-3. With each of the three in two parts that is 1.7e-3, and 8 x 4096 training
+// takes 693 us for 388, packed episodes of 64-wide heads 251 for 179: three products
+// more, and parts that take turns in the shared memory that is left. (S alone in two
+// parts: 2.3e-3; 497 and 196 us.)
 //
 // 8 x 4096, 16 heads of 128: 105 us, 5.1 TB/s, on the 128 SMs that have work; a
 // chunk takes 3900 clocks when its tiles are there, and 5300 as they come. What
@@ -955,9 +960,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 // ---------------------------------------------------------------------------
 // What a segment adds to the state: sum a^left y z^T over its tokens, left the
 // steps to its end. Float32 results come from here, so a decayed key is held in
-// two bfloat16 parts, off by at most 2^-16 together: two products. (Last states
-// are within 2e-6 of 64 bits.) 131072 tokens, 8 heads of 128, in 38 segments: 99
-// us, 5.4 TB/s; joining them 18 us.
+// two bfloat16 parts, off by at most 2^-17 together: two products. Tokens that
+// count the most are added last, as the sum is cut off to float32 at each addition:
+// states are within 3e-6 of 64 bits (2-norm; first states' gradients 1.2e-5 in the
+// other order). A third part made fast heads' 2e-7, left those of decays above 0.999
+// at 2.5e-6, and took 27 us more of 301. 131072 tokens, 8 heads of 128, in 38
+// segments: 99 us, 5.4 TB/s; joining them 18 us.
 // ---------------------------------------------------------------------------
 struct SumArgs {
   const float *log_decay;
@@ -1045,11 +1053,14 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
   volatile int *abort = &sm.abort;
   const uint32_t lead = lane == 0;
+  const auto first_of = [&](int it) {  // the first row, in the segment, of an item's tile
+    return (BACK ? chunks - 1 - it / p.ny : it / p.ny) * kChunk;
+  };
   if (warp == 8) {
     if (lane == 0)
       for (int it = 0; it < items; ++it) {
         const int st = it % kSumStages, use = it / kSumStages;
-        const int token = g.lo + g.first + it / p.ny * kChunk, head = h * p.ny + it % p.ny;
+        const int token = g.lo + g.first + first_of(it), head = h * p.ny + it % p.ny;
         if (use > 0 && !tc::mbar_wait(&sm.empty[st], (use - 1) & 1, abort)) break;
         mbar_arrive_expect_tx(&sm.full[st], DP * 256 * 2);
 #pragma unroll
@@ -1060,7 +1071,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       }
   } else if (warp == 9) {
     for (int it = 0; it < items; ++it) {
-      const int st = it % kSumStages, n = g.rows - it / p.ny * kChunk;
+      const int st = it % kSumStages, n = g.rows - first_of(it);
       if (!tc::warp_wait(&sm.full[st], (it / kSumStages) & 1, abort)) break;
       if (n < kChunk) {
         tc::clear_rows<DP, kChunk>(sm.z[st], n, lane);
@@ -1077,7 +1088,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     tc::commit(lead, &sm.done);
   } else {
     for (int it = 0; it < items; ++it) {
-      const int st = it % kSumStages, first = it / p.ny * kChunk;
+      const int st = it % kSumStages, first = first_of(it);
       tc::warp_wait(&sm.full[st], (it / kSumStages) & 1, abort);
       if (it > 0) tc::warp_wait(&sm.rest_free, (it - 1) & 1, abort);
       uint4 *y = reinterpret_cast<uint4 *>(sm.y[st]), *rest = reinterpret_cast<uint4 *>(sm.rest);
