@@ -20,16 +20,20 @@
  * argument errors returned before anything is launched):
  *
  * Types.     logits and dlogits are float32 or bfloat16 (`dtype`); every other
- *            number is float32, and so are sums over a row. A log probability
- *            whose difference from another counts is formed in two parts.
+ *            number is float32, and so are sums over a row. The policy loss forms
+ *            its action's log probability in two parts, so that its differences
+ *            from old_logp and ref_logp keep their digits; distillation forms log
+ *            q and log p in one, each from its distance to the largest logit.
  * Layout.    logits rows start `row_stride` elements apart (at least V), on any
  *            boundary of the element type; dlogits is contiguous. dlogits may be
  *            the logits themselves (same address, row_stride = V), no other
  *            overlap of an output with an input or another output is allowed.
  * Mask.      mask [tokens] uint8 may be NULL; a token whose mask is 0 gets
  *            zeros in every result, and nothing else of it is read.
- * Rows.      A logit of -infinity (or the type's lowest value) is an action
- *            that cannot be taken: probability 0, gradient 0. A row without a
+ * Rows.      A logit of -infinity (or the type's lowest value, or any other far
+ *            below the row's largest) is an action that cannot be taken:
+ *            probability 0, gradient 0. Logits of any finite size are taken as
+ *            they are, and all alike are equally likely. A row without a
  *            logit above -infinity, or with a NaN or +infinity, has no
  *            distribution: its results are NaN, other rows' are not touched.
  * Order.     No atomics: repeated calls on the same inputs give the same bits.
@@ -86,7 +90,9 @@ rlcs_status rlcs_policy_loss_backward(
  *   loss = sum_j q_j (log q_j - log p_{top_ids_j}).
  * teacher_lse [tokens] is the log of the sum of exp(logits / T) over all of the
  * teacher's logits; the q_j then add up to less than 1, and what they leave
- * adds nothing to the loss. Entries whose id lies outside [0, V) or whose
+ * adds nothing to the loss. q depends on differences of the top_logits alone
+ * (teacher_lse NULL); one at float32's lowest value has no weight beside others,
+ * at any temperature. Entries whose id lies outside [0, V) or whose
  * logit is -infinity are absent; a token all of whose entries are absent has
  * loss 0 and gradient 0, whatever its logits. An id may occur more
  * than once: its entries are separate terms. loss [tokens]. 1e-6 <=

@@ -445,11 +445,11 @@ __device__ __forceinline__ Stats few_stats(const float *x, int V, float c) {
 //
 // The next row's words come into shared memory, by one bulk copy, while this
 // row's are worked on in registers. Policy loss and gradient of 16384 x 32768
-// bfloat16, a quarter masked: 304 us, 6.2 TB/s, 0.92 of the copy rate (326 with
+// bfloat16, a quarter masked: 307 us, 6.1 TB/s, 0.91 of the copy rate (326 with
 // loads to registers as these were used up; 391 with fixed rows, 16 warps of half
 // as many words and no leader, where every warp worked out every row's scalars).
-// Distillation over 4096 x 131072 bfloat16, 64 entries, four blocks to a row: 383
-// us, 5.6 TB/s (453 without the teacher's warp).
+// Distillation over 4096 x 131072 bfloat16, 64 entries, four blocks to a row: 390
+// us, 5.5 TB/s (453 without the teacher's warp).
 // ---------------------------------------------------------------------------
 constexpr int kTeam = 256, kLongBlock = kTeam + 32, kMaxRanks = 8;
 constexpr int long_blocks(int nv) { return nv >= 16 ? 2 : (nv == 8 ? 3 : 4); }  // to an SM
@@ -821,8 +821,8 @@ rlcs_status launch_long(const Args &p, int threads, int ranks, size_t entries, c
 
 // How a call's rows are spread: the smallest team that holds a row. A row that
 // starts inside a word may straddle one more than it fills. `On` has the
-// kernels: few, team<TEAM, NV>, block<NV> and any. (524288 rows of 6 float32:
-// 78 us by teams of eight lanes, 25 by threads.)
+// kernels: few, team<TEAM, NV>, block<NV> and any. (In a graph, 524288 rows of 6
+// float32: 79 us by teams of eight lanes, 14 by threads; 200000 of 32: 26 and 16.)
 template <class T, class On, class Args>
 rlcs_status spread(const Args &p, size_t entries, cudaStream_t st) {
   const bool whole = aligned(p.logits, 16) && (p.tokens == 1 || p.row_stride % kWord<T> == 0);

@@ -79,9 +79,12 @@ __device__ __forceinline__ Segment whole_sequence(const int32_t *cu, int tokens,
   return g;
 }
 // Sequences that are not cut, the longest first, in shared memory: a block's
-// threads count for each how many come before it. (48 packed episodes of up to
-// 1024, 12 heads of 64 on 4: forward 52 us and gradient 118, in their own order
-// 72 and 170.)
+// threads count for each how many come before it. (Packed episodes of up to 1024,
+// forward and gradient, against their own order: 48, 12 heads of 64 on 4: 45 and 124
+// us, 59 and 165; 128, 16 heads of 128 on 4: 161 and 415, 211 and 523.) Of more than
+// 128 the order does not fit beside the tiles, and a caller may sort them: 129 take
+// 213 and 535 us as they come, 163 and 422 longest first; 256 take 366 and 945, 316
+// and 808.
 constexpr int kOrdered = 128;
 __device__ __forceinline__ void order_sequences(const int32_t *cu, int sequences, int tokens,
                                                 int *len, uint8_t *order) {
@@ -1229,10 +1232,15 @@ struct Walk {
 };
 
 // How a walk is laid out. Heads of x that share a state go to one block, which
-// then reads y and z and forms the state once, as far as two blocks to an SM
-// are left. Where sequences and heads alone leave SMs without work, sequences
-// are cut into segments: that costs a second reading of y and z and a pass over
-// the states, and none is under 1024 tokens.
+// then reads y and z and forms the state once, as far as a block to an SM is left.
+// Where sequences and heads alone are fewer than 3/4 of the SMs, sequences are cut
+// into segments: that costs a second reading of y and z and a pass over the states,
+// and none is under 1024 tokens. Forward, heads of 128, one sequence, uncut and cut:
+// 4 heads of 2048 tokens 39 us and 48 (so none of up to 2048 is cut), of 4096 71 and
+// 49; 16 of 16384 300 and 122; 48 of 4096 87 and 105, of 16384 317 and 259; 96 of
+// 16384 350 and 460. Of sequences that are alike more than about 56 are better left
+// whole. But lengths are not known here: one long sequence among short ones, left
+// whole, is a chain to a head, so the limit is higher; past it that is the case.
 struct Layout {
   int64_t length;  // of a segment
   int nx;          // heads of x to a block
