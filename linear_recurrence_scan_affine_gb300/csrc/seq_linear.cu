@@ -155,7 +155,7 @@ __device__ uint32_t device_status;
 // more, and parts that take turns in the shared memory that is left. (S alone in two
 // parts: 2.3e-3; 497 and 196 us.)
 //
-// 8 x 4096, 16 heads of 128: 105 us, 5.1 TB/s, on the 128 SMs that have work; a
+// 8 x 4096, 16 heads of 128: 101 us, 5.3 TB/s, on the 128 SMs that have work; a
 // chunk takes 3900 clocks when its tiles are there, and 5300 as they come. What
 // a chunk spent its time on, by clocks stamped in the kernel: decays from a
 // table for each element 1900 clocks (a product of two powers: 1100), results
