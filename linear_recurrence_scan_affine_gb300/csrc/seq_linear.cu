@@ -316,6 +316,7 @@ __device__ __forceinline__ void add_seen(const WalkArgs &p, const Unit *u, int j
   };
   // Tokens in the order seen (backwards from the last): how many a row may see before
   // one makes a column, or by its key all of them, not finite for good.
+  const bool closed = u->g.rows > 1 && u->power[1] == 0.0f;
   int until[kPairs][2], all = kChunk;
 #pragma unroll
   for (int m = 0; m < kPairs; ++m) until[m][0] = until[m][1] = kChunk;
@@ -334,7 +335,8 @@ __device__ __forceinline__ void add_seen(const WalkArgs &p, const Unit *u, int j
   all = __reduce_min_sync(kFull, all);
 #pragma unroll 1
   for (int r = 0; r < n; ++r) {
-    const int sees = BACK ? n - r : r + 1;  // tokens
+    // tokens (of a head that keeps nothing its own, and no other's place counts)
+    const int sees = closed ? 1 : (BACK ? n - r : r + 1);
     const bf *xr = x.p + (token + r) * x.token + head * x.head;
     uint32_t own = 0;
 #pragma unroll
@@ -350,7 +352,7 @@ __device__ __forceinline__ void add_seen(const WalkArgs &p, const Unit *u, int j
       for (int e = 0; e < 2; ++e) {
         const int col = 2 * lane + 64 * m + e;
         fix[m][e] = odd[col / (DP / 2) * 4 + r / 32] >> col % (DP / 2) & 1;
-        const bool lost = min(lasts, until[m][e]) < sees;
+        const bool lost = !closed && min(lasts, until[m][e]) < sees;
         sum[m][e] = lost ? NAN : 0.0f;
         wanted |= fix[m][e] && !lost;
       }
@@ -946,6 +948,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         for (int i = 0; i < HC / 32; ++i)
           tc::ld32(tU + lanes + half * HC + i * 32, *reinterpret_cast<uint32_t(*)[32]>(s + i * 32));
         tc::wait_ld();
+        // (a head that keeps nothing has no state, whatever has been added to it)
+        if (unit->power[1] == 0.0f)
+#pragma unroll
+          for (int e = 0; e < HC; ++e) s[e] = 0.0f;
         hand_over(unit->power[rows_of(g, c + 1)]);
       }
       unit_done(k);
@@ -1035,7 +1041,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const Segment g = sm.segment;
+  Segment g = sm.segment;
   // a segment that no other follows in the walk is summed for the last state alone
   const bool followed = BACK ? g.first > 0 : g.first + g.rows < g.len;
   const bool work = g.any && !sm.abort && (p.all || followed);
@@ -1052,7 +1058,13 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     if (p.beside) pdl_wait();
     return;
   }
-  const int chunks = (g.rows + kChunk - 1) / kChunk, items = chunks * p.ny;
+  // A head that keeps nothing adds a segment's last token, or backwards nothing.
+  const float kept = p.final ? power(l2, g.rows) : 0.0f;
+  if (power(l2, 1) == 0.0f) {
+    g.first += g.rows - 1;
+    g.rows = BACK ? 0 : 1;
+  }
+  const int chunks = g.rows ? (g.rows + kChunk - 1) / kChunk : 1, items = chunks * p.ny;
   const uint32_t tmem = __shfl_sync(kFull, sm.tmem, 0);
   volatile int *abort = &sm.abort;
   const uint32_t lead = lane == 0;
@@ -1134,7 +1146,6 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     const bool fine = tc::warp_wait(&sm.done, 0, abort);
     tc::fence_after_sync();
     const int64_t at = ((p.final ? (int64_t)g.seq : (int64_t)slot) * p.Hk + h) * p.D * p.D;
-    const float keep = p.final ? power(l2, g.rows) : 0.0f;
 #pragma unroll
     for (int i = 0; i < DP / 64; ++i) {
       const int col = half * (DP / 2) + i * 32;
@@ -1148,12 +1159,12 @@ __global__ void __launch_bounds__(kSumThreads, 1)
             const int64_t to = at + (int64_t)r * p.D + col + e;
             float4 v = make_float4(__uint_as_float(u[e]), __uint_as_float(u[e + 1]),
                                    __uint_as_float(u[e + 2]), __uint_as_float(u[e + 3]));
-            if (p.init && keep != 0.0f) {
+            if (p.init && kept != 0.0f) {
               const float4 o = __ldg(reinterpret_cast<const float4 *>(p.init + to));
-              v.x = fmaf(keep, o.x, v.x);
-              v.y = fmaf(keep, o.y, v.y);
-              v.z = fmaf(keep, o.z, v.z);
-              v.w = fmaf(keep, o.w, v.w);
+              v.x = fmaf(kept, o.x, v.x);
+              v.y = fmaf(kept, o.y, v.y);
+              v.z = fmaf(kept, o.z, v.z);
+              v.w = fmaf(kept, o.w, v.w);
             }
             *reinterpret_cast<float4 *>(p.sums + to) = v;
           }
