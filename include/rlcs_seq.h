@@ -241,7 +241,8 @@ rlcs_status rlcs_attention_step(const void *q, const void *k_cache, int64_t k_ba
  * sequence, and nothing else: no earlier token, sequence or head.
  * Keys' products with queries, decayed keys and the state, where a product
  * takes them, are rounded to bfloat16 for it; sums and the state itself are
- * float32.
+ * float32, and products within a tile of 128 tokens, of later tokens' keys too,
+ * have to be in its range.
  * `scratch`: rlcs_linear_attention_scratch_bytes(...) bytes, 16-byte aligned,
  * used as that of rlcs_attention_backward. What waits that ran out leave
  * behind is in rlcs_attention_status too. */
